@@ -54,7 +54,8 @@ typedef enum {
   SDPA_ERR_UNSUPPORTED_DEVICE = 3, /* no CUDA device, or not an sm_103 GPU */
   SDPA_ERR_WORKSPACE = 4,          /* workspace null or smaller than mha_workspace_size() */
   SDPA_ERR_CUDA = 5,               /* a CUDA runtime/driver call failed */
-  SDPA_ERR_DEVICE_TIMEOUT = 6      /* a kernel gave up on a bounded wait (sdpa_device_check) */
+  SDPA_ERR_DEVICE_TIMEOUT = 6,     /* a kernel gave up on a bounded wait (sdpa_device_check) */
+  SDPA_ERR_BAD_PAGE = 7            /* a page table named a page outside the cache (sdpa_device_check) */
 } sdpa_status;
 
 enum { SDPA_MASK_NONE = 0, SDPA_MASK_CAUSAL = 1, SDPA_MASK_PADDING = 2 };
@@ -232,6 +233,87 @@ sdpa_status sdpa_decode(const void* q, const void* k, const void* v, void* out, 
                         const int32_t* kv_lengths, float scale, void* stream);
 
 /*
+ * Serving from a paged cache.  The keys and values of b sequences lie in
+ * pages of page_size positions that a table hands out:
+ *   k_pages, v_pages [n_pages, h_kv, page_size, d]  bf16, device
+ *   page_table  device int32 [b, pages_per_seq]: position j of sequence s is
+ *               row j % page_size of page page_table[s][j / page_size].  Only
+ *               the entries of positions below the sequence's length are read;
+ *               sequences may share pages (a common prefix).
+ *   kv_lengths  device int32 [b]: positions of each sequence, the new tokens
+ *               of this step included (clamped into [0, pages_per_seq *
+ *               page_size]).
+ *   q_starts    device int32 [b + 1]: the new tokens of all sequences come
+ *               packed, those of sequence s as rows [q_starts[s],
+ *               q_starts[s+1]) of n_tokens rows.  Not decreasing; a sequence
+ *               may have none; rows before q_starts[0] and from q_starts[b] on
+ *               belong to no sequence, and nothing is written for them.
+ * New token i of the n of sequence s sits at position kv_lengths[s] - n + i.
+ * All three arrays are read on the device when the call runs, so a captured
+ * graph follows their values.  Head shapes: d in {16, 32, 64, 128, 256},
+ * h = group * h_kv with group <= 128 (query head x reads key-value head
+ * x / group), page_size a power of two of at least 8, pages_per_seq *
+ * page_size < 2^30; else SDPA_ERR_UNSUPPORTED.
+ * With n_tokens == 0 nothing is enqueued, and the row pointers may be NULL.
+ * A page number outside [0, n_pages) is never followed: the append skips that
+ * token's key and value, the attention takes the page as zeros, and
+ * sdpa_device_check then returns SDPA_ERR_BAD_PAGE.
+ *
+ * sdpa_paged_append stores the keys and values of the new tokens, rotating
+ * queries and keys by their positions on the way:
+ *   q [n_tokens, h, d], k, v [n_tokens, h_kv, d]  bf16, device; token rows are
+ *     q_stride, k_stride, v_stride elements apart (multiples of 8, at least
+ *     the row itself), so the three may be columns of one projection's output
+ *   q_out [n_tokens, h, d]  bf16, device, written, dense: the rotated queries.
+ *     It may be q itself when q_stride == h * d.  q and q_out may both be NULL
+ *     to append alone.
+ *   rope_freqs  device fp32 [d_rot / 2]: radians per position.  With angle
+ *     t = position * rope_freqs[j], the pair (a, b) becomes
+ *     (a cos t - b sin t, b cos t + a sin t); angles are exact to about 1e-6
+ *     at any position.  Pair j is columns j and j + d_rot / 2, or 2 j and
+ *     2 j + 1 with interleaved != 0; columns from d_rot on stay as they are.
+ *   d_rot  a multiple of 16, 0 <= d_rot <= d; 0 copies (rope_freqs may be NULL)
+ * Arithmetic is fp32, rounded once to bf16.  A token at a negative position
+ * (more new tokens than the length) is rotated but not stored.  Two tokens
+ * that the tables send to one place race.
+ */
+sdpa_status sdpa_paged_append(const void* q, const void* k, const void* v, void* q_out,
+                              void* k_pages, void* v_pages, int b, int n_tokens, int h, int h_kv,
+                              int d, int page_size, int n_pages, int pages_per_seq,
+                              const int32_t* page_table, const int32_t* q_starts,
+                              const int32_t* kv_lengths, long long q_stride, long long k_stride,
+                              long long v_stride, const float* rope_freqs, int d_rot,
+                              int interleaved, void* stream);
+
+/*
+ * Attention of the new tokens over the cache (their own keys and values
+ * appended before): the token at position i sees keys 0 .. i of its sequence
+ * (section 3.2.3).  Any mixture of single tokens, chunks behind a cached
+ * prefix and whole prompts is one call.
+ *   q   [n_tokens, h, d]  bf16, device, token rows q_stride elements apart (a
+ *       multiple of 8, at least h * d)
+ *   out [n_tokens, h, d]  bf16, device, written, dense (must not overlap q);
+ *       rows are zero for a token at a negative position
+ *   workspace: device buffer of ws_bytes >= sdpa_paged_workspace_size(...)
+ *       (may be NULL when that size is 0), 16-byte aligned, caller-owned and
+ *       reusable once the stream passes the call.  Calls that overlap on the
+ *       GPU need one each.  The size depends on the current device's SM
+ *       count: ask on the device the call runs on.
+ * Scores, softmax statistics and sums are fp32; the softmax weights enter the
+ * products with the values rounded to bf16.  Cache rows past a sequence's
+ * length may hold anything; those below it must be finite.
+ */
+size_t sdpa_paged_workspace_size(int b, int n_tokens, int h, int h_kv, int d, int page_size,
+                                 int pages_per_seq);
+
+sdpa_status sdpa_paged_forward(const void* q, const void* k_pages, const void* v_pages, void* out,
+                               void* workspace, size_t ws_bytes, int b, int n_tokens, int h,
+                               int h_kv, int d, int page_size, int n_pages, int pages_per_seq,
+                               const int32_t* page_table, const int32_t* q_starts,
+                               const int32_t* kv_lengths, long long q_stride, float scale,
+                               void* stream);
+
+/*
  * Bytes of device workspace mha_forward needs: the projected Q [b*n_q, h*d_k],
  * K [b*n_k, h*d_k], V [b*n_k, h*d_v] and the concatenated heads
  * [b*n_q, h*d_v], bf16, each rounded up to 256 bytes.  Returns 0 for
@@ -303,7 +385,8 @@ sdpa_status linear_forward(const void* x, const void* w, void* y, int m, int n, 
  * Waits for the current device to finish its queued work, then reads and
  * clears the kernels' error word.  Returns SDPA_ERR_DEVICE_TIMEOUT if a
  * kernel abandoned a bounded wait since the last check (its output is then
- * undefined), SDPA_ERR_CUDA if the synchronisation failed, else SDPA_OK.
+ * undefined), else SDPA_ERR_BAD_PAGE if a page table named a page outside the
+ * cache, SDPA_ERR_CUDA if the synchronisation failed, else SDPA_OK.
  */
 sdpa_status sdpa_device_check(void);
 

@@ -28,12 +28,13 @@ SDPA_MASK_PADDING = 2
 
 STATUS_NAMES = {0: "SDPA_OK", 1: "SDPA_ERR_INVALID_ARG", 2: "SDPA_ERR_UNSUPPORTED",
                 3: "SDPA_ERR_UNSUPPORTED_DEVICE", 4: "SDPA_ERR_WORKSPACE", 5: "SDPA_ERR_CUDA",
-                6: "SDPA_ERR_DEVICE_TIMEOUT"}
+                6: "SDPA_ERR_DEVICE_TIMEOUT", 7: "SDPA_ERR_BAD_PAGE"}
 
 # Every symbol include/sdpa.h declares.
 EXPORTS = ("sdpa_forward", "sdpa_forward_restricted", "sdpa_forward_lse", "sdpa_forward_host",
            "sdpa_backward_workspace_size", "sdpa_backward", "sdpa_forward_f32",
-           "sdpa_decode_workspace_size", "sdpa_decode", "mha_workspace_size",
+           "sdpa_decode_workspace_size", "sdpa_decode", "sdpa_paged_append",
+           "sdpa_paged_workspace_size", "sdpa_paged_forward", "mha_workspace_size",
            "mha_forward",
            "mha_forward_noalloc", "linear_forward", "sdpa_set_kernel_choice", "sdpa_device_check",
            "sdpa_status_string")
@@ -81,6 +82,14 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
     lib.sdpa_decode_workspace_size.restype = SZ
     lib.sdpa_decode.argtypes = [P, P, P, P, P, SZ, I, I, I, I, I, I, P, F, P]
     lib.sdpa_decode.restype = I
+    L = ctypes.c_longlong
+    lib.sdpa_paged_append.argtypes = [P, P, P, P, P, P, I, I, I, I, I, I, I, I, P, P, P, L, L, L, P, I,
+                                      I, P]
+    lib.sdpa_paged_append.restype = I
+    lib.sdpa_paged_workspace_size.argtypes = [I, I, I, I, I, I, I]
+    lib.sdpa_paged_workspace_size.restype = SZ
+    lib.sdpa_paged_forward.argtypes = [P, P, P, P, P, SZ, I, I, I, I, I, I, I, I, P, P, P, L, F, P]
+    lib.sdpa_paged_forward.restype = I
     lib.mha_workspace_size.argtypes = [I, I, I, I, I, I]
     lib.mha_workspace_size.restype = SZ
     lib.mha_forward.argtypes = [P, P, P, P, P, P, P, P, SZ, I, I, I, I, I, I, I, I, P, F, P]
@@ -115,6 +124,29 @@ def _stream(stream) -> int | None:
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
+
+
+class _on_stream:
+    """Makes `stream` (None, a torch stream or a raw handle) torch's current
+    one inside the block, so that what torch allocates there belongs to the
+    stream that the kernels run on."""
+
+    def __init__(self, stream):
+        self.context = None
+        if stream is not None:
+            import torch
+            if isinstance(stream, int):
+                stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+            self.context = torch.cuda.stream(stream)
+
+    def __enter__(self):
+        if self.context is not None:
+            self.context.__enter__()
+
+    def __exit__(self, *exc):
+        if self.context is not None:
+            self.context.__exit__(*exc)
+        return False
 
 
 def _check(status: int, where: str) -> None:
@@ -197,6 +229,134 @@ def decode_step(q, k, v, kv_lengths=None, scale=0.0, workspace=None, stream=None
     out = torch.empty((b, h, n_q, d_v), dtype=q.dtype, device=q.device)
     sdpa_decode(q, k, v, out, workspace, 0 if workspace is None else workspace.numel(), b, h, n_q,
                 n_k, d_k, d_v, kv_lengths, scale, stream)
+    return out
+
+
+def sdpa_paged_append(q, k, v, q_out, k_pages, v_pages, b, n_tokens, h, h_kv, d, page_size, n_pages,
+                      pages_per_seq, page_table, q_starts, kv_lengths, q_stride, k_stride, v_stride,
+                      rope_freqs=None, d_rot=0, interleaved=False, stream=None) -> None:
+    """New keys and values into a paged cache, queries and keys rotated by
+    their positions (see include/sdpa.h)."""
+    _check(load_library().sdpa_paged_append(
+        _addr(q), _addr(k), _addr(v), _addr(q_out), _addr(k_pages), _addr(v_pages), b, n_tokens, h,
+        h_kv, d, page_size, n_pages, pages_per_seq, _addr(page_table), _addr(q_starts),
+        _addr(kv_lengths), q_stride, k_stride, v_stride, _addr(rope_freqs), d_rot, int(interleaved),
+        _stream(stream)), "sdpa_paged_append")
+
+
+def sdpa_paged_workspace_size(b, n_tokens, h, h_kv, d, page_size, pages_per_seq) -> int:
+    return int(load_library().sdpa_paged_workspace_size(b, n_tokens, h, h_kv, d, page_size,
+                                                        pages_per_seq))
+
+
+def sdpa_paged_forward(q, k_pages, v_pages, out, workspace, ws_bytes, b, n_tokens, h, h_kv, d,
+                       page_size, n_pages, pages_per_seq, page_table, q_starts, kv_lengths, q_stride,
+                       scale=0.0, stream=None) -> None:
+    """Attention of packed new tokens over a paged cache (see include/sdpa.h)."""
+    _check(load_library().sdpa_paged_forward(
+        _addr(q), _addr(k_pages), _addr(v_pages), _addr(out), _addr(workspace), int(ws_bytes), b,
+        n_tokens, h, h_kv, d, page_size, n_pages, pages_per_seq, _addr(page_table), _addr(q_starts),
+        _addr(kv_lengths), q_stride, float(scale), _stream(stream)), "sdpa_paged_forward")
+
+
+def _paged_shapes(where, rows, k_pages, v_pages, page_table, q_starts, kv_lengths):
+    """(b, h_kv, d, page_size, n_pages, pages_per_seq) of a paged cache, after
+    checking what the C entry points cannot see: types, shapes, layout and
+    devices.  `rows` are the packed [n_tokens, heads, d] tensors of the call
+    (token rows may be strided)."""
+    import torch
+    n_pages, h_kv, page_size, d = k_pages.shape
+    b, pages_per_seq = page_table.shape
+    good = (k_pages.dtype == torch.bfloat16 and v_pages.dtype == torch.bfloat16 and
+            v_pages.shape == k_pages.shape and k_pages.is_contiguous() and v_pages.is_contiguous() and
+            page_table.dtype == torch.int32 and page_table.is_contiguous() and
+            q_starts.dtype == torch.int32 and q_starts.is_contiguous() and q_starts.numel() == b + 1 and
+            kv_lengths.dtype == torch.int32 and kv_lengths.is_contiguous() and kv_lengths.numel() == b)
+    device = k_pages.get_device()
+    good = good and device == torch.cuda.current_device() and all(
+        x.get_device() == device for x in (v_pages, page_table, q_starts, kv_lengths))
+    n_tokens = rows[0].shape[0]
+    for x in rows:
+        good = (good and x.dtype == torch.bfloat16 and x.dim() == 3 and x.shape[0] == n_tokens and
+                x.shape[2] == d and x.stride(2) == 1 and (x.shape[1] == 1 or x.stride(1) == d) and
+                x.get_device() == device)
+    if not good:
+        raise SdpaError(1, where)
+    return b, h_kv, d, page_size, n_pages, pages_per_seq
+
+
+def _row_stride(x):
+    # the stride of a single token says nothing
+    return x.stride(0) if x.shape[0] > 1 else x.shape[1] * x.shape[2]
+
+
+def paged_append(q, k, v, k_pages, v_pages, page_table, q_starts, kv_lengths, rope_freqs=None,
+                 interleaved=False, q_out=None, stream=None):
+    """Calls sdpa_paged_append on packed bf16 rows q [t,h,d], k, v [t,h_kv,d]
+    (token rows may be strided: columns of one projection's output) and a
+    cache k_pages, v_pages [n_pages,h_kv,page,d]; the first 2 *
+    rope_freqs.numel() columns are rotated.  Returns the rotated queries
+    (q_out, or a tensor allocated with torch); q = None appends alone."""
+    import torch
+    rows = (k, v) if q is None else (q, k, v)
+    with _on_stream(stream):
+        b, h_kv, d, page, n_pages, per_seq = _paged_shapes("paged_append", rows, k_pages, v_pages, page_table,
+                                                           q_starts, kv_lengths)
+        t = k.shape[0]
+        h = h_kv if q is None else q.shape[1]
+        good = k.shape[1] == h_kv and v.shape[1] == h_kv
+        if q is not None and q_out is None:
+            q_out = torch.empty((t, h, d), dtype=q.dtype, device=q.device)
+        if q is None:
+            good = good and q_out is None
+        else:
+            good = (good and q_out.shape == q.shape and q_out.dtype == q.dtype and q_out.is_contiguous() and
+                    q_out.get_device() == q.get_device())
+        d_rot = 0
+        if rope_freqs is not None:
+            d_rot = 2 * rope_freqs.numel()
+            good = (good and rope_freqs.dtype == torch.float32 and rope_freqs.is_contiguous() and
+                    rope_freqs.get_device() == k.get_device())
+        if not good:
+            raise SdpaError(1, "paged_append")
+        sdpa_paged_append(q, k, v, q_out, k_pages, v_pages, b, t, h, h_kv, d, page, n_pages, per_seq, page_table,
+                          q_starts, kv_lengths, 0 if q is None else _row_stride(q), _row_stride(k),
+                          _row_stride(v), rope_freqs, d_rot, interleaved, stream)
+    return q_out
+
+
+def paged_workspace(q, k_pages, page_table):
+    """Allocates with torch the workspace of paged_attention for these shapes
+    (None where it needs none).  A serving loop keeps it from step to step and
+    layer to layer; calls that may overlap on the GPU need one each."""
+    import torch
+    n_pages, h_kv, page, d = k_pages.shape
+    need = sdpa_paged_workspace_size(page_table.shape[0], q.shape[0], q.shape[1], h_kv, d, page,
+                                     page_table.shape[1])
+    return torch.empty(need, dtype=torch.uint8, device=q.device) if need > 0 else None
+
+
+def paged_attention(q, k_pages, v_pages, page_table, q_starts, kv_lengths, scale=0.0, out=None, workspace=None,
+                    stream=None):
+    """Calls sdpa_paged_forward on packed bf16 rows q [t,h,d] (token rows may
+    be strided) and a paged cache; allocates the output and the workspace
+    with torch where they are not given.  Returns the output [t,h,d]."""
+    import torch
+    with _on_stream(stream):
+        b, h_kv, d, page, n_pages, per_seq = _paged_shapes("paged_attention", (q,), k_pages, v_pages, page_table,
+                                                           q_starts, kv_lengths)
+        t, h = q.shape[0], q.shape[1]
+        if out is None:
+            out = torch.empty((t, h, d), dtype=q.dtype, device=q.device)
+        elif not (out.shape == q.shape and out.dtype == q.dtype and out.is_contiguous() and
+                  out.get_device() == q.get_device()):
+            raise SdpaError(1, "paged_attention")
+        if workspace is None:
+            workspace = paged_workspace(q, k_pages, page_table)
+        sdpa_paged_forward(q, k_pages, v_pages, out, workspace,
+                           0 if workspace is None else workspace.numel() * workspace.element_size(), b, t, h,
+                           h_kv, d, page, n_pages, per_seq, page_table, q_starts, kv_lengths, _row_stride(q),
+                           scale, stream)
     return out
 
 

@@ -122,6 +122,27 @@ bool make_map_4d(CUtensorMap* map, const void* base, int d, int n, int h, int b,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// 3-D bf16 map over packed token rows (d, h, n_tokens), tokens `stride`
+// elements apart; boxes of min(d, 64) columns x box_heads x box_tokens, so a
+// box lands as box_tokens * box_heads consecutive rows.
+bool make_map_rows(CUtensorMap* map, const void* base, int d, int h, int n_tokens, long long stride,
+                   int box_heads, int box_tokens) {
+  auto enc = encode_fn();
+  if (enc == nullptr) return false;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(h),
+                              static_cast<cuuint64_t>(n_tokens)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(d) * 2, static_cast<cuuint64_t>(stride) * 2};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(d < 64 ? d : 64), static_cast<cuuint32_t>(box_heads),
+                             static_cast<cuuint32_t>(box_tokens)};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUtensorMapSwizzle swz = d >= 64 ? CU_TENSOR_MAP_SWIZZLE_128B
+                                         : (d == 32 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                                    : CU_TENSOR_MAP_SWIZZLE_32B);
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box,
+             estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swz, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // 3-D fp32 map over the backward's dQ accumulator [bh][n_q][d]: boxes of
 // min(32, d) columns x box_rows rows, unswizzled, for the kernel's tensor
 // reduce-adds; rows past n_q are clipped by the copy engine.
@@ -347,6 +368,54 @@ sdpa_status host_pipeline(HostPipeline** out) {
 // CTAs; the workspace is sized for the most any shape can take.
 int decode_target_ctas(int resident) {
   return sdpa::kDecodeWaves * resident * sdpa::device_sm_count();
+}
+
+// Shared rules of the paged entry points (host-only checks): sizes, the
+// page geometry and the three device arrays.
+sdpa_status check_paged_args(const void* k_pages, const void* v_pages, int b, int n_tokens, int h,
+                             int h_kv, int d, int page_size, int n_pages, int pages_per_seq,
+                             const int32_t* page_table, const int32_t* q_starts,
+                             const int32_t* kv_lengths) {
+  auto aligned4 = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; };
+  if (k_pages == nullptr || v_pages == nullptr || page_table == nullptr || q_starts == nullptr ||
+      kv_lengths == nullptr)
+    return SDPA_ERR_INVALID_ARG;
+  if (!aligned16(k_pages) || !aligned16(v_pages) || !aligned4(page_table) || !aligned4(q_starts) ||
+      !aligned4(kv_lengths))
+    return SDPA_ERR_INVALID_ARG;
+  if (b < 1 || n_tokens < 0 || h < 1 || h_kv < 1 || d < 1 || page_size < 1 || n_pages < 1 ||
+      pages_per_seq < 1 || h % h_kv != 0)
+    return SDPA_ERR_INVALID_ARG;
+  if (!sdpa::paged_supports(d) || h / h_kv > 128 || page_size < sdpa::kPagedMinPage ||
+      (page_size & (page_size - 1)) != 0 || 1ll * pages_per_seq * page_size >= (1ll << 30) ||
+      n_tokens > (1 << 24) || b > (1 << 24) || h > 65536)
+    return SDPA_ERR_UNSUPPORTED;
+  // the largest tensor-map stride (bytes from page to page) and the whole cache
+  if (1ll * h_kv * page_size * d * 2 >= (1ll << 40) || n_pages >= (1 << 30) ||
+      1ll * h_kv * page_size * d > (1ll << 40) / n_pages)
+    return SDPA_ERR_UNSUPPORTED;
+  return SDPA_OK;
+}
+
+int log2_of(int x) {
+  int s = 0;
+  while ((1 << s) < x) ++s;
+  return s;
+}
+
+// CTAs of the split kernel: every resident one, or as many as runs of
+// kPagedMinTiles key tiles could ever be filled.
+int paged_split_ctas(int b, int n_tokens, int h_kv, int group, int d, long long max_len) {
+  const long long tile_tokens = 128 / group;
+  const long long units = (n_tokens / tile_tokens + std::min(b, n_tokens)) * h_kv;
+  const long long tiles = units * (max_len / sdpa::kPagedKeyTile + 1);
+  const long long runs = (tiles + sdpa::kPagedMinTiles - 1) / sdpa::kPagedMinTiles;
+  const long long most = 1ll * sdpa::paged_resident_ctas(d) * sdpa::device_sm_count();
+  return static_cast<int>(std::max(1ll, std::min(most, runs)));
+}
+
+int paged_slot_rows(int n_tokens, int group) {
+  return static_cast<int>(std::min(128ll, 1ll * n_tokens * group));
 }
 
 }  // namespace
@@ -670,6 +739,129 @@ sdpa_status sdpa_decode(const void* q, const void* k, const void* v, void* out, 
              : SDPA_ERR_CUDA;
 }
 
+sdpa_status sdpa_paged_append(const void* q, const void* k, const void* v, void* q_out,
+                              void* k_pages, void* v_pages, int b, int n_tokens, int h, int h_kv,
+                              int d, int page_size, int n_pages, int pages_per_seq,
+                              const int32_t* page_table, const int32_t* q_starts,
+                              const int32_t* kv_lengths, long long q_stride, long long k_stride,
+                              long long v_stride, const float* rope_freqs, int d_rot,
+                              int interleaved, void* stream) {
+  // an empty tensor of rows has no address
+  if (n_tokens != 0 && (k == nullptr || v == nullptr || (q == nullptr) != (q_out == nullptr)))
+    return SDPA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out))
+    return SDPA_ERR_INVALID_ARG;
+  sdpa_status st = check_paged_args(k_pages, v_pages, b, n_tokens, h, h_kv, d, page_size, n_pages,
+                                    pages_per_seq, page_table, q_starts, kv_lengths);
+  if (st != SDPA_OK) return st;
+  const long long kv_row = 1ll * h_kv * d, q_row = 1ll * h * d;
+  if (d_rot < 0 || d_rot > d || k_stride < kv_row || v_stride < kv_row ||
+      (q != nullptr && q_stride < q_row) || (d_rot > 0 && rope_freqs == nullptr) ||
+      (reinterpret_cast<uintptr_t>(rope_freqs) & 3u) != 0 || (q != nullptr && q == q_out && q_stride != q_row))
+    return SDPA_ERR_INVALID_ARG;
+  const long long most = 1ll << 38;
+  if (d_rot % 16 != 0 || k_stride % 8 != 0 || v_stride % 8 != 0 || k_stride > most || v_stride > most ||
+      (q != nullptr && (q_stride % 8 != 0 || q_stride > most)))
+    return SDPA_ERR_UNSUPPORTED;
+  unsigned* status = nullptr;
+  st = current_device(&status);
+  if (st != SDPA_OK) return st;
+  if (n_tokens == 0) return SDPA_OK;
+  sdpa::PagedAppendParams p;
+  p.q = static_cast<const uint16_t*>(q);
+  p.k = static_cast<const uint16_t*>(k);
+  p.v = static_cast<const uint16_t*>(v);
+  p.q_out = static_cast<uint16_t*>(q_out);
+  p.k_pages = static_cast<uint16_t*>(k_pages);
+  p.v_pages = static_cast<uint16_t*>(v_pages);
+  p.freqs = rope_freqs;
+  p.page_table = page_table;
+  p.q_starts = q_starts;
+  p.kv_lengths = kv_lengths;
+  p.status = status;
+  p.q_stride = q_stride;
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  p.b = b;
+  p.n_tokens = n_tokens;
+  p.h = h;
+  p.h_kv = h_kv;
+  p.d = d;
+  p.d_rot = d_rot;
+  p.interleaved = interleaved != 0;
+  p.page_shift = log2_of(page_size);
+  p.n_pages = n_pages;
+  p.pages_per_seq = pages_per_seq;
+  return sdpa::launch_sdpa_paged_append(p, static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? SDPA_OK
+             : SDPA_ERR_CUDA;
+}
+
+size_t sdpa_paged_workspace_size(int b, int n_tokens, int h, int h_kv, int d, int page_size,
+                                 int pages_per_seq) {
+  if (b < 1 || n_tokens < 1 || h < 1 || h_kv < 1 || h % h_kv != 0 || h / h_kv > 128 || page_size < 1 ||
+      pages_per_seq < 1 || !sdpa::paged_supports(d))
+    return 0;
+  const int group = h / h_kv;
+  const int ctas = paged_split_ctas(b, n_tokens, h_kv, group, d, 1ll * pages_per_seq * page_size);
+  if (ctas == 1) return 0;
+  const size_t rows = 2 * static_cast<size_t>(ctas) * paged_slot_rows(n_tokens, group);
+  return round256(rows * d * 4) + round256(rows * 2 * 4);
+}
+
+sdpa_status sdpa_paged_forward(const void* q, const void* k_pages, const void* v_pages, void* out,
+                               void* workspace, size_t ws_bytes, int b, int n_tokens, int h,
+                               int h_kv, int d, int page_size, int n_pages, int pages_per_seq,
+                               const int32_t* page_table, const int32_t* q_starts,
+                               const int32_t* kv_lengths, long long q_stride, float scale,
+                               void* stream) {
+  if (n_tokens != 0 && (q == nullptr || out == nullptr)) return SDPA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(out)) return SDPA_ERR_INVALID_ARG;
+  sdpa_status st = check_paged_args(k_pages, v_pages, b, n_tokens, h, h_kv, d, page_size, n_pages,
+                                    pages_per_seq, page_table, q_starts, kv_lengths);
+  if (st != SDPA_OK) return st;
+  if (!std::isfinite(scale) || scale < 0.f || q_stride < 1ll * h * d) return SDPA_ERR_INVALID_ARG;
+  if (q_stride % 8 != 0 || q_stride >= (1ll << 38)) return SDPA_ERR_UNSUPPORTED;
+  const size_t need = sdpa_paged_workspace_size(b, n_tokens, h, h_kv, d, page_size, pages_per_seq);
+  if (need > 0 && (workspace == nullptr || !aligned16(workspace) || ws_bytes < need))
+    return SDPA_ERR_WORKSPACE;
+  unsigned* status = nullptr;
+  st = current_device(&status);
+  if (st != SDPA_OK) return st;
+  if (n_tokens == 0) return SDPA_OK;
+  sdpa::PagedParams p;
+  p.group = h / h_kv;
+  p.tile_tokens = 128 / p.group;
+  if (!make_map_rows(&p.tm_q, q, d, h, n_tokens, q_stride, p.group, p.tile_tokens) ||
+      !make_map_4d(&p.tm_k, k_pages, d, page_size, h_kv, n_pages, d, 1ll * page_size * d,
+                   1ll * h_kv * page_size * d, std::min(page_size, sdpa::kPagedKeyTile)) ||
+      !make_map_4d(&p.tm_v, v_pages, d, page_size, h_kv, n_pages, d, 1ll * page_size * d,
+                   1ll * h_kv * page_size * d, std::min(page_size, sdpa::kPagedKeyTile)))
+    return SDPA_ERR_CUDA;
+  p.out = static_cast<uint16_t*>(out);
+  p.page_table = page_table;
+  p.q_starts = q_starts;
+  p.kv_lengths = kv_lengths;
+  p.status = status;
+  p.b = b;
+  p.n_tokens = n_tokens;
+  p.h = h;
+  p.h_kv = h_kv;
+  p.page_shift = log2_of(page_size);
+  p.n_pages = n_pages;
+  p.pages_per_seq = pages_per_seq;
+  p.split_ctas = paged_split_ctas(b, n_tokens, h_kv, p.group, d, 1ll * pages_per_seq * page_size);
+  p.min_tiles = sdpa::kPagedMinTiles;
+  p.slot_rows = paged_slot_rows(n_tokens, p.group);
+  const size_t rows = 2 * static_cast<size_t>(p.split_ctas) * p.slot_rows;
+  p.part_o = need > 0 ? static_cast<float*>(workspace) : nullptr;
+  p.part_ml = need > 0 ? reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + round256(rows * d * 4))
+                       : nullptr;
+  p.scale_log2 = effective_scale(scale, d) * 1.4426950408889634f;
+  return sdpa::launch_sdpa_paged(p, d, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SDPA_OK
+                                                                                          : SDPA_ERR_CUDA;
+}
+
 size_t mha_workspace_size(int b, int n_q, int n_k, int h, int d_k, int d_v) {
   if (b < 0 || n_q < 0 || n_k < 0 || h < 0 || d_k < 0 || d_v < 0) return 0;
   const size_t bq = static_cast<size_t>(b) * n_q, bk = static_cast<size_t>(b) * n_k;
@@ -787,7 +979,8 @@ sdpa_status sdpa_device_check(void) {
     cudaGetLastError();
     return SDPA_ERR_CUDA;
   }
-  return (word & sdpa::kStatusTimeout) ? SDPA_ERR_DEVICE_TIMEOUT : SDPA_OK;
+  if (word & sdpa::kStatusTimeout) return SDPA_ERR_DEVICE_TIMEOUT;
+  return (word & sdpa::kStatusBadPage) ? SDPA_ERR_BAD_PAGE : SDPA_OK;
 }
 
 const char* sdpa_status_string(sdpa_status status) {
@@ -799,6 +992,7 @@ const char* sdpa_status_string(sdpa_status status) {
     case SDPA_ERR_WORKSPACE: return "SDPA_ERR_WORKSPACE";
     case SDPA_ERR_CUDA: return "SDPA_ERR_CUDA";
     case SDPA_ERR_DEVICE_TIMEOUT: return "SDPA_ERR_DEVICE_TIMEOUT";
+    case SDPA_ERR_BAD_PAGE: return "SDPA_ERR_BAD_PAGE";
   }
   return "SDPA_ERR_UNKNOWN";
 }

@@ -9,6 +9,7 @@ namespace sdpa {
 
 // Error bits of the device status word (read back by sdpa_device_check).
 constexpr unsigned kStatusTimeout = 1u;
+constexpr unsigned kStatusBadPage = 2u;   // a page number outside the cache (paged.cu)
 
 // Fused bf16 attention on the tensor cores.  The four tensor maps view
 // Q, K, V and O as 4-D (d, n, h, b) arrays with 64 x 128 boxes, 128-byte
@@ -100,6 +101,46 @@ int decode_resident_ctas(int d_k, int d_v);
 // split at least kDecodeMinKeysPerSplit keys, at most kDecodeMaxSplits).
 int decode_splits(int b, int h, int n_k, int target_ctas);
 cudaError_t launch_sdpa_decode(const DecodeParams& p, int d_k, int d_v, cudaStream_t stream);
+
+// Attention of packed new tokens over a paged cache (csrc/paged.cu).
+struct PagedParams {
+  CUtensorMap tm_q;           // 3-D (d, h, n_tokens) map, boxes of min(d, 64) x group x tile_tokens
+  CUtensorMap tm_k, tm_v;     // 4-D (d, page rows, h_kv, n_pages) maps, boxes of min(d, 64)
+                              // columns x min(page, kPagedKeyTile) rows
+  uint16_t* out;              // bf16 [n_tokens][h][d]
+  float* part_o;              // [2 split_ctas][slot_rows][d]  (split_ctas > 1)
+  float* part_ml;             // [2 split_ctas][slot_rows][2]  (split_ctas > 1)
+  const int32_t* page_table;  // [b][pages_per_seq]
+  const int32_t* q_starts;    // [b + 1]
+  const int32_t* kv_lengths;  // [b]
+  unsigned* status;
+  int b, n_tokens, h, h_kv;
+  int group, tile_tokens;     // h / h_kv; tokens per row tile, 128 / group
+  int page_shift, n_pages, pages_per_seq;
+  int split_ctas;             // CTAs of the split kernel (runs, at most)
+  int min_tiles;              // key tiles of a run, at least (while there are runs to spare)
+  int slot_rows;              // rows of a workspace slot
+  float scale_log2;
+};
+constexpr int kPagedKeyTile = 64;
+constexpr int kPagedMinPage = 8;
+constexpr int kPagedMinTiles = 4;
+bool paged_supports(int d);
+int paged_resident_ctas(int d);   // split CTAs that share an SM
+cudaError_t launch_sdpa_paged(const PagedParams& p, int d, cudaStream_t stream);
+
+// The append: rotation of new queries and keys, keys and values into pages.
+struct PagedAppendParams {
+  const uint16_t *q, *k, *v;  // rows of n_tokens tokens, strides in elements (q may be null)
+  uint16_t *q_out, *k_pages, *v_pages;
+  const float* freqs;         // [d_rot / 2] radians per position
+  const int32_t *page_table, *q_starts, *kv_lengths;
+  unsigned* status;
+  long long q_stride, k_stride, v_stride;
+  int b, n_tokens, h, h_kv, d, d_rot, interleaved;
+  int page_shift, n_pages, pages_per_seq;
+};
+cudaError_t launch_sdpa_paged_append(const PagedAppendParams& p, cudaStream_t stream);
 
 // Gradients of attention (bf16 BHSD tensors, fp32 accumulation).
 struct SdpaBwdParams {
