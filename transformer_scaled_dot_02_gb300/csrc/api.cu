@@ -806,7 +806,8 @@ size_t sdpa_paged_workspace_size(int b, int n_tokens, int h, int h_kv, int d, in
   const int ctas = paged_split_ctas(b, n_tokens, h_kv, group, d, 1ll * pages_per_seq * page_size);
   if (ctas == 1) return 0;
   const size_t rows = 2 * static_cast<size_t>(ctas) * paged_slot_rows(n_tokens, group);
-  return round256(rows * d * 4) + round256(rows * 2 * 4);
+  return round256(rows * d * 4) + round256(rows * 2 * 4) +
+         round256(static_cast<size_t>(ctas) * sizeof(sdpa::PagedRun));
 }
 
 sdpa_status sdpa_paged_forward(const void* q, const void* k_pages, const void* v_pages, void* out,
@@ -833,6 +834,8 @@ sdpa_status sdpa_paged_forward(const void* q, const void* k_pages, const void* v
   p.group = h / h_kv;
   p.tile_tokens = 128 / p.group;
   if (!make_map_rows(&p.tm_q, q, d, h, n_tokens, q_stride, p.group, p.tile_tokens) ||
+      !make_map_rows(&p.tm_q_narrow, q, d, h, n_tokens, q_stride, p.group,
+                     p.group <= 32 ? 32 / p.group : p.tile_tokens) ||
       !make_map_4d(&p.tm_k, k_pages, d, page_size, h_kv, n_pages, d, 1ll * page_size * d,
                    1ll * h_kv * page_size * d, std::min(page_size, sdpa::kPagedKeyTile)) ||
       !make_map_4d(&p.tm_v, v_pages, d, page_size, h_kv, n_pages, d, 1ll * page_size * d,
@@ -854,9 +857,11 @@ sdpa_status sdpa_paged_forward(const void* q, const void* k_pages, const void* v
   p.min_tiles = sdpa::kPagedMinTiles;
   p.slot_rows = paged_slot_rows(n_tokens, p.group);
   const size_t rows = 2 * static_cast<size_t>(p.split_ctas) * p.slot_rows;
-  p.part_o = need > 0 ? static_cast<float*>(workspace) : nullptr;
-  p.part_ml = need > 0 ? reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + round256(rows * d * 4))
-                       : nullptr;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  p.part_o = need > 0 ? reinterpret_cast<float*>(ws) : nullptr;
+  p.part_ml = need > 0 ? reinterpret_cast<float*>(ws + round256(rows * d * 4)) : nullptr;
+  p.runs = need > 0 ? reinterpret_cast<sdpa::PagedRun*>(ws + round256(rows * d * 4) + round256(rows * 2 * 4))
+                    : nullptr;
   p.scale_log2 = effective_scale(scale, d) * 1.4426950408889634f;
   return sdpa::launch_sdpa_paged(p, d, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SDPA_OK
                                                                                           : SDPA_ERR_CUDA;

@@ -20,6 +20,11 @@
 // sdpa_paged_combine<D>   merges the pieces of each unit that was cut:
 //   O = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s, M = max_s m_s.
 //
+// Row tiles of at most 32 rows (single tokens) would leave three of the four
+// softmax warps idle and one with the whole row: their queries are copied to
+// all four quarters of the tile instead, each warp takes 16 of a tile's 64
+// keys, and the quarters' (O, m, l) are merged when the piece ends.
+//
 // The roles of a split CTA are those of the one-tile forward kernel (TMA
 // producer, MMA issuer, four softmax warps of one thread per row, S double
 // buffered and O in tensor memory), kept running from piece to piece: tile
@@ -39,6 +44,8 @@ constexpr int kBN = kPagedKeyTile;         // keys per tile
 constexpr int kThreads = 192;
 constexpr int kProducerWarp = 4;
 constexpr int kMmaWarp = 5;
+constexpr int kNarrowRows = 32;            // rows of a tile that every softmax warp holds
+constexpr int kQuarterKeys = kBN / 4;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units, as in the other forward kernels
 
 // ------------------------------------------------------------------ schedule
@@ -54,7 +61,7 @@ __device__ __forceinline__ Seq load_seq(const PagedParams& p, int s) {
   q.start = min(max(p.q_starts[s], 0), p.n_tokens);
   q.n = min(max(p.q_starts[s + 1], q.start), p.n_tokens) - q.start;
   q.len = min(max(p.kv_lengths[s], 0), cap);
-  q.tiles = (q.n + p.tile_tokens - 1) / p.tile_tokens;
+  q.tiles = q.n <= p.tile_tokens ? min(q.n, 1) : (q.n + p.tile_tokens - 1) / p.tile_tokens;
   return q;
 }
 
@@ -104,28 +111,42 @@ struct Place {
 };
 
 struct ScheduleShared {
-  long long warp_sum[8];
+  long long warp_sum[kThreads / 32];
   long long rem;
-  int s;
   Place at;
+  Seq q;
 };
 
-__device__ __forceinline__ long long run_begin(long long work, int c, int ctas) {
-  return work / ctas * c + work % ctas * c / ctas;
+// Most work counts fit 32 bits, where a division costs a tenth of one in 64.
+__device__ __forceinline__ long long divide(long long a, long long b) {
+  if (((a | b) >> 32) == 0) return static_cast<unsigned>(a) / static_cast<unsigned>(b);
+  return a / b;
 }
 
-// The whole block: total work, and the place of work item `work * c / ctas`
-// for the number of runs `ctas` that follows from the total.  Returns false
-// (everywhere) when there is no such run.
-template <int NT>
-__device__ bool find_place(const PagedParams& p, ScheduleShared* sh, int c, int max_ctas,
-                           long long* work, int* ctas, Place* at) {
+// Work is cut into runs: run c of `ctas` is [floor(work c / ctas), floor(work (c + 1) / ctas)).
+struct Cut {
+  long long work, each;
+  int ctas, over;
+  __device__ Cut(long long w, int n) : work(w), ctas(n) {
+    each = divide(w, n);
+    over = static_cast<int>(w - each * n);
+  }
+  __device__ long long begin(int c) const { return each * c + over * c / ctas; }   // over, c < 2^15
+  // the run that holds item x: the last c with work c / ctas < x + 1
+  __device__ int run_of(long long x) const { return static_cast<int>(divide((x + 1) * ctas - 1, work)); }
+};
+
+// The whole block: how the work is cut, and the place where run c begins.
+// Returns false (everywhere) when there is no such run.
+__device__ bool find_place(const PagedParams& p, ScheduleShared* sh, int c, int max_ctas, Cut* cut,
+                           Place* at, Seq* seq) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int per = (p.b + NT - 1) / NT;
+  const int per = (p.b + kThreads - 1) / kThreads;
   const int s0 = min(tid * per, p.b), s1 = min(s0 + per, p.b);
   long long mine = 0;
+  Seq q;
   for (int s = s0; s < s1; ++s) {
-    const Seq q = load_seq(p, s);
+    q = load_seq(p, s);
     mine += cost_before(p, q, q.tiles) * p.h_kv;
   }
   long long incl = mine;
@@ -138,54 +159,54 @@ __device__ bool find_place(const PagedParams& p, ScheduleShared* sh, int c, int 
   __syncthreads();
   long long total = 0, excl = incl - mine;
 #pragma unroll
-  for (int w = 0; w < NT / 32; ++w) {
+  for (int w = 0; w < kThreads / 32; ++w) {
     if (w < warp) excl += sh->warp_sum[w];
     total += sh->warp_sum[w];
   }
-  const long long want = (total + p.min_tiles - 1) / p.min_tiles;
-  const int n = static_cast<int>(min(static_cast<long long>(max_ctas), want));
-  *work = total;
-  *ctas = n;
+  const int n = static_cast<int>(min(static_cast<long long>(max_ctas), divide(total + p.min_tiles - 1, p.min_tiles)));
   if (c >= n) return false;
-  const long long x = run_begin(total, c, n);
+  *cut = Cut(total, n);
+  const long long x = cut->begin(c);
   if (mine > 0 && excl <= x && x < excl + mine) {
     long long rem = x - excl;
-    for (int s = s0; s < s1; ++s) {
-      const Seq q = load_seq(p, s);
-      const long long w = cost_before(p, q, q.tiles) * p.h_kv;
-      if (rem < w) {
-        sh->s = s;
-        sh->rem = rem;
-        break;
+    Place pl;
+    pl.s = s0;
+    if (per > 1) {
+      for (pl.s = s0; pl.s < s1; ++pl.s) {
+        q = load_seq(p, pl.s);
+        const long long w = cost_before(p, q, q.tiles) * p.h_kv;
+        if (rem < w) break;
+        rem -= w;
       }
-      rem -= w;
     }
+    const long long head = cost_before(p, q, q.tiles);
+    pl.hk = static_cast<int>(divide(rem, head));
+    rem -= pl.hk * head;
+    pl.r = 0;
+    pl.kt = static_cast<int>(rem);                           // the place, for a single row tile
+    sh->at = pl;
+    sh->rem = rem;
+    sh->q = q;
   }
   __syncthreads();
-  if (warp == 0) {
-    Place pl;
-    pl.s = sh->s;
-    const Seq q = load_seq(p, pl.s);
-    const long long head = cost_before(p, q, q.tiles);
-    long long rem = sh->rem;
-    pl.hk = static_cast<int>(rem / head);
-    rem -= pl.hk * head;
-    // the last row tile that begins at or before rem: 32 probes a round
-    int lo = 0, hi = q.tiles;
+  *at = sh->at;
+  *seq = sh->q;
+  if (seq->tiles > 1) {
+    // the last row tile that begins at or before rem: 32 probes a round (every
+    // warp does it for itself)
+    const long long rem = sh->rem;
+    int lo = 0, hi = seq->tiles;
     while (hi - lo > 1) {
       const int step = (hi - lo + 31) / 32;
       const int probe = lo + lane * step;
-      const bool le = probe < hi && cost_before(p, q, probe) <= rem;
+      const bool le = probe < hi && cost_before(p, *seq, probe) <= rem;
       const int k = 31 - __clz(__ballot_sync(0xffffffffu, le));
       lo += k * step;
       hi = min(hi, lo + step);
     }
-    pl.r = lo;
-    pl.kt = static_cast<int>(rem - cost_before(p, q, lo));
-    if (lane == 0) sh->at = pl;
+    at->r = lo;
+    at->kt = static_cast<int>(rem - cost_before(p, *seq, lo));
   }
-  __syncthreads();
-  *at = sh->at;
   return true;
 }
 
@@ -196,13 +217,18 @@ struct Walk {
   int keys, cost;
   long long left;
 
-  __device__ void begin(const PagedParams& p, const Place& a, long long run) {
+  __device__ void begin(const PagedParams& p, const Place& a, const Seq& first, long long run) {
     at = a;
     left = run;
-    q = load_seq(p, at.s);
+    q = first;
     keys = tile_keys(p, q, at.r);
     cost = tile_cost(keys);
   }
+  // rows of this row tile that are queries; few enough for a quarter?
+  __device__ int rows(const PagedParams& p) const {
+    return min(p.tile_tokens, q.n - at.r * p.tile_tokens) * p.group;
+  }
+  __device__ bool narrow(const PagedParams& p) const { return rows(p) <= kNarrowRows; }
   // key tiles of this piece: [at.kt, end()); those with keys: [at.kt, real_end())
   __device__ int end() const {
     return static_cast<int>(min(static_cast<long long>(cost), at.kt + left));
@@ -246,12 +272,24 @@ struct PCfg {
   static constexpr int kRing = D >= 128 ? 2 : 4;
   static constexpr int kKOff = kQBytes;
   static constexpr int kVOff = kKOff + kRing * kKVBytes;
-  static constexpr int kBarOff = kVOff + kRing * kKVBytes;
-  // q_full, q_empty, k_full[R], v_full[R], s_full[R], o_full[R], p_full[2], o_last, o_free, drain
-  static constexpr int kNumBars = 2 + 4 * kRing + 2 + 3;
+  // exchange of a narrow tile's quarters: O chunks of three warps (rows padded
+  // by 16 bytes, so that eight lanes' vectors hit all banks), (m, l) of four
+  static constexpr int kOChunk = D < 32 ? D : 32;
+  static constexpr int kXRow = kOChunk * 4 + 16;
+  static constexpr int kXSlot = kNarrowRows * kXRow;
+  // a wide tile's warps turn their rows through the same memory, 64 bytes of
+  // each at a time (rows padded by 16)
+  static constexpr int kTurnRow = 64 + 16;
+  static constexpr int kTurnSlot = 32 * kTurnRow;
+  static_assert(D < 32 || 4 * kTurnSlot <= 3 * kXSlot, "turning rows");
+  static constexpr int kXOff = kVOff + kRing * kKVBytes;
+  static constexpr int kXmlOff = kXOff + 3 * kXSlot;
+  static constexpr int kBarOff = kXmlOff + 4 * kNarrowRows * 8;
+  // q_full, q_empty, k_full[R], v_full[R], s_full[R], o_full[R], p_full[2], o_last, o_free,
+  // x_full, x_free, drain
+  static constexpr int kNumBars = 2 + 4 * kRing + 2 + 5;
   static constexpr int kSmemBytes = kBarOff + kNumBars * 8 + 16 + 1024;
   static constexpr uint32_t kOCol = 2 * kBN;
-  static constexpr int kOChunk = D < 32 ? D : 32;
   static constexpr uint32_t kTmemCols = kOCol + D <= 256 ? 256u : 512u;
   static constexpr int kMinBlocks = static_cast<int>(512u / kTmemCols);
   static constexpr uint32_t kIdescS = idesc_bf16(kBlockM, kBN, false, false);
@@ -282,7 +320,9 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
   uint64_t* p_full = o_full + R;
   uint64_t* o_last = p_full + 2;      // once a piece, after its last O += P V
   uint64_t* o_free = o_last + 1;      // once a piece, when the softmax warps have read O
-  uint64_t* drain = o_free + 1;
+  uint64_t* x_full = o_free + 1;      // a step of the quarters' exchange is written
+  uint64_t* x_free = x_full + 1;      // an exchanged chunk is read
+  uint64_t* drain = x_free + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const AbortState ab{abort_flag, p.status};
@@ -301,6 +341,8 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
     for (int s = 0; s < 2; ++s) mbar_init(p_full + s, kBlockM);
     mbar_init(o_last, 1);
     mbar_init(o_free, kBlockM);
+    mbar_init(x_full, kBlockM);
+    mbar_init(x_free, 32);
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -315,12 +357,28 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
   // it starts, the kernels that wrote them having completed.
   griddep_launch_dependents();
 
-  long long work = 0;
-  int ctas = 0;
+  Cut cut(0, 1);
   Place first;
+  Seq first_seq;
   const int cta = static_cast<int>(blockIdx.x);
-  const bool any = find_place<kThreads>(p, &sched, cta, static_cast<int>(gridDim.x), &work, &ctas, &first);
-  const long long run = any ? run_begin(work, cta + 1, ctas) - run_begin(work, cta, ctas) : 0;
+  const bool any = find_place(p, &sched, cta, static_cast<int>(gridDim.x), &cut, &first, &first_seq);
+  const long long run = any ? cut.begin(cta + 1) - cut.begin(cta) : 0;
+  if (threadIdx.x == 0 && p.runs != nullptr) {
+    // what the combine kernel has to know of the unit that this run begins in
+    PagedRun r;
+    r.work = any ? cut.work : 0;
+    r.unit = any ? cut.begin(cta) - first.kt : 0;
+    r.ctas = any ? cut.ctas : 0;
+    r.inside = any && first.kt > 0;
+    if (r.inside) {
+      const int token0 = first.r * p.tile_tokens;
+      r.cost = tile_cost(tile_keys(p, first_seq, first.r));
+      r.rows = min(p.tile_tokens, first_seq.n - token0) * p.group;
+      r.token = first_seq.start + token0;
+      r.head = first.hk * p.group;
+    }
+    p.runs[cta] = r;
+  }
 
   if (run > 0 && warp == kProducerWarp) {
     // ---------------------------------------------------------- producer
@@ -332,12 +390,13 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
     const bool copies = part < kBN / box_rows;
     if (lane == 0) {
       tma_prefetch_desc(&p.tm_q);
+      tma_prefetch_desc(&p.tm_q_narrow);
       tma_prefetch_desc(&p.tm_k);
       tma_prefetch_desc(&p.tm_v);
     }
     const uint32_t dst = static_cast<uint32_t>(col * C::kKVBox + part * box_rows * C::kRowBytes);
     Walk w;
-    w.begin(p, first, run);
+    w.begin(p, first, first_seq, run);
     int u0 = 0, pieces = 0, k_issued = 0, v_issued = 0;
     bool go = true;
     do {
@@ -371,11 +430,18 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
       int page_k = page_v;
       // Q, once the scores of the piece before are done with it
       if (pieces > 0 && !(go = mbar_wait_warp(q_empty, static_cast<uint32_t>(pieces - 1) & 1u, ab))) break;
-      if (lane == 0) {
-        mbar_arrive_expect_tx(q_full, static_cast<uint32_t>(p.tile_tokens * p.group * C::kRowBytes * C::kBoxes));
-        for (int c = 0; c < C::kBoxes; ++c)
-          tma_load_3d(&p.tm_q, q_full, smem + c * C::kQBox, c * C::kBoxCols, w.at.hk * p.group,
-                      w.q.start + w.at.r * p.tile_tokens);
+      {
+        // lane c * 4 + y: column box c, for a narrow tile into quarter y
+        const bool narrow = w.narrow(p);
+        const int rows = (narrow ? kNarrowRows / p.group : p.tile_tokens) * p.group;
+        if (lane == 0)
+          mbar_arrive_expect_tx(q_full, static_cast<uint32_t>((narrow ? 4 : 1) * rows * C::kRowBytes * C::kBoxes));
+        __syncwarp();
+        const int c = lane >> 2, y = lane & 3;
+        if (c < C::kBoxes && (narrow || y == 0))
+          tma_load_3d(narrow ? &p.tm_q_narrow : &p.tm_q, q_full,
+                      smem + c * C::kQBox + y * kNarrowRows * C::kRowBytes, c * C::kBoxCols,
+                      w.at.hk * p.group, w.q.start + w.at.r * p.tile_tokens);
       }
       ++pieces;
       auto load_k = [&](int i) -> bool {
@@ -439,7 +505,7 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
                          (accumulate || k > 0) ? 1u : 0u);
     };
     Walk w;
-    w.begin(p, first, run);
+    w.begin(p, first, first_seq, run);
     int u = 0, pieces = 0;
     bool ok = true;
     do {
@@ -474,183 +540,380 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
     mbar_wait_drain(drain, 0);
   } else if (run > 0) {
     // ---------------------------------------------------------- softmax
-    const int row = (warp & 3) * 32 + lane;                  // row of the tile, tensor-memory lane
-    const int token = row / p.group, head = row % p.group;
-    const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    const int quarter = warp & 3;
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
     const float scale_log2 = p.scale_log2;
+    const float2 sc2 = make_float2(scale_log2, scale_log2);
     Walk w;
-    w.begin(p, first, run);
-    int u = 0, pieces = 0;
+    w.begin(p, first, first_seq, run);
+    int u = 0, pieces = 0, exchanged = 0;                    // exchanged: steps of x_full so far
+    int freed = 0;                                           // ... of x_free
     bool ok = true;
+
+    // Rows of V past the length hold whatever the page held (or an older
+    // tile): their weights are zero, but zero times an infinity or a NaN is a
+    // NaN, so they are cleared.  (All four warps, before P is handed over.)
+    auto clear_tail = [&](int key0) -> bool {
+      if (key0 + kBN <= w.q.len) return true;
+      if (!mbar_wait_warp(v_full + u % R, static_cast<uint32_t>(u / R) & 1u, ab)) return false;
+      uint8_t* v = smem + C::kVOff + (u % R) * C::kKVBytes;
+      const int keep = w.q.len - key0;                       // in [1, kBN)
+      constexpr int kPerRow = C::kRowBytes / 16;
+      for (int x = threadIdx.x; x < (kBN - keep) * kPerRow; x += kBlockM)
+#pragma unroll
+        for (int c = 0; c < C::kBoxes; ++c)
+          *reinterpret_cast<uint4*>(v + c * C::kKVBox + keep * C::kRowBytes + x * 16) = make_uint4(0, 0, 0, 0);
+      fence_proxy_async_smem();
+      return true;
+    };
+    // The running maximum of a row, given this tile's: moves only when it
+    // grew by more than the threshold (always on the first tile).  Returns
+    // the factor for what was summed so far.  O is rescaled after O += P(u-1)
+    // V(u-1): that barrier's previous phase is complete (S(u) was issued
+    // after it) and its next one needs this softmax's next P, so the parity
+    // wait is exact.  Rows that are no query hold leftovers and never ask.
+    auto move_max = [&](int i, float mx, bool valid, float& m_used, float& l, float& alpha, bool& rescale) -> bool {
+      const float m_new = fmaxf(m_used, mx * scale_log2);
+      alpha = 1.f;
+      rescale = false;
+      if (i == 0) {
+        m_used = m_new;
+        return true;
+      }
+      const bool need = valid && m_new > m_used + kRescaleThreshold;
+      rescale = __any_sync(0xffffffffu, need);
+      if (need) {
+        alpha = ex2_approx(m_used - m_new);
+        m_used = m_new;
+        l *= alpha;
+      }
+      if (rescale) {
+        if (!mbar_wait_warp(o_full + (u - 1) % R, static_cast<uint32_t>((u - 1) / R) & 1u, ab)) return false;
+        tc_fence_after();
+      }
+      return true;
+    };
+    auto rescale_o = [&](float alpha) {
+#pragma unroll
+      for (int c = 0; c < D / C::kOChunk; ++c) {
+        uint32_t o[C::kOChunk];
+        tmem_ld_chunk(lane_base + C::kOCol + c * C::kOChunk, o);
+        tmem_ld_wait();
+        reg_fence(o);
+#pragma unroll
+        for (int e = 0; e < C::kOChunk; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+        tmem_st_chunk(lane_base + C::kOCol + c * C::kOChunk, o);
+      }
+    };
+
     do {
       const int kt0 = w.at.kt, n = w.real_end() - kt0;
+      const int rows = w.rows(p);
+      const bool narrow = rows <= kNarrowRows;
+      const int row = narrow ? lane : quarter * 32 + lane;   // row of the tile
+      const int token = row / p.group, head = row % p.group;
       const int token0 = w.at.r * p.tile_tokens;
-      const bool valid = token < p.tile_tokens && token0 + token < w.q.n;
-      const bool busy = __any_sync(0xffffffffu, valid);      // some row of this warp is a query
+      const bool valid = row < rows;
       const int pos0 = w.q.len - w.q.n + token0;             // position of the tile's first row
       const int pos = pos0 + token;                          // this row sees keys 0 .. pos
-      float m_used = -INFINITY, l = 0.f;
-      for (int i = 0; i < n; ++i, ++u) {
-        const uint32_t s_col = static_cast<uint32_t>((u & 1) * kBN);
-        const int key0 = (kt0 + i) * kBN;
-        ok = mbar_wait_warp(s_full + u % R, static_cast<uint32_t>(u / R) & 1u, ab);
-        if (!ok) break;
-        tc_fence_after();
-        if (key0 + kBN > w.q.len) {
-          // Rows of V past the length hold whatever the page held (or an
-          // older tile): their weights are zero, but zero times an infinity
-          // or a NaN is a NaN, so they are cleared.
-          ok = mbar_wait_warp(v_full + u % R, static_cast<uint32_t>(u / R) & 1u, ab);
-          if (!ok) break;
-          uint8_t* v = smem + C::kVOff + (u % R) * C::kKVBytes;
-          const int keep = w.q.len - key0;                   // in [1, kBN)
-          constexpr int kPerRow = C::kRowBytes / 16;
-          for (int x = threadIdx.x; x < (kBN - keep) * kPerRow; x += kBlockM)
+      const bool whole = kt0 == 0 && w.end() == w.cost;
+      const long long out_row =
+          static_cast<long long>(w.q.start + token0 + token) * p.h + w.at.hk * p.group + head;
+      const long long part_row =
+          (static_cast<long long>(cta) * 2 + (kt0 > 0 ? 0 : 1)) * p.slot_rows + row;
+      // O columns [c kOChunk, +kOChunk) of this row: normalised into the
+      // output if the piece is a whole unit, as they are into the workspace
+      // if it is a part of one
+      auto store = [&](int c, const uint32_t (&o)[C::kOChunk], float inv_l) {
+        if (whole) {
+          uint4* dst = reinterpret_cast<uint4*>(p.out + out_row * D + c * C::kOChunk);
 #pragma unroll
-            for (int c = 0; c < C::kBoxes; ++c)
-              *reinterpret_cast<uint4*>(v + c * C::kKVBox + keep * C::kRowBytes + x * 16) =
-                  make_uint4(0, 0, 0, 0);
-          fence_proxy_async_smem();
-        }
-        if (busy) {
-          float s[kBN];
-          {
-            uint32_t sr[32];
-#pragma unroll
-            for (int c = 0; c < kBN / 32; ++c) {
-              tmem_ld32(lane_base + s_col + c * 32, sr);
-              tmem_ld_wait();
-              reg_fence(sr);
-#pragma unroll
-              for (int e = 0; e < 32; ++e) s[c * 32 + e] = __uint_as_float(sr[e]);
-            }
+          for (int e = 0; e < C::kOChunk / 8; ++e) {
+            uint4 x;
+            x.x = pack_bf16x2(__uint_as_float(o[e * 8 + 0]) * inv_l, __uint_as_float(o[e * 8 + 1]) * inv_l);
+            x.y = pack_bf16x2(__uint_as_float(o[e * 8 + 2]) * inv_l, __uint_as_float(o[e * 8 + 3]) * inv_l);
+            x.z = pack_bf16x2(__uint_as_float(o[e * 8 + 4]) * inv_l, __uint_as_float(o[e * 8 + 5]) * inv_l);
+            x.w = pack_bf16x2(__uint_as_float(o[e * 8 + 6]) * inv_l, __uint_as_float(o[e * 8 + 7]) * inv_l);
+            dst[e] = x;
           }
-          if (key0 + kBN - 1 > pos0) {
-            const int hi_c = pos - key0;                     // visible columns [0, hi_c]
+        } else {
+          uint4* dst = reinterpret_cast<uint4*>(p.part_o + part_row * D + c * C::kOChunk);
 #pragma unroll
-            for (int c = 0; c < kBN; ++c)
+          for (int e = 0; e < C::kOChunk / 4; ++e)
+            dst[e] = make_uint4(o[e * 4], o[e * 4 + 1], o[e * 4 + 2], o[e * 4 + 3]);
+        }
+      };
+      if (n <= 0) {
+        // nothing to see: rows of zeros
+        if (valid) {
+          uint32_t o[C::kOChunk];
+#pragma unroll
+          for (int e = 0; e < C::kOChunk; ++e) o[e] = 0u;
+          for (int c = narrow ? quarter : 0; c < D / C::kOChunk; c += narrow ? 4 : 1) store(c, o, 0.f);
+        }
+        continue;
+      }
+      float m_used = -INFINITY, l = 0.f, alpha;
+      bool rescale;
+      if (narrow) {
+        // ---- each warp: all rows, keys [16 quarter, +16) of a tile
+        for (int i = 0; i < n; ++i, ++u) {
+          const uint32_t s_col = static_cast<uint32_t>((u & 1) * kBN);
+          const int key0 = (kt0 + i) * kBN;
+          ok = mbar_wait_warp(s_full + u % R, static_cast<uint32_t>(u / R) & 1u, ab);
+          if (!ok) break;
+          tc_fence_after();
+          if (!(ok = clear_tail(key0))) break;
+          uint32_t sr[kQuarterKeys];
+          tmem_ld_chunk(lane_base + s_col + quarter * kQuarterKeys, sr);
+          tmem_ld_wait();
+          reg_fence(sr);
+          float s[kQuarterKeys];
+#pragma unroll
+          for (int c = 0; c < kQuarterKeys; ++c) s[c] = __uint_as_float(sr[c]);
+          if (key0 + kBN - 1 > pos0) {
+            const int hi_c = pos - key0 - quarter * kQuarterKeys;
+#pragma unroll
+            for (int c = 0; c < kQuarterKeys; ++c)
               if (c > hi_c) s[c] = -INFINITY;
           }
-          float mx4[4];
+          float mx = fmax3(s[0], s[1], s[2]);
+          float mx1 = fmax3(s[3], s[4], s[5]);
 #pragma unroll
-          for (int x = 0; x < 4; ++x) mx4[x] = s[x];
-#pragma unroll
-          for (int c = 4; c < kBN; c += 8)
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-              mx4[x] = fmax3(mx4[x], s[c + x], c + 4 + x < kBN ? s[c + 4 + x] : s[c + x]);
-          const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
-          const float m_new = fmaxf(m_used, mx * scale_log2);
-          float alpha = 1.f;
-          bool rescale_warp = false;
-          if (i == 0) {
-            m_used = m_new;
-          } else {
-            // rows that are no query hold leftovers: they never ask for a rescale
-            const bool need = valid && m_new > m_used + kRescaleThreshold;
-            rescale_warp = __any_sync(0xffffffffu, need);
-            if (need) {
-              alpha = ex2_approx(m_used - m_new);
-              m_used = m_new;
-              l *= alpha;
-            }
-            // the rescale follows O += P(u-1) V(u-1): its barrier's previous
-            // phase is complete (S(u) was issued after it) and its next one
-            // needs this softmax's next P, so the parity wait is exact
-            if (rescale_warp) {
-              ok = mbar_wait_warp(o_full + (u - 1) % R, static_cast<uint32_t>((u - 1) / R) & 1u, ab);
-              if (!ok) break;
-              tc_fence_after();
-            }
+          for (int c = 6; c + 4 <= kQuarterKeys; c += 4) {
+            mx = fmax3(mx, s[c], s[c + 1]);
+            mx1 = fmax3(mx1, s[c + 2], s[c + 3]);
           }
+          mx = fmax3(mx, mx1, fmaxf(s[kQuarterKeys - 2], s[kQuarterKeys - 1]));
+          if (!(ok = move_max(i, mx, valid, m_used, l, alpha, rescale))) break;
           const float m_sub = (m_used == -INFINITY) ? 0.f : m_used;
-          const float2 sc2 = make_float2(scale_log2, scale_log2);
           const float2 neg2 = make_float2(-m_sub, -m_sub);
-          float2 acc[4];
+          float2 acc = make_float2(0.f, 0.f);
+          uint32_t pq[kQuarterKeys / 2];
 #pragma unroll
-          for (int x = 0; x < 4; ++x) acc[x] = make_float2(0.f, 0.f);
-          uint32_t pk[kBN / 2];
-#pragma unroll
-          for (int e = 0; e < kBN / 2; ++e) {
+          for (int e = 0; e < kQuarterKeys / 2; ++e) {
             const float2 x = __ffma2_rn(make_float2(s[2 * e], s[2 * e + 1]), sc2, neg2);
             const float2 pe = make_float2(ex2_approx(x.x), ex2_approx(x.y));
-            acc[e & 3] = __fadd2_rn(acc[e & 3], pe);
-            pk[e] = pack_bf16x2(pe.x, pe.y);
+            acc = __fadd2_rn(acc, pe);
+            pq[e] = pack_bf16x2(pe.x, pe.y);
           }
+          // the other quarters' keys weigh nothing in this quarter's rows
+          uint32_t pk[kBN / 2];
+#pragma unroll
+          for (int e = 0; e < kBN / 2; ++e)
+            pk[e] = e / (kQuarterKeys / 2) == quarter ? pq[e % (kQuarterKeys / 2)] : 0u;
           tmem_st32(lane_base + s_col, pk);
-          const float2 a = __fadd2_rn(__fadd2_rn(acc[0], acc[1]), __fadd2_rn(acc[2], acc[3]));
-          if (rescale_warp) {
-#pragma unroll
-            for (int c = 0; c < D / C::kOChunk; ++c) {
-              uint32_t o[C::kOChunk];
-              tmem_ld_chunk(lane_base + C::kOCol + c * C::kOChunk, o);
-              tmem_ld_wait();
-              reg_fence(o);
-#pragma unroll
-              for (int e = 0; e < C::kOChunk; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-              tmem_st_chunk(lane_base + C::kOCol + c * C::kOChunk, o);
-            }
-          }
-          l += a.x + a.y;
+          if (rescale) rescale_o(alpha);
+          l += acc.x + acc.y;
           tmem_st_wait();
+          tc_fence_before();
+          mbar_arrive(p_full + (u & 1));
         }
-        tc_fence_before();
-        mbar_arrive(p_full + (u & 1));
-      }
-      if (!ok) break;
-      // ---- end of the piece: a whole unit is normalised and stored, a part
-      // goes to the workspace as it is
-      const bool whole = kt0 == 0 && w.end() == w.cost;
-      if (n > 0) {
+        if (!ok) break;
         ok = mbar_wait_warp(o_last, static_cast<uint32_t>(pieces) & 1u, ab);
         if (!ok) break;
         tc_fence_after();
-      }
-      if (busy) {
-        const float inv_l = (n > 0 && l > 0.f) ? 1.f / l : 0.f;
-        const long long out_row =
-            static_cast<long long>(w.q.start + token0 + token) * p.h + w.at.hk * p.group + head;
-        const long long slot = static_cast<long long>(cta) * 2 + (kt0 > 0 ? 0 : 1);
-        const long long part_row = slot * p.slot_rows + row;
+        // ---- merge the quarters: (m, l) first, then O chunk by chunk, chunk c
+        // summed and stored by warp c % 4 from its own registers and the
+        // other three warps' rows in shared memory
+        float2* xml = reinterpret_cast<float2*>(smem + C::kXmlOff);
+        xml[quarter * kNarrowRows + lane] = make_float2(m_used, l);
+        mbar_arrive(x_full);
+        ok = mbar_wait_warp(x_full, static_cast<uint32_t>(exchanged) & 1u, ab);
+        if (!ok) break;
+        ++exchanged;
+        float mm = m_used;
 #pragma unroll
-        for (int c = 0; c < D / C::kOChunk; ++c) {
+        for (int y = 0; y < 4; ++y) mm = fmaxf(mm, xml[y * kNarrowRows + lane].x);
+        float ll = 0.f;
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          const float2 ml = xml[y * kNarrowRows + lane];
+          ll += (ml.x == -INFINITY) ? 0.f : ml.y * ex2_approx(ml.x - mm);
+        }
+        const float f = (m_used == -INFINITY) ? 0.f : ex2_approx(m_used - mm);
+        const float inv_l = ll > 0.f ? 1.f / ll : 0.f;
+#pragma unroll 1
+        for (int c = 0; ok && c < D / C::kOChunk; ++c) {
           uint32_t o[C::kOChunk];
-          __syncwarp();
-          if (n > 0) {
-            tmem_ld_chunk(lane_base + C::kOCol + c * C::kOChunk, o);
-            tmem_ld_wait();
-            reg_fence(o);
-          } else {
+          tmem_ld_chunk(lane_base + C::kOCol + c * C::kOChunk, o);
+          tmem_ld_wait();
+          reg_fence(o);
 #pragma unroll
-            for (int e = 0; e < C::kOChunk; ++e) o[e] = 0u;
-          }
-          if (valid && whole) {
-            uint4* dst = reinterpret_cast<uint4*>(p.out + out_row * D + c * C::kOChunk);
-#pragma unroll
-            for (int e = 0; e < C::kOChunk / 8; ++e) {
-              uint4 x;
-              x.x = pack_bf16x2(__uint_as_float(o[e * 8 + 0]) * inv_l, __uint_as_float(o[e * 8 + 1]) * inv_l);
-              x.y = pack_bf16x2(__uint_as_float(o[e * 8 + 2]) * inv_l, __uint_as_float(o[e * 8 + 3]) * inv_l);
-              x.z = pack_bf16x2(__uint_as_float(o[e * 8 + 4]) * inv_l, __uint_as_float(o[e * 8 + 5]) * inv_l);
-              x.w = pack_bf16x2(__uint_as_float(o[e * 8 + 6]) * inv_l, __uint_as_float(o[e * 8 + 7]) * inv_l);
-              dst[e] = x;
-            }
-          } else if (valid) {
-            uint4* dst = reinterpret_cast<uint4*>(p.part_o + part_row * D + c * C::kOChunk);
+          for (int e = 0; e < C::kOChunk; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+          // the chunk before has been read
+          if (freed > 0 && !(ok = mbar_wait_warp(x_free, static_cast<uint32_t>(freed - 1) & 1u, ab))) break;
+          const int owner = c & 3;
+          const int slot = (quarter - owner - 1) & 3;        // 0 .. 2; 3 for the owner
+          if (quarter != owner) {
+            uint4* dst = reinterpret_cast<uint4*>(smem + C::kXOff + slot * C::kXSlot + lane * C::kXRow);
 #pragma unroll
             for (int e = 0; e < C::kOChunk / 4; ++e)
               dst[e] = make_uint4(o[e * 4], o[e * 4 + 1], o[e * 4 + 2], o[e * 4 + 3]);
           }
+          mbar_arrive(x_full);
+          if (quarter == owner) {
+            ok = mbar_wait_warp(x_full, static_cast<uint32_t>(exchanged) & 1u, ab);
+            if (!ok) break;
+#pragma unroll
+            for (int y = 0; y < 3; ++y) {
+              const float4* src = reinterpret_cast<const float4*>(smem + C::kXOff + y * C::kXSlot + lane * C::kXRow);
+#pragma unroll
+              for (int e = 0; e < C::kOChunk / 4; ++e) {
+                const float4 v = src[e];
+                o[e * 4] = __float_as_uint(__uint_as_float(o[e * 4]) + v.x);
+                o[e * 4 + 1] = __float_as_uint(__uint_as_float(o[e * 4 + 1]) + v.y);
+                o[e * 4 + 2] = __float_as_uint(__uint_as_float(o[e * 4 + 2]) + v.z);
+                o[e * 4 + 3] = __float_as_uint(__uint_as_float(o[e * 4 + 3]) + v.w);
+              }
+            }
+            mbar_arrive(x_free);
+            if (valid) store(c, o, inv_l);
+            __syncwarp();
+          }
+          ++exchanged;
+          ++freed;
         }
-        if (!whole && valid)
-          *reinterpret_cast<float2*>(p.part_ml + part_row * 2) = make_float2(m_used, l);
+        if (!ok) break;
+        if (!whole && valid && quarter == 0)
+          *reinterpret_cast<float2*>(p.part_ml + part_row * 2) = make_float2(mm, ll);
+      } else {
+        const bool busy = quarter * 32 < rows;               // some row of this warp is a query
+        for (int i = 0; i < n; ++i, ++u) {
+          const uint32_t s_col = static_cast<uint32_t>((u & 1) * kBN);
+          const int key0 = (kt0 + i) * kBN;
+          ok = mbar_wait_warp(s_full + u % R, static_cast<uint32_t>(u / R) & 1u, ab);
+          if (!ok) break;
+          tc_fence_after();
+          if (!(ok = clear_tail(key0))) break;
+          if (busy) {
+            float s[kBN];
+            {
+              uint32_t sr[32];
+#pragma unroll
+              for (int c = 0; c < kBN / 32; ++c) {
+                tmem_ld32(lane_base + s_col + c * 32, sr);
+                tmem_ld_wait();
+                reg_fence(sr);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) s[c * 32 + e] = __uint_as_float(sr[e]);
+              }
+            }
+            if (key0 + kBN - 1 > pos0) {
+              const int hi_c = pos - key0;                   // visible columns [0, hi_c]
+#pragma unroll
+              for (int c = 0; c < kBN; ++c)
+                if (c > hi_c) s[c] = -INFINITY;
+            }
+            float mx4[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) mx4[x] = s[x];
+#pragma unroll
+            for (int c = 4; c < kBN; c += 8)
+#pragma unroll
+              for (int x = 0; x < 4; ++x)
+                mx4[x] = fmax3(mx4[x], s[c + x], c + 4 + x < kBN ? s[c + 4 + x] : s[c + x]);
+            const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
+            if (!(ok = move_max(i, mx, valid, m_used, l, alpha, rescale))) break;
+            const float m_sub = (m_used == -INFINITY) ? 0.f : m_used;
+            const float2 neg2 = make_float2(-m_sub, -m_sub);
+            float2 acc[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) acc[x] = make_float2(0.f, 0.f);
+            uint32_t pk[kBN / 2];
+#pragma unroll
+            for (int e = 0; e < kBN / 2; ++e) {
+              const float2 x = __ffma2_rn(make_float2(s[2 * e], s[2 * e + 1]), sc2, neg2);
+              const float2 pe = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+              acc[e & 3] = __fadd2_rn(acc[e & 3], pe);
+              pk[e] = pack_bf16x2(pe.x, pe.y);
+            }
+            tmem_st32(lane_base + s_col, pk);
+            const float2 a = __fadd2_rn(__fadd2_rn(acc[0], acc[1]), __fadd2_rn(acc[2], acc[3]));
+            if (rescale) rescale_o(alpha);
+            l += a.x + a.y;
+            tmem_st_wait();
+          }
+          tc_fence_before();
+          mbar_arrive(p_full + (u & 1));
+        }
+        if (!ok) break;
+        ok = mbar_wait_warp(o_last, static_cast<uint32_t>(pieces) & 1u, ab);
+        if (!ok) break;
+        tc_fence_after();
+        if (busy) {
+          const float inv_l = l > 0.f ? 1.f / l : 0.f;
+          if constexpr (D < 32) {
+            uint32_t o[C::kOChunk];
+            tmem_ld_chunk(lane_base + C::kOCol, o);
+            tmem_ld_wait();
+            reg_fence(o);
+            if (valid) store(0, o, inv_l);
+          } else {
+            // Stores straight from the rows' owners would touch 32 lines with
+            // 16 bytes each; turned through shared memory, four lanes write
+            // 64 bytes of a row.
+            const int rows_here = min(32, rows - quarter * 32);
+            uint8_t* turn = smem + C::kXOff + quarter * C::kTurnSlot;
+            const int r0 = lane >> 2, piece = lane & 3;
+            // 64-byte steps of a row: 32 columns as bf16 or 16 as fp32
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t o[32];
+              __syncwarp();
+              tmem_ld32(lane_base + C::kOCol + c * 32, o);
+              tmem_ld_wait();
+              reg_fence(o);
+              uint4* mine = reinterpret_cast<uint4*>(turn + lane * C::kTurnRow);
+              if (whole) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  uint4 x;
+                  x.x = pack_bf16x2(__uint_as_float(o[e * 8 + 0]) * inv_l, __uint_as_float(o[e * 8 + 1]) * inv_l);
+                  x.y = pack_bf16x2(__uint_as_float(o[e * 8 + 2]) * inv_l, __uint_as_float(o[e * 8 + 3]) * inv_l);
+                  x.z = pack_bf16x2(__uint_as_float(o[e * 8 + 4]) * inv_l, __uint_as_float(o[e * 8 + 5]) * inv_l);
+                  x.w = pack_bf16x2(__uint_as_float(o[e * 8 + 6]) * inv_l, __uint_as_float(o[e * 8 + 7]) * inv_l);
+                  mine[e] = x;
+                }
+                __syncwarp();
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  const int x = r0 + 8 * k;                  // row of this warp
+                  const uint4 v = *reinterpret_cast<const uint4*>(turn + x * C::kTurnRow + piece * 16);
+                  const int rr = quarter * 32 + x, tok = rr / p.group;
+                  if (x < rows_here)
+                    *reinterpret_cast<uint4*>(
+                        p.out + (static_cast<long long>(w.q.start + token0 + tok) * p.h + w.at.hk * p.group +
+                                 rr - tok * p.group) * D + c * 32 + piece * 8) = v;
+                }
+                __syncwarp();
+              } else {
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+#pragma unroll
+                  for (int e = 0; e < 4; ++e)
+                    mine[e] = make_uint4(o[half * 16 + e * 4], o[half * 16 + e * 4 + 1], o[half * 16 + e * 4 + 2],
+                                         o[half * 16 + e * 4 + 3]);
+                  __syncwarp();
+#pragma unroll
+                  for (int k = 0; k < 4; ++k) {
+                    const int x = r0 + 8 * k;
+                    const uint4 v = *reinterpret_cast<const uint4*>(turn + x * C::kTurnRow + piece * 16);
+                    if (x < rows_here)
+                      *reinterpret_cast<uint4*>(p.part_o + (part_row - lane + x) * D + c * 32 + half * 16 + piece * 4) = v;
+                  }
+                  __syncwarp();
+                }
+              }
+            }
+          }
+          if (!whole && valid) *reinterpret_cast<float2*>(p.part_ml + part_row * 2) = make_float2(m_used, l);
+        }
       }
-      if (n > 0) {
-        __syncwarp();
-        tc_fence_before();
-        mbar_arrive(o_free);
-        ++pieces;
-      }
+      __syncwarp();
+      tc_fence_before();
+      mbar_arrive(o_free);
+      ++pieces;
     } while (w.next(p));
   }
 
@@ -663,57 +926,74 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
 }
 
 // ------------------------------------------------------------------- combine
-// Block c - 1 looks after run boundary c: if it is the first one inside its
-// unit, the block merges the unit's pieces.  The unit's first piece is the
-// last of run c - 1 (slot 1), the others begin runs c, c + 1, ... (slot 0).
-constexpr int kCombineThreads = 256;
+// The runs that begin inside a unit merge its pieces: the last piece of the
+// run that the unit begins in (slot 1) and the first ones of the runs after
+// it (slot 0).  Each takes a share of the unit's (row, 4 columns) items, so a
+// walk cut into many pieces is merged by as many blocks.
+constexpr int kCombineThreads = 128;
 
 template <int D>
 __global__ void __launch_bounds__(kCombineThreads) sdpa_paged_combine(const __grid_constant__ PagedParams p) {
-  __shared__ ScheduleShared sched;
   const int c = static_cast<int>(blockIdx.x) + 1;
-  long long work = 0;
-  int ctas = 0;
-  Place at;
-  // the lengths were complete before the split kernel passed its own wait
-  const bool any = find_place<kCombineThreads>(p, &sched, c, p.split_ctas, &work, &ctas, &at);
   griddep_launch_dependents();
   griddep_wait();
-  if (!any || at.kt == 0) return;
-  const long long begin = run_begin(work, c, ctas) - at.kt;
-  if (run_begin(work, c - 1, ctas) > begin) return;
-  const Seq q = load_seq(p, at.s);
-  const long long end = begin + tile_cost(tile_keys(p, q, at.r));
-  int last = c;
-  while (last + 1 < ctas && run_begin(work, last + 1, ctas) < end) ++last;
-  const int token0 = at.r * p.tile_tokens;
-  const int rows = min(p.tile_tokens, q.n - token0) * p.group;
+  const PagedRun r = p.runs[c];
+  if (!r.inside) return;
+  const Cut cut(r.work, r.ctas);
+  const int c0 = cut.run_of(r.unit), last = cut.run_of(r.unit + r.cost - 1);
   constexpr int kVec = D / 4;
-  for (int x = threadIdx.x + blockIdx.y * kCombineThreads; x < rows * kVec;
-       x += kCombineThreads * gridDim.y) {
-    const int row = x / kVec, col = x % kVec * 4;
-    auto part_row = [&](int run) {   // run c-1 .. last
-      return (static_cast<long long>(run) * 2 + (run < c ? 1 : 0)) * p.slot_rows + row;
+  const int items = r.rows * kVec;
+  const int share_of = (last - c0) * static_cast<int>(gridDim.y);
+  const int share = (items + share_of - 1) / share_of;
+  const int item0 = ((c - c0 - 1) * static_cast<int>(gridDim.y) + static_cast<int>(blockIdx.y)) * share;
+  const int item1 = min(item0 + share, items);
+  // `lanes` lanes of a warp split an item's pieces among them, as far as the
+  // share leaves threads over
+  const int pieces = last - c0 + 1;
+  int lanes = 1;
+  while (lanes < 32 && lanes * 2 * share <= kCombineThreads && lanes < pieces) lanes *= 2;
+  const int wide = 32 / lanes;                                // items of a warp at a time
+  const int lane = threadIdx.x & 31;
+  const int y = lane / wide;
+  for (int base = item0 + static_cast<int>(threadIdx.x >> 5) * wide; base < item1;
+       base += kCombineThreads / lanes) {
+    const int x = base + lane % wide;
+    const int row = min(x, items - 1) / kVec, col = x % kVec * 4;
+    auto part = [&](int i) {                                  // piece i: run c0 + i
+      return (static_cast<long long>(c0 + i) * 2 + (i == 0 ? 1 : 0)) * p.slot_rows + row;
     };
-    float mm = -INFINITY;
-    for (int r = c - 1; r <= last; ++r) mm = fmaxf(mm, p.part_ml[part_row(r) * 2]);
+    float m = -INFINITY;
+#pragma unroll 4
+    for (int i = y; i < pieces; i += lanes) m = fmaxf(m, p.part_ml[part(i) * 2]);
+    for (int o = wide; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const float sub = m == -INFINITY ? 0.f : m;
     float l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int r = c - 1; r <= last; ++r) {
-      const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + part_row(r) * 2);
-      const float4 v = *reinterpret_cast<const float4*>(p.part_o + part_row(r) * D + col);
-      const float sc = (ml.x == -INFINITY) ? 0.f : ex2_approx(ml.x - mm);
-      l += ml.y * sc;
-      o.x += v.x * sc;
-      o.y += v.y * sc;
-      o.z += v.z * sc;
-      o.w += v.w * sc;
+    float4 o4 = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int i = y; i < pieces; i += lanes) {
+      const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + part(i) * 2);
+      const float4 v = *reinterpret_cast<const float4*>(p.part_o + part(i) * D + col);
+      const float f = ex2_approx(ml.x - sub);
+      l += ml.y * f;
+      o4.x += v.x * f;
+      o4.y += v.y * f;
+      o4.z += v.z * f;
+      o4.w += v.w * f;
     }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-    const long long out_row =
-        static_cast<long long>(q.start + token0 + row / p.group) * p.h + at.hk * p.group + row % p.group;
-    *reinterpret_cast<uint2*>(p.out + out_row * D + col) =
-        make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+    for (int o = wide; o < 32; o <<= 1) {
+      l += __shfl_xor_sync(0xffffffffu, l, o);
+      o4.x += __shfl_xor_sync(0xffffffffu, o4.x, o);
+      o4.y += __shfl_xor_sync(0xffffffffu, o4.y, o);
+      o4.z += __shfl_xor_sync(0xffffffffu, o4.z, o);
+      o4.w += __shfl_xor_sync(0xffffffffu, o4.w, o);
+    }
+    if (y == 0 && x < item1) {
+      const float inv = l > 0.f ? 1.f / l : 0.f;
+      const int token = row / p.group;
+      const long long out_row = static_cast<long long>(r.token + token) * p.h + r.head + row - token * p.group;
+      *reinterpret_cast<uint2*>(p.out + out_row * D + col) =
+          make_uint2(pack_bf16x2(o4.x * inv, o4.y * inv), pack_bf16x2(o4.z * inv, o4.w * inv));
+    }
   }
 }
 
@@ -726,7 +1006,8 @@ cudaError_t launch_paged_impl(const PagedParams& p, cudaStream_t stream) {
   err = launch_kernel(sdpa_paged_split<D>, dim3(static_cast<unsigned>(p.split_ctas)), dim3(kThreads), smem,
                       stream, true, p);
   if (err != cudaSuccess || p.split_ctas == 1) return err;
-  const int y = (p.slot_rows * (D / 4) + 4 * kCombineThreads - 1) / (4 * kCombineThreads);
+  // up to four blocks a run (all of them are resident at once)
+  const int y = min((p.slot_rows * (D / 4) + 4 * kCombineThreads - 1) / (4 * kCombineThreads), 4);
   return launch_kernel(sdpa_paged_combine<D>,
                        dim3(static_cast<unsigned>(p.split_ctas - 1), static_cast<unsigned>(y)),
                        dim3(kCombineThreads), 0, stream, true, p);
