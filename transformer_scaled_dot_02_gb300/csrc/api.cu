@@ -4,6 +4,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <chrono>
 #include <cmath>
 #include <cstdint>
 #include <mutex>
@@ -403,19 +404,34 @@ int log2_of(int x) {
   return s;
 }
 
-// CTAs of the split kernel: every resident one, or as many as runs of
-// kPagedMinTiles key tiles could ever be filled.
+// CTAs of the split kernel: every resident one, or as many as there could
+// ever be key tiles.
 int paged_split_ctas(int b, int n_tokens, int h_kv, int group, int d, long long max_len) {
   const long long tile_tokens = 128 / group;
   const long long units = (n_tokens / tile_tokens + std::min(b, n_tokens)) * h_kv;
   const long long tiles = units * (max_len / sdpa::kPagedKeyTile + 1);
-  const long long runs = (tiles + sdpa::kPagedMinTiles - 1) / sdpa::kPagedMinTiles;
-  const long long most = 1ll * sdpa::paged_resident_ctas(d) * sdpa::device_sm_count();
-  return static_cast<int>(std::max(1ll, std::min(most, runs)));
+  const long long most =
+      std::min<long long>(sdpa::kPagedMaxRuns, 1ll * sdpa::paged_resident_ctas(d) * sdpa::device_sm_count());
+  return static_cast<int>(std::max(1ll, std::min(most, tiles)));
 }
 
-int paged_slot_rows(int n_tokens, int group) {
-  return static_cast<int>(std::min(128ll, 1ll * n_tokens * group));
+// The number that marks a call's workspace slots as written.  Every reader
+// clears what it read, so a replayed launch may use its number again; what an
+// unwritten workspace holds must only not be this number, so the numbers are
+// a sequence of 64-bit steps from a place that differs from process to process.
+unsigned long long paged_call_number() {
+  static std::atomic<unsigned long long> next{
+      static_cast<unsigned long long>(std::chrono::system_clock::now().time_since_epoch().count()) *
+          0xd1342543de82ef95ull ^
+      reinterpret_cast<uintptr_t>(&g_mutex)};
+  const unsigned long long z = next.fetch_add(0x9e3779b97f4a7c15ull, std::memory_order_relaxed);
+  return z != 0 ? z : 1;
+}
+
+// Bytes of a workspace slot: fp32 O and two statistics a row.
+int paged_slot_bytes(int n_tokens, int group, int d) {
+  const long long rows = std::min(128ll, 1ll * n_tokens * group);
+  return static_cast<int>(round256(static_cast<size_t>(rows) * (d * 4 + 8) + 8));
 }
 
 }  // namespace
@@ -805,9 +821,8 @@ size_t sdpa_paged_workspace_size(int b, int n_tokens, int h, int h_kv, int d, in
   const int group = h / h_kv;
   const int ctas = paged_split_ctas(b, n_tokens, h_kv, group, d, 1ll * pages_per_seq * page_size);
   if (ctas == 1) return 0;
-  const size_t rows = 2 * static_cast<size_t>(ctas) * paged_slot_rows(n_tokens, group);
-  return round256(rows * d * 4) + round256(rows * 2 * 4) +
-         round256(static_cast<size_t>(ctas) * sizeof(sdpa::PagedRun));
+  return static_cast<size_t>(ctas) * paged_slot_bytes(n_tokens, group, d) +
+         round256(static_cast<size_t>(ctas) * 8);
 }
 
 sdpa_status sdpa_paged_forward(const void* q, const void* k_pages, const void* v_pages, void* out,
@@ -854,14 +869,12 @@ sdpa_status sdpa_paged_forward(const void* q, const void* k_pages, const void* v
   p.n_pages = n_pages;
   p.pages_per_seq = pages_per_seq;
   p.split_ctas = paged_split_ctas(b, n_tokens, h_kv, p.group, d, 1ll * pages_per_seq * page_size);
-  p.min_tiles = sdpa::kPagedMinTiles;
-  p.slot_rows = paged_slot_rows(n_tokens, p.group);
-  const size_t rows = 2 * static_cast<size_t>(p.split_ctas) * p.slot_rows;
-  uint8_t* ws = static_cast<uint8_t*>(workspace);
-  p.part_o = need > 0 ? reinterpret_cast<float*>(ws) : nullptr;
-  p.part_ml = need > 0 ? reinterpret_cast<float*>(ws + round256(rows * d * 4)) : nullptr;
-  p.runs = need > 0 ? reinterpret_cast<sdpa::PagedRun*>(ws + round256(rows * d * 4) + round256(rows * 2 * 4))
-                    : nullptr;
+  p.slot_bytes = paged_slot_bytes(n_tokens, p.group, d);
+  p.slots = need > 0 ? static_cast<uint8_t*>(workspace) : nullptr;
+  p.flags = need > 0 ? reinterpret_cast<unsigned long long*>(
+                           p.slots + static_cast<size_t>(p.split_ctas) * p.slot_bytes)
+                     : nullptr;
+  p.call = paged_call_number();
   p.scale_log2 = effective_scale(scale, d) * 1.4426950408889634f;
   return sdpa::launch_sdpa_paged(p, d, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SDPA_OK
                                                                                           : SDPA_ERR_CUDA;

@@ -103,22 +103,16 @@ int decode_splits(int b, int h, int n_k, int target_ctas);
 cudaError_t launch_sdpa_decode(const DecodeParams& p, int d_k, int d_v, cudaStream_t stream);
 
 // Attention of packed new tokens over a paged cache (csrc/paged.cu).
-// What the split kernel's run c tells the combine kernel.
-struct PagedRun {
-  long long work, unit;       // key tiles in all; where the unit that the run begins in begins
-  int ctas, inside;           // runs in all; whether the run begins inside that unit, which
-  int cost, rows;             // takes `cost` key tiles and has `rows` rows,
-  int token, head;            // the first of them this token's and this head's
-};
 struct PagedParams {
   CUtensorMap tm_q;           // 3-D (d, h, n_tokens) map, boxes of min(d, 64) x group x tile_tokens
   CUtensorMap tm_q_narrow;    // the same with boxes of 32 / group tokens (tm_q for groups over 32)
   CUtensorMap tm_k, tm_v;     // 4-D (d, page rows, h_kv, n_pages) maps, boxes of min(d, 64)
                               // columns x min(page, kPagedKeyTile) rows
   uint16_t* out;              // bf16 [n_tokens][h][d]
-  float* part_o;              // [2 split_ctas][slot_rows][d]  (split_ctas > 1)
-  float* part_ml;             // [2 split_ctas][slot_rows][2]  (split_ctas > 1)
-  PagedRun* runs;             // [split_ctas]  (split_ctas > 1)
+  // workspace (split_ctas > 1)
+  uint8_t* slots;             // [split_ctas][slot_bytes]: a published piece's O, then its (m, l)
+  unsigned long long* flags;  // [split_ctas]
+  unsigned long long call;    // the call's number: no other call's flags have it
   const int32_t* page_table;  // [b][pages_per_seq]
   const int32_t* q_starts;    // [b + 1]
   const int32_t* kv_lengths;  // [b]
@@ -127,13 +121,12 @@ struct PagedParams {
   int group, tile_tokens;     // h / h_kv; tokens per row tile, 128 / group
   int page_shift, n_pages, pages_per_seq;
   int split_ctas;             // CTAs of the split kernel (runs, at most)
-  int min_tiles;              // key tiles of a run, at least (while there are runs to spare)
-  int slot_rows;              // rows of a workspace slot
+  int slot_bytes;             // of 128 rows, or as many as the call has
   float scale_log2;
 };
 constexpr int kPagedKeyTile = 64;
 constexpr int kPagedMinPage = 8;
-constexpr int kPagedMinTiles = 1;
+constexpr int kPagedMaxRuns = 1 << 12;
 bool paged_supports(int d);
 int paged_resident_ctas(int d);   // split CTAs that share an SM
 cudaError_t launch_sdpa_paged(const PagedParams& p, int d, cudaStream_t stream);

@@ -8,17 +8,23 @@
 // sequence s is row j % P of page page_table[s][j / P].  Query head x reads
 // key-value head x / (h / h_kv).
 //
-// sdpa_paged_split<D>     A UNIT is (sequence, key-value head, row tile): the
-//   rows of a tile are tile_tokens tokens x the group's heads (at most 128),
-//   so one walk over the keys serves every query head of the group.  A
-//   unit's walk is its visible keys in tiles of 64; all walks laid end to
-//   end are cut into equal runs of tiles, one per CTA, so that one long
-//   sequence, many short ones and any mixture load the SMs alike.  A CTA
-//   whose run begins or ends inside a unit leaves that piece's (O, m, l) in
-//   the workspace.  The cut is worked out on the device from the lengths, so
-//   a captured launch follows them.
-// sdpa_paged_combine<D>   merges the pieces of each unit that was cut:
+// sdpa_paged_split<D>: a UNIT is (sequence, key-value head, row tile); the
+// rows of a tile are tile_tokens tokens x the group's heads (at most 128), so
+// one walk over the keys serves every query head of the group.  A unit's walk
+// is its visible keys in tiles of 64; all walks laid end to end are cut into
+// equal runs of tiles, one per CTA, so that one long sequence, many short
+// ones and any mixture load the SMs alike.  The cut is worked out on the
+// device from the lengths, so a captured launch follows them.
+//
+// A CTA works its run from the end to the beginning.  If the run ends inside
+// a unit, that piece comes first and its (O, m, l) is published in the
+// workspace; if it begins inside a unit, that piece comes last, and the CTA
+// merges the pieces that the runs before it published:
 //   O = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s, M = max_s m_s.
+// So a CTA waits for CTAs of lower index only, which were dispatched before
+// it: there is no order of execution in which the waits do not end.  Units cut
+// into many pieces are merged as a tree.  The pieces merge in an order fixed
+// by the cut, so results repeat bit by bit.
 //
 // Row tiles of at most 32 rows (single tokens) would leave three of the four
 // softmax warps idle and one with the whole row: their queries are copied to
@@ -76,7 +82,7 @@ __device__ __forceinline__ int tile_cost(int keys) { return max(1, (keys + kBN -
 // the last tile see A + (i + 1) t keys, A = len - n: z of them cost one, the
 // others ceil((A + (i + 1) t) / 64), whose sum over 64 consecutive i grows by
 // 64 t from one such block to the next.
-__device__ long long cost_before(const PagedParams& p, const Seq& q, int r) {
+__device__ __noinline__ long long cost_before(const PagedParams& p, const Seq& q, int r) {
   const int t = p.tile_tokens;
   const int f = min(r, q.tiles - 1);
   long long sum = 0;
@@ -87,6 +93,24 @@ __device__ long long cost_before(const PagedParams& p, const Seq& q, int r) {
     const int cnt = f - z;
     if (cnt > 0) {
       const int base = a + t * (z + 1) + kBN - 1;   // > kBN
+      if ((t & (t - 1)) == 0) {                      // groups that are powers of two
+        const long long n = cnt;
+        sum += n * (base / kBN);
+        if (t >= kBN) {
+          sum += t / kBN * (n * (n - 1) / 2);
+        } else {
+          // floor((o + t i) / 64) = floor((o / t + i) / (64 / t)), summed below m:
+          const int log_t = __ffs(t) - 1, log_per = 6 - log_t;
+          auto below = [&](long long m) {
+            const long long q = m >> log_per;
+            return (q * (q - 1) / 2 << log_per) + q * (m - (q << log_per));
+          };
+          const int o = (base % kBN) >> log_t;
+          sum += below(o + n) - below(o);
+        }
+        if (r == q.tiles) sum += tile_cost(q.len);
+        return sum;
+      }
       const int blocks = cnt / kBN, rest = cnt % kBN;
       long long head = 0, full = 0;                  // the first `rest` terms; the first 64
       const int walk = blocks > 0 ? kBN : rest;
@@ -104,8 +128,8 @@ __device__ long long cost_before(const PagedParams& p, const Seq& q, int r) {
   return sum;
 }
 
-// A place in the laid-out work: key tile kt of row tile r of head hk of
-// sequence s.
+// A place in the laid-out work: before key tile kt of row tile r of head hk
+// of sequence s (kt > 0).
 struct Place {
   int s, hk, r, kt;
 };
@@ -123,20 +147,23 @@ __device__ __forceinline__ long long divide(long long a, long long b) {
   return a / b;
 }
 
-// Work is cut into runs: run c of `ctas` is [floor(work c / ctas), floor(work (c + 1) / ctas)).
+// Work is cut into runs of `each` items, the first `over` of them one longer.
 struct Cut {
-  long long work, each;
-  int ctas, over;
-  __device__ Cut(long long w, int n) : work(w), ctas(n) {
-    each = divide(w, n);
-    over = static_cast<int>(w - each * n);
+  long long each, longer;                                    // longer: items in the longer runs
+  int over;
+  __device__ Cut(long long work, int ctas) {
+    each = divide(work, ctas);
+    over = static_cast<int>(work - each * ctas);
+    longer = over * (each + 1);
   }
-  __device__ long long begin(int c) const { return each * c + over * c / ctas; }   // over, c < 2^15
-  // the run that holds item x: the last c with work c / ctas < x + 1
-  __device__ int run_of(long long x) const { return static_cast<int>(divide((x + 1) * ctas - 1, work)); }
+  __device__ long long begin(int c) const { return each * c + min(c, over); }
+  // the run that holds item x
+  __device__ int run_of(long long x) const {
+    return static_cast<int>(x < longer ? divide(x, each + 1) : over + divide(x - longer, each));
+  }
 };
 
-// The whole block: how the work is cut, and the place where run c begins.
+// The whole block: how the work is cut, and the place where run c ends.
 // Returns false (everywhere) when there is no such run.
 __device__ bool find_place(const PagedParams& p, ScheduleShared* sh, int c, int max_ctas, Cut* cut,
                            Place* at, Seq* seq) {
@@ -163,10 +190,10 @@ __device__ bool find_place(const PagedParams& p, ScheduleShared* sh, int c, int 
     if (w < warp) excl += sh->warp_sum[w];
     total += sh->warp_sum[w];
   }
-  const int n = static_cast<int>(min(static_cast<long long>(max_ctas), divide(total + p.min_tiles - 1, p.min_tiles)));
+  const int n = static_cast<int>(min(static_cast<long long>(max_ctas), total));   // a tile a run at least
   if (c >= n) return false;
   *cut = Cut(total, n);
-  const long long x = cut->begin(c);
+  const long long x = cut->begin(c + 1) - 1;                 // its last item
   if (mine > 0 && excl <= x && x < excl + mine) {
     long long rem = x - excl;
     Place pl;
@@ -183,7 +210,7 @@ __device__ bool find_place(const PagedParams& p, ScheduleShared* sh, int c, int 
     pl.hk = static_cast<int>(divide(rem, head));
     rem -= pl.hk * head;
     pl.r = 0;
-    pl.kt = static_cast<int>(rem);                           // the place, for a single row tile
+    pl.kt = static_cast<int>(rem) + 1;                       // for a single row tile
     sh->at = pl;
     sh->rem = rem;
     sh->q = q;
@@ -205,55 +232,97 @@ __device__ bool find_place(const PagedParams& p, ScheduleShared* sh, int c, int 
       hi = min(hi, lo + step);
     }
     at->r = lo;
-    at->kt = static_cast<int>(rem - cost_before(p, *seq, lo));
+    at->kt = static_cast<int>(rem - cost_before(p, *seq, lo)) + 1;
   }
   return true;
 }
 
-// The pieces of one run, in order; every role walks its own copy.
+// The pieces of one run, from the last to the first; every role walks its
+// own copy.
 struct Walk {
-  Place at;
+  Place at;                                                  // where the piece ends
   Seq q;
   int keys, cost;
   long long left;
 
-  __device__ void begin(const PagedParams& p, const Place& a, const Seq& first, long long run) {
-    at = a;
+  __device__ void begin(const PagedParams& p, const Place& end, const Seq& seq, long long run) {
+    at = end;
     left = run;
-    q = first;
+    q = seq;
     keys = tile_keys(p, q, at.r);
     cost = tile_cost(keys);
   }
-  // rows of this row tile that are queries; few enough for a quarter?
+  // rows of this row tile that are queries
   __device__ int rows(const PagedParams& p) const {
     return min(p.tile_tokens, q.n - at.r * p.tile_tokens) * p.group;
   }
-  __device__ bool narrow(const PagedParams& p) const { return rows(p) <= kNarrowRows; }
-  // key tiles of this piece: [at.kt, end()); those with keys: [at.kt, real_end())
-  __device__ int end() const {
-    return static_cast<int>(min(static_cast<long long>(cost), at.kt + left));
-  }
-  __device__ int real_end() const { return min(end(), (keys + kBN - 1) / kBN); }
+  // key tiles of this piece: [first(), at.kt); those with keys: [first(), first() + count())
+  __device__ int first() const { return static_cast<int>(max(0ll, at.kt - left)); }
+  __device__ int count() const { return min(at.kt, (keys + kBN - 1) / kBN) - first(); }
   __device__ bool next(const PagedParams& p) {
-    const int e = end();
-    left -= e - at.kt;
+    left -= at.kt - first();
     if (left <= 0) return false;
-    at.kt = 0;
-    if (++at.r == q.tiles) {
-      at.r = 0;
-      if (++at.hk == p.h_kv) {
-        at.hk = 0;
+    if (--at.r < 0) {
+      if (--at.hk < 0) {
         do {
-          if (++at.s >= p.b) return false;
+          if (--at.s < 0) return false;
           q = load_seq(p, at.s);
         } while (q.n == 0);
+        at.hk = p.h_kv - 1;
       }
+      at.r = q.tiles - 1;
     }
     keys = tile_keys(p, q, at.r);
     cost = tile_cost(keys);
+    at.kt = cost;
     return true;
   }
 };
+
+// --------------------------------------------------------------------- merge
+// Workspace slots: what run c publishes is slot c: O as [D / 4][rows] vectors
+// of four columns and, right behind, (m, l) as [rows].  A slot has a flag,
+// which is the call's number once the slot is written and is put back to zero
+// by its only reader.  A run merges at its end, when its K and V stages are
+// idle: the published pieces come into that memory by bulk copies.
+//
+// The unit's pieces j = 0, 1, .. (runs c0 + j) form a tree of radix R = 2^bits:
+// before it publishes, piece j merges the size(j) - 1 pieces below it, size(j)
+// the largest power of R that divides j + 1; the last piece merges all.  What
+// a piece reads are the tops of the blocks that make up its range.  Reading
+// R - 1 pieces a level costs R - 1 pieces' bytes on one SM, a level costs a
+// wait: narrow pieces (a few KB) take R = 16, wide ones (up to 128 KB) R = 4.
+constexpr int kMaxSources = 48;            // 15 a level: runs up to 2^12 (narrow), 2^32 (wide)
+static_assert(kPagedMaxRuns <= 1 << 12, "sources");
+
+__device__ __forceinline__ int block_size(int j, int bits) {
+  return 1 << ((__ffs(j + 1) - 1) / bits * bits);
+}
+
+// Waits until the flag is this call's number, and clears it.
+__device__ __forceinline__ bool take_flag(unsigned long long* flag, unsigned long long call, const AbortState& ab) {
+  const long long t0 = clock64();
+  while (true) {
+    unsigned long long v;
+    asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(flag) : "memory");
+    if (v == call) break;
+    if (*ab.flag) return false;
+    if (clock64() - t0 > kWaitLimitCycles) {
+      *ab.flag = 1;
+      atomicOr(ab.status, kStatusTimeout);
+      return false;
+    }
+  }
+  *flag = 0;
+  return true;
+}
+
+__device__ __forceinline__ void set_flag(unsigned long long* flag, unsigned long long call) {
+  asm volatile("st.release.gpu.global.u64 [%0], %1;" ::"l"(flag), "l"(call) : "memory");
+}
+
+// 2^(m - sub), 0 for a piece that saw nothing
+__device__ __forceinline__ float weight(float m, float sub) { return ex2_approx(m - sub); }
 
 // --------------------------------------------------------------------- split
 template <int D>
@@ -272,21 +341,25 @@ struct PCfg {
   static constexpr int kRing = D >= 128 ? 2 : 4;
   static constexpr int kKOff = kQBytes;
   static constexpr int kVOff = kKOff + kRing * kKVBytes;
-  // exchange of a narrow tile's quarters: O chunks of three warps (rows padded
-  // by 16 bytes, so that eight lanes' vectors hit all banks), (m, l) of four
+  // O columns of a tensor-memory load
   static constexpr int kOChunk = D < 32 ? D : 32;
-  static constexpr int kXRow = kOChunk * 4 + 16;
-  static constexpr int kXSlot = kNarrowRows * kXRow;
-  // a wide tile's warps turn their rows through the same memory, 64 bytes of
-  // each at a time (rows padded by 16)
+  // Exchange memory: a narrow tile's quarters lay their rows here to be summed
+  // (16 columns of 32 rows at least), a wide tile's warps turn theirs, 64 bytes
+  // of each at a time (rows padded by 16).
+  static constexpr int kXOff = kVOff + kRing * kKVBytes;
+  static constexpr int kXBytes = 4 * kNarrowRows * 16 * 4 > 12288 ? 4 * kNarrowRows * 16 * 4 : 12288;
   static constexpr int kTurnRow = 64 + 16;
   static constexpr int kTurnSlot = 32 * kTurnRow;
-  static_assert(D < 32 || 4 * kTurnSlot <= 3 * kXSlot, "turning rows");
-  static constexpr int kXOff = kVOff + kRing * kKVBytes;
-  static constexpr int kXmlOff = kXOff + 3 * kXSlot;
-  static constexpr int kBarOff = kXmlOff + 4 * kNarrowRows * 8;
+  static_assert(4 * kTurnSlot <= kXBytes, "turning rows");
+  static constexpr int kXmlOff = kXOff + kXBytes;            // the quarters' (m, l)
+  // merging: the idle K and V stages and the exchange memory behind them hold
+  // one wide piece, or a narrow tile's own and at least one more
+  static constexpr int kMergeBytes = 2 * kRing * kKVBytes + kXBytes;
+  static_assert(kMergeBytes >= kBlockM * (D * 4 + 8) && kMergeBytes >= 2 * kNarrowRows * (D * 4 + 8), "pieces");
+  static constexpr int kXinvOff = kXmlOff + 4 * kNarrowRows * 8;   // 1 / l of their sum
+  static constexpr int kBarOff = kXinvOff + kNarrowRows * 4;
   // q_full, q_empty, k_full[R], v_full[R], s_full[R], o_full[R], p_full[2], o_last, o_free,
-  // x_full, x_free, drain
+  // merge, copied, drain
   static constexpr int kNumBars = 2 + 4 * kRing + 2 + 5;
   static constexpr int kSmemBytes = kBarOff + kNumBars * 8 + 16 + 1024;
   static constexpr uint32_t kOCol = 2 * kBN;
@@ -308,6 +381,7 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
   constexpr int R = C::kRing;
   extern __shared__ uint8_t smem_raw[];
   __shared__ ScheduleShared sched;
+  __shared__ int source_runs[kMaxSources];
   const uint32_t raw_u32 = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + (((raw_u32 + 1023u) & ~1023u) - raw_u32);
   const uint32_t smem_base = smem_u32(smem);
@@ -320,9 +394,9 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
   uint64_t* p_full = o_full + R;
   uint64_t* o_last = p_full + 2;      // once a piece, after its last O += P V
   uint64_t* o_free = o_last + 1;      // once a piece, when the softmax warps have read O
-  uint64_t* x_full = o_free + 1;      // a step of the quarters' exchange is written
-  uint64_t* x_free = x_full + 1;      // an exchanged chunk is read
-  uint64_t* drain = x_free + 1;
+  uint64_t* merge = o_free + 1;       // steps of exchanging, publishing and merging
+  uint64_t* copied = merge + 1;       // published pieces have come into shared memory
+  uint64_t* drain = copied + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const AbortState ab{abort_flag, p.status};
@@ -341,44 +415,26 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
     for (int s = 0; s < 2; ++s) mbar_init(p_full + s, kBlockM);
     mbar_init(o_last, 1);
     mbar_init(o_free, kBlockM);
-    mbar_init(x_full, kBlockM);
-    mbar_init(x_free, 32);
+    mbar_init(merge, kBlockM);
+    mbar_init(copied, 1);
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
   if (warp == kMmaWarp) tmem_alloc(tmem_slot, C::kTmemCols);
   tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
-  griddep_wait();
-  // After the wait: the combine kernel may then read the lengths as soon as
-  // it starts, the kernels that wrote them having completed.
   griddep_launch_dependents();
+  griddep_wait();
 
   Cut cut(0, 1);
-  Place first;
-  Seq first_seq;
+  Place last;
+  Seq last_seq;
   const int cta = static_cast<int>(blockIdx.x);
-  const bool any = find_place(p, &sched, cta, static_cast<int>(gridDim.x), &cut, &first, &first_seq);
+  // (its barriers also stand between the set-up above and the roles below)
+  const bool any = find_place(p, &sched, cta, static_cast<int>(gridDim.x), &cut, &last, &last_seq);
   const long long run = any ? cut.begin(cta + 1) - cut.begin(cta) : 0;
-  if (threadIdx.x == 0 && p.runs != nullptr) {
-    // what the combine kernel has to know of the unit that this run begins in
-    PagedRun r;
-    r.work = any ? cut.work : 0;
-    r.unit = any ? cut.begin(cta) - first.kt : 0;
-    r.ctas = any ? cut.ctas : 0;
-    r.inside = any && first.kt > 0;
-    if (r.inside) {
-      const int token0 = first.r * p.tile_tokens;
-      r.cost = tile_cost(tile_keys(p, first_seq, first.r));
-      r.rows = min(p.tile_tokens, first_seq.n - token0) * p.group;
-      r.token = first_seq.start + token0;
-      r.head = first.hk * p.group;
-    }
-    p.runs[cta] = r;
-  }
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
 
   if (run > 0 && warp == kProducerWarp) {
     // ---------------------------------------------------------- producer
@@ -396,14 +452,15 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
     }
     const uint32_t dst = static_cast<uint32_t>(col * C::kKVBox + part * box_rows * C::kRowBytes);
     Walk w;
-    w.begin(p, first, first_seq, run);
+    w.begin(p, last, last_seq, run);
     int u0 = 0, pieces = 0, k_issued = 0, v_issued = 0;
     bool go = true;
     do {
-      const int n = w.real_end() - w.at.kt;
+      const int n = w.count();
       if (n <= 0) continue;
+      const int kt0 = w.first();
       const int32_t* pages = p.page_table + static_cast<long long>(w.at.s) * p.pages_per_seq;
-      const int key_first = w.at.kt * kBN + part * box_rows;
+      const int key_first = kt0 * kBN + part * box_rows;
       // page of this lane's part of tile i; -1: no position there holds a key
       auto page_of = [&](int i) -> int {
         const int key = key_first + i * kBN;
@@ -412,7 +469,7 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
       // page numbers outside the cache read as zeros and are reported
       auto has = [&](int i) { return copies && key_first + i * kBN < w.q.len; };
       auto load = [&](const CUtensorMap* map, uint64_t* bar, uint8_t* stage, int i, int page) {
-        const int key = w.at.kt * kBN + i * kBN;
+        const int key = (kt0 + i) * kBN;
         const int parts = min(kBN / box_rows, (w.q.len - key + box_rows - 1) / box_rows);
         if (lane == 0)
           mbar_arrive_expect_tx(bar, static_cast<uint32_t>(parts * box_rows * C::kRowBytes * C::kBoxes));
@@ -428,11 +485,19 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
       };
       int page_v = page_of(0);
       int page_k = page_v;
+      auto load_k = [&](int i) -> bool {
+        const int u = u0 + i, s = u % R;
+        if (u >= R && !mbar_wait_warp(s_full + s, static_cast<uint32_t>(u / R - 1) & 1u, ab)) return false;
+        load(&p.tm_k, k_full + s, smem + C::kKOff + s * C::kKVBytes, i, page_k);
+        k_issued = u + 1;
+        return true;
+      };
+      if (!(go = load_k(0))) break;
       // Q, once the scores of the piece before are done with it
       if (pieces > 0 && !(go = mbar_wait_warp(q_empty, static_cast<uint32_t>(pieces - 1) & 1u, ab))) break;
       {
         // lane c * 4 + y: column box c, for a narrow tile into quarter y
-        const bool narrow = w.narrow(p);
+        const bool narrow = w.rows(p) <= kNarrowRows;
         const int rows = (narrow ? kNarrowRows / p.group : p.tile_tokens) * p.group;
         if (lane == 0)
           mbar_arrive_expect_tx(q_full, static_cast<uint32_t>((narrow ? 4 : 1) * rows * C::kRowBytes * C::kBoxes));
@@ -444,14 +509,6 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
                       w.at.hk * p.group, w.q.start + w.at.r * p.tile_tokens);
       }
       ++pieces;
-      auto load_k = [&](int i) -> bool {
-        const int u = u0 + i, s = u % R;
-        if (u >= R && !mbar_wait_warp(s_full + s, static_cast<uint32_t>(u / R - 1) & 1u, ab)) return false;
-        load(&p.tm_k, k_full + s, smem + C::kKOff + s * C::kKVBytes, i, page_k);
-        k_issued = u + 1;
-        return true;
-      };
-      go = load_k(0);
       for (int i = 0; go && i < n; ++i) {
         // K of the next tile goes ahead of V of this one: its stage is free earlier
         page_k = page_of(i + 1);
@@ -505,11 +562,11 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
                          (accumulate || k > 0) ? 1u : 0u);
     };
     Walk w;
-    w.begin(p, first, first_seq, run);
+    w.begin(p, last, last_seq, run);
     int u = 0, pieces = 0;
     bool ok = true;
     do {
-      const int n = w.real_end() - w.at.kt;
+      const int n = w.count();
       if (n <= 0) continue;
       ok = mbar_wait_warp(q_full, static_cast<uint32_t>(pieces) & 1u, ab);
       if (!ok) break;
@@ -545,9 +602,9 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
     const float scale_log2 = p.scale_log2;
     const float2 sc2 = make_float2(scale_log2, scale_log2);
     Walk w;
-    w.begin(p, first, first_seq, run);
-    int u = 0, pieces = 0, exchanged = 0;                    // exchanged: steps of x_full so far
-    int freed = 0;                                           // ... of x_free
+    w.begin(p, last, last_seq, run);
+    int u = 0, pieces = 0;
+    int merged = 0, copies = 0, fetched = 0;                 // steps of merge and copied; begun (thread 0)
     bool ok = true;
 
     // Rows of V past the length hold whatever the page held (or an older
@@ -607,7 +664,7 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
     };
 
     do {
-      const int kt0 = w.at.kt, n = w.real_end() - kt0;
+      const int kt0 = w.first(), n = w.count();
       const int rows = w.rows(p);
       const bool narrow = rows <= kNarrowRows;
       const int row = narrow ? lane : quarter * 32 + lane;   // row of the tile
@@ -616,32 +673,79 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
       const bool valid = row < rows;
       const int pos0 = w.q.len - w.q.n + token0;             // position of the tile's first row
       const int pos = pos0 + token;                          // this row sees keys 0 .. pos
-      const bool whole = kt0 == 0 && w.end() == w.cost;
+      // a piece of a unit that later runs merge, or that this run merges with
+      // what earlier runs published
+      const bool open_above = w.at.kt < w.cost, open_below = kt0 > 0;
+      const bool whole = !open_above && !open_below;
+      int sources = 0;
+      if (!whole) {
+        // the pieces that this one merges, in the order of the list
+        const long long unit = open_above ? cut.begin(cta + 1) - w.at.kt : cut.begin(cta) - kt0;
+        const int c0 = cut.run_of(unit), j = cta - c0, bits = narrow ? 4 : 2;
+        const int low = open_above ? j + 1 - block_size(j, bits) : 0;
+        for (int at = j; at > low; at -= block_size(at - 1, bits)) {
+          if (threadIdx.x == 0) source_runs[sources] = c0 + at - 1;
+          ++sources;
+        }
+      }
       const long long out_row =
           static_cast<long long>(w.q.start + token0 + token) * p.h + w.at.hk * p.group + head;
-      const long long part_row =
-          (static_cast<long long>(cta) * 2 + (kt0 > 0 ? 0 : 1)) * p.slot_rows + row;
-      // O columns [c kOChunk, +kOChunk) of this row: normalised into the
-      // output if the piece is a whole unit, as they are into the workspace
-      // if it is a part of one
+      // a published piece of this unit: its bytes, run sl's slot, its (m, l)
+      const int o_bytes = rows * D * 4, piece_bytes = o_bytes + (rows * 8 + 15) / 16 * 16;
+      auto slot = [&](int sl) { return p.slots + static_cast<long long>(sl) * p.slot_bytes; };
+      auto ml_of = [&](uint8_t* piece) { return reinterpret_cast<float2*>(piece + o_bytes); };
+      uint8_t* ring = smem + C::kKOff;
+      // All softmax threads: what was written before is there for all after.
+      auto meet = [&]() -> bool {
+        mbar_arrive(merge);
+        return mbar_wait_warp(merge, static_cast<uint32_t>(merged++) & 1u, ab);
+      };
+      // The slot is written: its flag, released after everybody's writes (which
+      // bulk copies will read, hence the proxy fence).
+      auto publish = [&]() -> bool {
+        fence_proxy_async_all();
+        if (!meet()) return false;
+        if (threadIdx.x == 0) set_flag(p.flags + cta, p.call);
+        return true;
+      };
+      // Brings sources [i0, i1) into the ring, `at` pieces in (one thread).
+      auto fetch = [&](int i0, int i1, int at) {
+        if (threadIdx.x != 0) return;
+        fence_proxy_async_all();
+        mbar_arrive_expect_tx(copied, static_cast<uint32_t>((i1 - i0) * piece_bytes));
+        for (int i = i0; i < i1; ++i)
+          tma_load_1d(ring + (at + i - i0) * piece_bytes, slot(source_runs[i]),
+                      static_cast<uint32_t>(piece_bytes), copied);
+        ++fetched;
+      };
+      // Everything this run merges has been published, and the ring is idle.
+      auto wait_sources = [&]() -> bool {
+        if (!meet()) return false;                           // the list is there
+        bool got = true;
+        if (static_cast<int>(threadIdx.x) < sources)
+          got = take_flag(p.flags + source_runs[threadIdx.x], p.call, ab);
+        return __all_sync(0xffffffffu, got) && meet();
+      };
+      // O columns [c kOChunk, +kOChunk) of this row, normalised into the output
       auto store = [&](int c, const uint32_t (&o)[C::kOChunk], float inv_l) {
-        if (whole) {
-          uint4* dst = reinterpret_cast<uint4*>(p.out + out_row * D + c * C::kOChunk);
+        uint4* dst = reinterpret_cast<uint4*>(p.out + out_row * D + c * C::kOChunk);
 #pragma unroll
-          for (int e = 0; e < C::kOChunk / 8; ++e) {
-            uint4 x;
-            x.x = pack_bf16x2(__uint_as_float(o[e * 8 + 0]) * inv_l, __uint_as_float(o[e * 8 + 1]) * inv_l);
-            x.y = pack_bf16x2(__uint_as_float(o[e * 8 + 2]) * inv_l, __uint_as_float(o[e * 8 + 3]) * inv_l);
-            x.z = pack_bf16x2(__uint_as_float(o[e * 8 + 4]) * inv_l, __uint_as_float(o[e * 8 + 5]) * inv_l);
-            x.w = pack_bf16x2(__uint_as_float(o[e * 8 + 6]) * inv_l, __uint_as_float(o[e * 8 + 7]) * inv_l);
-            dst[e] = x;
-          }
-        } else {
-          uint4* dst = reinterpret_cast<uint4*>(p.part_o + part_row * D + c * C::kOChunk);
-#pragma unroll
-          for (int e = 0; e < C::kOChunk / 4; ++e)
-            dst[e] = make_uint4(o[e * 4], o[e * 4 + 1], o[e * 4 + 2], o[e * 4 + 3]);
+        for (int e = 0; e < C::kOChunk / 8; ++e) {
+          uint4 x;
+          x.x = pack_bf16x2(__uint_as_float(o[e * 8 + 0]) * inv_l, __uint_as_float(o[e * 8 + 1]) * inv_l);
+          x.y = pack_bf16x2(__uint_as_float(o[e * 8 + 2]) * inv_l, __uint_as_float(o[e * 8 + 3]) * inv_l);
+          x.z = pack_bf16x2(__uint_as_float(o[e * 8 + 4]) * inv_l, __uint_as_float(o[e * 8 + 5]) * inv_l);
+          x.w = pack_bf16x2(__uint_as_float(o[e * 8 + 6]) * inv_l, __uint_as_float(o[e * 8 + 7]) * inv_l);
+          dst[e] = x;
         }
+      };
+      // four columns of row rw of the tile into the output
+      auto write_out = [&](int rw, int col, const float4& v, float inv) {
+        const int tok = rw / p.group;
+        *reinterpret_cast<uint2*>(
+            p.out + (static_cast<long long>(w.q.start + token0 + tok) * p.h + w.at.hk * p.group + rw -
+                     tok * p.group) * D + col) =
+            make_uint2(pack_bf16x2(v.x * inv, v.y * inv), pack_bf16x2(v.z * inv, v.w * inv));
       };
       if (n <= 0) {
         // nothing to see: rows of zeros
@@ -713,70 +817,119 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
         ok = mbar_wait_warp(o_last, static_cast<uint32_t>(pieces) & 1u, ab);
         if (!ok) break;
         tc_fence_after();
-        // ---- merge the quarters: (m, l) first, then O chunk by chunk, chunk c
-        // summed and stored by warp c % 4 from its own registers and the
-        // other three warps' rows in shared memory
+        // ---- sum the quarters: (m, l) first, then as many columns at a time
+        // as the exchange memory holds of the rows there are
         float2* xml = reinterpret_cast<float2*>(smem + C::kXmlOff);
+        float* xinv = reinterpret_cast<float*>(smem + C::kXinvOff);
         xml[quarter * kNarrowRows + lane] = make_float2(m_used, l);
-        mbar_arrive(x_full);
-        ok = mbar_wait_warp(x_full, static_cast<uint32_t>(exchanged) & 1u, ab);
-        if (!ok) break;
-        ++exchanged;
-        float mm = m_used;
+        if (!(ok = meet())) break;
+        float mm = m_used, ll = 0.f;
 #pragma unroll
         for (int y = 0; y < 4; ++y) mm = fmaxf(mm, xml[y * kNarrowRows + lane].x);
-        float ll = 0.f;
+        const float sub = mm == -INFINITY ? 0.f : mm;
 #pragma unroll
         for (int y = 0; y < 4; ++y) {
           const float2 ml = xml[y * kNarrowRows + lane];
-          ll += (ml.x == -INFINITY) ? 0.f : ml.y * ex2_approx(ml.x - mm);
+          ll += ml.y * weight(ml.x, sub);
         }
-        const float f = (m_used == -INFINITY) ? 0.f : ex2_approx(m_used - mm);
-        const float inv_l = ll > 0.f ? 1.f / ll : 0.f;
+        const float f = weight(m_used, sub);
+        // own piece: where it is kept while it is not whole
+        uint8_t* own = sources > 0 ? ring : slot(cta);
+        if (valid && quarter == 0) {
+          if (!whole) ml_of(own)[row] = make_float2(mm, ll);
+          xinv[row] = ll > 0.f ? 1.f / ll : 0.f;
+        }
+        int cols = 16;
+        while (cols < D && 2 * cols * rows * 16 <= C::kXBytes) cols *= 2;
+        float4* lay = reinterpret_cast<float4*>(smem + C::kXOff);     // [quarter][cols / 4][rows]
 #pragma unroll 1
-        for (int c = 0; ok && c < D / C::kOChunk; ++c) {
-          uint32_t o[C::kOChunk];
-          tmem_ld_chunk(lane_base + C::kOCol + c * C::kOChunk, o);
-          tmem_ld_wait();
-          reg_fence(o);
-#pragma unroll
-          for (int e = 0; e < C::kOChunk; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-          // the chunk before has been read
-          if (freed > 0 && !(ok = mbar_wait_warp(x_free, static_cast<uint32_t>(freed - 1) & 1u, ab))) break;
-          const int owner = c & 3;
-          const int slot = (quarter - owner - 1) & 3;        // 0 .. 2; 3 for the owner
-          if (quarter != owner) {
-            uint4* dst = reinterpret_cast<uint4*>(smem + C::kXOff + slot * C::kXSlot + lane * C::kXRow);
-#pragma unroll
-            for (int e = 0; e < C::kOChunk / 4; ++e)
-              dst[e] = make_uint4(o[e * 4], o[e * 4 + 1], o[e * 4 + 2], o[e * 4 + 3]);
-          }
-          mbar_arrive(x_full);
-          if (quarter == owner) {
-            ok = mbar_wait_warp(x_full, static_cast<uint32_t>(exchanged) & 1u, ab);
-            if (!ok) break;
-#pragma unroll
-            for (int y = 0; y < 3; ++y) {
-              const float4* src = reinterpret_cast<const float4*>(smem + C::kXOff + y * C::kXSlot + lane * C::kXRow);
-#pragma unroll
-              for (int e = 0; e < C::kOChunk / 4; ++e) {
-                const float4 v = src[e];
-                o[e * 4] = __float_as_uint(__uint_as_float(o[e * 4]) + v.x);
-                o[e * 4 + 1] = __float_as_uint(__uint_as_float(o[e * 4 + 1]) + v.y);
-                o[e * 4 + 2] = __float_as_uint(__uint_as_float(o[e * 4 + 2]) + v.z);
-                o[e * 4 + 3] = __float_as_uint(__uint_as_float(o[e * 4 + 3]) + v.w);
-              }
-            }
-            mbar_arrive(x_free);
-            if (valid) store(c, o, inv_l);
+        for (int c0 = 0; c0 < D; c0 += cols) {
+          if (c0 > 0 && !(ok = meet())) break;               // the columns before are summed
+#pragma unroll 1
+          for (int c = 0; c < cols; c += 16) {
+            uint32_t o[16];
             __syncwarp();
+            tmem_ld_chunk(lane_base + C::kOCol + c0 + c, o);
+            tmem_ld_wait();
+            reg_fence(o);
+            if (valid) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                lay[(quarter * (cols / 4) + c / 4 + e) * rows + row] =
+                    make_float4(__uint_as_float(o[e * 4]) * f, __uint_as_float(o[e * 4 + 1]) * f,
+                                __uint_as_float(o[e * 4 + 2]) * f, __uint_as_float(o[e * 4 + 3]) * f);
+            }
           }
-          ++exchanged;
-          ++freed;
+          if (!(ok = meet())) break;
+          const int items = rows * (cols / 4);
+          for (int x = threadIdx.x; x < items; x += kBlockM) {
+            float4 v = lay[x];
+#pragma unroll
+            for (int y = 1; y < 4; ++y) {
+              const float4 o = lay[y * items + x];
+              v.x += o.x;
+              v.y += o.y;
+              v.z += o.z;
+              v.w += o.w;
+            }
+            if (whole) write_out(x % rows, c0 + x / rows * 4, v, xinv[x % rows]);
+            else reinterpret_cast<float4*>(own)[c0 / 4 * rows + x] = v;
+          }
         }
         if (!ok) break;
-        if (!whole && valid && quarter == 0)
-          *reinterpret_cast<float2*>(p.part_ml + part_row * 2) = make_float2(mm, ll);
+        if (sources > 0) {
+          // ---- merge: this run's own piece lies at the front, `fit` others
+          // at a time come in behind it
+          const int fit = C::kMergeBytes / piece_bytes - 1;
+          if (!(ok = wait_sources())) break;
+          for (int i0 = 0; i0 < sources; i0 += fit) {
+            const int count = min(fit, sources - i0);
+            const bool more = i0 + count < sources;
+            fetch(i0, i0 + count, 1);
+            ok = mbar_wait_warp(copied, static_cast<uint32_t>(copies++) & 1u, ab);
+            if (!ok) break;
+            float2 ml_row = make_float2(0.f, 0.f);
+            for (int x = threadIdx.x; x < rows * (D / 4); x += kBlockM) {
+              const int rw = x % rows;
+              float4 acc = reinterpret_cast<float4*>(ring)[x];
+              const float2 ml = ml_of(ring)[rw];
+              float top = ml.x;
+#pragma unroll 4
+              for (int i = 1; i <= count; ++i) top = fmaxf(top, ml_of(ring + i * piece_bytes)[rw].x);
+              const float base = top == -INFINITY ? 0.f : top;
+              const float fo = weight(ml.x, base);
+              float sum = ml.y * fo;
+              acc.x *= fo; acc.y *= fo; acc.z *= fo; acc.w *= fo;
+#pragma unroll 4
+              for (int i = 1; i <= count; ++i) {
+                const float2 mi = ml_of(ring + i * piece_bytes)[rw];
+                const float4 v = reinterpret_cast<float4*>(ring + i * piece_bytes)[x];
+                const float fi = weight(mi.x, base);
+                sum += mi.y * fi;
+                acc.x += v.x * fi;
+                acc.y += v.y * fi;
+                acc.z += v.z * fi;
+                acc.w += v.w * fi;
+              }
+              if (x < rows) ml_row = make_float2(top, sum);
+              if (more) {
+                reinterpret_cast<float4*>(ring)[x] = acc;
+              } else if (open_above) {
+                reinterpret_cast<float4*>(slot(cta))[x] = acc;
+                if (x < rows) ml_of(slot(cta))[rw] = ml_row;
+              } else {
+                write_out(rw, x / rows * 4, acc, sum > 0.f ? 1.f / sum : 0.f);
+              }
+            }
+            if (more) {
+              // (every row's own (m, l) has been read: they move on)
+              if (!(ok = meet())) break;
+              if (static_cast<int>(threadIdx.x) < rows) ml_of(ring)[threadIdx.x] = ml_row;
+              if (!(ok = meet())) break;
+            }
+          }
+          if (!ok) break;
+        }
       } else {
         const bool busy = quarter * 32 < rows;               // some row of this warp is a query
         for (int i = 0; i < n; ++i, ++u) {
@@ -841,80 +994,107 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
         ok = mbar_wait_warp(o_last, static_cast<uint32_t>(pieces) & 1u, ab);
         if (!ok) break;
         tc_fence_after();
-        if (busy) {
-          const float inv_l = l > 0.f ? 1.f / l : 0.f;
-          if constexpr (D < 32) {
-            uint32_t o[C::kOChunk];
-            tmem_ld_chunk(lane_base + C::kOCol, o);
-            tmem_ld_wait();
-            reg_fence(o);
-            if (valid) store(0, o, inv_l);
-          } else {
-            // Stores straight from the rows' owners would touch 32 lines with
-            // 16 bytes each; turned through shared memory, four lanes write
-            // 64 bytes of a row.
-            const int rows_here = min(32, rows - quarter * 32);
-            uint8_t* turn = smem + C::kXOff + quarter * C::kTurnSlot;
-            const int r0 = lane >> 2, piece = lane & 3;
-            // 64-byte steps of a row: 32 columns as bf16 or 16 as fp32
+        float mm = m_used, ll = l;                           // of this piece and the ones merged into it
+        if (sources > 0) {
+          // Merge: O stays in tensor memory, the published pieces come into the
+          // ring one after the other.
+          if (!(ok = wait_sources())) break;
+          const int rw = min(row, rows - 1);
+          for (int i = 0; i < sources; ++i) {
+            if (i > 0 && !(ok = meet())) break;              // the piece before is summed
+            fetch(i, i + 1, 0);
+            ok = mbar_wait_warp(copied, static_cast<uint32_t>(copies++) & 1u, ab);
+            if (!ok) break;
+            if (!busy) continue;
+            const float2 ml = ml_of(ring)[rw];
+            const float top = fmaxf(mm, ml.x), base = top == -INFINITY ? 0.f : top;
+            const float fo = weight(mm, base), fi = weight(ml.x, base);
+            mm = top;
+            ll = ll * fo + ml.y * fi;
+            const float4* src = reinterpret_cast<const float4*>(ring) + rw;
 #pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-              uint32_t o[32];
+            for (int c = 0; c < D / C::kOChunk; ++c) {
+              uint32_t o[C::kOChunk];
               __syncwarp();
-              tmem_ld32(lane_base + C::kOCol + c * 32, o);
+              tmem_ld_chunk(lane_base + C::kOCol + c * C::kOChunk, o);
               tmem_ld_wait();
               reg_fence(o);
+#pragma unroll
+              for (int e = 0; e < C::kOChunk / 4; ++e) {
+                const float4 v = src[(c * (C::kOChunk / 4) + e) * rows];
+                o[e * 4] = __float_as_uint(fmaf(v.x, fi, __uint_as_float(o[e * 4]) * fo));
+                o[e * 4 + 1] = __float_as_uint(fmaf(v.y, fi, __uint_as_float(o[e * 4 + 1]) * fo));
+                o[e * 4 + 2] = __float_as_uint(fmaf(v.z, fi, __uint_as_float(o[e * 4 + 2]) * fo));
+                o[e * 4 + 3] = __float_as_uint(fmaf(v.w, fi, __uint_as_float(o[e * 4 + 3]) * fo));
+              }
+              tmem_st_chunk(lane_base + C::kOCol + c * C::kOChunk, o);
+            }
+            tmem_st_wait();
+          }
+          if (!ok) break;
+          if (!(ok = meet())) break;                         // (the rows turn in memory that held the piece)
+        }
+        if (busy) {
+          const float inv_l = ll > 0.f ? 1.f / ll : 0.f;
+          const int rows_here = min(32, rows - quarter * 32);
+          uint8_t* turn = smem + C::kXOff + quarter * C::kTurnSlot;
+          const int r0 = lane >> 2, piece = lane & 3;
+#pragma unroll 1
+          for (int c = 0; c < D / C::kOChunk; ++c) {
+            uint32_t o[C::kOChunk];
+            __syncwarp();
+            tmem_ld_chunk(lane_base + C::kOCol + c * C::kOChunk, o);
+            tmem_ld_wait();
+            reg_fence(o);
+            if (open_above) {
+              if (valid) {
+                float4* dst = reinterpret_cast<float4*>(slot(cta)) + row;
+#pragma unroll
+                for (int e = 0; e < C::kOChunk / 4; ++e)
+                  dst[(c * (C::kOChunk / 4) + e) * rows] =
+                      make_float4(__uint_as_float(o[e * 4]), __uint_as_float(o[e * 4 + 1]),
+                                  __uint_as_float(o[e * 4 + 2]), __uint_as_float(o[e * 4 + 3]));
+              }
+            } else if constexpr (D < 32) {
+              if (valid) store(c, o, inv_l);
+            } else {
+              // Stores straight from the rows' owners would touch 32 lines
+              // with 16 bytes each; turned through shared memory, four lanes
+              // write 64 bytes of a row.
               uint4* mine = reinterpret_cast<uint4*>(turn + lane * C::kTurnRow);
-              if (whole) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  uint4 x;
-                  x.x = pack_bf16x2(__uint_as_float(o[e * 8 + 0]) * inv_l, __uint_as_float(o[e * 8 + 1]) * inv_l);
-                  x.y = pack_bf16x2(__uint_as_float(o[e * 8 + 2]) * inv_l, __uint_as_float(o[e * 8 + 3]) * inv_l);
-                  x.z = pack_bf16x2(__uint_as_float(o[e * 8 + 4]) * inv_l, __uint_as_float(o[e * 8 + 5]) * inv_l);
-                  x.w = pack_bf16x2(__uint_as_float(o[e * 8 + 6]) * inv_l, __uint_as_float(o[e * 8 + 7]) * inv_l);
-                  mine[e] = x;
-                }
-                __syncwarp();
+              for (int e = 0; e < 4; ++e) {
+                uint4 x;
+                x.x = pack_bf16x2(__uint_as_float(o[e * 8 + 0]) * inv_l, __uint_as_float(o[e * 8 + 1]) * inv_l);
+                x.y = pack_bf16x2(__uint_as_float(o[e * 8 + 2]) * inv_l, __uint_as_float(o[e * 8 + 3]) * inv_l);
+                x.z = pack_bf16x2(__uint_as_float(o[e * 8 + 4]) * inv_l, __uint_as_float(o[e * 8 + 5]) * inv_l);
+                x.w = pack_bf16x2(__uint_as_float(o[e * 8 + 6]) * inv_l, __uint_as_float(o[e * 8 + 7]) * inv_l);
+                mine[e] = x;
+              }
+              __syncwarp();
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  const int x = r0 + 8 * k;                  // row of this warp
-                  const uint4 v = *reinterpret_cast<const uint4*>(turn + x * C::kTurnRow + piece * 16);
-                  const int rr = quarter * 32 + x, tok = rr / p.group;
-                  if (x < rows_here)
-                    *reinterpret_cast<uint4*>(
-                        p.out + (static_cast<long long>(w.q.start + token0 + tok) * p.h + w.at.hk * p.group +
-                                 rr - tok * p.group) * D + c * 32 + piece * 8) = v;
-                }
-                __syncwarp();
-              } else {
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-#pragma unroll
-                  for (int e = 0; e < 4; ++e)
-                    mine[e] = make_uint4(o[half * 16 + e * 4], o[half * 16 + e * 4 + 1], o[half * 16 + e * 4 + 2],
-                                         o[half * 16 + e * 4 + 3]);
-                  __syncwarp();
-#pragma unroll
-                  for (int k = 0; k < 4; ++k) {
-                    const int x = r0 + 8 * k;
-                    const uint4 v = *reinterpret_cast<const uint4*>(turn + x * C::kTurnRow + piece * 16);
-                    if (x < rows_here)
-                      *reinterpret_cast<uint4*>(p.part_o + (part_row - lane + x) * D + c * 32 + half * 16 + piece * 4) = v;
-                  }
-                  __syncwarp();
-                }
+              for (int k = 0; k < 4; ++k) {
+                const int x = r0 + 8 * k;                    // row of this warp
+                const uint4 v = *reinterpret_cast<const uint4*>(turn + x * C::kTurnRow + piece * 16);
+                const int rr = quarter * 32 + x, tok = rr / p.group;
+                if (x < rows_here)
+                  *reinterpret_cast<uint4*>(
+                      p.out + (static_cast<long long>(w.q.start + token0 + tok) * p.h + w.at.hk * p.group +
+                               rr - tok * p.group) * D + c * 32 + piece * 8) = v;
               }
             }
           }
-          if (!whole && valid) *reinterpret_cast<float2*>(p.part_ml + part_row * 2) = make_float2(m_used, l);
+          if (open_above && valid) ml_of(slot(cta))[row] = make_float2(mm, ll);
         }
       }
+      if (open_above && !(ok = publish())) break;
       __syncwarp();
       tc_fence_before();
       mbar_arrive(o_free);
       ++pieces;
     } while (w.next(p));
+    // a wait ran out: let the copies under way land before the CTA can exit
+    if (fetched > copies) mbar_wait_drain(copied, static_cast<uint32_t>(copies) & 1u);
   }
 
   tc_fence_before();
@@ -925,92 +1105,14 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
   }
 }
 
-// ------------------------------------------------------------------- combine
-// The runs that begin inside a unit merge its pieces: the last piece of the
-// run that the unit begins in (slot 1) and the first ones of the runs after
-// it (slot 0).  Each takes a share of the unit's (row, 4 columns) items, so a
-// walk cut into many pieces is merged by as many blocks.
-constexpr int kCombineThreads = 128;
-
-template <int D>
-__global__ void __launch_bounds__(kCombineThreads) sdpa_paged_combine(const __grid_constant__ PagedParams p) {
-  const int c = static_cast<int>(blockIdx.x) + 1;
-  griddep_launch_dependents();
-  griddep_wait();
-  const PagedRun r = p.runs[c];
-  if (!r.inside) return;
-  const Cut cut(r.work, r.ctas);
-  const int c0 = cut.run_of(r.unit), last = cut.run_of(r.unit + r.cost - 1);
-  constexpr int kVec = D / 4;
-  const int items = r.rows * kVec;
-  const int share_of = (last - c0) * static_cast<int>(gridDim.y);
-  const int share = (items + share_of - 1) / share_of;
-  const int item0 = ((c - c0 - 1) * static_cast<int>(gridDim.y) + static_cast<int>(blockIdx.y)) * share;
-  const int item1 = min(item0 + share, items);
-  // `lanes` lanes of a warp split an item's pieces among them, as far as the
-  // share leaves threads over
-  const int pieces = last - c0 + 1;
-  int lanes = 1;
-  while (lanes < 32 && lanes * 2 * share <= kCombineThreads && lanes < pieces) lanes *= 2;
-  const int wide = 32 / lanes;                                // items of a warp at a time
-  const int lane = threadIdx.x & 31;
-  const int y = lane / wide;
-  for (int base = item0 + static_cast<int>(threadIdx.x >> 5) * wide; base < item1;
-       base += kCombineThreads / lanes) {
-    const int x = base + lane % wide;
-    const int row = min(x, items - 1) / kVec, col = x % kVec * 4;
-    auto part = [&](int i) {                                  // piece i: run c0 + i
-      return (static_cast<long long>(c0 + i) * 2 + (i == 0 ? 1 : 0)) * p.slot_rows + row;
-    };
-    float m = -INFINITY;
-#pragma unroll 4
-    for (int i = y; i < pieces; i += lanes) m = fmaxf(m, p.part_ml[part(i) * 2]);
-    for (int o = wide; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const float sub = m == -INFINITY ? 0.f : m;
-    float l = 0.f;
-    float4 o4 = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int i = y; i < pieces; i += lanes) {
-      const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + part(i) * 2);
-      const float4 v = *reinterpret_cast<const float4*>(p.part_o + part(i) * D + col);
-      const float f = ex2_approx(ml.x - sub);
-      l += ml.y * f;
-      o4.x += v.x * f;
-      o4.y += v.y * f;
-      o4.z += v.z * f;
-      o4.w += v.w * f;
-    }
-    for (int o = wide; o < 32; o <<= 1) {
-      l += __shfl_xor_sync(0xffffffffu, l, o);
-      o4.x += __shfl_xor_sync(0xffffffffu, o4.x, o);
-      o4.y += __shfl_xor_sync(0xffffffffu, o4.y, o);
-      o4.z += __shfl_xor_sync(0xffffffffu, o4.z, o);
-      o4.w += __shfl_xor_sync(0xffffffffu, o4.w, o);
-    }
-    if (y == 0 && x < item1) {
-      const float inv = l > 0.f ? 1.f / l : 0.f;
-      const int token = row / p.group;
-      const long long out_row = static_cast<long long>(r.token + token) * p.h + r.head + row - token * p.group;
-      *reinterpret_cast<uint2*>(p.out + out_row * D + col) =
-          make_uint2(pack_bf16x2(o4.x * inv, o4.y * inv), pack_bf16x2(o4.z * inv, o4.w * inv));
-    }
-  }
-}
-
 template <int D>
 cudaError_t launch_paged_impl(const PagedParams& p, cudaStream_t stream) {
   constexpr int smem = PCfg<D>::kSmemBytes;
   cudaError_t err =
       cudaFuncSetAttribute(sdpa_paged_split<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (err != cudaSuccess) return err;
-  err = launch_kernel(sdpa_paged_split<D>, dim3(static_cast<unsigned>(p.split_ctas)), dim3(kThreads), smem,
-                      stream, true, p);
-  if (err != cudaSuccess || p.split_ctas == 1) return err;
-  // up to four blocks a run (all of them are resident at once)
-  const int y = min((p.slot_rows * (D / 4) + 4 * kCombineThreads - 1) / (4 * kCombineThreads), 4);
-  return launch_kernel(sdpa_paged_combine<D>,
-                       dim3(static_cast<unsigned>(p.split_ctas - 1), static_cast<unsigned>(y)),
-                       dim3(kCombineThreads), 0, stream, true, p);
+  return launch_kernel(sdpa_paged_split<D>, dim3(static_cast<unsigned>(p.split_ctas)), dim3(kThreads), smem,
+                       stream, true, p);
 }
 
 // -------------------------------------------------------------------- append
