@@ -126,6 +126,14 @@ def _stream(stream) -> int | None:
     return stream.cuda_stream
 
 
+def _current_stream(device: int) -> int:
+    """Handle of torch's current stream on `device`, without the stream object
+    that torch.cuda.current_stream() makes (3 us of a call's 10)."""
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(device) if raw is not None else torch.cuda.current_stream(device).cuda_stream
+
+
 class _on_stream:
     """Makes `stream` (None, a torch stream or a raw handle) torch's current
     one inside the block, so that what torch allocates there belongs to the
@@ -259,35 +267,37 @@ def sdpa_paged_forward(q, k_pages, v_pages, out, workspace, ws_bytes, b, n_token
         _addr(kv_lengths), q_stride, float(scale), _stream(stream)), "sdpa_paged_forward")
 
 
-def _paged_shapes(where, rows, k_pages, v_pages, page_table, q_starts, kv_lengths):
-    """(b, h_kv, d, page_size, n_pages, pages_per_seq) of a paged cache, after
-    checking what the C entry points cannot see: types, shapes, layout and
-    devices.  `rows` are the packed [n_tokens, heads, d] tensors of the call
-    (token rows may be strided)."""
+def _paged_cache(where, k_pages, v_pages, page_table, q_starts, kv_lengths):
+    """(device, b, h_kv, d, page_size, n_pages, pages_per_seq) of a paged
+    cache, after checking what the C entry points cannot see: types, shapes,
+    layout and device (the current one)."""
     import torch
-    n_pages, h_kv, page_size, d = k_pages.shape
-    b, pages_per_seq = page_table.shape
-    good = (k_pages.dtype == torch.bfloat16 and v_pages.dtype == torch.bfloat16 and
-            v_pages.shape == k_pages.shape and k_pages.is_contiguous() and v_pages.is_contiguous() and
-            page_table.dtype == torch.int32 and page_table.is_contiguous() and
-            q_starts.dtype == torch.int32 and q_starts.is_contiguous() and q_starts.numel() == b + 1 and
-            kv_lengths.dtype == torch.int32 and kv_lengths.is_contiguous() and kv_lengths.numel() == b)
+    shape = k_pages.shape
+    b, per_seq = page_table.shape
     device = k_pages.get_device()
-    good = good and device == torch.cuda.current_device() and all(
-        x.get_device() == device for x in (v_pages, page_table, q_starts, kv_lengths))
-    n_tokens = rows[0].shape[0]
-    for x in rows:
-        good = (good and x.dtype == torch.bfloat16 and x.dim() == 3 and x.shape[0] == n_tokens and
-                x.shape[2] == d and x.stride(2) == 1 and (x.shape[1] == 1 or x.stride(1) == d) and
-                x.get_device() == device)
-    if not good:
+    bf16, i32 = torch.bfloat16, torch.int32
+    if not (len(shape) == 4 and v_pages.shape == shape and
+            k_pages.dtype is bf16 and v_pages.dtype is bf16 and page_table.dtype is i32 and
+            q_starts.dtype is i32 and kv_lengths.dtype is i32 and
+            q_starts.shape == (b + 1,) and kv_lengths.shape == (b,) and
+            k_pages.is_contiguous() and v_pages.is_contiguous() and page_table.is_contiguous() and
+            q_starts.is_contiguous() and kv_lengths.is_contiguous() and
+            device >= 0 and device == torch.cuda.current_device() and v_pages.get_device() == device and
+            page_table.get_device() == device and q_starts.get_device() == device and
+            kv_lengths.get_device() == device):
         raise SdpaError(1, where)
-    return b, h_kv, d, page_size, n_pages, pages_per_seq
+    return device, b, shape[1], shape[3], shape[2], shape[0], per_seq
 
 
-def _row_stride(x):
-    # the stride of a single token says nothing
-    return x.stride(0) if x.shape[0] > 1 else x.shape[1] * x.shape[2]
+def _paged_rows(where, x, n_tokens, heads, d, device):
+    """Token stride of packed rows x [n_tokens, heads, d] (a single token's
+    says nothing), after checking them."""
+    import torch
+    stride = x.stride()
+    if not (x.dtype is torch.bfloat16 and x.shape == (n_tokens, heads, d) and stride[2] == 1 and
+            (stride[1] == d or heads == 1) and x.get_device() == device):
+        raise SdpaError(1, where)
+    return stride[0] if n_tokens > 1 else heads * d
 
 
 def paged_append(q, k, v, k_pages, v_pages, page_table, q_starts, kv_lengths, rope_freqs=None,
@@ -298,30 +308,39 @@ def paged_append(q, k, v, k_pages, v_pages, page_table, q_starts, kv_lengths, ro
     rope_freqs.numel() columns are rotated.  Returns the rotated queries
     (q_out, or a tensor allocated with torch); q = None appends alone."""
     import torch
-    rows = (k, v) if q is None else (q, k, v)
-    with _on_stream(stream):
-        b, h_kv, d, page, n_pages, per_seq = _paged_shapes("paged_append", rows, k_pages, v_pages, page_table,
-                                                           q_starts, kv_lengths)
-        t = k.shape[0]
-        h = h_kv if q is None else q.shape[1]
-        good = k.shape[1] == h_kv and v.shape[1] == h_kv
-        if q is not None and q_out is None:
-            q_out = torch.empty((t, h, d), dtype=q.dtype, device=q.device)
-        if q is None:
-            good = good and q_out is None
-        else:
-            good = (good and q_out.shape == q.shape and q_out.dtype == q.dtype and q_out.is_contiguous() and
-                    q_out.get_device() == q.get_device())
-        d_rot = 0
-        if rope_freqs is not None:
-            d_rot = 2 * rope_freqs.numel()
-            good = (good and rope_freqs.dtype == torch.float32 and rope_freqs.is_contiguous() and
-                    rope_freqs.get_device() == k.get_device())
-        if not good:
-            raise SdpaError(1, "paged_append")
-        sdpa_paged_append(q, k, v, q_out, k_pages, v_pages, b, t, h, h_kv, d, page, n_pages, per_seq, page_table,
-                          q_starts, kv_lengths, 0 if q is None else _row_stride(q), _row_stride(k),
-                          _row_stride(v), rope_freqs, d_rot, interleaved, stream)
+    if stream is not None:
+        with _on_stream(stream):
+            return paged_append(q, k, v, k_pages, v_pages, page_table, q_starts, kv_lengths, rope_freqs,
+                                interleaved, q_out)
+    where = "paged_append"
+    device, b, h_kv, d, page, n_pages, per_seq = _paged_cache(where, k_pages, v_pages, page_table, q_starts,
+                                                              kv_lengths)
+    t = k.shape[0]
+    k_stride = _paged_rows(where, k, t, h_kv, d, device)
+    v_stride = _paged_rows(where, v, t, h_kv, d, device)
+    h, q_stride, q_ptr, out_ptr = h_kv, 0, None, None
+    if q is not None:
+        h = q.shape[1]
+        q_stride = _paged_rows(where, q, t, h, d, device)
+        if q_out is None:
+            q_out = torch.empty((t, h, d), dtype=torch.bfloat16, device=k.device)
+        elif not (q_out.is_contiguous() and _paged_rows(where, q_out, t, h, d, device)):
+            raise SdpaError(1, where)
+        q_ptr, out_ptr = q.data_ptr(), q_out.data_ptr()
+    elif q_out is not None:
+        raise SdpaError(1, where)
+    d_rot, freqs = 0, None
+    if rope_freqs is not None:
+        if not (rope_freqs.dtype is torch.float32 and rope_freqs.is_contiguous() and
+                rope_freqs.get_device() == device):
+            raise SdpaError(1, where)
+        d_rot, freqs = 2 * rope_freqs.numel(), rope_freqs.data_ptr()
+    status = load_library().sdpa_paged_append(
+        q_ptr, k.data_ptr(), v.data_ptr(), out_ptr, k_pages.data_ptr(), v_pages.data_ptr(), b, t, h, h_kv, d, page,
+        n_pages, per_seq, page_table.data_ptr(), q_starts.data_ptr(), kv_lengths.data_ptr(), q_stride, k_stride,
+        v_stride, freqs, d_rot, 1 if interleaved else 0, _current_stream(device))
+    if status != 0:
+        raise SdpaError(status, where)
     return q_out
 
 
@@ -342,21 +361,31 @@ def paged_attention(q, k_pages, v_pages, page_table, q_starts, kv_lengths, scale
     be strided) and a paged cache; allocates the output and the workspace
     with torch where they are not given.  Returns the output [t,h,d]."""
     import torch
-    with _on_stream(stream):
-        b, h_kv, d, page, n_pages, per_seq = _paged_shapes("paged_attention", (q,), k_pages, v_pages, page_table,
-                                                           q_starts, kv_lengths)
-        t, h = q.shape[0], q.shape[1]
-        if out is None:
-            out = torch.empty((t, h, d), dtype=q.dtype, device=q.device)
-        elif not (out.shape == q.shape and out.dtype == q.dtype and out.is_contiguous() and
-                  out.get_device() == q.get_device()):
-            raise SdpaError(1, "paged_attention")
-        if workspace is None:
-            workspace = paged_workspace(q, k_pages, page_table)
-        sdpa_paged_forward(q, k_pages, v_pages, out, workspace,
-                           0 if workspace is None else workspace.numel() * workspace.element_size(), b, t, h,
-                           h_kv, d, page, n_pages, per_seq, page_table, q_starts, kv_lengths, _row_stride(q),
-                           scale, stream)
+    if stream is not None:
+        with _on_stream(stream):
+            return paged_attention(q, k_pages, v_pages, page_table, q_starts, kv_lengths, scale, out, workspace)
+    where = "paged_attention"
+    device, b, h_kv, d, page, n_pages, per_seq = _paged_cache(where, k_pages, v_pages, page_table, q_starts,
+                                                              kv_lengths)
+    t, h, _ = q.shape
+    q_stride = _paged_rows(where, q, t, h, d, device)
+    if out is None:
+        out = torch.empty((t, h, d), dtype=torch.bfloat16, device=q.device)
+    elif not (out.is_contiguous() and _paged_rows(where, out, t, h, d, device)):
+        raise SdpaError(1, where)
+    if workspace is None:
+        workspace = paged_workspace(q, k_pages, page_table)
+    ws_ptr, ws_bytes = None, 0
+    if workspace is not None:
+        if workspace.get_device() != device or not workspace.is_contiguous():
+            raise SdpaError(1, where)
+        ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    status = load_library().sdpa_paged_forward(
+        q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), out.data_ptr(), ws_ptr, ws_bytes, b, t, h, h_kv, d,
+        page, n_pages, per_seq, page_table.data_ptr(), q_starts.data_ptr(), kv_lengths.data_ptr(), q_stride, scale,
+        _current_stream(device))
+    if status != 0:
+        raise SdpaError(status, where)
     return out
 
 

@@ -36,6 +36,7 @@
 // buffered and O in tensor memory), kept running from piece to piece: tile
 // and piece counters carry on, and two more barriers hand over Q (q_empty)
 // and O (o_free).
+#include <atomic>
 #include <climits>
 #include <cmath>
 
@@ -284,15 +285,16 @@ struct Walk {
 // of four columns and, right behind, (m, l) as [rows].  A slot has a flag,
 // which is the call's number once the slot is written and is put back to zero
 // by its only reader.  A run merges at its end, when its K and V stages are
-// idle: the published pieces come into that memory by bulk copies.
+// idle: the published pieces come into that memory by asynchronous copies.
 //
 // The unit's pieces j = 0, 1, .. (runs c0 + j) form a tree of radix R = 2^bits:
 // before it publishes, piece j merges the size(j) - 1 pieces below it, size(j)
 // the largest power of R that divides j + 1; the last piece merges all.  What
 // a piece reads are the tops of the blocks that make up its range.  Reading
 // R - 1 pieces a level costs R - 1 pieces' bytes on one SM, a level costs a
-// wait: narrow pieces (a few KB) take R = 16, wide ones (up to 128 KB) R = 4.
-constexpr int kMaxSources = 48;            // 15 a level: runs up to 2^12 (narrow), 2^32 (wide)
+// wait: narrow pieces (a few KB) take R = 16, wide ones (up to 128 KB) R = 8.
+constexpr int kNarrowBits = 4, kWideBits = 3;
+constexpr int kMaxSources = 48;            // 15 a level: 3 levels for up to 2^12 runs
 static_assert(kPagedMaxRuns <= 1 << 12, "sources");
 
 __device__ __forceinline__ int block_size(int j, int bits) {
@@ -352,15 +354,15 @@ struct PCfg {
   static constexpr int kTurnSlot = 32 * kTurnRow;
   static_assert(4 * kTurnSlot <= kXBytes, "turning rows");
   static constexpr int kXmlOff = kXOff + kXBytes;            // the quarters' (m, l)
-  // merging: the idle K and V stages and the exchange memory behind them hold
-  // one wide piece, or a narrow tile's own and at least one more
+  // merging: the idle K and V stages hold a wide piece's O, or with the exchange
+  // memory behind them a narrow tile's own piece and at least one more
   static constexpr int kMergeBytes = 2 * kRing * kKVBytes + kXBytes;
-  static_assert(kMergeBytes >= kBlockM * (D * 4 + 8) && kMergeBytes >= 2 * kNarrowRows * (D * 4 + 8), "pieces");
+  static_assert(2 * kRing * kKVBytes >= kBlockM * D * 4 && kMergeBytes >= 2 * kNarrowRows * (D * 4 + 8), "pieces");
   static constexpr int kXinvOff = kXmlOff + 4 * kNarrowRows * 8;   // 1 / l of their sum
   static constexpr int kBarOff = kXinvOff + kNarrowRows * 4;
   // q_full, q_empty, k_full[R], v_full[R], s_full[R], o_full[R], p_full[2], o_last, o_free,
-  // merge, copied, drain
-  static constexpr int kNumBars = 2 + 4 * kRing + 2 + 5;
+  // merge, drain
+  static constexpr int kNumBars = 2 + 4 * kRing + 2 + 4;
   static constexpr int kSmemBytes = kBarOff + kNumBars * 8 + 16 + 1024;
   static constexpr uint32_t kOCol = 2 * kBN;
   static constexpr uint32_t kTmemCols = kOCol + D <= 256 ? 256u : 512u;
@@ -395,8 +397,7 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
   uint64_t* o_last = p_full + 2;      // once a piece, after its last O += P V
   uint64_t* o_free = o_last + 1;      // once a piece, when the softmax warps have read O
   uint64_t* merge = o_free + 1;       // steps of exchanging, publishing and merging
-  uint64_t* copied = merge + 1;       // published pieces have come into shared memory
-  uint64_t* drain = copied + 1;
+  uint64_t* drain = merge + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const AbortState ab{abort_flag, p.status};
@@ -416,7 +417,6 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
     mbar_init(o_last, 1);
     mbar_init(o_free, kBlockM);
     mbar_init(merge, kBlockM);
-    mbar_init(copied, 1);
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -604,7 +604,7 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
     Walk w;
     w.begin(p, last, last_seq, run);
     int u = 0, pieces = 0;
-    int merged = 0, copies = 0, fetched = 0;                 // steps of merge and copied; begun (thread 0)
+    int merged = 0;                                          // steps of merge
     bool ok = true;
 
     // Rows of V past the length hold whatever the page held (or an older
@@ -681,7 +681,7 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
       if (!whole) {
         // the pieces that this one merges, in the order of the list
         const long long unit = open_above ? cut.begin(cta + 1) - w.at.kt : cut.begin(cta) - kt0;
-        const int c0 = cut.run_of(unit), j = cta - c0, bits = narrow ? 4 : 2;
+        const int c0 = cut.run_of(unit), j = cta - c0, bits = narrow ? kNarrowBits : kWideBits;
         const int low = open_above ? j + 1 - block_size(j, bits) : 0;
         for (int at = j; at > low; at -= block_size(at - 1, bits)) {
           if (threadIdx.x == 0) source_runs[sources] = c0 + at - 1;
@@ -700,23 +700,11 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
         mbar_arrive(merge);
         return mbar_wait_warp(merge, static_cast<uint32_t>(merged++) & 1u, ab);
       };
-      // The slot is written: its flag, released after everybody's writes (which
-      // bulk copies will read, hence the proxy fence).
+      // The slot is written: its flag, released after everybody's writes.
       auto publish = [&]() -> bool {
-        fence_proxy_async_all();
         if (!meet()) return false;
         if (threadIdx.x == 0) set_flag(p.flags + cta, p.call);
         return true;
-      };
-      // Brings sources [i0, i1) into the ring, `at` pieces in (one thread).
-      auto fetch = [&](int i0, int i1, int at) {
-        if (threadIdx.x != 0) return;
-        fence_proxy_async_all();
-        mbar_arrive_expect_tx(copied, static_cast<uint32_t>((i1 - i0) * piece_bytes));
-        for (int i = i0; i < i1; ++i)
-          tma_load_1d(ring + (at + i - i0) * piece_bytes, slot(source_runs[i]),
-                      static_cast<uint32_t>(piece_bytes), copied);
-        ++fetched;
       };
       // Everything this run merges has been published, and the ring is idle.
       auto wait_sources = [&]() -> bool {
@@ -885,9 +873,14 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
           for (int i0 = 0; i0 < sources; i0 += fit) {
             const int count = min(fit, sources - i0);
             const bool more = i0 + count < sources;
-            fetch(i0, i0 + count, 1);
-            ok = mbar_wait_warp(copied, static_cast<uint32_t>(copies++) & 1u, ab);
-            if (!ok) break;
+            for (int i = quarter; i < count; i += 4) {       // a warp for a piece
+              const uint8_t* src = slot(source_runs[i0 + i]);
+              uint8_t* dst = ring + (1 + i) * piece_bytes;
+#pragma unroll 8
+              for (int x = lane * 16; x < piece_bytes; x += 32 * 16) cp_async16(dst + x, src + x);
+            }
+            cp_async_wait<0>();
+            if (!(ok = meet())) break;
             float2 ml_row = make_float2(0.f, 0.f);
             for (int x = threadIdx.x; x < rows * (D / 4); x += kBlockM) {
               const int rw = x % rows;
@@ -997,42 +990,56 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
         float mm = m_used, ll = l;                           // of this piece and the ones merged into it
         if (sources > 0) {
           // Merge: O stays in tensor memory, the published pieces come into the
-          // ring one after the other.
+          // ring, every thread fetching its own row's vectors, the columns of
+          // one load at a time: those of the next piece follow as soon as
+          // these are summed.
           if (!(ok = wait_sources())) break;
-          const int rw = min(row, rows - 1);
-          for (int i = 0; i < sources; ++i) {
-            if (i > 0 && !(ok = meet())) break;              // the piece before is summed
-            fetch(i, i + 1, 0);
-            ok = mbar_wait_warp(copied, static_cast<uint32_t>(copies++) & 1u, ab);
-            if (!ok) break;
-            if (!busy) continue;
-            const float2 ml = ml_of(ring)[rw];
-            const float top = fmaxf(mm, ml.x), base = top == -INFINITY ? 0.f : top;
-            const float fo = weight(mm, base), fi = weight(ml.x, base);
-            mm = top;
-            ll = ll * fo + ml.y * fi;
-            const float4* src = reinterpret_cast<const float4*>(ring) + rw;
-#pragma unroll 1
-            for (int c = 0; c < D / C::kOChunk; ++c) {
-              uint32_t o[C::kOChunk];
-              __syncwarp();
-              tmem_ld_chunk(lane_base + C::kOCol + c * C::kOChunk, o);
-              tmem_ld_wait();
-              reg_fence(o);
+          if (busy) {
+            constexpr int kSteps = D / C::kOChunk, kVec = C::kOChunk / 4;
+            const int rw = min(row, rows - 1);
+            auto fetch = [&](int i, int c) {
+              if (i < sources) {
+                const float4* src = reinterpret_cast<const float4*>(slot(source_runs[i])) + rw;
+                float4* dst = reinterpret_cast<float4*>(ring) + row;
 #pragma unroll
-              for (int e = 0; e < C::kOChunk / 4; ++e) {
-                const float4 v = src[(c * (C::kOChunk / 4) + e) * rows];
-                o[e * 4] = __float_as_uint(fmaf(v.x, fi, __uint_as_float(o[e * 4]) * fo));
-                o[e * 4 + 1] = __float_as_uint(fmaf(v.y, fi, __uint_as_float(o[e * 4 + 1]) * fo));
-                o[e * 4 + 2] = __float_as_uint(fmaf(v.z, fi, __uint_as_float(o[e * 4 + 2]) * fo));
-                o[e * 4 + 3] = __float_as_uint(fmaf(v.w, fi, __uint_as_float(o[e * 4 + 3]) * fo));
+                for (int e = 0; e < kVec; ++e)
+                  cp_async16(dst + (c * kVec + e) * kBlockM, src + (c * kVec + e) * rows);
               }
-              tmem_st_chunk(lane_base + C::kOCol + c * C::kOChunk, o);
+              cp_async_commit();
+            };
+#pragma unroll 1
+            for (int c = 0; c < kSteps; ++c) fetch(0, c);
+            float2 ml = __ldcg(ml_of(slot(source_runs[0])) + rw);
+#pragma unroll 1
+            for (int i = 0; i < sources; ++i) {
+              const float top = fmaxf(mm, ml.x), base = top == -INFINITY ? 0.f : top;
+              const float fo = weight(mm, base), fi = weight(ml.x, base);
+              mm = top;
+              ll = ll * fo + ml.y * fi;
+              if (i + 1 < sources) ml = __ldcg(ml_of(slot(source_runs[i + 1])) + rw);
+#pragma unroll 1
+              for (int c = 0; c < kSteps; ++c) {
+                uint32_t o[C::kOChunk];
+                __syncwarp();
+                tmem_ld_chunk(lane_base + C::kOCol + c * C::kOChunk, o);
+                cp_async_wait<kSteps - 1>();
+                tmem_ld_wait();
+                reg_fence(o);
+                const float4* src = reinterpret_cast<const float4*>(ring) + row;
+#pragma unroll
+                for (int e = 0; e < kVec; ++e) {
+                  const float4 v = src[(c * kVec + e) * kBlockM];
+                  o[e * 4] = __float_as_uint(fmaf(v.x, fi, __uint_as_float(o[e * 4]) * fo));
+                  o[e * 4 + 1] = __float_as_uint(fmaf(v.y, fi, __uint_as_float(o[e * 4 + 1]) * fo));
+                  o[e * 4 + 2] = __float_as_uint(fmaf(v.z, fi, __uint_as_float(o[e * 4 + 2]) * fo));
+                  o[e * 4 + 3] = __float_as_uint(fmaf(v.w, fi, __uint_as_float(o[e * 4 + 3]) * fo));
+                }
+                tmem_st_chunk(lane_base + C::kOCol + c * C::kOChunk, o);
+                fetch(i + 1, c);
+              }
             }
             tmem_st_wait();
           }
-          if (!ok) break;
-          if (!(ok = meet())) break;                         // (the rows turn in memory that held the piece)
         }
         if (busy) {
           const float inv_l = ll > 0.f ? 1.f / ll : 0.f;
@@ -1093,8 +1100,7 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
       mbar_arrive(o_free);
       ++pieces;
     } while (w.next(p));
-    // a wait ran out: let the copies under way land before the CTA can exit
-    if (fetched > copies) mbar_wait_drain(copied, static_cast<uint32_t>(copies) & 1u);
+    cp_async_wait<0>();                                      // (a wait may have run out above)
   }
 
   tc_fence_before();
@@ -1108,9 +1114,17 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
 template <int D>
 cudaError_t launch_paged_impl(const PagedParams& p, cudaStream_t stream) {
   constexpr int smem = PCfg<D>::kSmemBytes;
-  cudaError_t err =
-      cudaFuncSetAttribute(sdpa_paged_split<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  // the kernel's shared-memory limit is set once on each device
+  static std::atomic<unsigned long long> prepared{0};
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
   if (err != cudaSuccess) return err;
+  const unsigned long long bit = 1ull << (dev & 63);
+  if (dev > 63 || !(prepared.load(std::memory_order_acquire) & bit)) {
+    err = cudaFuncSetAttribute(sdpa_paged_split<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (err != cudaSuccess) return err;
+    if (dev <= 63) prepared.fetch_or(bit, std::memory_order_release);
+  }
   return launch_kernel(sdpa_paged_split<D>, dim3(static_cast<unsigned>(p.split_ctas)), dim3(kThreads), smem,
                        stream, true, p);
 }
