@@ -123,6 +123,32 @@ bool make_map_4d(CUtensorMap* map, const void* base, int d, int n, int h, int b,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// 5-D bf16 map over cache pages [n_pages][h_kv][page][d], a row's columns in
+// blocks of min(d, 64): (columns, rows, blocks, heads, pages).  A box is a key
+// tile's rows of every block; of pages smaller than that, a page's rows of
+// one block.  Pages past n_pages read as zeros.
+bool make_map_pages(CUtensorMap* map, const void* base, int d, int page, int h_kv, int n_pages) {
+  auto enc = encode_fn();
+  if (enc == nullptr) return false;
+  const int cols = d < 64 ? d : 64;
+  const cuuint64_t dims[5] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(page),
+                              static_cast<cuuint64_t>(d / cols), static_cast<cuuint64_t>(h_kv),
+                              static_cast<cuuint64_t>(n_pages)};
+  const cuuint64_t row = static_cast<cuuint64_t>(d) * 2;
+  const cuuint64_t strides[4] = {row, static_cast<cuuint64_t>(cols) * 2, row * page, row * page * h_kv};
+  const bool whole = page >= sdpa::kPagedKeyTile;
+  const cuuint32_t box[5] = {static_cast<cuuint32_t>(cols),
+                             static_cast<cuuint32_t>(whole ? sdpa::kPagedKeyTile : page),
+                             static_cast<cuuint32_t>(whole ? d / cols : 1), 1, 1};
+  const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  const CUtensorMapSwizzle swz = d >= 64 ? CU_TENSOR_MAP_SWIZZLE_128B
+                                         : (d == 32 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                                    : CU_TENSOR_MAP_SWIZZLE_32B);
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(base), dims, strides, box,
+             estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swz, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // 3-D bf16 map over packed token rows (d, h, n_tokens), tokens `stride`
 // elements apart; boxes of min(d, 64) columns x box_heads x box_tokens, so a
 // box lands as box_tokens * box_heads consecutive rows.
@@ -851,10 +877,8 @@ sdpa_status sdpa_paged_forward(const void* q, const void* k_pages, const void* v
   if (!make_map_rows(&p.tm_q, q, d, h, n_tokens, q_stride, p.group, p.tile_tokens) ||
       !make_map_rows(&p.tm_q_narrow, q, d, h, n_tokens, q_stride, p.group,
                      p.group <= 32 ? 32 / p.group : p.tile_tokens) ||
-      !make_map_4d(&p.tm_k, k_pages, d, page_size, h_kv, n_pages, d, 1ll * page_size * d,
-                   1ll * h_kv * page_size * d, std::min(page_size, sdpa::kPagedKeyTile)) ||
-      !make_map_4d(&p.tm_v, v_pages, d, page_size, h_kv, n_pages, d, 1ll * page_size * d,
-                   1ll * h_kv * page_size * d, std::min(page_size, sdpa::kPagedKeyTile)))
+      !make_map_pages(&p.tm_k, k_pages, d, page_size, h_kv, n_pages) ||
+      !make_map_pages(&p.tm_v, v_pages, d, page_size, h_kv, n_pages))
     return SDPA_ERR_CUDA;
   p.out = static_cast<uint16_t*>(out);
   p.page_table = page_table;

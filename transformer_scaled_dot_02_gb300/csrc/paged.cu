@@ -11,10 +11,11 @@
 // sdpa_paged_split<D>: a UNIT is (sequence, key-value head, row tile); the
 // rows of a tile are tile_tokens tokens x the group's heads (at most 128), so
 // one walk over the keys serves every query head of the group.  A unit's walk
-// is its visible keys in tiles of 64; all walks laid end to end are cut into
-// equal runs of tiles, one per CTA, so that one long sequence, many short
-// ones and any mixture load the SMs alike.  The cut is worked out on the
-// device from the lengths, so a captured launch follows them.
+// is its visible keys in tiles of 64; all units laid end to end, each as long
+// as it is expected to take, are cut into equal runs, one per CTA, so that one
+// long sequence, many short ones and any mixture load the SMs alike.  The cut
+// is worked out on the device from the lengths, so a captured launch follows
+// them.
 //
 // A CTA works its run from the end to the beginning.  If the run ends inside
 // a unit, that piece comes first and its (O, m, l) is published in the
@@ -48,6 +49,8 @@ namespace {
 
 constexpr int kBlockM = 128;
 constexpr int kBN = kPagedKeyTile;         // keys per tile
+constexpr int kBNShift = 6;
+static_assert(kBN == 1 << kBNShift, "key tile");
 constexpr int kThreads = 192;
 constexpr int kProducerWarp = 4;
 constexpr int kMmaWarp = 5;
@@ -72,71 +75,96 @@ __device__ __forceinline__ Seq load_seq(const PagedParams& p, int s) {
   return q;
 }
 
-// Keys that some row of row tile r sees, and the tile's cost in key tiles
-// (at least one: a tile that sees nothing still writes its zeros).
+// Keys that some row of row tile r sees, and the tile's walk in key tiles (at
+// least one: a tile that sees nothing still writes its zeros).
 __device__ __forceinline__ int tile_keys(const PagedParams& p, const Seq& q, int r) {
   return max(0, q.len - q.n + min((r + 1) * p.tile_tokens, q.n));
 }
-__device__ __forceinline__ int tile_cost(int keys) { return max(1, (keys + kBN - 1) / kBN); }
+__device__ __forceinline__ int walk_tiles(int keys) { return max(1, (keys + kBN - 1) / kBN); }
 
-// Cost of row tiles 0 .. r-1 (r <= q.tiles) of one key-value head.  All but
-// the last tile see A + (i + 1) t keys, A = len - n: z of them cost one, the
-// others ceil((A + (i + 1) t) / 64), whose sum over 64 consecutive i grows by
-// 64 t from one such block to the next.
-__device__ __noinline__ long long cost_before(const PagedParams& p, const Seq& q, int r) {
+// What a unit is expected to take: `start` (loading Q, storing O) and `tile`
+// for each key tile.  In quarters of a wide tile's key tile: measured on GB300
+// with two CTAs per SM at d = 128, a wide key tile takes 0.88 us and the ends
+// of a walk 1.9 us; at d = 64 a narrow key tile takes two thirds of a wide one.
+// Without the ends, the CTAs with a prompt's shortest walks finished 20 % after
+// the others.  Where there are few key tiles for each CTA (`few`), a single one
+// more counts for more than all that: then only key tiles are counted.
+struct Weight {
+  int start, tile;
+};
+__device__ __forceinline__ Weight weight_of(bool few, bool narrow) {
+  return few ? Weight{0, 1} : (narrow ? Weight{14, 4} : Weight{18, 4});
+}
+constexpr int kFewTiles = 8;
+
+__device__ __forceinline__ int tile_rows(const PagedParams& p, const Seq& q, int r) {
+  return min(p.tile_tokens, q.n - r * p.tile_tokens) * p.group;
+}
+__device__ __forceinline__ long long unit_cost(const PagedParams& p, const Seq& q, int r, bool few) {
+  const Weight w = weight_of(few, tile_rows(p, q, r) <= kNarrowRows);
+  return w.start + static_cast<long long>(w.tile) * walk_tiles(tile_keys(p, q, r));
+}
+
+// Key tiles of the first f row tiles, f < q.tiles.  They see A + (i + 1) t
+// keys, A = len - n: z of them walk one tile, the others ceil((A + (i + 1) t)
+// / 64).
+__device__ __noinline__ long long tiles_before(const PagedParams& p, const Seq& q, int f) {
   const int t = p.tile_tokens;
+  const int a = q.len - q.n;
+  const int z = kBN - a >= t ? min(f, (kBN - a) / t) : 0;
+  const int cnt = f - z;
+  if (cnt <= 0) return z;
+  const int base = a + t * (z + 1) + kBN - 1;       // > 64
+  const long long n = cnt;
+  long long sum = z;
+  if ((t & (t - 1)) == 0) {                          // groups that are powers of two
+    sum += n * (base / kBN);
+    if (t >= kBN) return sum + t / kBN * (n * (n - 1) / 2);
+    // floor((o + t i) / 64) = floor((o / t + i) / (64 / t)), summed below m:
+    const int log_t = __ffs(t) - 1, log_per = 6 - log_t;
+    auto below = [&](long long m) {
+      const long long q2 = m >> log_per;
+      return (q2 * (q2 - 1) / 2 << log_per) + q2 * (m - (q2 << log_per));
+    };
+    const int o = (base % kBN) >> log_t;
+    return sum + below(o + n) - below(o);
+  }
+  // the sum over 64 consecutive i grows by 64 t from one such block to the next
+  const int blocks = cnt / kBN, rest = cnt % kBN;
+  long long head = 0, full = 0;                      // the first `rest` terms; the first 64
+  const int walk = blocks > 0 ? kBN : rest;
+  for (int i = 0; i < walk; ++i) {
+    const int c = (base + t * i) / kBN;
+    full += c;
+    if (i < rest) head += c;
+  }
+  const long long m = blocks;
+  return sum + m * full + static_cast<long long>(kBN) * t * (m * (m - 1) / 2) + head +
+         static_cast<long long>(rest) * t * m;
+}
+
+// Cost of row tiles 0 .. r-1 (r <= q.tiles) of one key-value head: all but
+// the last are wide (a full tile has more than 64 rows).
+__device__ __forceinline__ long long cost_before(const PagedParams& p, const Seq& q, int r, bool few) {
   const int f = min(r, q.tiles - 1);
   long long sum = 0;
   if (f > 0) {
-    const int a = q.len - q.n;
-    const int z = kBN - a >= t ? min(f, (kBN - a) / t) : 0;
-    sum = z;
-    const int cnt = f - z;
-    if (cnt > 0) {
-      const int base = a + t * (z + 1) + kBN - 1;   // > kBN
-      if ((t & (t - 1)) == 0) {                      // groups that are powers of two
-        const long long n = cnt;
-        sum += n * (base / kBN);
-        if (t >= kBN) {
-          sum += t / kBN * (n * (n - 1) / 2);
-        } else {
-          // floor((o + t i) / 64) = floor((o / t + i) / (64 / t)), summed below m:
-          const int log_t = __ffs(t) - 1, log_per = 6 - log_t;
-          auto below = [&](long long m) {
-            const long long q = m >> log_per;
-            return (q * (q - 1) / 2 << log_per) + q * (m - (q << log_per));
-          };
-          const int o = (base % kBN) >> log_t;
-          sum += below(o + n) - below(o);
-        }
-        if (r == q.tiles) sum += tile_cost(q.len);
-        return sum;
-      }
-      const int blocks = cnt / kBN, rest = cnt % kBN;
-      long long head = 0, full = 0;                  // the first `rest` terms; the first 64
-      const int walk = blocks > 0 ? kBN : rest;
-      for (int i = 0; i < walk; ++i) {
-        const int c = (base + t * i) / kBN;
-        full += c;
-        if (i < rest) head += c;
-      }
-      const long long m = blocks;
-      sum += m * full + static_cast<long long>(kBN) * t * (m * (m - 1) / 2) + head +
-             static_cast<long long>(rest) * t * m;
-    }
+    const Weight w = weight_of(few, false);
+    sum = static_cast<long long>(w.start) * f + w.tile * tiles_before(p, q, f);
   }
-  if (r == q.tiles && r > 0) sum += tile_cost(q.len);
+  if (r == q.tiles && r > 0) sum += unit_cost(p, q, r - 1, few);
   return sum;
 }
 
-// A place in the laid-out work: before key tile kt of row tile r of head hk
-// of sequence s (kt > 0).
+// A place in the laid-out work: unit (s, hk, r), and the item of it that the
+// place is behind.
 struct Place {
-  int s, hk, r, kt;
+  int s, hk, r;
+  long long item;
 };
 
 struct ScheduleShared {
-  long long warp_sum[kThreads / 32];
+  longlong2 warp_sum[kThreads / 32];
   long long rem;
   Place at;
   Seq q;
@@ -152,7 +180,8 @@ __device__ __forceinline__ long long divide(long long a, long long b) {
 struct Cut {
   long long each, longer;                                    // longer: items in the longer runs
   int over;
-  __device__ Cut(long long work, int ctas) {
+  bool few;                                                  // how units are weighed
+  __device__ Cut(long long work, int ctas, bool few_tiles) : few(few_tiles) {
     each = divide(work, ctas);
     over = static_cast<int>(work - each * ctas);
     longer = over * (each + 1);
@@ -171,47 +200,67 @@ __device__ bool find_place(const PagedParams& p, ScheduleShared* sh, int c, int 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int per = (p.b + kThreads - 1) / kThreads;
   const int s0 = min(tid * per, p.b), s1 = min(s0 + per, p.b);
-  long long mine = 0;
+  // both ways of weighing, x: key tiles alone
+  longlong2 mine = make_longlong2(0, 0);
   Seq q;
   for (int s = s0; s < s1; ++s) {
     q = load_seq(p, s);
-    mine += cost_before(p, q, q.tiles) * p.h_kv;
+    if (q.tiles == 1) {
+      const int walk = walk_tiles(q.len);
+      const Weight w = weight_of(false, q.n * p.group <= kNarrowRows);
+      mine.x += static_cast<long long>(walk) * p.h_kv;
+      mine.y += (w.start + static_cast<long long>(w.tile) * walk) * p.h_kv;
+    } else if (q.tiles > 0) {
+      mine.x += cost_before(p, q, q.tiles, true) * p.h_kv;
+      mine.y += cost_before(p, q, q.tiles, false) * p.h_kv;
+    }
   }
-  long long incl = mine;
+  longlong2 incl = mine;
 #pragma unroll
   for (int x = 1; x < 32; x <<= 1) {
-    const long long o = __shfl_up_sync(0xffffffffu, incl, x);
-    if (lane >= x) incl += o;
+    const long long ox = __shfl_up_sync(0xffffffffu, incl.x, x), oy = __shfl_up_sync(0xffffffffu, incl.y, x);
+    if (lane >= x) {
+      incl.x += ox;
+      incl.y += oy;
+    }
   }
   if (lane == 31) sh->warp_sum[warp] = incl;
   __syncthreads();
-  long long total = 0, excl = incl - mine;
+  longlong2 sum = make_longlong2(0, 0), before = make_longlong2(incl.x - mine.x, incl.y - mine.y);
 #pragma unroll
   for (int w = 0; w < kThreads / 32; ++w) {
-    if (w < warp) excl += sh->warp_sum[w];
-    total += sh->warp_sum[w];
+    const longlong2 v = sh->warp_sum[w];
+    if (w < warp) {
+      before.x += v.x;
+      before.y += v.y;
+    }
+    sum.x += v.x;
+    sum.y += v.y;
   }
-  const int n = static_cast<int>(min(static_cast<long long>(max_ctas), total));   // a tile a run at least
+  // (a run is never shorter than a key tile, so no run inside a unit is empty)
+  const bool few = sum.x < 1ll * kFewTiles * max_ctas;
+  const int n = static_cast<int>(min(static_cast<long long>(max_ctas), sum.x));
   if (c >= n) return false;
-  *cut = Cut(total, n);
+  const long long total = few ? sum.x : sum.y, own = few ? mine.x : mine.y, excl = few ? before.x : before.y;
+  *cut = Cut(total, n, few);
   const long long x = cut->begin(c + 1) - 1;                 // its last item
-  if (mine > 0 && excl <= x && x < excl + mine) {
+  if (own > 0 && excl <= x && x < excl + own) {
     long long rem = x - excl;
     Place pl;
     pl.s = s0;
     if (per > 1) {
       for (pl.s = s0; pl.s < s1; ++pl.s) {
         q = load_seq(p, pl.s);
-        const long long w = cost_before(p, q, q.tiles) * p.h_kv;
+        const long long w = cost_before(p, q, q.tiles, few) * p.h_kv;
         if (rem < w) break;
         rem -= w;
       }
     }
-    const long long head = cost_before(p, q, q.tiles);
+    const long long head = cost_before(p, q, q.tiles, few);
     pl.hk = static_cast<int>(divide(rem, head));
     rem -= pl.hk * head;
     pl.r = 0;
-    pl.kt = static_cast<int>(rem) + 1;                       // for a single row tile
+    pl.item = rem + 1;                                       // for a single row tile
     sh->at = pl;
     sh->rem = rem;
     sh->q = q;
@@ -227,57 +276,71 @@ __device__ bool find_place(const PagedParams& p, ScheduleShared* sh, int c, int 
     while (hi - lo > 1) {
       const int step = (hi - lo + 31) / 32;
       const int probe = lo + lane * step;
-      const bool le = probe < hi && cost_before(p, *seq, probe) <= rem;
+      const bool le = probe < hi && cost_before(p, *seq, probe, few) <= rem;
       const int k = 31 - __clz(__ballot_sync(0xffffffffu, le));
       lo += k * step;
       hi = min(hi, lo + step);
     }
     at->r = lo;
-    at->kt = static_cast<int>(rem - cost_before(p, *seq, lo)) + 1;
+    at->item = rem - cost_before(p, *seq, lo, few) + 1;
   }
   return true;
 }
 
 // The pieces of one run, from the last to the first; every role walks its
-// own copy.
+// own copy.  A key tile belongs to the run that its last item lies in.
 struct Walk {
-  Place at;                                                  // where the piece ends
+  int s, hk, r;                                              // the piece's unit
   Seq q;
-  int keys, cost;
-  long long left;
+  int kt0, kt1, cost;                                        // its key tiles [kt0, kt1) of `cost`
+  int keys, rows;                                            // the unit's keys, rows that are queries
+  Weight w;
+  bool few;
+  long long off;                                             // where the unit begins, seen from the run's begin
 
-  __device__ void begin(const PagedParams& p, const Place& end, const Seq& seq, long long run) {
-    at = end;
-    left = run;
+  // Key tiles that lie before item x of the unit.
+  __device__ __forceinline__ int tiles_at(long long x) const {
+    return x <= w.start ? 0 : static_cast<int>(divide(x - w.start, w.tile));
+  }
+  __device__ __forceinline__ void load(const PagedParams& p) {
+    keys = tile_keys(p, q, r);
+    cost = walk_tiles(keys);
+    rows = tile_rows(p, q, r);
+    w = weight_of(few, rows <= kNarrowRows);
+  }
+  // The first piece of a run of `run` items that ends at `end`; false: none.
+  __device__ bool begin(const PagedParams& p, const Place& end, const Seq& seq, long long run, bool few_tiles) {
+    few = few_tiles;
+    s = end.s;
+    hk = end.hk;
+    r = end.r;
     q = seq;
-    keys = tile_keys(p, q, at.r);
-    cost = tile_cost(keys);
+    load(p);
+    off = run - end.item;
+    kt1 = tiles_at(end.item);
+    kt0 = tiles_at(-off);
+    return kt1 > kt0 || next(p);
   }
-  // rows of this row tile that are queries
-  __device__ int rows(const PagedParams& p) const {
-    return min(p.tile_tokens, q.n - at.r * p.tile_tokens) * p.group;
-  }
-  // key tiles of this piece: [first(), at.kt); those with keys: [first(), first() + count())
-  __device__ int first() const { return static_cast<int>(max(0ll, at.kt - left)); }
-  __device__ int count() const { return min(at.kt, (keys + kBN - 1) / kBN) - first(); }
   __device__ bool next(const PagedParams& p) {
-    left -= at.kt - first();
-    if (left <= 0) return false;
-    if (--at.r < 0) {
-      if (--at.hk < 0) {
+    if (off <= 0) return false;
+    if (--r < 0) {
+      if (--hk < 0) {
         do {
-          if (--at.s < 0) return false;
-          q = load_seq(p, at.s);
+          if (--s < 0) return false;
+          q = load_seq(p, s);
         } while (q.n == 0);
-        at.hk = p.h_kv - 1;
+        hk = p.h_kv - 1;
       }
-      at.r = q.tiles - 1;
+      r = q.tiles - 1;
     }
-    keys = tile_keys(p, q, at.r);
-    cost = tile_cost(keys);
-    at.kt = cost;
+    load(p);
+    off -= w.start + static_cast<long long>(w.tile) * cost;
+    kt0 = tiles_at(-off);
+    kt1 = cost;
     return true;
   }
+  // key tiles of the piece that hold keys (all, but for a unit that sees none)
+  __device__ int count() const { return min(kt1, (keys + kBN - 1) / kBN) - kt0; }
 };
 
 // --------------------------------------------------------------------- merge
@@ -372,8 +435,7 @@ struct PCfg {
   static constexpr uint32_t kDescHi = (kSBO >> 4) | (1u << 14) | (kLayout << 29);
   static_assert(kSmemBytes * kMinBlocks <= 232448 - 1024 * kMinBlocks, "CTAs per SM");
   static_assert(kKOff % 1024 == 0 && kVOff % 1024 == 0 && kKVBox % 1024 == 0, "alignment");
-  // one lane of the producer warp per TMA box of a tile (pages of 8 rows at least)
-  static_assert(kBoxes * (kBN / kPagedMinPage) <= 32, "boxes of a tile");
+  static_assert(kBoxes * (kBN / kPagedMinPage) <= 32, "a lane of the producer warp for each box of a tile's parts");
 };
 
 template <int D>
@@ -426,7 +488,7 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
   griddep_launch_dependents();
   griddep_wait();
 
-  Cut cut(0, 1);
+  Cut cut(0, 1, true);
   Place last;
   Seq last_seq;
   const int cta = static_cast<int>(blockIdx.x);
@@ -438,53 +500,51 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
 
   if (run > 0 && warp == kProducerWarp) {
     // ---------------------------------------------------------- producer
-    // Lane i < boxes copies column box i % kBoxes of the page part i / kBoxes
-    // of a tile; it reads its page of the tile after next ahead of time.
-    const int page_rows = 1 << p.page_shift;
-    const int box_rows = min(page_rows, kBN);
-    const int part = lane / C::kBoxes, col = lane % C::kBoxes;
-    const bool copies = part < kBN / box_rows;
+    // A tile of 64 keys that lies in one page is one copy of all its column
+    // boxes.  Smaller pages are `parts` of a tile: lane part * kBoxes + c
+    // copies column box c of its part, all lanes at once (one lane doing them
+    // one after the other took 270 clk for each).  A lane reads the page of its
+    // part two tiles ahead and looks at it only when it uses it: waiting for
+    // each read took 700 clk a tile.
+    const int box_shift = min(p.page_shift, kBNShift);
+    const int box_rows = 1 << box_shift, tile_parts = kBN >> box_shift;
+    const int row_mask = (1 << p.page_shift) - 1;
+    const int part = tile_parts == 1 ? 0 : lane / C::kBoxes, col = tile_parts == 1 ? 0 : lane % C::kBoxes;
+    const bool copies = tile_parts == 1 ? lane == 0 : part < tile_parts;
+    const uint32_t dst = static_cast<uint32_t>(col * C::kKVBox + (part << box_shift) * C::kRowBytes);
     if (lane == 0) {
       tma_prefetch_desc(&p.tm_q);
       tma_prefetch_desc(&p.tm_q_narrow);
       tma_prefetch_desc(&p.tm_k);
       tma_prefetch_desc(&p.tm_v);
     }
-    const uint32_t dst = static_cast<uint32_t>(col * C::kKVBox + part * box_rows * C::kRowBytes);
     Walk w;
-    w.begin(p, last, last_seq, run);
     int u0 = 0, pieces = 0, k_issued = 0, v_issued = 0;
     bool go = true;
-    do {
+    for (bool more = w.begin(p, last, last_seq, run, cut.few); more; more = go && w.next(p)) {
       const int n = w.count();
       if (n <= 0) continue;
-      const int kt0 = w.first();
-      const int32_t* pages = p.page_table + static_cast<long long>(w.at.s) * p.pages_per_seq;
-      const int key_first = kt0 * kBN + part * box_rows;
-      // page of this lane's part of tile i; -1: no position there holds a key
-      auto page_of = [&](int i) -> int {
-        const int key = key_first + i * kBN;
-        return (copies && i < n && key < w.q.len) ? pages[key >> p.page_shift] : -1;
-      };
-      // page numbers outside the cache read as zeros and are reported
-      auto has = [&](int i) { return copies && key_first + i * kBN < w.q.len; };
+      const int kt0 = w.kt0;
+      const int32_t* pages = p.page_table + static_cast<long long>(w.s) * p.pages_per_seq;
+      const int key_lane = kt0 * kBN + (part << box_shift);
+      // this lane's part of tile i: does it hold keys, and in which page
+      auto holds = [&](int i) { return copies && i < n && key_lane + i * kBN < w.q.len; };
+      auto page_of = [&](int i) -> int { return holds(i) ? pages[(key_lane + i * kBN) >> p.page_shift] : 0; };
       auto load = [&](const CUtensorMap* map, uint64_t* bar, uint8_t* stage, int i, int page) {
         const int key = (kt0 + i) * kBN;
-        const int parts = min(kBN / box_rows, (w.q.len - key + box_rows - 1) / box_rows);
-        if (lane == 0)
-          mbar_arrive_expect_tx(bar, static_cast<uint32_t>(parts * box_rows * C::kRowBytes * C::kBoxes));
+        const int parts = min(tile_parts, (w.q.len - key + box_rows - 1) >> box_shift);
+        if (lane == 0) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(parts << box_shift) * (C::kRowBytes * C::kBoxes));
         __syncwarp();
-        if (has(i)) {
+        if (holds(i)) {
+          // page numbers outside the cache read as zeros and are reported
           if (page < 0 || page >= p.n_pages) {
             atomicOr(p.status, kStatusBadPage);
             page = p.n_pages;
           }
-          tma_load_4d(map, bar, stage + dst, col * C::kBoxCols,
-                      (key_first + i * kBN) & (page_rows - 1), w.at.hk, page);
+          tma_load_5d(map, bar, stage + dst, 0, (key_lane + i * kBN) & row_mask, col, w.hk, page);
         }
       };
-      int page_v = page_of(0);
-      int page_k = page_v;
+      int page_v = page_of(0), page_k = page_v, page_n = page_of(1);
       auto load_k = [&](int i) -> bool {
         const int u = u0 + i, s = u % R;
         if (u >= R && !mbar_wait_warp(s_full + s, static_cast<uint32_t>(u / R - 1) & 1u, ab)) return false;
@@ -497,7 +557,7 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
       if (pieces > 0 && !(go = mbar_wait_warp(q_empty, static_cast<uint32_t>(pieces - 1) & 1u, ab))) break;
       {
         // lane c * 4 + y: column box c, for a narrow tile into quarter y
-        const bool narrow = w.rows(p) <= kNarrowRows;
+        const bool narrow = w.rows <= kNarrowRows;
         const int rows = (narrow ? kNarrowRows / p.group : p.tile_tokens) * p.group;
         if (lane == 0)
           mbar_arrive_expect_tx(q_full, static_cast<uint32_t>((narrow ? 4 : 1) * rows * C::kRowBytes * C::kBoxes));
@@ -506,12 +566,13 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
         if (c < C::kBoxes && (narrow || y == 0))
           tma_load_3d(narrow ? &p.tm_q_narrow : &p.tm_q, q_full,
                       smem + c * C::kQBox + y * kNarrowRows * C::kRowBytes, c * C::kBoxCols,
-                      w.at.hk * p.group, w.q.start + w.at.r * p.tile_tokens);
+                      w.hk * p.group, w.q.start + w.r * p.tile_tokens);
       }
       ++pieces;
       for (int i = 0; go && i < n; ++i) {
         // K of the next tile goes ahead of V of this one: its stage is free earlier
-        page_k = page_of(i + 1);
+        page_k = page_n;
+        page_n = page_of(i + 2);
         if (i + 1 < n && !(go = load_k(i + 1))) break;
         const int u = u0 + i, s = u % R;
         if (u >= R && !(go = mbar_wait_warp(o_full + s, static_cast<uint32_t>(u / R - 1) & 1u, ab))) break;
@@ -520,7 +581,7 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
         v_issued = u + 1;
       }
       u0 += n;
-    } while (go && w.next(p));
+    }
     // let every copy land before the CTA can exit
     if (pieces > 0) mbar_wait_drain(q_full, static_cast<uint32_t>(pieces - 1) & 1u);
     for (int u = max(0, k_issued - R); u < k_issued; ++u)
@@ -562,10 +623,9 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
                          (accumulate || k > 0) ? 1u : 0u);
     };
     Walk w;
-    w.begin(p, last, last_seq, run);
     int u = 0, pieces = 0;
     bool ok = true;
-    do {
+    for (bool more = w.begin(p, last, last_seq, run, cut.few); more; more = ok && w.next(p)) {
       const int n = w.count();
       if (n <= 0) continue;
       ok = mbar_wait_warp(q_full, static_cast<uint32_t>(pieces) & 1u, ab);
@@ -592,7 +652,7 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
         if (i + 1 == n) mma_commit_warp(o_last);
       }
       ++pieces;
-    } while (ok && w.next(p));
+    }
     mma_commit_warp(drain);
     mbar_wait_drain(drain, 0);
   } else if (run > 0) {
@@ -602,7 +662,7 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
     const float scale_log2 = p.scale_log2;
     const float2 sc2 = make_float2(scale_log2, scale_log2);
     Walk w;
-    w.begin(p, last, last_seq, run);
+    bool more = w.begin(p, last, last_seq, run, cut.few);
     int u = 0, pieces = 0;
     int merged = 0;                                          // steps of merge
     bool ok = true;
@@ -663,25 +723,25 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
       }
     };
 
-    do {
-      const int kt0 = w.first(), n = w.count();
-      const int rows = w.rows(p);
+    for (; more; more = w.next(p)) {
+      const int kt0 = w.kt0, n = w.count();
+      const int rows = w.rows;
       const bool narrow = rows <= kNarrowRows;
       const int row = narrow ? lane : quarter * 32 + lane;   // row of the tile
       const int token = row / p.group, head = row % p.group;
-      const int token0 = w.at.r * p.tile_tokens;
+      const int token0 = w.r * p.tile_tokens;
       const bool valid = row < rows;
       const int pos0 = w.q.len - w.q.n + token0;             // position of the tile's first row
       const int pos = pos0 + token;                          // this row sees keys 0 .. pos
       // a piece of a unit that later runs merge, or that this run merges with
       // what earlier runs published
-      const bool open_above = w.at.kt < w.cost, open_below = kt0 > 0;
+      const bool open_above = w.kt1 < w.cost, open_below = kt0 > 0;
       const bool whole = !open_above && !open_below;
       int sources = 0;
       if (!whole) {
         // the pieces that this one merges, in the order of the list
-        const long long unit = open_above ? cut.begin(cta + 1) - w.at.kt : cut.begin(cta) - kt0;
-        const int c0 = cut.run_of(unit), j = cta - c0, bits = narrow ? kNarrowBits : kWideBits;
+        // (the first key tile's last item says which run it belongs to)
+        const int c0 = cut.run_of(cut.begin(cta) + w.off + w.w.start + w.w.tile - 1), j = cta - c0, bits = narrow ? kNarrowBits : kWideBits;
         const int low = open_above ? j + 1 - block_size(j, bits) : 0;
         for (int at = j; at > low; at -= block_size(at - 1, bits)) {
           if (threadIdx.x == 0) source_runs[sources] = c0 + at - 1;
@@ -689,7 +749,7 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
         }
       }
       const long long out_row =
-          static_cast<long long>(w.q.start + token0 + token) * p.h + w.at.hk * p.group + head;
+          static_cast<long long>(w.q.start + token0 + token) * p.h + w.hk * p.group + head;
       // a published piece of this unit: its bytes, run sl's slot, its (m, l)
       const int o_bytes = rows * D * 4, piece_bytes = o_bytes + (rows * 8 + 15) / 16 * 16;
       auto slot = [&](int sl) { return p.slots + static_cast<long long>(sl) * p.slot_bytes; };
@@ -731,7 +791,7 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
       auto write_out = [&](int rw, int col, const float4& v, float inv) {
         const int tok = rw / p.group;
         *reinterpret_cast<uint2*>(
-            p.out + (static_cast<long long>(w.q.start + token0 + tok) * p.h + w.at.hk * p.group + rw -
+            p.out + (static_cast<long long>(w.q.start + token0 + tok) * p.h + w.hk * p.group + rw -
                      tok * p.group) * D + col) =
             make_uint2(pack_bf16x2(v.x * inv, v.y * inv), pack_bf16x2(v.z * inv, v.w * inv));
       };
@@ -872,7 +932,7 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
           if (!(ok = wait_sources())) break;
           for (int i0 = 0; i0 < sources; i0 += fit) {
             const int count = min(fit, sources - i0);
-            const bool more = i0 + count < sources;
+            const bool further = i0 + count < sources;
             for (int i = quarter; i < count; i += 4) {       // a warp for a piece
               const uint8_t* src = slot(source_runs[i0 + i]);
               uint8_t* dst = ring + (1 + i) * piece_bytes;
@@ -905,7 +965,7 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
                 acc.w += v.w * fi;
               }
               if (x < rows) ml_row = make_float2(top, sum);
-              if (more) {
+              if (further) {
                 reinterpret_cast<float4*>(ring)[x] = acc;
               } else if (open_above) {
                 reinterpret_cast<float4*>(slot(cta))[x] = acc;
@@ -914,7 +974,7 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
                 write_out(rw, x / rows * 4, acc, sum > 0.f ? 1.f / sum : 0.f);
               }
             }
-            if (more) {
+            if (further) {
               // (every row's own (m, l) has been read: they move on)
               if (!(ok = meet())) break;
               if (static_cast<int>(threadIdx.x) < rows) ml_of(ring)[threadIdx.x] = ml_row;
@@ -1045,7 +1105,15 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
           const float inv_l = ll > 0.f ? 1.f / ll : 0.f;
           const int rows_here = min(32, rows - quarter * 32);
           uint8_t* turn = smem + C::kXOff + quarter * C::kTurnSlot;
+          // where this lane's 16 bytes of rows lane / 4 + 8 k go
           const int r0 = lane >> 2, piece = lane & 3;
+          uint16_t* dst[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int rr = quarter * 32 + r0 + 8 * k, tok = rr / p.group;
+            dst[k] = p.out + (static_cast<long long>(w.q.start + token0 + tok) * p.h + w.hk * p.group + rr -
+                              tok * p.group) * D + piece * 8;
+          }
 #pragma unroll 1
           for (int c = 0; c < D / C::kOChunk; ++c) {
             uint32_t o[C::kOChunk];
@@ -1083,11 +1151,7 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
               for (int k = 0; k < 4; ++k) {
                 const int x = r0 + 8 * k;                    // row of this warp
                 const uint4 v = *reinterpret_cast<const uint4*>(turn + x * C::kTurnRow + piece * 16);
-                const int rr = quarter * 32 + x, tok = rr / p.group;
-                if (x < rows_here)
-                  *reinterpret_cast<uint4*>(
-                      p.out + (static_cast<long long>(w.q.start + token0 + tok) * p.h + w.at.hk * p.group +
-                               rr - tok * p.group) * D + c * 32 + piece * 8) = v;
+                if (x < rows_here) *reinterpret_cast<uint4*>(dst[k] + c * 32) = v;
               }
             }
           }
@@ -1099,7 +1163,7 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
       tc_fence_before();
       mbar_arrive(o_free);
       ++pieces;
-    } while (w.next(p));
+    }
     cp_async_wait<0>();                                      // (a wait may have run out above)
   }
 
