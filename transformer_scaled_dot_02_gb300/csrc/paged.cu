@@ -211,8 +211,11 @@ __device__ bool find_place(const PagedParams& p, ScheduleShared* sh, int c, int 
       mine.x += static_cast<long long>(walk) * p.h_kv;
       mine.y += (w.start + static_cast<long long>(w.tile) * walk) * p.h_kv;
     } else if (q.tiles > 0) {
-      mine.x += cost_before(p, q, q.tiles, true) * p.h_kv;
-      mine.y += cost_before(p, q, q.tiles, false) * p.h_kv;
+      const int f = q.tiles - 1;
+      const Weight w = weight_of(false, false);
+      const long long walk = tiles_before(p, q, f);
+      mine.x += (walk + walk_tiles(q.len)) * p.h_kv;
+      mine.y += (static_cast<long long>(w.start) * f + w.tile * walk + unit_cost(p, q, f, false)) * p.h_kv;
     }
   }
   longlong2 incl = mine;
@@ -273,16 +276,18 @@ __device__ bool find_place(const PagedParams& p, ScheduleShared* sh, int c, int 
     // warp does it for itself)
     const long long rem = sh->rem;
     int lo = 0, hi = seq->tiles;
+    long long before_lo = 0;
     while (hi - lo > 1) {
       const int step = (hi - lo + 31) / 32;
       const int probe = lo + lane * step;
-      const bool le = probe < hi && cost_before(p, *seq, probe, few) <= rem;
-      const int k = 31 - __clz(__ballot_sync(0xffffffffu, le));
+      const long long cost = probe < hi ? cost_before(p, *seq, probe, few) : rem + 1;
+      const int k = 31 - __clz(__ballot_sync(0xffffffffu, cost <= rem));
+      before_lo = __shfl_sync(0xffffffffu, cost, k);
       lo += k * step;
       hi = min(hi, lo + step);
     }
     at->r = lo;
-    at->item = rem - cost_before(p, *seq, lo, few) + 1;
+    at->item = rem - before_lo + 1;
   }
   return true;
 }
