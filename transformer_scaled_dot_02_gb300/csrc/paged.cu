@@ -40,6 +40,7 @@
 #include <atomic>
 #include <climits>
 #include <cmath>
+#include <type_traits>
 
 #include "kernels.h"
 #include "ptx.cuh"
@@ -892,26 +893,36 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
           if (!whole) ml_of(own)[row] = make_float2(mm, ll);
           xinv[row] = ll > 0.f ? 1.f / ll : 0.f;
         }
-        int cols = 16;
-        while (cols < D && 2 * cols * rows * 16 <= C::kXBytes) cols *= 2;
-        float4* lay = reinterpret_cast<float4*>(smem + C::kXOff);     // [quarter][cols / 4][rows]
+        // (at the end of the run the idle K and V stages serve, behind the place
+        // of the own piece)
+        const bool at_end = w.off <= 0;
+        float4* lay = reinterpret_cast<float4*>(at_end ? ring + piece_bytes : smem + C::kXOff);
+        const int room = at_end ? C::kMergeBytes - piece_bytes : C::kXBytes;
+        int cols = 16;                                       // lay: [quarter][cols / 4][rows]
+        while (cols < D && 2 * cols * rows * 16 <= room) cols *= 2;
 #pragma unroll 1
         for (int c0 = 0; c0 < D; c0 += cols) {
           if (c0 > 0 && !(ok = meet())) break;               // the columns before are summed
-#pragma unroll 1
-          for (int c = 0; c < cols; c += 16) {
-            uint32_t o[16];
+          auto lay_columns = [&](int c, auto width) {
+            constexpr int kWidth = decltype(width)::value;
+            uint32_t o[kWidth];
             __syncwarp();
             tmem_ld_chunk(lane_base + C::kOCol + c0 + c, o);
             tmem_ld_wait();
             reg_fence(o);
             if (valid) {
 #pragma unroll
-              for (int e = 0; e < 4; ++e)
+              for (int e = 0; e < kWidth / 4; ++e)
                 lay[(quarter * (cols / 4) + c / 4 + e) * rows + row] =
                     make_float4(__uint_as_float(o[e * 4]) * f, __uint_as_float(o[e * 4 + 1]) * f,
                                 __uint_as_float(o[e * 4 + 2]) * f, __uint_as_float(o[e * 4 + 3]) * f);
             }
+          };
+          if (cols == 16) {
+            lay_columns(0, std::integral_constant<int, 16>{});
+          } else {
+#pragma unroll 1
+            for (int c = 0; c < cols; c += 32) lay_columns(c, std::integral_constant<int, 32>{});
           }
           if (!(ok = meet())) break;
           const int items = rows * (cols / 4);
@@ -952,13 +963,13 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
               float4 acc = reinterpret_cast<float4*>(ring)[x];
               const float2 ml = ml_of(ring)[rw];
               float top = ml.x;
-#pragma unroll 4
+#pragma unroll 8
               for (int i = 1; i <= count; ++i) top = fmaxf(top, ml_of(ring + i * piece_bytes)[rw].x);
               const float base = top == -INFINITY ? 0.f : top;
               const float fo = weight(ml.x, base);
               float sum = ml.y * fo;
               acc.x *= fo; acc.y *= fo; acc.z *= fo; acc.w *= fo;
-#pragma unroll 4
+#pragma unroll 8
               for (int i = 1; i <= count; ++i) {
                 const float2 mi = ml_of(ring + i * piece_bytes)[rw];
                 const float4 v = reinterpret_cast<float4*>(ring + i * piece_bytes)[x];
@@ -1000,14 +1011,15 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
           if (busy) {
             float s[kBN];
             {
-              uint32_t sr[32];
+              uint32_t sr[kBN / 32][32];
+#pragma unroll
+              for (int c = 0; c < kBN / 32; ++c) tmem_ld32(lane_base + s_col + c * 32, sr[c]);
+              tmem_ld_wait();
 #pragma unroll
               for (int c = 0; c < kBN / 32; ++c) {
-                tmem_ld32(lane_base + s_col + c * 32, sr);
-                tmem_ld_wait();
-                reg_fence(sr);
+                reg_fence(sr[c]);
 #pragma unroll
-                for (int e = 0; e < 32; ++e) s[c * 32 + e] = __uint_as_float(sr[e]);
+                for (int e = 0; e < 32; ++e) s[c * 32 + e] = __uint_as_float(sr[c][e]);
               }
             }
             if (key0 + kBN - 1 > pos0) {
