@@ -141,6 +141,8 @@ struct PagedAppendParams {
   unsigned* status;
   long long q_stride, k_stride, v_stride;
   int b, n_tokens, h, h_kv, d, d_rot, interleaved;
+  int log_pairs;              // of d / 16
+  unsigned items_magic;       // ceil(2^32 / ((h + 2 h_kv) d / 16)), 0 if that is too large to divide by
   int page_shift, n_pages, pages_per_seq;
 };
 cudaError_t launch_sdpa_paged_append(const PagedAppendParams& p, cudaStream_t stream);
