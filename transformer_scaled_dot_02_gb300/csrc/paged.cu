@@ -91,10 +91,11 @@ __device__ __forceinline__ int walk_tiles(int keys) { return max(1, (keys + kBN 
 // the others.  Where there are few key tiles for each CTA (`few`), a single one
 // more counts for more than all that: then only key tiles are counted.
 struct Weight {
-  int start, tile;
+  int start, log_tile;
+  __device__ long long of(long long tiles) const { return start + (tiles << log_tile); }
 };
 __device__ __forceinline__ Weight weight_of(bool few, bool narrow) {
-  return few ? Weight{0, 1} : (narrow ? Weight{14, 4} : Weight{18, 4});
+  return few ? Weight{0, 0} : (narrow ? Weight{14, 2} : Weight{18, 2});
 }
 constexpr int kFewTiles = 8;
 
@@ -103,7 +104,7 @@ __device__ __forceinline__ int tile_rows(const PagedParams& p, const Seq& q, int
 }
 __device__ __forceinline__ long long unit_cost(const PagedParams& p, const Seq& q, int r, bool few) {
   const Weight w = weight_of(few, tile_rows(p, q, r) <= kNarrowRows);
-  return w.start + static_cast<long long>(w.tile) * walk_tiles(tile_keys(p, q, r));
+  return w.of(walk_tiles(tile_keys(p, q, r)));
 }
 
 // Key tiles of the first f row tiles, f < q.tiles.  They see A + (i + 1) t
@@ -151,7 +152,7 @@ __device__ __forceinline__ long long cost_before(const PagedParams& p, const Seq
   long long sum = 0;
   if (f > 0) {
     const Weight w = weight_of(few, false);
-    sum = static_cast<long long>(w.start) * f + w.tile * tiles_before(p, q, f);
+    sum = static_cast<long long>(w.start) * f + (tiles_before(p, q, f) << w.log_tile);
   }
   if (r == q.tiles && r > 0) sum += unit_cost(p, q, r - 1, few);
   return sum;
@@ -182,8 +183,9 @@ struct Cut {
   long long each, longer;                                    // longer: items in the longer runs
   int over;
   bool few;                                                  // how units are weighed
-  __device__ Cut(long long work, int ctas, bool few_tiles) : few(few_tiles) {
-    each = divide(work, ctas);
+  // `magic`: ceil(2^64 / max_ctas), for the usual number of runs
+  __device__ Cut(long long work, int ctas, int max_ctas, unsigned long long magic, bool few_tiles) : few(few_tiles) {
+    each = ctas == max_ctas && ctas > 1 ? static_cast<long long>(__umul64hi(work, magic)) : divide(work, ctas);
     over = static_cast<int>(work - each * ctas);
     longer = over * (each + 1);
   }
@@ -210,13 +212,13 @@ __device__ bool find_place(const PagedParams& p, ScheduleShared* sh, int c, int 
       const int walk = walk_tiles(q.len);
       const Weight w = weight_of(false, q.n * p.group <= kNarrowRows);
       mine.x += static_cast<long long>(walk) * p.h_kv;
-      mine.y += (w.start + static_cast<long long>(w.tile) * walk) * p.h_kv;
+      mine.y += w.of(walk) * p.h_kv;
     } else if (q.tiles > 0) {
       const int f = q.tiles - 1;
       const Weight w = weight_of(false, false);
       const long long walk = tiles_before(p, q, f);
       mine.x += (walk + walk_tiles(q.len)) * p.h_kv;
-      mine.y += (static_cast<long long>(w.start) * f + w.tile * walk + unit_cost(p, q, f, false)) * p.h_kv;
+      mine.y += (static_cast<long long>(w.start) * f + (walk << w.log_tile) + unit_cost(p, q, f, false)) * p.h_kv;
     }
   }
   longlong2 incl = mine;
@@ -246,7 +248,7 @@ __device__ bool find_place(const PagedParams& p, ScheduleShared* sh, int c, int 
   const int n = static_cast<int>(min(static_cast<long long>(max_ctas), sum.x));
   if (c >= n) return false;
   const long long total = few ? sum.x : sum.y, own = few ? mine.x : mine.y, excl = few ? before.x : before.y;
-  *cut = Cut(total, n, few);
+  *cut = Cut(total, n, max_ctas, p.ctas_magic, few);
   const long long x = cut->begin(c + 1) - 1;                 // its last item
   if (own > 0 && excl <= x && x < excl + own) {
     long long rem = x - excl;
@@ -306,7 +308,7 @@ struct Walk {
 
   // Key tiles that lie before item x of the unit.
   __device__ __forceinline__ int tiles_at(long long x) const {
-    return x <= w.start ? 0 : static_cast<int>(divide(x - w.start, w.tile));
+    return x <= w.start ? 0 : static_cast<int>((x - w.start) >> w.log_tile);
   }
   __device__ __forceinline__ void load(const PagedParams& p) {
     keys = tile_keys(p, q, r);
@@ -340,7 +342,7 @@ struct Walk {
       r = q.tiles - 1;
     }
     load(p);
-    off -= w.start + static_cast<long long>(w.tile) * cost;
+    off -= w.of(cost);
     kt0 = tiles_at(-off);
     kt1 = cost;
     return true;
@@ -494,7 +496,7 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
   griddep_launch_dependents();
   griddep_wait();
 
-  Cut cut(0, 1, true);
+  Cut cut(0, 1, 0, 0, true);
   Place last;
   Seq last_seq;
   const int cta = static_cast<int>(blockIdx.x);
@@ -747,7 +749,7 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
       if (!whole) {
         // the pieces that this one merges, in the order of the list
         // (the first key tile's last item says which run it belongs to)
-        const int c0 = cut.run_of(cut.begin(cta) + w.off + w.w.start + w.w.tile - 1), j = cta - c0, bits = narrow ? kNarrowBits : kWideBits;
+        const int c0 = cut.run_of(cut.begin(cta) + w.off + w.w.of(1) - 1), j = cta - c0, bits = narrow ? kNarrowBits : kWideBits;
         const int low = open_above ? j + 1 - block_size(j, bits) : 0;
         for (int at = j; at > low; at -= block_size(at - 1, bits)) {
           if (threadIdx.x == 0) source_runs[sources] = c0 + at - 1;
