@@ -296,9 +296,11 @@ sdpa_status sdpa_paged_append(const void* q, const void* k, const void* v, void*
  *       rows are zero for a token at a negative position
  *   workspace: device buffer of ws_bytes >= sdpa_paged_workspace_size(...)
  *       (may be NULL when that size is 0), 16-byte aligned, caller-owned and
- *       reusable once the stream passes the call.  Calls that overlap on the
- *       GPU need one each.  The size depends on the current device's SM
- *       count: ask on the device the call runs on.
+ *       reusable once the stream passes the call, whatever it holds.  Calls
+ *       that overlap on the GPU (two captured graphs among them) need one
+ *       each.  The size depends on the current device's SM count: ask on the
+ *       device the call runs on.  After SDPA_ERR_DEVICE_TIMEOUT, clear it before
+ *       a captured call uses it again.
  * Scores, softmax statistics and sums are fp32; the softmax weights enter the
  * products with the values rounded to bf16.  Cache rows past a sequence's
  * length may hold anything; those below it must be finite.

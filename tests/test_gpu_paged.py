@@ -86,11 +86,46 @@ def test_attention_head_groups(d, h, h_kv):
     (64, 4, 4, [1, 1, 1, 1], [5000, 3, 9000, 64]),
     (128, 4, 1, [96, 1], [4000, 7000]),                          # rows of several tiles, each cut
     (256, 2, 1, [3], [12000]),
+    (128, 32, 1, [1], [20000]),                                  # pieces that come in a few at a time
+    (256, 16, 1, [2, 1], [9000, 5000]),
+    (64, 33, 1, [1, 1], [9000, 4100]),                           # groups wider than a quarter tile
+    (16, 8, 2, [4], [30000]),
     (32, 3, 1, [200], [3000])])
 def test_attention_split_walks(d, h, h_kv, new, lens):
     rng = np.random.default_rng(400 + d + h)
     case = _case(rng, new, lens, h, h_kv, d, 64)
     _check(_run(*case), *case)
+
+
+def test_attention_uneven_walks_fill_every_run():
+    """A prompt's walks from one key tile to many, among single tokens over
+    long caches: units are cut by what they are expected to take."""
+    rng = np.random.default_rng(512)
+    new = [700] + [1] * 12 + [90]
+    lens = [700] + [int(x) for x in rng.integers(1500, 6000, size=12)] + [2500]
+    case = _case(rng, new, lens, 16, 4, 64, 64)
+    _check(_run(*case), *case)
+
+
+def test_attention_one_workspace_for_calls_of_all_shapes():
+    """A workspace that holds other calls' leftovers, or anything."""
+    import torch
+    rng = np.random.default_rng(513)
+    cases = [_case(rng, new, lens, h, h_kv, d, 32) for new, lens, h, h_kv, d in
+             (([1], [4000], 8, 1, 128), ([40, 1], [300, 5000], 4, 2, 64), ([3], [9000], 2, 2, 256),
+              ([130], [900], 6, 2, 32))]
+    ready = []
+    for cache, dense, starts, q in cases:
+        kp, vp = (dev(cache.pages_of(x, np.nan)) for x in dense)
+        args = (dev(q), kp, vp, dev_int(cache.table), dev_int(starts), dev_int(cache.lens))
+        ready.append((args, sd.paged_attention(*args)))
+    size = max(sd.paged_workspace(a[0], a[1], a[3]).numel() for a, _ in ready)
+    for fill in (0x00, 0xff, 0x7f):
+        ws = torch.full((size,), fill, dtype=torch.uint8, device="cuda")
+        for _ in range(3):
+            for args, want in ready:
+                assert torch.equal(_raw(sd.paged_attention(*args, workspace=ws)), _raw(want))
+    sd.sdpa_device_check()
 
 
 def test_attention_many_sequences():

@@ -22,8 +22,8 @@
 // workspace; if it begins inside a unit, that piece comes last, and the CTA
 // merges the pieces that the runs before it published:
 //   O = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s, M = max_s m_s.
-// So a CTA waits for CTAs of lower index only, which were dispatched before
-// it: there is no order of execution in which the waits do not end.  Units cut
+// So a CTA waits for CTAs of lower index only, which are dispatched before it:
+// the waits end however few CTAs run at a time.  Units cut
 // into many pieces are merged as a tree.  The pieces merge in an order fixed
 // by the cut, so results repeat bit by bit.
 //
@@ -83,13 +83,14 @@ __device__ __forceinline__ int tile_keys(const PagedParams& p, const Seq& q, int
 }
 __device__ __forceinline__ int walk_tiles(int keys) { return max(1, (keys + kBN - 1) / kBN); }
 
-// What a unit is expected to take: `start` (loading Q, storing O) and `tile`
-// for each key tile.  In quarters of a wide tile's key tile: measured on GB300
-// with two CTAs per SM at d = 128, a wide key tile takes 0.88 us and the ends
-// of a walk 1.9 us; at d = 64 a narrow key tile takes two thirds of a wide one.
-// Without the ends, the CTAs with a prompt's shortest walks finished 20 % after
-// the others.  Where there are few key tiles for each CTA (`few`), a single one
-// more counts for more than all that: then only key tiles are counted.
+// What a unit is expected to take: `start` (loading Q, storing O) and 2^log_tile
+// for each key tile, in quarters of a key tile.  From least squares over the
+// CTAs' times on GB300: two prompts of 8192 tokens (16 heads of 128) take 4.4 us
+// a walk and 0.94 us a wide key tile, 16 x 4 drafted tokens (64 wide) 2.4 us
+// and 0.67 us a narrow one.  Counting key tiles alone, the CTAs with a prompt's
+// shortest walks finished 20 % after the others (514 us instead of 396).  Where
+// there are few key tiles for each CTA (`few`), a single one more counts for
+// more than all that: then only key tiles are counted.
 struct Weight {
   int start, log_tile;
   __device__ long long of(long long tiles) const { return start + (tiles << log_tile); }
@@ -372,15 +373,18 @@ __device__ __forceinline__ int block_size(int j, int bits) {
   return 1 << ((__ffs(j + 1) - 1) / bits * bits);
 }
 
-// Waits until the flag is this call's number, and clears it.
-__device__ __forceinline__ bool take_flag(unsigned long long* flag, unsigned long long call, const AbortState& ab) {
+// Waits until the flag is this call's number, and clears it.  `limit`: clock
+// cycles; runs take about equally long, and a run's items well below 4096
+// cycles each, so it grows by that with the run.
+__device__ __forceinline__ bool take_flag(unsigned long long* flag, unsigned long long call, long long limit,
+                                          const AbortState& ab) {
   const long long t0 = clock64();
   while (true) {
     unsigned long long v;
     asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(flag) : "memory");
     if (v == call) break;
     if (*ab.flag) return false;
-    if (clock64() - t0 > kWaitLimitCycles) {
+    if (clock64() - t0 > limit) {
       *ab.flag = 1;
       atomicOr(ab.status, kStatusTimeout);
       return false;
@@ -779,7 +783,7 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
         if (!meet()) return false;                           // the list is there
         bool got = true;
         if (static_cast<int>(threadIdx.x) < sources)
-          got = take_flag(p.flags + source_runs[threadIdx.x], p.call, ab);
+          got = take_flag(p.flags + source_runs[threadIdx.x], p.call, kWaitLimitCycles + 4096 * run, ab);
         return __all_sync(0xffffffffu, got) && meet();
       };
       // O columns [c kOChunk, +kOChunk) of this row, normalised into the output
@@ -1271,7 +1275,7 @@ __device__ int find_seq(const PagedAppendParams& p, int t, int lane) {
 template <int kTokens, int kAhead, int kBlocks>
 __global__ void __launch_bounds__(kAppendThreads, kBlocks) sdpa_paged_append_kernel(const PagedAppendParams p) {
   static_assert(kTokens <= kAppendThreads / 32, "a warp finds each token's place");
-  extern __shared__ float2 angles[];                          // [kTokens][d_rot / 2]
+  extern __shared__ __align__(16) float2 angles[];            // [kTokens][d_rot / 2]
   __shared__ long long row_of[kTokens];                       // page row of the token, head 0 (-1: not stored)
   __shared__ int pos_of[kTokens];                             // position (INT_MIN: no sequence's token)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
