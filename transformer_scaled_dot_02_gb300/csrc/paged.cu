@@ -416,6 +416,11 @@ struct PCfg {
   static constexpr int kKVBytes = kBoxes * kKVBox;           // one tile of K or of V
   // K and V stages: what fits next to Q with two CTAs per SM (one at d = 256)
   static constexpr int kRing = D >= 128 ? 2 : 4;
+  // With four stages K and V of a tile come together, on one barrier (k_full),
+  // and are free together: the producer's wait and its announcement of the
+  // bytes take as long as the copies of a small tile.  With two, K's stage is
+  // worth having back before V's.
+  static constexpr bool kJoint = kRing >= 4;
   static constexpr int kKOff = kQBytes;
   static constexpr int kVOff = kKOff + kRing * kKVBytes;
   // O columns of a tensor-memory load
@@ -521,8 +526,11 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
     const int box_shift = min(p.page_shift, kBNShift);
     const int box_rows = 1 << box_shift, tile_parts = kBN >> box_shift;
     const int row_mask = (1 << p.page_shift) - 1;
-    const int part = tile_parts == 1 ? 0 : lane / C::kBoxes, col = tile_parts == 1 ? 0 : lane % C::kBoxes;
-    const bool copies = tile_parts == 1 ? lane == 0 : part < tile_parts;
+    // (together: lanes 0 - 7 copy K, lanes 8 - 15 V)
+    static_assert(!C::kJoint || C::kBoxes * (kBN / kPagedMinPage) <= 8, "lanes");
+    const int lane_kv = C::kJoint ? lane & 7 : lane;
+    const int part = tile_parts == 1 ? 0 : lane_kv / C::kBoxes, col = tile_parts == 1 ? 0 : lane_kv % C::kBoxes;
+    const bool copies = (tile_parts == 1 ? lane_kv == 0 : part < tile_parts) && (!C::kJoint || lane < 16);
     const uint32_t dst = static_cast<uint32_t>(col * C::kKVBox + (part << box_shift) * C::kRowBytes);
     if (lane == 0) {
       tma_prefetch_desc(&p.tm_q);
@@ -545,7 +553,9 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
       auto load = [&](const CUtensorMap* map, uint64_t* bar, uint8_t* stage, int i, int page) {
         const int key = (kt0 + i) * kBN;
         const int parts = min(tile_parts, (w.q.len - key + box_rows - 1) >> box_shift);
-        if (lane == 0) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(parts << box_shift) * (C::kRowBytes * C::kBoxes));
+        if (lane == 0)
+          mbar_arrive_expect_tx(bar, static_cast<uint32_t>(parts << box_shift) *
+                                         (C::kRowBytes * C::kBoxes * (C::kJoint ? 2 : 1)));
         __syncwarp();
         if (holds(i)) {
           // page numbers outside the cache read as zeros and are reported
@@ -559,8 +569,10 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
       int page_v = page_of(0), page_k = page_v, page_n = page_of(1);
       auto load_k = [&](int i) -> bool {
         const int u = u0 + i, s = u % R;
-        if (u >= R && !mbar_wait_warp(s_full + s, static_cast<uint32_t>(u / R - 1) & 1u, ab)) return false;
-        load(&p.tm_k, k_full + s, smem + C::kKOff + s * C::kKVBytes, i, page_k);
+        if (u >= R && !mbar_wait_warp((C::kJoint ? o_full : s_full) + s, static_cast<uint32_t>(u / R - 1) & 1u, ab))
+          return false;
+        const bool v = C::kJoint && lane >= 8;
+        load(v ? &p.tm_v : &p.tm_k, k_full + s, smem + (v ? C::kVOff : C::kKOff) + s * C::kKVBytes, i, page_k);
         k_issued = u + 1;
         return true;
       };
@@ -586,6 +598,7 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
         page_k = page_n;
         page_n = page_of(i + 2);
         if (i + 1 < n && !(go = load_k(i + 1))) break;
+        if constexpr (C::kJoint) continue;
         const int u = u0 + i, s = u % R;
         if (u >= R && !(go = mbar_wait_warp(o_full + s, static_cast<uint32_t>(u / R - 1) & 1u, ab))) break;
         load(&p.tm_v, v_full + s, smem + C::kVOff + s * C::kKVBytes, i, page_v);
@@ -656,7 +669,7 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
             !(ok = mbar_wait_warp(o_free, static_cast<uint32_t>(pieces - 1) & 1u, ab)))
           break;
         ok = mbar_wait_warp(p_full + (u & 1), static_cast<uint32_t>(u >> 1) & 1u, ab) &&
-             mbar_wait_warp(v_full + u % R, static_cast<uint32_t>(u / R) & 1u, ab);
+             (C::kJoint || mbar_wait_warp(v_full + u % R, static_cast<uint32_t>(u / R) & 1u, ab));
         if (!ok) break;
         tc_fence_after();
         issue_pv(u, i > 0);
@@ -684,7 +697,7 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
     // NaN, so they are cleared.  (All four warps, before P is handed over.)
     auto clear_tail = [&](int key0) -> bool {
       if (key0 + kBN <= w.q.len) return true;
-      if (!mbar_wait_warp(v_full + u % R, static_cast<uint32_t>(u / R) & 1u, ab)) return false;
+      if (!mbar_wait_warp((C::kJoint ? k_full : v_full) + u % R, static_cast<uint32_t>(u / R) & 1u, ab)) return false;
       uint8_t* v = smem + C::kVOff + (u % R) * C::kKVBytes;
       const int keep = w.q.len - key0;                       // in [1, kBN)
       constexpr int kPerRow = C::kRowBytes / 16;
