@@ -99,6 +99,14 @@ __device__ __forceinline__ Weight weight_of(bool few, bool narrow) {
   return few ? Weight{0, 0} : (narrow ? Weight{14, 2} : Weight{18, 2});
 }
 constexpr int kFewTiles = 8;
+// Where there are few, a piece of up to 8 KB may be a single key tile, a larger
+// one has at least eight, one over 32 KB twelve: a further cut by four saves
+// three quarters of its key tiles' time (0.5 to 0.9 us each) and costs a level
+// more of merging (4 to 9 us).  Over 8192 positions of 4 key-value heads, 32 new
+// tokens of 16 heads (64 KB pieces) take 24 us so, 43 with single key tiles; 200
+// tokens of 128 take 32 and 36.
+constexpr int kSmallPiece = 8 << 10, kMiddlePiece = 32 << 10;
+constexpr int kMiddlePieceTiles = 8, kLargePieceTiles = 12;
 
 __device__ __forceinline__ int tile_rows(const PagedParams& p, const Seq& q, int r) {
   return min(p.tile_tokens, q.n - r * p.tile_tokens) * p.group;
@@ -166,8 +174,19 @@ struct Place {
   long long item;
 };
 
+// What there is to do: key tiles, the pieces that they may be cut into, and the
+// units' weights.
+struct Work {
+  long long tiles, pieces, cost;
+  __device__ void add(const Work& o) {
+    tiles += o.tiles;
+    pieces += o.pieces;
+    cost += o.cost;
+  }
+};
+
 struct ScheduleShared {
-  longlong2 warp_sum[kThreads / 32];
+  Work warp_sum[kThreads / 32];
   long long rem;
   Place at;
   Seq q;
@@ -199,56 +218,56 @@ struct Cut {
 
 // The whole block: how the work is cut, and the place where run c ends.
 // Returns false (everywhere) when there is no such run.
+template <int D>
 __device__ bool find_place(const PagedParams& p, ScheduleShared* sh, int c, int max_ctas, Cut* cut,
                            Place* at, Seq* seq) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int per = (p.b + kThreads - 1) / kThreads;
   const int s0 = min(tid * per, p.b), s1 = min(s0 + per, p.b);
-  // both ways of weighing, x: key tiles alone
-  longlong2 mine = make_longlong2(0, 0);
+  Work mine = {0, 0, 0};
   Seq q;
   for (int s = s0; s < s1; ++s) {
     q = load_seq(p, s);
-    if (q.tiles == 1) {
-      const int walk = walk_tiles(q.len);
-      const Weight w = weight_of(false, q.n * p.group <= kNarrowRows);
-      mine.x += static_cast<long long>(walk) * p.h_kv;
-      mine.y += w.of(walk) * p.h_kv;
-    } else if (q.tiles > 0) {
-      const int f = q.tiles - 1;
+    if (q.tiles == 0) continue;
+    const int f = q.tiles - 1;                               // full tiles, the last one aside
+    long long walk = walk_tiles(q.len);
+    long long cost = weight_of(false, tile_rows(p, q, f) <= kNarrowRows).of(walk);
+    if (f > 0) {
       const Weight w = weight_of(false, false);
-      const long long walk = tiles_before(p, q, f);
-      mine.x += (walk + walk_tiles(q.len)) * p.h_kv;
-      mine.y += (static_cast<long long>(w.start) * f + (walk << w.log_tile) + unit_cost(p, q, f, false)) * p.h_kv;
+      const long long full = tiles_before(p, q, f);
+      walk += full;
+      cost += static_cast<long long>(w.start) * f + (full << w.log_tile);
     }
+    walk *= p.h_kv;
+    mine.tiles += walk;
+    mine.cost += cost * p.h_kv;
+    const int bytes = min(p.tile_tokens, q.n) * p.group * D * 4;
+    mine.pieces += bytes <= kSmallPiece ? walk
+                   : bytes <= kMiddlePiece ? (walk + kMiddlePieceTiles - 1) / kMiddlePieceTiles
+                                           : (walk + kLargePieceTiles - 1) / kLargePieceTiles;
   }
-  longlong2 incl = mine;
+  Work incl = mine;
 #pragma unroll
   for (int x = 1; x < 32; x <<= 1) {
-    const long long ox = __shfl_up_sync(0xffffffffu, incl.x, x), oy = __shfl_up_sync(0xffffffffu, incl.y, x);
-    if (lane >= x) {
-      incl.x += ox;
-      incl.y += oy;
-    }
+    const Work o = {__shfl_up_sync(0xffffffffu, incl.tiles, x), __shfl_up_sync(0xffffffffu, incl.pieces, x),
+                    __shfl_up_sync(0xffffffffu, incl.cost, x)};
+    if (lane >= x) incl.add(o);
   }
   if (lane == 31) sh->warp_sum[warp] = incl;
   __syncthreads();
-  longlong2 sum = make_longlong2(0, 0), before = make_longlong2(incl.x - mine.x, incl.y - mine.y);
+  Work sum = {0, 0, 0}, before = {incl.tiles - mine.tiles, 0, incl.cost - mine.cost};
 #pragma unroll
   for (int w = 0; w < kThreads / 32; ++w) {
-    const longlong2 v = sh->warp_sum[w];
-    if (w < warp) {
-      before.x += v.x;
-      before.y += v.y;
-    }
-    sum.x += v.x;
-    sum.y += v.y;
+    const Work v = sh->warp_sum[w];
+    if (w < warp) before.add(v);
+    sum.add(v);
   }
   // (a run is never shorter than a key tile, so no run inside a unit is empty)
-  const bool few = sum.x < 1ll * kFewTiles * max_ctas;
-  const int n = static_cast<int>(min(static_cast<long long>(max_ctas), sum.x));
+  const bool few = sum.tiles < 1ll * kFewTiles * max_ctas;
+  const int n = static_cast<int>(min(static_cast<long long>(max_ctas), few ? sum.pieces : sum.tiles));
   if (c >= n) return false;
-  const long long total = few ? sum.x : sum.y, own = few ? mine.x : mine.y, excl = few ? before.x : before.y;
+  const long long total = few ? sum.tiles : sum.cost, own = few ? mine.tiles : mine.cost,
+                  excl = few ? before.tiles : before.cost;
   *cut = Cut(total, n, max_ctas, p.ctas_magic, few);
   const long long x = cut->begin(c + 1) - 1;                 // its last item
   if (own > 0 && excl <= x && x < excl + own) {
@@ -363,10 +382,16 @@ struct Walk {
 // before it publishes, piece j merges the size(j) - 1 pieces below it, size(j)
 // the largest power of R that divides j + 1; the last piece merges all.  What
 // a piece reads are the tops of the blocks that make up its range.  Reading
-// R - 1 pieces a level costs R - 1 pieces' bytes on one SM, a level costs a
-// wait: narrow pieces (a few KB) take R = 16, wide ones (up to 128 KB) R = 8.
-constexpr int kNarrowBits = 4, kWideBits = 3;
-constexpr int kMaxSources = 48;            // 15 a level: 3 levels for up to 2^12 runs
+// R - 1 pieces a level costs R - 1 pieces' bytes on one SM (64 KB take about a
+// microsecond), a level costs a wait of two: pieces of up to 8 KB take R = 16,
+// larger ones (128 rows of 256: 128 KB) R = 4.  Pieces that make up little (a
+// narrow tile's come in a few at a time, so less) are merged by the last at once.
+__device__ __forceinline__ int radix_bits(int pieces, int bytes, bool narrow) {
+  const int at_once = narrow ? 128 << 10 : 512 << 10;
+  if (pieces <= 1 << 5 && (pieces - 1) * bytes <= at_once) return 5;
+  return bytes <= kSmallPiece ? 4 : 2;
+}
+constexpr int kMaxSources = 48;            // 31 at once, or 15 a level of three for up to 2^12 runs
 static_assert(kPagedMaxRuns <= 1 << 12, "sources");
 
 __device__ __forceinline__ int block_size(int j, int bits) {
@@ -510,7 +535,7 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
   Seq last_seq;
   const int cta = static_cast<int>(blockIdx.x);
   // (its barriers also stand between the set-up above and the roles below)
-  const bool any = find_place(p, &sched, cta, static_cast<int>(gridDim.x), &cut, &last, &last_seq);
+  const bool any = find_place<D>(p, &sched, cta, static_cast<int>(gridDim.x), &cut, &last, &last_seq);
   const long long run = any ? cut.begin(cta + 1) - cut.begin(cta) : 0;
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
@@ -766,7 +791,9 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
       if (!whole) {
         // the pieces that this one merges, in the order of the list
         // (the first key tile's last item says which run it belongs to)
-        const int c0 = cut.run_of(cut.begin(cta) + w.off + w.w.of(1) - 1), j = cta - c0, bits = narrow ? kNarrowBits : kWideBits;
+        const long long unit = cut.begin(cta) + w.off;
+        const int c0 = cut.run_of(unit + w.w.of(1) - 1), j = cta - c0;
+        const int bits = radix_bits(cut.run_of(unit + w.w.of(w.cost) - 1) - c0 + 1, rows * D * 4, narrow);
         const int low = open_above ? j + 1 - block_size(j, bits) : 0;
         for (int at = j; at > low; at -= block_size(at - 1, bits)) {
           if (threadIdx.x == 0) source_runs[sources] = c0 + at - 1;
