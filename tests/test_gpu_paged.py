@@ -89,6 +89,8 @@ def test_attention_head_groups(d, h, h_kv):
     (128, 32, 1, [1], [20000]),                                  # pieces that come in a few at a time
     (256, 16, 1, [2, 1], [9000, 5000]),
     (64, 33, 1, [1, 1], [9000, 4100]),                           # groups wider than a quarter tile
+    (128, 16, 1, [1], [20000]),
+    (256, 16, 1, [1, 1], [12000, 3000]),
     (16, 8, 2, [4], [30000]),
     (32, 3, 1, [200], [3000])])
 def test_attention_split_walks(d, h, h_kv, new, lens):

@@ -883,7 +883,7 @@ sdpa_status sdpa_paged_forward(const void* q, const void* k_pages, const void* v
   p.tile_tokens = 128 / p.group;
   if (!make_map_rows(&p.tm_q, q, d, h, n_tokens, q_stride, p.group, p.tile_tokens) ||
       !make_map_rows(&p.tm_q_narrow, q, d, h, n_tokens, q_stride, p.group,
-                     p.group <= 32 ? 32 / p.group : p.tile_tokens) ||
+                     p.group <= 16 ? 16 / p.group : p.tile_tokens) ||
       !make_map_pages(&p.tm_k, k_pages, d, page_size, h_kv, n_pages) ||
       !make_map_pages(&p.tm_v, v_pages, d, page_size, h_kv, n_pages))
     return SDPA_ERR_CUDA;

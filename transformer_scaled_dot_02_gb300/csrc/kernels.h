@@ -105,7 +105,7 @@ cudaError_t launch_sdpa_decode(const DecodeParams& p, int d_k, int d_v, cudaStre
 // Attention of packed new tokens over a paged cache (csrc/paged.cu).
 struct PagedParams {
   CUtensorMap tm_q;           // 3-D (d, h, n_tokens) map, boxes of min(d, 64) x group x tile_tokens
-  CUtensorMap tm_q_narrow;    // the same with boxes of 32 / group tokens (tm_q for groups over 32)
+  CUtensorMap tm_q_narrow;    // the same with boxes of 16 / group tokens (tm_q for groups over 16)
   CUtensorMap tm_k, tm_v;     // 5-D (64 columns, page rows, d / 64, h_kv, n_pages) maps; boxes of
                               // kPagedKeyTile rows of every column block, or of a smaller page's
                               // rows of one

@@ -27,9 +27,9 @@
 // into many pieces are merged as a tree.  The pieces merge in an order fixed
 // by the cut, so results repeat bit by bit.
 //
-// Row tiles of at most 32 rows (single tokens) would leave three of the four
-// softmax warps idle and one with the whole row: their queries are copied to
-// all four quarters of the tile instead, each warp takes 16 of a tile's 64
+// Row tiles of at most 16 rows (single tokens) would leave three of the four
+// softmax warps idle and one with the whole row: they are NARROW, their queries
+// are copied to all four quarters of the tile, each warp takes 16 of a tile's 64
 // keys, and the quarters' (O, m, l) are merged when the piece ends.
 //
 // The roles of a split CTA are those of the one-tile forward kernel (TMA
@@ -55,7 +55,12 @@ static_assert(kBN == 1 << kBNShift, "key tile");
 constexpr int kThreads = 192;
 constexpr int kProducerWarp = 4;
 constexpr int kMmaWarp = 5;
-constexpr int kNarrowRows = 32;            // rows of a tile that every softmax warp holds
+constexpr int kQuarter = 32;               // rows (tensor-memory lanes) of a softmax warp
+// Rows of a tile that all four softmax warps hold, at most.  One walk of 16384
+// positions, 4 key-value heads of 128, takes 18 / 21 / 28 us with 4 / 8 / 16 rows
+// so and 39 with a warp for them; with 24 and 32 rows both take 36, and 128
+// sequences of 200 to 1000 positions 41 and 44 us against 37.
+constexpr int kNarrowRows = 16;
 constexpr int kQuarterKeys = kBN / 4;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units, as in the other forward kernels
 
@@ -451,19 +456,19 @@ struct PCfg {
   // O columns of a tensor-memory load
   static constexpr int kOChunk = D < 32 ? D : 32;
   // Exchange memory: a narrow tile's quarters lay their rows here to be summed
-  // (16 columns of 32 rows at least), a wide tile's warps turn theirs, 64 bytes
+  // (16 columns of 16 rows at least), a wide tile's warps turn theirs, 64 bytes
   // of each at a time (rows padded by 16).
   static constexpr int kXOff = kVOff + kRing * kKVBytes;
-  static constexpr int kXBytes = 4 * kNarrowRows * 16 * 4 > 12288 ? 4 * kNarrowRows * 16 * 4 : 12288;
   static constexpr int kTurnRow = 64 + 16;
   static constexpr int kTurnSlot = 32 * kTurnRow;
-  static_assert(4 * kTurnSlot <= kXBytes, "turning rows");
+  static constexpr int kXBytes = 4 * kTurnSlot;
+  static_assert(4 * kNarrowRows * 16 * 4 <= kXBytes, "quarters");
   static constexpr int kXmlOff = kXOff + kXBytes;            // the quarters' (m, l)
   // merging: the idle K and V stages hold a wide piece's O, or with the exchange
   // memory behind them a narrow tile's own piece and at least one more
   static constexpr int kMergeBytes = 2 * kRing * kKVBytes + kXBytes;
   static_assert(2 * kRing * kKVBytes >= kBlockM * D * 4 && kMergeBytes >= 2 * kNarrowRows * (D * 4 + 8), "pieces");
-  static constexpr int kXinvOff = kXmlOff + 4 * kNarrowRows * 8;   // 1 / l of their sum
+  static constexpr int kXinvOff = kXmlOff + 4 * kQuarter * 8;   // 1 / l of their sum
   static constexpr int kBarOff = kXinvOff + kNarrowRows * 4;
   // q_full, q_empty, k_full[R], v_full[R], s_full[R], o_full[R], p_full[2], o_last, o_free,
   // merge, drain
@@ -607,14 +612,14 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
       {
         // lane c * 4 + y: column box c, for a narrow tile into quarter y
         const bool narrow = w.rows <= kNarrowRows;
-        const int rows = (narrow ? kNarrowRows / p.group : p.tile_tokens) * p.group;
+        const int rows = (narrow ? kNarrowRows / p.group : p.tile_tokens) * p.group;   // of the box
         if (lane == 0)
           mbar_arrive_expect_tx(q_full, static_cast<uint32_t>((narrow ? 4 : 1) * rows * C::kRowBytes * C::kBoxes));
         __syncwarp();
         const int c = lane >> 2, y = lane & 3;
         if (c < C::kBoxes && (narrow || y == 0))
           tma_load_3d(narrow ? &p.tm_q_narrow : &p.tm_q, q_full,
-                      smem + c * C::kQBox + y * kNarrowRows * C::kRowBytes, c * C::kBoxCols,
+                      smem + c * C::kQBox + y * kQuarter * C::kRowBytes, c * C::kBoxCols,
                       w.hk * p.group, w.q.start + w.r * p.tile_tokens);
       }
       ++pieces;
@@ -921,15 +926,15 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
         // as the exchange memory holds of the rows there are
         float2* xml = reinterpret_cast<float2*>(smem + C::kXmlOff);
         float* xinv = reinterpret_cast<float*>(smem + C::kXinvOff);
-        xml[quarter * kNarrowRows + lane] = make_float2(m_used, l);
+        xml[quarter * kQuarter + lane] = make_float2(m_used, l);
         if (!(ok = meet())) break;
         float mm = m_used, ll = 0.f;
 #pragma unroll
-        for (int y = 0; y < 4; ++y) mm = fmaxf(mm, xml[y * kNarrowRows + lane].x);
+        for (int y = 0; y < 4; ++y) mm = fmaxf(mm, xml[y * kQuarter + lane].x);
         const float sub = mm == -INFINITY ? 0.f : mm;
 #pragma unroll
         for (int y = 0; y < 4; ++y) {
-          const float2 ml = xml[y * kNarrowRows + lane];
+          const float2 ml = xml[y * kQuarter + lane];
           ll += ml.y * weight(ml.x, sub);
         }
         const float f = weight(m_used, sub);
