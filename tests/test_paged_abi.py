@@ -137,20 +137,40 @@ def test_workspace_size_follows_the_shapes(lib):
     assert size(1, 1, 8, 1, 128, 64, 2048) <= 2 * 152 * 8 * 130 * 4 + (1 << 18)
 
 
-@pytest.mark.skipif(_gpu_visible(), reason="needs a machine without a GPU")
-def test_helpers_refuse_what_the_library_cannot_see(lib):
-    """Wrong types, shapes and devices: tensors on the CPU are refused here
-    before the library is asked."""
-    torch = pytest.importorskip("torch")
-    q = torch.zeros(1, 2, 64, dtype=torch.bfloat16)
+def _cpu_tensors(torch):
+    rows = torch.zeros(1, 2, 64, dtype=torch.bfloat16)
     pages = torch.zeros(4, 2, 16, 64, dtype=torch.bfloat16)
     table, ints = torch.zeros(1, 2, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
-    try:
-        torch.cuda.current_device()
-    except Exception:
-        pytest.skip("torch has no current CUDA device here")
+    return rows, pages, table, ints
+
+
+def test_helpers_refuse_what_the_library_cannot_see(lib):
+    """Tensors on the CPU are refused before the library is asked."""
+    torch = pytest.importorskip("torch")
+    rows, pages, table, ints = _cpu_tensors(torch)
     with pytest.raises(sd.SdpaError):
-        sd.paged_attention(q, pages, pages, table, ints, ints[:1])
+        sd.paged_attention(rows, pages, pages, table, ints, ints[:1], workspace=ints)
+    with pytest.raises(sd.SdpaError):
+        sd.paged_append(rows, rows, rows, pages, pages, table, ints, ints[:1])
+    with pytest.raises(sd.SdpaError):
+        sd.paged_append(None, rows, rows, pages, pages, table, ints, ints[:1])
+
+
+def test_helpers_refuse_what_is_no_tensor(lib):
+    torch = pytest.importorskip("torch")
+    rows, pages, table, ints = _cpu_tensors(torch)
+    for at in range(1, 6):
+        args = [rows, pages, pages, table, ints, ints[:1]]
+        args[at] = None if at != 3 else 7
+        with pytest.raises((TypeError, AttributeError)):
+            sd.paged_attention(*args, workspace=ints)
+    for at in range(1, 8):
+        args = [rows, rows, rows, pages, pages, table, ints, ints[:1]]
+        args[at] = None if at != 3 else A
+        with pytest.raises(TypeError):
+            sd.paged_append(*args)
+    with pytest.raises(TypeError):
+        sd.paged_attention(rows, pages, pages, table, ints, ints[:1], scale="1", workspace=ints)
 
 
 def _bf16(rng, shape):

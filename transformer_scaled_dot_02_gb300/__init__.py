@@ -5,10 +5,12 @@ The functions below carry the names of the C entry points in include/sdpa.h
 and only marshal arguments: every step of the computation runs in the CUDA
 kernels of libsdpa.so.  Tensor arguments may be torch tensors (their
 ``data_ptr()`` is passed) or raw device addresses as ints.  ``stream`` defaults
-to PyTorch's current CUDA stream.
+to PyTorch's current CUDA stream.  The paged helpers check and pass their
+tensors through a small extension, _bind.so (csrc/bind.cpp): a call takes 3 us
+so, 10 us in Python and ctypes.
 
-There is no fallback: if libsdpa.so is missing or fails to load, importing the
-functions raises, and every call returns the library's status as an exception.
+There is no fallback: if libsdpa.so (or, for the paged helpers, _bind.so) is
+missing or fails to load, importing the functions raises, and every call returns the library's status as an exception.
 
 The library picks kernels and tile sizes from the shapes;
 ``sdpa_set_kernel_choice`` (or the ``kernel_choice`` context manager) pins
@@ -124,18 +126,6 @@ def _stream(stream) -> int | None:
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
-
-
-# torch.cuda.current_stream() makes a stream object (3 us), torch.cuda.current_device()
-# looks for CUDA first (0.3 us): the calls below them take 0.1 us.
-def _current_stream(torch, device: int) -> int:
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    return raw(device) if raw is not None else torch.cuda.current_stream(device).cuda_stream
-
-
-def _current_device(torch) -> int:
-    raw = getattr(torch._C, "_cuda_getDevice", None)
-    return raw() if raw is not None else torch.cuda.current_device()
 
 
 class _on_stream:
@@ -271,37 +261,24 @@ def sdpa_paged_forward(q, k_pages, v_pages, out, workspace, ws_bytes, b, n_token
         _addr(kv_lengths), q_stride, float(scale), _stream(stream)), "sdpa_paged_forward")
 
 
-def _paged_cache(torch, where, k_pages, v_pages, page_table, q_starts, kv_lengths):
-    """(device, b, h_kv, d, page_size, n_pages, pages_per_seq) of a paged
-    cache, after checking what the C entry points cannot see: types, shapes,
-    layout and device (the current one)."""
-    shape = k_pages.shape
-    b, per_seq = page_table.shape
-    device = k_pages.get_device()
-    bf16, i32 = torch.bfloat16, torch.int32
-    if not (len(shape) == 4 and v_pages.shape == shape and
-            k_pages.dtype is bf16 and v_pages.dtype is bf16 and page_table.dtype is i32 and
-            q_starts.dtype is i32 and kv_lengths.dtype is i32 and
-            q_starts.shape == (b + 1,) and kv_lengths.shape == (b,) and
-            k_pages.is_contiguous() and v_pages.is_contiguous() and page_table.is_contiguous() and
-            q_starts.is_contiguous() and kv_lengths.is_contiguous() and
-            device >= 0 and device == _current_device(torch) and v_pages.get_device() == device and
-            page_table.get_device() == device and q_starts.get_device() == device and
-            kv_lengths.get_device() == device):
-        raise SdpaError(1, where)
-    n_pages, h_kv, page, d = shape
-    return device, b, h_kv, d, page, n_pages, per_seq
+_bind_module = None
 
 
-def _paged_rows(torch, where, x, shape, device):
-    """Token stride of packed rows x [n_tokens, heads, d] (a single token's
-    says nothing), after checking them."""
-    n_tokens, heads, d = shape
-    stride, by_head, by_column = x.stride()
-    if not (x.dtype is torch.bfloat16 and x.shape == shape and by_column == 1 and
-            (by_head == d or heads == 1) and x.get_device() == device):
-        raise SdpaError(1, where)
-    return stride if n_tokens > 1 else heads * d
+def _paged():
+    """The extension that checks the paged helpers' tensors and calls the two
+    entry points (csrc/bind.cpp)."""
+    global _bind_module
+    if _bind_module is None:
+        import torch  # noqa: F401 (its libraries resolve the extension's symbols)
+        lib = load_library()
+        try:
+            from . import _bind as module
+        except ImportError as e:
+            raise ImportError("_bind.so not built; run transformer_scaled_dot_02_gb300.build") from e
+        address = lambda f: ctypes.cast(f, ctypes.c_void_p).value
+        module.bind(address(lib.sdpa_paged_append), address(lib.sdpa_paged_forward))
+        _bind_module = module
+    return _bind_module
 
 
 def paged_append(q, k, v, k_pages, v_pages, page_table, q_starts, kv_lengths, rope_freqs=None,
@@ -311,43 +288,15 @@ def paged_append(q, k, v, k_pages, v_pages, page_table, q_starts, kv_lengths, ro
     cache k_pages, v_pages [n_pages,h_kv,page,d]; the first 2 *
     rope_freqs.numel() columns are rotated.  Returns the rotated queries
     (q_out, or a tensor allocated with torch); q = None appends alone."""
-    import torch
     if stream is not None:
         with _on_stream(stream):
             return paged_append(q, k, v, k_pages, v_pages, page_table, q_starts, kv_lengths, rope_freqs,
                                 interleaved, q_out)
-    where = "paged_append"
-    device, b, h_kv, d, page, n_pages, per_seq = _paged_cache(torch, where, k_pages, v_pages, page_table, q_starts,
-                                                              kv_lengths)
-    t = k.shape[0]
-    shape = (t, h_kv, d)
-    k_stride = _paged_rows(torch, where, k, shape, device)
-    v_stride = _paged_rows(torch, where, v, shape, device)
-    h, q_stride, q_ptr, out_ptr = h_kv, 0, None, None
-    if q is not None:
-        h = q.shape[1]
-        shape = (t, h, d)
-        q_stride = _paged_rows(torch, where, q, shape, device)
-        if q_out is None:
-            q_out = torch.empty(shape, dtype=torch.bfloat16, device=k.device)
-        elif _paged_rows(torch, where, q_out, shape, device) != h * d or not q_out.is_contiguous():
-            raise SdpaError(1, where)
-        q_ptr, out_ptr = q.data_ptr(), q_out.data_ptr()
-    elif q_out is not None:
-        raise SdpaError(1, where)
-    d_rot, freqs = 0, None
-    if rope_freqs is not None:
-        if not (rope_freqs.dtype is torch.float32 and rope_freqs.is_contiguous() and
-                rope_freqs.get_device() == device):
-            raise SdpaError(1, where)
-        d_rot, freqs = 2 * rope_freqs.numel(), rope_freqs.data_ptr()
-    status = load_library().sdpa_paged_append(
-        q_ptr, k.data_ptr(), v.data_ptr(), out_ptr, k_pages.data_ptr(), v_pages.data_ptr(), b, t, h, h_kv, d, page,
-        n_pages, per_seq, page_table.data_ptr(), q_starts.data_ptr(), kv_lengths.data_ptr(), q_stride, k_stride,
-        v_stride, freqs, d_rot, 1 if interleaved else 0, _current_stream(torch, device))
-    if status != 0:
-        raise SdpaError(status, where)
-    return q_out
+    done = (_bind_module or _paged()).append(q, k, v, k_pages, v_pages, page_table, q_starts, kv_lengths, rope_freqs,
+                                            interleaved, q_out)
+    if type(done) is int:
+        raise SdpaError(done, "paged_append")
+    return done
 
 
 def paged_workspace(q, k_pages, page_table):
@@ -366,34 +315,16 @@ def paged_attention(q, k_pages, v_pages, page_table, q_starts, kv_lengths, scale
     """Calls sdpa_paged_forward on packed bf16 rows q [t,h,d] (token rows may
     be strided) and a paged cache; allocates the output and the workspace
     with torch where they are not given.  Returns the output [t,h,d]."""
-    import torch
     if stream is not None:
         with _on_stream(stream):
             return paged_attention(q, k_pages, v_pages, page_table, q_starts, kv_lengths, scale, out, workspace)
-    where = "paged_attention"
-    device, b, h_kv, d, page, n_pages, per_seq = _paged_cache(torch, where, k_pages, v_pages, page_table, q_starts,
-                                                              kv_lengths)
-    t, h, _ = q.shape
-    shape = (t, h, d)
-    q_stride = _paged_rows(torch, where, q, shape, device)
-    if out is None:
-        out = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
-    elif _paged_rows(torch, where, out, shape, device) != h * d or not out.is_contiguous():
-        raise SdpaError(1, where)
     if workspace is None:
         workspace = paged_workspace(q, k_pages, page_table)
-    ws_ptr, ws_bytes = None, 0
-    if workspace is not None:
-        if workspace.get_device() != device or not workspace.is_contiguous():
-            raise SdpaError(1, where)
-        ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    status = load_library().sdpa_paged_forward(
-        q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), out.data_ptr(), ws_ptr, ws_bytes, b, t, h, h_kv, d,
-        page, n_pages, per_seq, page_table.data_ptr(), q_starts.data_ptr(), kv_lengths.data_ptr(), q_stride, scale,
-        _current_stream(torch, device))
-    if status != 0:
-        raise SdpaError(status, where)
-    return out
+    done = (_bind_module or _paged()).forward(q, k_pages, v_pages, page_table, q_starts, kv_lengths, scale, out,
+                                             workspace)
+    if type(done) is int:
+        raise SdpaError(done, "paged_attention")
+    return done
 
 
 def mha_workspace_size(b, n_q, n_k, h, d_k, d_v) -> int:

@@ -1,16 +1,21 @@
-"""Builds libsdpa.so in-tree with nvcc for sm_103a.
+"""Builds libsdpa.so in-tree with nvcc for sm_103a, and the paged helpers'
+CPython extension _bind.so with the host compiler.
 
 Each CUDA translation unit is compiled in parallel, then linked into one
-shared library with the CUDA runtime linked statically.  Usage:
+shared library with the CUDA runtime linked statically.  The extension is
+built against the installed torch (where there is none, the library alone is).
+Usage:
     python -m transformer_scaled_dot_02_gb300.build [--force]
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -18,6 +23,8 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libsdpa.so")
+BIND = os.path.join(HERE, "_bind.so")
+BIND_SOURCE = os.path.join(CSRC, "bind.cpp")
 SOURCES = ["api.cu", "sdpa_tc.cu", "sdpa_one_tile.cu", "sdpa_bwd.cu", "sdpa_f32.cu", "gemm_tc.cu",
            "decode.cu", "mha_noalloc.cu", "sdpa_bwd_wide.cu", "paged.cu"]
 HEADERS = ["kernels.h", "ptx.cuh"]
@@ -34,6 +41,19 @@ def _nvcc() -> str:
 def _flags() -> list[str]:
     return ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE,
                    "-I", CSRC, "--expt-relaxed-constexpr"]
+
+
+def _bind_command(nvcc: str, out: str) -> list[str] | None:
+    """Compiles and links the extension; None without torch."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None or spec.origin is None:
+        return None
+    torch = os.path.dirname(spec.origin)
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc))), "include")
+    return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-I", INCLUDE,
+            "-isystem", os.path.join(torch, "include"), "-isystem", cuda, "-I", sysconfig.get_paths()["include"],
+            BIND_SOURCE, "-o", out, "-L", os.path.join(torch, "lib"),
+            "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
 
 
 def _stale(target: str, deps: list[str]) -> bool:
@@ -59,13 +79,20 @@ def build(force: bool = False, verbose: bool = False) -> str:
     def run(cmd):
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
-            raise RuntimeError("nvcc failed:\n%s\n%s%s" % (" ".join(cmd), r.stdout, r.stderr))
+            raise RuntimeError("%s failed:\n%s\n%s%s" % (os.path.basename(cmd[0]), " ".join(cmd), r.stdout, r.stderr))
         if verbose and (r.stdout or r.stderr):
             sys.stderr.write(r.stdout + r.stderr)
 
-    if jobs:
-        with cf.ThreadPoolExecutor(max_workers=len(jobs)) as ex:
-            list(ex.map(run, jobs))
+    bind_tmp = BIND + ".tmp%d" % os.getpid()
+    bind = None
+    if force or _stale(BIND, [BIND_SOURCE, os.path.join(INCLUDE, "sdpa.h"), __file__]):
+        bind = _bind_command(nvcc, bind_tmp)
+    commands = jobs + ([bind] if bind else [])
+    if commands:
+        with cf.ThreadPoolExecutor(max_workers=len(commands)) as ex:
+            list(ex.map(run, commands))
+    if bind:
+        os.replace(bind_tmp, BIND)
     if force or jobs or _stale(LIB, objs):
         tmp = LIB + ".tmp%d" % os.getpid()
         run([nvcc] + ARCH + ["-shared", "-cudart", "static", "-o", tmp] + objs)
