@@ -902,6 +902,7 @@ sdpa_status sdpa_paged_forward(const void* q, const void* k_pages, const void* v
   p.split_ctas = paged_split_ctas(b, n_tokens, h_kv, p.group, d, 1ll * pages_per_seq * page_size);
   p.ctas_magic = ~0ull / static_cast<unsigned>(p.split_ctas) + 1;
   p.slot_bytes = paged_slot_bytes(n_tokens, p.group, d);
+  p.row_bytes = 4 * d;
   p.slots = need > 0 ? static_cast<uint8_t*>(workspace) : nullptr;
   p.flags = need > 0 ? reinterpret_cast<unsigned long long*>(
                            p.slots + static_cast<size_t>(p.split_ctas) * p.slot_bytes)

@@ -123,6 +123,7 @@ struct PagedParams {
   int page_shift, n_pages, pages_per_seq;
   int split_ctas;             // CTAs of the split kernel (runs, at most)
   unsigned long long ctas_magic;   // ceil(2^64 / split_ctas)
+  int row_bytes;              // of a published row's O: 4 d
   int slot_bytes;             // of 128 rows, or as many as the call has
   float scale_log2;
 };

@@ -93,32 +93,49 @@ __device__ __forceinline__ int walk_tiles(int keys) { return max(1, (keys + kBN 
 // CTAs' times on GB300: two prompts of 8192 tokens (16 heads of 128) take 4.4 us
 // a walk and 0.94 us a wide key tile, 16 x 4 drafted tokens (64 wide) 2.4 us
 // and 0.67 us a narrow one.  Counting key tiles alone, the CTAs with a prompt's
-// shortest walks finished 20 % after the others (514 us instead of 396).  Where
-// there are few key tiles for each CTA (`few`), a single one more counts for
-// more than all that: then only key tiles are counted.
+// shortest walks finished 20 % after the others (514 us instead of 396).
 struct Weight {
   int start, log_tile;
   __device__ long long of(long long tiles) const { return start + (tiles << log_tile); }
 };
-__device__ __forceinline__ Weight weight_of(bool few, bool narrow) {
-  return few ? Weight{0, 0} : (narrow ? Weight{14, 2} : Weight{18, 2});
+// How the work is counted and cut.  kPieces: every unit in pieces of its own,
+// a run for each.  kTiles: key tiles alone, runs of equally many.  kWeighed: as above.
+enum Scheme { kWeighed, kTiles, kPieces };
+__device__ __forceinline__ Weight weight_of(Scheme scheme, bool narrow) {
+  return scheme != kWeighed ? Weight{0, 0} : (narrow ? Weight{14, 2} : Weight{18, 2});
 }
 constexpr int kFewTiles = 8;
-// Where there are few, a piece of up to 8 KB may be a single key tile, a larger
-// one has at least eight, one over 32 KB twelve: a further cut by four saves
-// three quarters of its key tiles' time (0.5 to 0.9 us each) and costs a level
-// more of merging (4 to 9 us).  Over 8192 positions of 4 key-value heads, 32 new
-// tokens of 16 heads (64 KB pieces) take 24 us so, 43 with single key tiles; 200
-// tokens of 128 take 32 and 36.
+// kPieces: a piece of up to 8 KB has a single key tile, a larger one up to
+// eight, one over 32 KB twelve: a further cut by four saves three quarters of its
+// key tiles' time (0.5 to 0.9 us each) and costs a level more of merging (4 to
+// 9 us).  Over 8192 positions of 4 key-value heads, 32 new tokens of 16 heads
+// (64 KB pieces) take 24 us so, 43 with single key tiles; 200 tokens of 128 take
+// 32 and 36.
 constexpr int kSmallPiece = 8 << 10, kMiddlePiece = 32 << 10;
 constexpr int kMiddlePieceTiles = 8, kLargePieceTiles = 12;
 
 __device__ __forceinline__ int tile_rows(const PagedParams& p, const Seq& q, int r) {
   return min(p.tile_tokens, q.n - r * p.tile_tokens) * p.group;
 }
-__device__ __forceinline__ long long unit_cost(const PagedParams& p, const Seq& q, int r, bool few) {
-  const Weight w = weight_of(few, tile_rows(p, q, r) <= kNarrowRows);
-  return w.of(walk_tiles(tile_keys(p, q, r)));
+// The pieces that a walk of `tiles` is worth with these rows.
+__device__ __forceinline__ int pieces_of(const PagedParams& p, int rows, int tiles) {
+  const int bytes = rows * p.row_bytes;
+  return bytes <= kSmallPiece    ? tiles
+         : bytes <= kMiddlePiece ? (tiles + kMiddlePieceTiles - 1) / kMiddlePieceTiles
+                                 : (tiles + kLargePieceTiles - 1) / kLargePieceTiles;
+}
+// Pieces of each full row tile of a sequence that has more than one: those of
+// the longest walk, or as many as there are key tiles.
+__device__ __forceinline__ int full_pieces(const PagedParams& p, const Seq& q) {
+  return pieces_of(p, p.tile_tokens * p.group, walk_tiles(q.len));
+}
+__device__ __forceinline__ int unit_pieces(const PagedParams& p, const Seq& q, int r, int tiles) {
+  return r + 1 < q.tiles ? min(full_pieces(p, q), tiles) : pieces_of(p, tile_rows(p, q, r), tiles);
+}
+__device__ __forceinline__ long long unit_cost(const PagedParams& p, const Seq& q, int r, Scheme scheme) {
+  const int tiles = walk_tiles(tile_keys(p, q, r));
+  if (scheme == kPieces) return unit_pieces(p, q, r, tiles);
+  return weight_of(scheme, tile_rows(p, q, r) <= kNarrowRows).of(tiles);
 }
 
 // Key tiles of the first f row tiles, f < q.tiles.  They see A + (i + 1) t
@@ -161,22 +178,34 @@ __device__ __noinline__ long long tiles_before(const PagedParams& p, const Seq& 
 
 // Cost of row tiles 0 .. r-1 (r <= q.tiles) of one key-value head: all but
 // the last are wide (a full tile has more than 64 rows).
-__device__ __forceinline__ long long cost_before(const PagedParams& p, const Seq& q, int r, bool few) {
+__device__ __forceinline__ long long full_pieces_before(const PagedParams& p, const Seq& q, int f) {
+  const int most = full_pieces(p, q);
+  const int short_keys = kBN * (most - 1) - (q.len - q.n);   // row tiles with no more keys walk less
+  const int z = most > 1 && short_keys >= p.tile_tokens ? min(f, short_keys / p.tile_tokens) : 0;
+  return static_cast<long long>(most) * (f - z) + (z > 0 ? tiles_before(p, q, z) : 0);
+}
+__device__ __forceinline__ long long cost_before(const PagedParams& p, const Seq& q, int r, Scheme scheme) {
   const int f = min(r, q.tiles - 1);
   long long sum = 0;
   if (f > 0) {
-    const Weight w = weight_of(few, false);
-    sum = static_cast<long long>(w.start) * f + (tiles_before(p, q, f) << w.log_tile);
+    if (scheme == kPieces) {
+      sum = full_pieces_before(p, q, f);
+    } else {
+      const Weight w = weight_of(scheme, false);
+      sum = static_cast<long long>(w.start) * f + (tiles_before(p, q, f) << w.log_tile);
+    }
   }
-  if (r == q.tiles && r > 0) sum += unit_cost(p, q, r - 1, few);
+  if (r == q.tiles && r > 0) sum += unit_cost(p, q, r - 1, scheme);
   return sum;
 }
 
 // A place in the laid-out work: unit (s, hk, r), and the item of it that the
-// place is behind.
+// place is behind.  kPieces: the unit's pieces, and the key tiles of the one
+// that ends there.
 struct Place {
   int s, hk, r;
   long long item;
+  int pieces, kt0, kt1;
 };
 
 // What there is to do: key tiles, the pieces that they may be cut into, and the
@@ -187,6 +216,9 @@ struct Work {
     tiles += o.tiles;
     pieces += o.pieces;
     cost += o.cost;
+  }
+  __device__ long long of(Scheme scheme) const {
+    return scheme == kPieces ? pieces : scheme == kTiles ? tiles : cost;
   }
 };
 
@@ -207,9 +239,9 @@ __device__ __forceinline__ long long divide(long long a, long long b) {
 struct Cut {
   long long each, longer;                                    // longer: items in the longer runs
   int over;
-  bool few;                                                  // how units are weighed
+  Scheme scheme;
   // `magic`: ceil(2^64 / max_ctas), for the usual number of runs
-  __device__ Cut(long long work, int ctas, int max_ctas, unsigned long long magic, bool few_tiles) : few(few_tiles) {
+  __device__ Cut(long long work, int ctas, int max_ctas, unsigned long long magic, Scheme how) : scheme(how) {
     each = ctas == max_ctas && ctas > 1 ? static_cast<long long>(__umul64hi(work, magic)) : divide(work, ctas);
     over = static_cast<int>(work - each * ctas);
     longer = over * (each + 1);
@@ -235,21 +267,19 @@ __device__ bool find_place(const PagedParams& p, ScheduleShared* sh, int c, int 
     q = load_seq(p, s);
     if (q.tiles == 0) continue;
     const int f = q.tiles - 1;                               // full tiles, the last one aside
-    long long walk = walk_tiles(q.len);
-    long long cost = weight_of(false, tile_rows(p, q, f) <= kNarrowRows).of(walk);
+    const int last = walk_tiles(q.len), rows = tile_rows(p, q, f);
+    Work w = {last, pieces_of(p, rows, last), weight_of(kWeighed, rows <= kNarrowRows).of(last)};
     if (f > 0) {
-      const Weight w = weight_of(false, false);
+      const Weight weight = weight_of(kWeighed, false);
       const long long full = tiles_before(p, q, f);
-      walk += full;
-      cost += static_cast<long long>(w.start) * f + (full << w.log_tile);
+      w.tiles += full;
+      w.pieces += full_pieces_before(p, q, f);
+      w.cost += static_cast<long long>(weight.start) * f + (full << weight.log_tile);
     }
-    walk *= p.h_kv;
-    mine.tiles += walk;
-    mine.cost += cost * p.h_kv;
-    const int bytes = min(p.tile_tokens, q.n) * p.group * D * 4;
-    mine.pieces += bytes <= kSmallPiece ? walk
-                   : bytes <= kMiddlePiece ? (walk + kMiddlePieceTiles - 1) / kMiddlePieceTiles
-                                           : (walk + kLargePieceTiles - 1) / kLargePieceTiles;
+    w.tiles *= p.h_kv;
+    w.pieces *= p.h_kv;
+    w.cost *= p.h_kv;
+    mine.add(w);
   }
   Work incl = mine;
 #pragma unroll
@@ -260,7 +290,7 @@ __device__ bool find_place(const PagedParams& p, ScheduleShared* sh, int c, int 
   }
   if (lane == 31) sh->warp_sum[warp] = incl;
   __syncthreads();
-  Work sum = {0, 0, 0}, before = {incl.tiles - mine.tiles, 0, incl.cost - mine.cost};
+  Work sum = {0, 0, 0}, before = {incl.tiles - mine.tiles, incl.pieces - mine.pieces, incl.cost - mine.cost};
 #pragma unroll
   for (int w = 0; w < kThreads / 32; ++w) {
     const Work v = sh->warp_sum[w];
@@ -268,12 +298,12 @@ __device__ bool find_place(const PagedParams& p, ScheduleShared* sh, int c, int 
     sum.add(v);
   }
   // (a run is never shorter than a key tile, so no run inside a unit is empty)
-  const bool few = sum.tiles < 1ll * kFewTiles * max_ctas;
-  const int n = static_cast<int>(min(static_cast<long long>(max_ctas), few ? sum.pieces : sum.tiles));
+  const Scheme scheme = sum.pieces <= max_ctas ? kPieces
+                        : sum.tiles < 1ll * kFewTiles * max_ctas && 2 * sum.pieces > sum.tiles ? kTiles : kWeighed;
+  const int n = static_cast<int>(min(static_cast<long long>(max_ctas), scheme == kPieces ? sum.pieces : sum.tiles));
   if (c >= n) return false;
-  const long long total = few ? sum.tiles : sum.cost, own = few ? mine.tiles : mine.cost,
-                  excl = few ? before.tiles : before.cost;
-  *cut = Cut(total, n, max_ctas, p.ctas_magic, few);
+  const long long own = mine.of(scheme), excl = before.of(scheme);
+  *cut = Cut(sum.of(scheme), n, max_ctas, p.ctas_magic, scheme);
   const long long x = cut->begin(c + 1) - 1;                 // its last item
   if (own > 0 && excl <= x && x < excl + own) {
     long long rem = x - excl;
@@ -282,12 +312,12 @@ __device__ bool find_place(const PagedParams& p, ScheduleShared* sh, int c, int 
     if (per > 1) {
       for (pl.s = s0; pl.s < s1; ++pl.s) {
         q = load_seq(p, pl.s);
-        const long long w = cost_before(p, q, q.tiles, few) * p.h_kv;
+        const long long w = cost_before(p, q, q.tiles, scheme) * p.h_kv;
         if (rem < w) break;
         rem -= w;
       }
     }
-    const long long head = cost_before(p, q, q.tiles, few);
+    const long long head = cost_before(p, q, q.tiles, scheme);
     pl.hk = static_cast<int>(divide(rem, head));
     rem -= pl.hk * head;
     pl.r = 0;
@@ -308,7 +338,7 @@ __device__ bool find_place(const PagedParams& p, ScheduleShared* sh, int c, int 
     while (hi - lo > 1) {
       const int step = (hi - lo + 31) / 32;
       const int probe = lo + lane * step;
-      const long long cost = probe < hi ? cost_before(p, *seq, probe, few) : rem + 1;
+      const long long cost = probe < hi ? cost_before(p, *seq, probe, scheme) : rem + 1;
       const int k = 31 - __clz(__ballot_sync(0xffffffffu, cost <= rem));
       before_lo = __shfl_sync(0xffffffffu, cost, k);
       lo += k * step;
@@ -316,6 +346,17 @@ __device__ bool find_place(const PagedParams& p, ScheduleShared* sh, int c, int 
     }
     at->r = lo;
     at->item = rem - before_lo + 1;
+  }
+  if (scheme == kPieces) {
+    const unsigned tiles = walk_tiles(tile_keys(p, *seq, at->r)), i = static_cast<unsigned>(at->item);
+    const unsigned pieces = unit_pieces(p, *seq, at->r, tiles);
+    at->pieces = pieces;
+    at->kt0 = i - 1;
+    at->kt1 = i;
+    if (pieces != tiles) {                                   // (a piece has up to 12: in 32 bits)
+      at->kt0 = (i - 1) * tiles / pieces;
+      at->kt1 = i * tiles / pieces;
+    }
   }
   return true;
 }
@@ -325,10 +366,10 @@ __device__ bool find_place(const PagedParams& p, ScheduleShared* sh, int c, int 
 struct Walk {
   int s, hk, r;                                              // the piece's unit
   Seq q;
-  int kt0, kt1, cost;                                        // its key tiles [kt0, kt1) of `cost`
+  int kt0, kt1, tiles;                                       // its key tiles [kt0, kt1) of `tiles`
   int keys, rows;                                            // the unit's keys, rows that are queries
   Weight w;
-  bool few;
+  Scheme scheme;
   long long off;                                             // where the unit begins, seen from the run's begin
 
   // Key tiles that lie before item x of the unit.
@@ -337,19 +378,24 @@ struct Walk {
   }
   __device__ __forceinline__ void load(const PagedParams& p) {
     keys = tile_keys(p, q, r);
-    cost = walk_tiles(keys);
+    tiles = walk_tiles(keys);
     rows = tile_rows(p, q, r);
-    w = weight_of(few, rows <= kNarrowRows);
+    w = weight_of(scheme, rows <= kNarrowRows);
   }
   // The first piece of a run of `run` items that ends at `end`; false: none.
-  __device__ bool begin(const PagedParams& p, const Place& end, const Seq& seq, long long run, bool few_tiles) {
-    few = few_tiles;
+  __device__ bool begin(const PagedParams& p, const Place& end, const Seq& seq, long long run, Scheme how) {
+    scheme = how;
     s = end.s;
     hk = end.hk;
     r = end.r;
     q = seq;
     load(p);
     off = run - end.item;
+    if (scheme == kPieces) {                                 // the whole run
+      kt0 = end.kt0;
+      kt1 = end.kt1;
+      return true;
+    }
     kt1 = tiles_at(end.item);
     kt0 = tiles_at(-off);
     return kt1 > kt0 || next(p);
@@ -367,9 +413,9 @@ struct Walk {
       r = q.tiles - 1;
     }
     load(p);
-    off -= w.of(cost);
+    off -= w.of(tiles);
     kt0 = tiles_at(-off);
-    kt1 = cost;
+    kt1 = tiles;
     return true;
   }
   // key tiles of the piece that hold keys (all, but for a unit that sees none)
@@ -535,7 +581,7 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
   griddep_launch_dependents();
   griddep_wait();
 
-  Cut cut(0, 1, 0, 0, true);
+  Cut cut(0, 1, 0, 0, kWeighed);
   Place last;
   Seq last_seq;
   const int cta = static_cast<int>(blockIdx.x);
@@ -571,7 +617,7 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
     Walk w;
     int u0 = 0, pieces = 0, k_issued = 0, v_issued = 0;
     bool go = true;
-    for (bool more = w.begin(p, last, last_seq, run, cut.few); more; more = go && w.next(p)) {
+    for (bool more = w.begin(p, last, last_seq, run, cut.scheme); more; more = go && w.next(p)) {
       const int n = w.count();
       if (n <= 0) continue;
       const int kt0 = w.kt0;
@@ -680,7 +726,7 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
     Walk w;
     int u = 0, pieces = 0;
     bool ok = true;
-    for (bool more = w.begin(p, last, last_seq, run, cut.few); more; more = ok && w.next(p)) {
+    for (bool more = w.begin(p, last, last_seq, run, cut.scheme); more; more = ok && w.next(p)) {
       const int n = w.count();
       if (n <= 0) continue;
       ok = mbar_wait_warp(q_full, static_cast<uint32_t>(pieces) & 1u, ab);
@@ -717,7 +763,7 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
     const float scale_log2 = p.scale_log2;
     const float2 sc2 = make_float2(scale_log2, scale_log2);
     Walk w;
-    bool more = w.begin(p, last, last_seq, run, cut.few);
+    bool more = w.begin(p, last, last_seq, run, cut.scheme);
     int u = 0, pieces = 0;
     int merged = 0;                                          // steps of merge
     bool ok = true;
@@ -790,15 +836,20 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
       const int pos = pos0 + token;                          // this row sees keys 0 .. pos
       // a piece of a unit that later runs merge, or that this run merges with
       // what earlier runs published
-      const bool open_above = w.kt1 < w.cost, open_below = kt0 > 0;
+      const bool open_above = w.kt1 < w.tiles, open_below = kt0 > 0;
       const bool whole = !open_above && !open_below;
       int sources = 0;
       if (!whole) {
         // the pieces that this one merges, in the order of the list
         // (the first key tile's last item says which run it belongs to)
-        const long long unit = cut.begin(cta) + w.off;
-        const int c0 = cut.run_of(unit + w.w.of(1) - 1), j = cta - c0;
-        const int bits = radix_bits(cut.run_of(unit + w.w.of(w.cost) - 1) - c0 + 1, rows * D * 4, narrow);
+        int j = static_cast<int>(last.item) - 1, pieces = last.pieces;
+        if (cut.scheme != kPieces) {
+          const long long unit = cut.begin(cta) + w.off;
+          const int first = cut.run_of(unit + w.w.of(1) - 1);
+          j = cta - first;
+          pieces = cut.run_of(unit + w.w.of(w.tiles) - 1) - first + 1;
+        }
+        const int c0 = cta - j, bits = radix_bits(pieces, rows * D * 4, narrow);
         const int low = open_above ? j + 1 - block_size(j, bits) : 0;
         for (int at = j; at > low; at -= block_size(at - 1, bits)) {
           if (threadIdx.x == 0) source_runs[sources] = c0 + at - 1;
