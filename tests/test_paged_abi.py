@@ -131,10 +131,10 @@ def test_workspace_size_follows_the_shapes(lib):
     assert size(1, 1, 1, 1, 64, 16, 3) == 0                   # one run: nothing to merge
     small, large = size(1, 1, 8, 8, 64, 16, 64), size(64, 4096, 8, 8, 64, 16, 64)
     assert 0 < small < large
-    # never more than a slot of 128 rows for every resident CTA
-    assert size(1 << 12, 1 << 20, 16, 16, 128, 64, 2048) <= 2 * 152 * 128 * 130 * 4 + (1 << 18)
+    # never more than four slots of 128 rows for every three resident CTAs
+    assert size(1 << 12, 1 << 20, 16, 16, 128, 64, 2048) <= 4 * 2 * 152 * 128 * 130 * 4 // 3 + (1 << 18)
     # ... and bounded by the rows of the call
-    assert size(1, 1, 8, 1, 128, 64, 2048) <= 2 * 152 * 8 * 130 * 4 + (1 << 18)
+    assert size(1, 1, 8, 1, 128, 64, 2048) <= 4 * 2 * 152 * 8 * 130 * 4 // 3 + (1 << 18)
 
 
 def _cpu_tensors(torch):

@@ -441,8 +441,8 @@ int paged_split_ctas(int b, int n_tokens, int h_kv, int group, int d, long long 
   return static_cast<int>(std::max(1ll, std::min(most, tiles)));
 }
 
-// The number that marks a call's workspace slots as written.  Every reader
-// clears what it read, so a replayed launch may use its number again; what an
+// The number that marks a call's workspace slots as written.  The call clears
+// its marks, so a replayed launch may use its number again; what an
 // unwritten workspace holds must only not be this number, so the numbers are
 // a sequence of 64-bit steps from a place that differs from process to process.
 unsigned long long paged_call_number() {
@@ -854,8 +854,8 @@ size_t sdpa_paged_workspace_size(int b, int n_tokens, int h, int h_kv, int d, in
   const int group = h / h_kv;
   const int ctas = paged_split_ctas(b, n_tokens, h_kv, group, d, 1ll * pages_per_seq * page_size);
   if (ctas == 1) return 0;
-  return static_cast<size_t>(ctas) * paged_slot_bytes(n_tokens, group, d) +
-         round256(static_cast<size_t>(ctas) * 8);
+  const size_t slots = sdpa::paged_slots(ctas);
+  return slots * paged_slot_bytes(n_tokens, group, d) + round256((slots + ctas) * 8);
 }
 
 sdpa_status sdpa_paged_forward(const void* q, const void* k_pages, const void* v_pages, void* out,
@@ -905,8 +905,9 @@ sdpa_status sdpa_paged_forward(const void* q, const void* k_pages, const void* v
   p.row_bytes = 4 * d;
   p.slots = need > 0 ? static_cast<uint8_t*>(workspace) : nullptr;
   p.flags = need > 0 ? reinterpret_cast<unsigned long long*>(
-                           p.slots + static_cast<size_t>(p.split_ctas) * p.slot_bytes)
+                           p.slots + static_cast<size_t>(sdpa::paged_slots(p.split_ctas)) * p.slot_bytes)
                      : nullptr;
+  p.states = need > 0 ? p.flags + sdpa::paged_slots(p.split_ctas) : nullptr;
   p.call = paged_call_number();
   p.scale_log2 = effective_scale(scale, d) * 1.4426950408889634f;
   return sdpa::launch_sdpa_paged(p, d, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SDPA_OK

@@ -111,8 +111,9 @@ struct PagedParams {
                               // rows of one
   uint16_t* out;              // bf16 [n_tokens][h][d]
   // workspace (split_ctas > 1)
-  uint8_t* slots;             // [split_ctas][slot_bytes]: a published piece's O, then its (m, l)
-  unsigned long long* flags;  // [split_ctas]
+  uint8_t* slots;             // [slots][slot_bytes]: a published piece's O, then its (m, l)
+  unsigned long long* flags;  // [slots]
+  unsigned long long* states; // [split_ctas]
   unsigned long long call;    // the call's number: no other call's flags have it
   const int32_t* page_table;  // [b][pages_per_seq]
   const int32_t* q_starts;    // [b + 1]
@@ -129,7 +130,9 @@ struct PagedParams {
 };
 constexpr int kPagedKeyTile = 64;
 constexpr int kPagedMinPage = 8;
-constexpr int kPagedMaxRuns = 1 << 12;
+// a slot for every run, and for every third one more
+constexpr int paged_slots(int split_ctas) { return split_ctas + (split_ctas + 2) / 3; }
+constexpr int kPagedMaxRuns = 640;
 bool paged_supports(int d);
 int paged_resident_ctas(int d);   // split CTAs that share an SM
 cudaError_t launch_sdpa_paged(const PagedParams& p, int d, cudaStream_t stream);

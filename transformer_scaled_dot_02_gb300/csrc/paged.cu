@@ -23,9 +23,10 @@
 // merges the pieces that the runs before it published:
 //   O = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s, M = max_s m_s.
 // So a CTA waits for CTAs of lower index only, which are dispatched before it:
-// the waits end however few CTAs run at a time.  Units cut
-// into many pieces are merged as a tree.  The pieces merge in an order fixed
-// by the cut, so results repeat bit by bit.
+// the waits end however few CTAs run at a time.  Units cut into many pieces are
+// merged in slices by several CTAs, which wait for one another, but not for long
+// (see merge).  The pieces merge in an order fixed by the cut, so results repeat
+// bit by bit.
 //
 // Row tiles of at most 16 rows (single tokens) would leave three of the four
 // softmax warps idle and one with the whole row: they are NARROW, their queries
@@ -105,14 +106,16 @@ __device__ __forceinline__ Weight weight_of(Scheme scheme, bool narrow) {
   return scheme != kWeighed ? Weight{0, 0} : (narrow ? Weight{14, 2} : Weight{18, 2});
 }
 constexpr int kFewTiles = 8;
-// kPieces: a piece of up to 8 KB has a single key tile, a larger one up to
-// eight, one over 32 KB twelve: a further cut by four saves three quarters of its
-// key tiles' time (0.5 to 0.9 us each) and costs a level more of merging (4 to
-// 9 us).  Over 8192 positions of 4 key-value heads, 32 new tokens of 16 heads
-// (64 KB pieces) take 24 us so, 43 with single key tiles; 200 tokens of 128 take
-// 32 and 36.
+// kPieces: a piece of up to 8 KB has up to four key tiles, a larger one eight, one
+// over 32 KB sixteen: a further cut saves time at the key tiles (0.5 to 0.9 us
+// each), but there are more pieces to merge.  14 single tokens over 749 to 1147
+// positions (2 key-value heads, 16 rows of 128: 8 KB) take 14.9 us with four, 20.3
+// with one, 15.3 with eight; 128 tokens over 4096 positions of 4 key-value heads
+// of 64 (32 KB) 18.4 us with eight, 20.3 with four, 19.2 with sixteen; 200 tokens over
+// 8192 positions of 4 key-value heads of 128 (64 KB) 29.9 us with sixteen, 32.3
+// with twelve, 31.7 with 24.
 constexpr int kSmallPiece = 8 << 10, kMiddlePiece = 32 << 10;
-constexpr int kMiddlePieceTiles = 8, kLargePieceTiles = 12;
+constexpr int kSmallPieceTiles = 4, kMiddlePieceTiles = 8, kLargePieceTiles = 16;
 
 __device__ __forceinline__ int tile_rows(const PagedParams& p, const Seq& q, int r) {
   return min(p.tile_tokens, q.n - r * p.tile_tokens) * p.group;
@@ -120,7 +123,7 @@ __device__ __forceinline__ int tile_rows(const PagedParams& p, const Seq& q, int
 // The pieces that a walk of `tiles` is worth with these rows.
 __device__ __forceinline__ int pieces_of(const PagedParams& p, int rows, int tiles) {
   const int bytes = rows * p.row_bytes;
-  return bytes <= kSmallPiece    ? tiles
+  return bytes <= kSmallPiece    ? (tiles + kSmallPieceTiles - 1) / kSmallPieceTiles
          : bytes <= kMiddlePiece ? (tiles + kMiddlePieceTiles - 1) / kMiddlePieceTiles
                                  : (tiles + kLargePieceTiles - 1) / kLargePieceTiles;
 }
@@ -424,49 +427,48 @@ struct Walk {
 
 // --------------------------------------------------------------------- merge
 // Workspace slots: what run c publishes is slot c: O as [D / 4][rows] vectors
-// of four columns and, right behind, (m, l) as [rows].  A slot has a flag,
-// which is the call's number once the slot is written and is put back to zero
-// by its only reader.  A run merges at its end, when its K and V stages are
-// idle: the published pieces come into that memory by asynchronous copies.
+// of four columns and, right behind, (m, l) as [rows].  (A run that publishes a
+// sliced unit's last piece, below, may publish the next one's first piece too:
+// last pieces have slots of their own, split_ctas + c / 3, as they are three runs
+// apart at least.)  A slot has a flag, which is the call's number once the slot
+// is written and is put back to zero when everybody has seen it.  A run merges at its end, when its K and V stages
+// are idle: the published pieces come into that memory by asynchronous copies.
 //
-// The unit's pieces j = 0, 1, .. (runs c0 + j) form a tree of radix R = 2^bits:
-// before it publishes, piece j merges the size(j) - 1 pieces below it, size(j)
-// the largest power of R that divides j + 1; the last piece merges all.  What
-// a piece reads are the tops of the blocks that make up its range.  Reading
-// R - 1 pieces a level costs R - 1 pieces' bytes on one SM (64 KB take about a
-// microsecond), a level costs a wait of two: pieces of up to 8 KB take R = 16,
-// larger ones (128 rows of 256: 128 KB) R = 4.  Pieces that make up little (a
-// narrow tile's come in a few at a time, so less) are merged by the last at once.
-__device__ __forceinline__ int radix_bits(int pieces, int bytes, bool narrow) {
-  const int at_once = narrow ? 128 << 10 : 512 << 10;
-  if (pieces <= 1 << 5 && (pieces - 1) * bytes <= at_once) return 5;
-  return bytes <= kSmallPiece ? 4 : 2;
-}
-constexpr int kMaxSources = 48;            // 31 at once, or 15 a level of three for up to 2^12 runs
-static_assert(kPagedMaxRuns <= 1 << 12, "sources");
+// The pieces j = 0, 1, .. of a unit are runs c0 + j.  Few are merged by the last
+// one, which keeps its own piece.  More are all published, and the runs that end
+// with them (SLICERS) merge a slice each, a range of rows or, if there are more
+// slicers than rows, of rows and columns: all of P pieces cost one SM P times a
+// piece's bytes (64 KB take about a microsecond), a slice of them no more than
+// one piece's, but publishing the last piece and asking for all others' takes 2 to
+// 3 us.  One sequence of 26595 positions, 69 new tokens of 2 heads of 64 (52
+// pieces of 18 KB a head) takes 17 us in slices and took 27 as a tree of radix 4.
+// At 7 pieces of 64 KB (2 chunks of 485 and 1 tokens, 20 heads of 128) the last one
+// alone takes 66 us, slices 79: there every SM merges at once, and slices read
+// every piece once more.
+// A slicer waits for pieces of later runs too, and those need not be running
+// (with another kernel on the GPU): it waits so long and then leaves its slice
+// to the unit's last run, whose own wait is for earlier ones alone.  A slicer's
+// STATE says what became of its slice: kOpen while it waits, kTaken, kLeft.
+constexpr int kTogether = 8, kTogetherNarrow = 16;   // pieces that the last run merges alone, at most
+constexpr int kSliceVectors = 16;          // of a slice, at least
+constexpr long long kPatience = 1 << 17;   // clock cycles, about 65 us: runs end within a few of each other
+enum State : unsigned long long { kOpen, kTaken, kLeft };
 
-__device__ __forceinline__ int block_size(int j, int bits) {
-  return 1 << ((__ffs(j + 1) - 1) / bits * bits);
+__device__ __forceinline__ unsigned long long load_acquire(const unsigned long long* x) {
+  unsigned long long v;
+  asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(x) : "memory");
+  return v;
 }
 
-// Waits until the flag is this call's number, and clears it.  `limit`: clock
-// cycles; runs take about equally long, and a run's items well below 4096
-// cycles each, so it grows by that with the run.
-__device__ __forceinline__ bool take_flag(unsigned long long* flag, unsigned long long call, long long limit,
+// Waits until the flag is this call's number (or the state is decided):
+// false after `limit` clock cycles, or when another thread has given up.
+template <class Ready>
+__device__ __forceinline__ bool wait_word(const unsigned long long* x, Ready ready, long long limit,
                                           const AbortState& ab) {
   const long long t0 = clock64();
-  while (true) {
-    unsigned long long v;
-    asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(flag) : "memory");
-    if (v == call) break;
-    if (*ab.flag) return false;
-    if (clock64() - t0 > limit) {
-      *ab.flag = 1;
-      atomicOr(ab.status, kStatusTimeout);
-      return false;
-    }
+  while (!ready(load_acquire(x))) {
+    if (*ab.flag || clock64() - t0 > limit) return false;
   }
-  *flag = 0;
   return true;
 }
 
@@ -476,6 +478,14 @@ __device__ __forceinline__ void set_flag(unsigned long long* flag, unsigned long
 
 // 2^(m - sub), 0 for a piece that saw nothing
 __device__ __forceinline__ float weight(float m, float sub) { return ex2_approx(m - sub); }
+
+__device__ __forceinline__ void add_weighed(float4& acc, float& sum, const float4& v, float l, float f) {
+  sum += l * f;
+  acc.x += v.x * f;
+  acc.y += v.y * f;
+  acc.z += v.z * f;
+  acc.w += v.w * f;
+}
 
 // --------------------------------------------------------------------- split
 template <int D>
@@ -511,9 +521,12 @@ struct PCfg {
   static_assert(4 * kNarrowRows * 16 * 4 <= kXBytes, "quarters");
   static constexpr int kXmlOff = kXOff + kXBytes;            // the quarters' (m, l)
   // merging: the idle K and V stages hold a wide piece's O, or with the exchange
-  // memory behind them a narrow tile's own piece and at least one more
+  // memory behind them three of a narrow tile's, or of every piece a vector and
+  // its (m, l) beside what the threads that share a vector exchange
   static constexpr int kMergeBytes = 2 * kRing * kKVBytes + kXBytes;
-  static_assert(2 * kRing * kKVBytes >= kBlockM * D * 4 && kMergeBytes >= 2 * kNarrowRows * (D * 4 + 8), "pieces");
+  static constexpr int kPartBytes = kBlockM * (16 + 8);
+  static_assert(2 * kRing * kKVBytes >= kBlockM * D * 4 && kMergeBytes >= 2 * kNarrowRows * (D * 4 + 8) &&
+                    kMergeBytes - kPartBytes >= kPagedMaxRuns * (16 + 8), "pieces");
   static constexpr int kXinvOff = kXmlOff + 4 * kQuarter * 8;   // 1 / l of their sum
   static constexpr int kBarOff = kXinvOff + kNarrowRows * 4;
   // q_full, q_empty, k_full[R], v_full[R], s_full[R], o_full[R], p_full[2], o_last, o_free,
@@ -531,6 +544,173 @@ struct PCfg {
   static_assert(kBoxes * (kBN / kPagedMinPage) <= 32, "a lane of the producer warp for each box of a tile's parts");
 };
 
+// Four columns of row rw of a tile into the output (row0: the tile's first token,
+// head0: the group's first head).
+template <int D>
+__device__ __forceinline__ void write_out(const PagedParams& p, int row0, int head0, int rw, int col, const float4& v,
+                                          float inv) {
+  const int tok = rw / p.group;
+  *reinterpret_cast<uint2*>(p.out + (static_cast<long long>(row0 + tok) * p.h + head0 + rw - tok * p.group) * D + col) =
+      make_uint2(pack_bf16x2(v.x * inv, v.y * inv), pack_bf16x2(v.z * inv, v.w * inv));
+}
+
+// Where the parts of a unit are: piece j of `of` (this run's) is run cta.
+struct Pieces {
+  int rows, row0, head0, cta, j, of;
+  bool sliced;
+  __device__ __forceinline__ int place(const PagedParams& p, int i) const {
+    const int c = cta - j + i;
+    return sliced && i == of - 1 ? p.split_ctas + c / 3 : c;
+  }
+};
+
+// All softmax threads meet at `bar` and see what each wrote before; `met`
+// counts the times.
+struct Meeting {
+  uint64_t* bar;
+  int met;
+  AbortState ab;
+  __device__ __forceinline__ bool operator()() {
+    mbar_arrive(bar);
+    return mbar_wait_warp(bar, static_cast<uint32_t>(met++) & 1u, ab);
+  }
+};
+
+__device__ __forceinline__ void time_out(const AbortState& ab) {
+  *ab.flag = 1;
+  atomicOr(ab.status, kStatusTimeout);
+}
+
+// Slice k of a unit's pieces, merged into the output: rows block k % row_blocks,
+// columns block k / row_blocks.  `ring`: kMergeBytes of idle memory.
+template <int D>
+__device__ __forceinline__ bool merge_slice(const PagedParams& p, const Pieces& u, uint8_t* ring, int k, int row_blocks,
+                                            int col_blocks, Meeting& meet) {
+  const int lane = threadIdx.x & 31, quarter = threadIdx.x >> 5;
+  const int rows = u.rows, of = u.of;
+  auto slot = [&](int i) { return p.slots + static_cast<long long>(u.place(p, i)) * p.slot_bytes; };
+  const int rb = k % row_blocks, cb = k / row_blocks;
+  const int r_begin = rb * rows / row_blocks, r_end = (rb + 1) * rows / row_blocks;
+  const int c_begin = cb * (D / 4) / col_blocks, c_end = (cb + 1) * (D / 4) / col_blocks;
+  // as many rows, and then columns, at a time as the memory holds of all pieces
+  constexpr int kRoom = PCfg<D>::kMergeBytes - PCfg<D>::kPartBytes;
+  const int room = kRoom / of;
+  const int most_rows = min(r_end - r_begin, room / 24);
+  const int most_cols = min(c_end - c_begin, (room / most_rows - 8) / 16);
+  float4* o = reinterpret_cast<float4*>(ring);
+  float4* part_o = reinterpret_cast<float4*>(ring + kRoom);
+  float2* part_ml = reinterpret_cast<float2*>(part_o + kBlockM);
+  for (int r0 = r_begin; r0 < r_end; r0 += most_rows) {
+    for (int c0 = c_begin; c0 < c_end; c0 += most_cols) {
+      const int nr = min(most_rows, r_end - r0), nc = min(most_cols, c_end - c0), nv = nr * nc;
+      float2* ml = reinterpret_cast<float2*>(o + of * nv);
+      if ((r0 > r_begin || c0 > c_begin) && !meet()) return false;
+      for (int v = lane; v < nv; v += 32) {                  // a warp takes every fourth piece
+        const int c = v / nr;
+        const int at = ((c0 + c) * rows + r0 + v - c * nr) * 16;
+#pragma unroll 4
+        for (int i = quarter; i < of; i += 4) cp_async16(o + i * nv + v, slot(i) + at);
+      }
+#pragma unroll 4
+      for (int x = threadIdx.x; x < of * nr; x += kBlockM) {
+        const int i = x / nr;
+        ml[x] = __ldcg(reinterpret_cast<const float2*>(slot(i) + rows * D * 4) + r0 + x - i * nr);
+      }
+      cp_async_wait<0>();
+      if (!meet()) return false;
+      // `parts` threads for a vector, each summing every parts'th piece
+      const int parts = max(1, kBlockM / nv);
+      for (int x = threadIdx.x; x < nv * parts; x += kBlockM) {
+        const int part = x / nv, v = x - part * nv, rw = v % nr;
+        float top = -INFINITY;
+#pragma unroll 4
+        for (int i = part; i < of; i += parts) top = fmaxf(top, ml[i * nr + rw].x);
+        const float base = top == -INFINITY ? 0.f : top;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        float sum = 0.f;
+#pragma unroll 4
+        for (int i = part; i < of; i += parts) {
+          const float2 mi = ml[i * nr + rw];
+          add_weighed(acc, sum, o[i * nv + v], mi.y, weight(mi.x, base));
+        }
+        if (parts == 1) {
+          write_out<D>(p, u.row0, u.head0, r0 + rw, (c0 + v / nr) * 4, acc, sum > 0.f ? 1.f / sum : 0.f);
+        } else {
+          part_o[x] = acc;
+          part_ml[x] = make_float2(top, sum);
+        }
+      }
+      if (parts > 1) {
+        if (!meet()) return false;
+        const int v = threadIdx.x;
+        if (v < nv) {
+          float top = -INFINITY;
+          for (int i = 0; i < parts; ++i) top = fmaxf(top, part_ml[i * nv + v].x);
+          const float base = top == -INFINITY ? 0.f : top;
+          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+          float sum = 0.f;
+          for (int i = 0; i < parts; ++i) {
+            const float2 mi = part_ml[i * nv + v];
+            add_weighed(acc, sum, part_o[i * nv + v], mi.y, weight(mi.x, base));
+          }
+          write_out<D>(p, u.row0, u.head0, r0 + v % nr, (c0 + v / nr) * 4, acc, sum > 0.f ? 1.f / sum : 0.f);
+        }
+      }
+    }
+  }
+  return true;
+}
+
+// All softmax threads of a run that has published its piece of a sliced unit: its
+// slice, if it takes one.  `most`: runs that can take one, the unit's last ones;
+// `left`: two words of shared memory, zero.  Returns how often the threads have
+// met, -1 if they gave up.
+template <int D>
+__device__ __forceinline__ int merge_slices(const PagedParams& p, const Pieces& u, uint8_t* ring, int most, uint64_t* bar,
+                                         int met, long long limit, volatile int* left, AbortState ab) {
+  Meeting meet{bar, met, ab};
+  most = min(most, max(1, u.rows * (D / 4) / kSliceVectors));
+  const int row_blocks = min(most, u.rows), col_blocks = most / row_blocks;
+  const int slicers = row_blocks * col_blocks;
+  const int first = u.cta - u.j + u.of - slicers;            // the first slice's run
+  const bool final = u.j == u.of - 1;
+  if (u.cta < first) return met;
+  bool got = true;
+  for (int x = threadIdx.x; x < u.of && got; x += kBlockM)
+    got = wait_word(p.flags + u.place(p, x), [&](unsigned long long v) { return v == p.call; },
+                    final ? limit : kPatience, ab);
+  if (!got) {
+    if (final) time_out(ab);
+    else left[0] = 1;
+  }
+  if (!meet() || *ab.flag != 0) return -1;
+  const bool taken = left[0] == 0;
+  if (threadIdx.x == 0)
+    asm volatile("st.release.gpu.global.u64 [%0], %1;" ::"l"(p.states + u.cta),
+                 "l"(static_cast<unsigned long long>(taken ? kTaken : kLeft)) : "memory");
+  if (!taken) return meet.met;
+  int k = u.cta - first;
+  while (true) {
+    if (!merge_slice<D>(p, u, ring, k, row_blocks, col_blocks, meet)) return -1;
+    if (!final) return meet.met;
+    if (k == slicers - 1) {
+      // what became of the others'?  Then nobody waits for the flags any more.
+      for (int x = threadIdx.x; x < slicers - 1; x += kBlockM) {
+        if (!wait_word(p.states + first + x, [](unsigned long long v) { return v != kOpen; }, limit, ab)) time_out(ab);
+        else if (load_acquire(p.states + first + x) == kLeft) left[1] = 1;
+      }
+      if (!meet() || *ab.flag != 0) return -1;
+      for (int x = threadIdx.x; x < u.of; x += kBlockM) p.flags[u.place(p, x)] = 0;
+      if (left[1] == 0) return meet.met;
+      k = -1;
+    } else if (!meet()) {                                    // (the memory has been read)
+      return -1;
+    }
+    do ++k; while (k < slicers - 1 && load_acquire(p.states + first + k) != kLeft);
+    if (k == slicers - 1) return meet.met;
+  }
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
     sdpa_paged_split(const __grid_constant__ PagedParams p) {
@@ -538,7 +718,7 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
   constexpr int R = C::kRing;
   extern __shared__ uint8_t smem_raw[];
   __shared__ ScheduleShared sched;
-  __shared__ int source_runs[kMaxSources];
+  __shared__ int left[2];                                    // slices left to the unit's last run: this one's, others'
   const uint32_t raw_u32 = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + (((raw_u32 + 1023u) & ~1023u) - raw_u32);
   const uint32_t smem_base = smem_u32(smem);
@@ -560,6 +740,7 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
   const int lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
+    left[0] = left[1] = 0;
     mbar_init(q_full, 1);
     mbar_init(q_empty, 1);
     for (int s = 0; s < R; ++s) {
@@ -765,7 +946,7 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
     Walk w;
     bool more = w.begin(p, last, last_seq, run, cut.scheme);
     int u = 0, pieces = 0;
-    int merged = 0;                                          // steps of merge
+    Meeting meet{merge, 0, ab};
     bool ok = true;
 
     // Rows of V past the length hold whatever the page held (or an older
@@ -838,24 +1019,23 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
       // what earlier runs published
       const bool open_above = w.kt1 < w.tiles, open_below = kt0 > 0;
       const bool whole = !open_above && !open_below;
-      int sources = 0;
+      // its pieces, and which of them this is (the first key tile's last item says
+      // which run it belongs to)
+      int of = 1, j = 0;
       if (!whole) {
-        // the pieces that this one merges, in the order of the list
-        // (the first key tile's last item says which run it belongs to)
-        int j = static_cast<int>(last.item) - 1, pieces = last.pieces;
+        j = static_cast<int>(last.item) - 1;
+        of = last.pieces;
         if (cut.scheme != kPieces) {
-          const long long unit = cut.begin(cta) + w.off;
-          const int first = cut.run_of(unit + w.w.of(1) - 1);
+          const long long begin = cut.begin(cta) + w.off;
+          const int first = cut.run_of(begin + w.w.of(1) - 1);
           j = cta - first;
-          pieces = cut.run_of(unit + w.w.of(w.tiles) - 1) - first + 1;
-        }
-        const int c0 = cta - j, bits = radix_bits(pieces, rows * D * 4, narrow);
-        const int low = open_above ? j + 1 - block_size(j, bits) : 0;
-        for (int at = j; at > low; at -= block_size(at - 1, bits)) {
-          if (threadIdx.x == 0) source_runs[sources] = c0 + at - 1;
-          ++sources;
+          of = cut.run_of(begin + w.w.of(w.tiles) - 1) - first + 1;
         }
       }
+      const bool sliced = of > (narrow ? kTogetherNarrow : kTogether), publishes = open_above || sliced;
+      const int sources = publishes ? 0 : of - 1;            // the runs before this one, merged here
+      const Pieces unit{rows, w.q.start + token0, w.hk * p.group, cta, j, of, sliced};
+      const int place = unit.place(p, j);                    // this piece's slot
       const long long out_row =
           static_cast<long long>(w.q.start + token0 + token) * p.h + w.hk * p.group + head;
       // a published piece of this unit: its bytes, run sl's slot, its (m, l)
@@ -863,23 +1043,22 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
       auto slot = [&](int sl) { return p.slots + static_cast<long long>(sl) * p.slot_bytes; };
       auto ml_of = [&](uint8_t* piece) { return reinterpret_cast<float2*>(piece + o_bytes); };
       uint8_t* ring = smem + C::kKOff;
-      // All softmax threads: what was written before is there for all after.
-      auto meet = [&]() -> bool {
-        mbar_arrive(merge);
-        return mbar_wait_warp(merge, static_cast<uint32_t>(merged++) & 1u, ab);
-      };
       // The slot is written: its flag, released after everybody's writes.
       auto publish = [&]() -> bool {
         if (!meet()) return false;
-        if (threadIdx.x == 0) set_flag(p.flags + cta, p.call);
+        if (threadIdx.x == 0) set_flag(p.flags + place, p.call);
         return true;
       };
-      // Everything this run merges has been published, and the ring is idle.
+      const long long patience = kWaitLimitCycles + 4096 * run;   // a run's items take well below 4096 each
+      // What this run merges alone has been published.
       auto wait_sources = [&]() -> bool {
-        if (!meet()) return false;                           // the list is there
         bool got = true;
-        if (static_cast<int>(threadIdx.x) < sources)
-          got = take_flag(p.flags + source_runs[threadIdx.x], p.call, kWaitLimitCycles + 4096 * run, ab);
+        if (static_cast<int>(threadIdx.x) < sources) {
+          unsigned long long* flag = p.flags + cta - 1 - static_cast<int>(threadIdx.x);
+          got = wait_word(flag, [&](unsigned long long v) { return v == p.call; }, patience, ab);
+          if (got) *flag = 0;
+          else time_out(ab);
+        }
         return __all_sync(0xffffffffu, got) && meet();
       };
       // O columns [c kOChunk, +kOChunk) of this row, normalised into the output
@@ -894,14 +1073,6 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
           x.w = pack_bf16x2(__uint_as_float(o[e * 8 + 6]) * inv_l, __uint_as_float(o[e * 8 + 7]) * inv_l);
           dst[e] = x;
         }
-      };
-      // four columns of row rw of the tile into the output
-      auto write_out = [&](int rw, int col, const float4& v, float inv) {
-        const int tok = rw / p.group;
-        *reinterpret_cast<uint2*>(
-            p.out + (static_cast<long long>(w.q.start + token0 + tok) * p.h + w.hk * p.group + rw -
-                     tok * p.group) * D + col) =
-            make_uint2(pack_bf16x2(v.x * inv, v.y * inv), pack_bf16x2(v.z * inv, v.w * inv));
       };
       if (n <= 0) {
         // nothing to see: rows of zeros
@@ -990,7 +1161,7 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
         }
         const float f = weight(m_used, sub);
         // own piece: where it is kept while it is not whole
-        uint8_t* own = sources > 0 ? ring : slot(cta);
+        uint8_t* own = publishes ? slot(place) : ring;
         if (valid && quarter == 0) {
           if (!whole) ml_of(own)[row] = make_float2(mm, ll);
           xinv[row] = ll > 0.f ? 1.f / ll : 0.f;
@@ -1038,7 +1209,7 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
               v.z += o.z;
               v.w += o.w;
             }
-            if (whole) write_out(x % rows, c0 + x / rows * 4, v, xinv[x % rows]);
+            if (whole) write_out<D>(p, unit.row0, unit.head0, x % rows, c0 + x / rows * 4, v, xinv[x % rows]);
             else reinterpret_cast<float4*>(own)[c0 / 4 * rows + x] = v;
           }
         }
@@ -1052,7 +1223,7 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
             const int count = min(fit, sources - i0);
             const bool further = i0 + count < sources;
             for (int i = quarter; i < count; i += 4) {       // a warp for a piece
-              const uint8_t* src = slot(source_runs[i0 + i]);
+              const uint8_t* src = slot(cta - 1 - i0 - i);
               uint8_t* dst = ring + (1 + i) * piece_bytes;
 #pragma unroll 8
               for (int x = lane * 16; x < piece_bytes; x += 32 * 16) cp_async16(dst + x, src + x);
@@ -1089,7 +1260,7 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
                 reinterpret_cast<float4*>(slot(cta))[x] = acc;
                 if (x < rows) ml_of(slot(cta))[rw] = ml_row;
               } else {
-                write_out(rw, x / rows * 4, acc, sum > 0.f ? 1.f / sum : 0.f);
+                write_out<D>(p, unit.row0, unit.head0, rw, x / rows * 4, acc, sum > 0.f ? 1.f / sum : 0.f);
               }
             }
             if (further) {
@@ -1178,7 +1349,7 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
             const int rw = min(row, rows - 1);
             auto fetch = [&](int i, int c) {
               if (i < sources) {
-                const float4* src = reinterpret_cast<const float4*>(slot(source_runs[i])) + rw;
+                const float4* src = reinterpret_cast<const float4*>(slot(cta - 1 - i)) + rw;
                 float4* dst = reinterpret_cast<float4*>(ring) + row;
 #pragma unroll
                 for (int e = 0; e < kVec; ++e)
@@ -1188,14 +1359,14 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
             };
 #pragma unroll 1
             for (int c = 0; c < kSteps; ++c) fetch(0, c);
-            float2 ml = __ldcg(ml_of(slot(source_runs[0])) + rw);
+            float2 ml = __ldcg(ml_of(slot(cta - 1)) + rw);
 #pragma unroll 1
             for (int i = 0; i < sources; ++i) {
               const float top = fmaxf(mm, ml.x), base = top == -INFINITY ? 0.f : top;
               const float fo = weight(mm, base), fi = weight(ml.x, base);
               mm = top;
               ll = ll * fo + ml.y * fi;
-              if (i + 1 < sources) ml = __ldcg(ml_of(slot(source_runs[i + 1])) + rw);
+              if (i + 1 < sources) ml = __ldcg(ml_of(slot(cta - 2 - i)) + rw);
 #pragma unroll 1
               for (int c = 0; c < kSteps; ++c) {
                 uint32_t o[C::kOChunk];
@@ -1240,9 +1411,9 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
             tmem_ld_chunk(lane_base + C::kOCol + c * C::kOChunk, o);
             tmem_ld_wait();
             reg_fence(o);
-            if (open_above) {
+            if (publishes) {
               if (valid) {
-                float4* dst = reinterpret_cast<float4*>(slot(cta)) + row;
+                float4* dst = reinterpret_cast<float4*>(slot(place)) + row;
 #pragma unroll
                 for (int e = 0; e < C::kOChunk / 4; ++e)
                   dst[(c * (C::kOChunk / 4) + e) * rows] =
@@ -1274,10 +1445,20 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
               }
             }
           }
-          if (open_above && valid) ml_of(slot(cta))[row] = make_float2(mm, ll);
+          if (publishes && valid) ml_of(slot(place))[row] = make_float2(mm, ll);
         }
       }
-      if (open_above && !(ok = publish())) break;
+      if (publishes) {
+        if (sliced && threadIdx.x == 0) p.states[cta] = kOpen;
+        if (!(ok = publish())) break;
+        if (sliced) {
+          // (a run's first piece, unless it is all of the run, is followed by
+          // others, and takes no slice)
+          const int most = of - (cut.scheme == kPieces ? 0 : 1);
+          meet.met = merge_slices<D>(p, unit, ring, most, merge, meet.met, patience, left, ab);
+          if (!(ok = meet.met >= 0)) break;
+        }
+      }
       __syncwarp();
       tc_fence_before();
       mbar_arrive(o_free);
