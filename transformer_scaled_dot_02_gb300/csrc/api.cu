@@ -441,6 +441,21 @@ int paged_split_ctas(int b, int n_tokens, int h_kv, int group, int d, long long 
   return static_cast<int>(std::max(1ll, std::min(most, tiles)));
 }
 
+// log_step, step_inverse and residues from tile_tokens.
+void paged_steps(sdpa::PagedParams* p) {
+  p->log_step = 0;
+  while (p->tile_tokens % (2 << p->log_step) == 0 && sdpa::kPagedKeyTile % (2 << p->log_step) == 0) ++p->log_step;
+  const int period = sdpa::kPagedKeyTile >> p->log_step, step = p->tile_tokens >> p->log_step;
+  p->step_inverse = 0;
+  int sum = 0;
+  for (int k = 0; k <= period; ++k) {
+    const int residue = k * step % period;
+    p->residues[k] = static_cast<uint16_t>(sum);
+    if (residue == 1 % period) p->step_inverse = k % period;
+    sum += residue;
+  }
+}
+
 // The number that marks a call's workspace slots as written.  The call clears
 // its marks, so a replayed launch may use its number again; what an
 // unwritten workspace holds must only not be this number, so the numbers are
@@ -881,6 +896,7 @@ sdpa_status sdpa_paged_forward(const void* q, const void* k_pages, const void* v
   sdpa::PagedParams p;
   p.group = h / h_kv;
   p.tile_tokens = 128 / p.group;
+  paged_steps(&p);
   if (!make_map_rows(&p.tm_q, q, d, h, n_tokens, q_stride, p.group, p.tile_tokens) ||
       !make_map_rows(&p.tm_q_narrow, q, d, h, n_tokens, q_stride, p.group,
                      p.group <= 16 ? 16 / p.group : p.tile_tokens) ||

@@ -120,7 +120,12 @@ struct PagedParams {
   const int32_t* kv_lengths;  // [b]
   unsigned* status;
   int b, n_tokens, h, h_kv;
-  int group, tile_tokens;     // h / h_kv; tokens per row tile, 128 / group
+  int group, tile_tokens;     // h / h_kv; tokens per row tile, t = 128 / group
+  // t = 2^log_step t', 2^log_step the largest power of two that divides t and the
+  // key tile, P = kPagedKeyTile / 2^log_step: t' 's inverse modulo P, and the sums
+  // of the first k of 0, t', 2 t', .. modulo P
+  int log_step, step_inverse;
+  uint16_t residues[65];
   int page_shift, n_pages, pages_per_seq;
   int split_ctas;             // CTAs of the split kernel (runs, at most)
   unsigned long long ctas_magic;   // ceil(2^64 / split_ctas)

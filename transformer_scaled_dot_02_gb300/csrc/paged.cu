@@ -99,13 +99,10 @@ struct Weight {
   int start, log_tile;
   __device__ long long of(long long tiles) const { return start + (tiles << log_tile); }
 };
-// How the work is counted and cut.  kPieces: every unit in pieces of its own,
-// a run for each.  kTiles: key tiles alone, runs of equally many.  kWeighed: as above.
-enum Scheme { kWeighed, kTiles, kPieces };
-__device__ __forceinline__ Weight weight_of(Scheme scheme, bool narrow) {
-  return scheme != kWeighed ? Weight{0, 0} : (narrow ? Weight{14, 2} : Weight{18, 2});
-}
-constexpr int kFewTiles = 8;
+__device__ __forceinline__ Weight weight_of(bool narrow) { return narrow ? Weight{14, 2} : Weight{18, 2}; }
+// How the work is cut.  kPieces: every unit into pieces of its own, a run for
+// each, where that many runs fit the GPU.  kWeighed: into equal runs by weight.
+enum Scheme { kWeighed, kPieces };
 // kPieces: a piece of up to 8 KB has up to four key tiles, a larger one eight, one
 // over 32 KB sixteen: a further cut saves time at the key tiles (0.5 to 0.9 us
 // each), but there are more pieces to merge.  14 single tokens over 749 to 1147
@@ -138,45 +135,30 @@ __device__ __forceinline__ int unit_pieces(const PagedParams& p, const Seq& q, i
 __device__ __forceinline__ long long unit_cost(const PagedParams& p, const Seq& q, int r, Scheme scheme) {
   const int tiles = walk_tiles(tile_keys(p, q, r));
   if (scheme == kPieces) return unit_pieces(p, q, r, tiles);
-  return weight_of(scheme, tile_rows(p, q, r) <= kNarrowRows).of(tiles);
+  return weight_of(tile_rows(p, q, r) <= kNarrowRows).of(tiles);
 }
 
 // Key tiles of the first f row tiles, f < q.tiles.  They see A + (i + 1) t
 // keys, A = len - n: z of them walk one tile, the others ceil((A + (i + 1) t)
-// / 64).
+// / 64).  With t = g t', 64 = g P, t' odd (or P = 1), the floor of (base + t i) / 64
+// is that of (b + t' i) / P, b = base / g, so their sum is
+//   (n b + t' n (n - 1) / 2 - sum_i (b + t' i) mod P) / P,
+// and the residues are P's in steps of t' from place b / t' mod P on: p.residues
+// holds the sums of the first k of them.
 __device__ __noinline__ long long tiles_before(const PagedParams& p, const Seq& q, int f) {
   const int t = p.tile_tokens;
   const int a = q.len - q.n;
   const int z = kBN - a >= t ? min(f, (kBN - a) / t) : 0;
   const int cnt = f - z;
   if (cnt <= 0) return z;
-  const int base = a + t * (z + 1) + kBN - 1;       // > 64
+  const int log_p = kBNShift - p.log_step, mask = (1 << log_p) - 1;
+  const int b = (a + t * (z + 1) + kBN - 1) >> p.log_step;   // > 0
   const long long n = cnt;
-  long long sum = z;
-  if ((t & (t - 1)) == 0) {                          // groups that are powers of two
-    sum += n * (base / kBN);
-    if (t >= kBN) return sum + t / kBN * (n * (n - 1) / 2);
-    // floor((o + t i) / 64) = floor((o / t + i) / (64 / t)), summed below m:
-    const int log_t = __ffs(t) - 1, log_per = 6 - log_t;
-    auto below = [&](long long m) {
-      const long long q2 = m >> log_per;
-      return (q2 * (q2 - 1) / 2 << log_per) + q2 * (m - (q2 << log_per));
-    };
-    const int o = (base % kBN) >> log_t;
-    return sum + below(o + n) - below(o);
-  }
-  // the sum over 64 consecutive i grows by 64 t from one such block to the next
-  const int blocks = cnt / kBN, rest = cnt % kBN;
-  long long head = 0, full = 0;                      // the first `rest` terms; the first 64
-  const int walk = blocks > 0 ? kBN : rest;
-  for (int i = 0; i < walk; ++i) {
-    const int c = (base + t * i) / kBN;
-    full += c;
-    if (i < rest) head += c;
-  }
-  const long long m = blocks;
-  return sum + m * full + static_cast<long long>(kBN) * t * (m * (m - 1) / 2) + head +
-         static_cast<long long>(rest) * t * m;
+  const int i0 = static_cast<int>(static_cast<unsigned>(b) * p.step_inverse) & mask, i1 = i0 + (cnt & mask);
+  const int full = p.residues[mask + 1];
+  const long long rest = (n >> log_p) * full + (i1 > mask ? full + p.residues[i1 - mask - 1] : p.residues[i1]) -
+                         p.residues[i0];
+  return z + ((n * b + (t >> p.log_step) * (n * (n - 1) / 2) - rest) >> log_p);
 }
 
 // Cost of row tiles 0 .. r-1 (r <= q.tiles) of one key-value head: all but
@@ -194,7 +176,7 @@ __device__ __forceinline__ long long cost_before(const PagedParams& p, const Seq
     if (scheme == kPieces) {
       sum = full_pieces_before(p, q, f);
     } else {
-      const Weight w = weight_of(scheme, false);
+      const Weight w = weight_of(false);
       sum = static_cast<long long>(w.start) * f + (tiles_before(p, q, f) << w.log_tile);
     }
   }
@@ -211,17 +193,15 @@ struct Place {
   int pieces, kt0, kt1;
 };
 
-// What there is to do: key tiles, the pieces that they may be cut into, and the
-// units' weights.
+// What there is to do: the pieces that the units may be cut into, and their weights.
 struct Work {
-  long long tiles, pieces, cost;
+  long long pieces, cost;
   __device__ void add(const Work& o) {
-    tiles += o.tiles;
     pieces += o.pieces;
     cost += o.cost;
   }
   __device__ long long of(Scheme scheme) const {
-    return scheme == kPieces ? pieces : scheme == kTiles ? tiles : cost;
+    return scheme == kPieces ? pieces : cost;
   }
 };
 
@@ -264,22 +244,20 @@ __device__ bool find_place(const PagedParams& p, ScheduleShared* sh, int c, int 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int per = (p.b + kThreads - 1) / kThreads;
   const int s0 = min(tid * per, p.b), s1 = min(s0 + per, p.b);
-  Work mine = {0, 0, 0};
+  Work mine = {0, 0}, one = {0, 0};                          // one: a head of the last sequence
   Seq q;
   for (int s = s0; s < s1; ++s) {
     q = load_seq(p, s);
     if (q.tiles == 0) continue;
     const int f = q.tiles - 1;                               // full tiles, the last one aside
     const int last = walk_tiles(q.len), rows = tile_rows(p, q, f);
-    Work w = {last, pieces_of(p, rows, last), weight_of(kWeighed, rows <= kNarrowRows).of(last)};
+    Work w = {pieces_of(p, rows, last), weight_of(rows <= kNarrowRows).of(last)};
     if (f > 0) {
-      const Weight weight = weight_of(kWeighed, false);
-      const long long full = tiles_before(p, q, f);
-      w.tiles += full;
+      const Weight weight = weight_of(false);
       w.pieces += full_pieces_before(p, q, f);
-      w.cost += static_cast<long long>(weight.start) * f + (full << weight.log_tile);
+      w.cost += static_cast<long long>(weight.start) * f + (tiles_before(p, q, f) << weight.log_tile);
     }
-    w.tiles *= p.h_kv;
+    one = w;
     w.pieces *= p.h_kv;
     w.cost *= p.h_kv;
     mine.add(w);
@@ -287,40 +265,37 @@ __device__ bool find_place(const PagedParams& p, ScheduleShared* sh, int c, int 
   Work incl = mine;
 #pragma unroll
   for (int x = 1; x < 32; x <<= 1) {
-    const Work o = {__shfl_up_sync(0xffffffffu, incl.tiles, x), __shfl_up_sync(0xffffffffu, incl.pieces, x),
-                    __shfl_up_sync(0xffffffffu, incl.cost, x)};
+    const Work o = {__shfl_up_sync(0xffffffffu, incl.pieces, x), __shfl_up_sync(0xffffffffu, incl.cost, x)};
     if (lane >= x) incl.add(o);
   }
   if (lane == 31) sh->warp_sum[warp] = incl;
   __syncthreads();
-  Work sum = {0, 0, 0}, before = {incl.tiles - mine.tiles, incl.pieces - mine.pieces, incl.cost - mine.cost};
+  Work sum = {0, 0}, before = {incl.pieces - mine.pieces, incl.cost - mine.cost};
 #pragma unroll
   for (int w = 0; w < kThreads / 32; ++w) {
     const Work v = sh->warp_sum[w];
     if (w < warp) before.add(v);
     sum.add(v);
   }
-  // (a run is never shorter than a key tile, so no run inside a unit is empty)
-  const Scheme scheme = sum.pieces <= max_ctas ? kPieces
-                        : sum.tiles < 1ll * kFewTiles * max_ctas && 2 * sum.pieces > sum.tiles ? kTiles : kWeighed;
-  const int n = static_cast<int>(min(static_cast<long long>(max_ctas), scheme == kPieces ? sum.pieces : sum.tiles));
+  // (there are no more pieces than key tiles: no run is shorter than a key tile)
+  const Scheme scheme = sum.pieces <= max_ctas ? kPieces : kWeighed;
+  const int n = scheme == kPieces ? static_cast<int>(sum.pieces) : max_ctas;
   if (c >= n) return false;
   const long long own = mine.of(scheme), excl = before.of(scheme);
   *cut = Cut(sum.of(scheme), n, max_ctas, p.ctas_magic, scheme);
   const long long x = cut->begin(c + 1) - 1;                 // its last item
   if (own > 0 && excl <= x && x < excl + own) {
-    long long rem = x - excl;
+    long long rem = x - excl, head = one.of(scheme);
     Place pl;
     pl.s = s0;
     if (per > 1) {
       for (pl.s = s0; pl.s < s1; ++pl.s) {
         q = load_seq(p, pl.s);
-        const long long w = cost_before(p, q, q.tiles, scheme) * p.h_kv;
-        if (rem < w) break;
-        rem -= w;
+        head = cost_before(p, q, q.tiles, scheme);
+        if (rem < head * p.h_kv) break;
+        rem -= head * p.h_kv;
       }
     }
-    const long long head = cost_before(p, q, q.tiles, scheme);
     pl.hk = static_cast<int>(divide(rem, head));
     rem -= pl.hk * head;
     pl.r = 0;
@@ -383,7 +358,7 @@ struct Walk {
     keys = tile_keys(p, q, r);
     tiles = walk_tiles(keys);
     rows = tile_rows(p, q, r);
-    w = weight_of(scheme, rows <= kNarrowRows);
+    w = weight_of(rows <= kNarrowRows);
   }
   // The first piece of a run of `run` items that ends at `end`; false: none.
   __device__ bool begin(const PagedParams& p, const Place& end, const Seq& seq, long long run, Scheme how) {
