@@ -130,6 +130,47 @@ def test_attention_one_workspace_for_calls_of_all_shapes():
     sd.sdpa_device_check()
 
 
+@pytest.mark.parametrize("d,h,h_kv,new,lens", [
+    (64, 2, 2, [69], [26595]),              # 52 pieces of 69 rows
+    (128, 16, 4, [32], [8192]),             # 8 of 128 rows, 4 times
+    (16, 128, 1, [1], [6000]),              # 24 of 128 rows
+    (32, 3, 1, [33], [12000]),              # 24 of 99 rows
+    (256, 5, 1, [3], [30000]),              # 59 of 15 rows
+    (64, 16, 1, [1, 1], [33000, 20000]),    # 129 and 79 of 16 rows
+    (128, 1, 1, [1], [40000]),              # 157 of a single row: slices of columns
+    (16, 32, 16, [1, 1], [30000, 100]),     # more than there are runs: cut by weight
+    (64, 16, 4, [1, 1], [70000, 300]),
+    (256, 16, 2, [17], [20000]),
+])
+def test_attention_in_slices(d, h, h_kv, new, lens):
+    """Units of so many pieces that several runs merge them, in a workspace that
+    holds anything; the same bits again, called and replayed."""
+    import torch
+    rng = np.random.default_rng(520 + d + sum(lens))
+    case = _case(rng, new, lens, h, h_kv, d, 64)
+    cache, dense, starts, q = case
+    kp, vp = (dev(cache.pages_of(x, np.nan)) for x in dense)
+    args = (dev(q), kp, vp, dev_int(cache.table), dev_int(starts), dev_int(cache.lens))
+    ws = sd.paged_workspace(args[0], kp, args[3])
+    ws.fill_(0xff)
+    out = torch.empty_like(args[0])
+    sd.paged_attention(*args, out=out, workspace=ws)
+    sd.sdpa_device_check()
+    _check(out, *case)
+    want = out.clone()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        for _ in range(3):
+            sd.paged_attention(*args, out=out, workspace=ws)
+    for _ in range(3):
+        out.fill_(float("nan"))
+        graph.replay()
+        assert torch.equal(_raw(out), _raw(want))
+    sd.sdpa_device_check()
+
+
 def test_attention_many_sequences():
     """More sequences than threads in a block, most of them short, some empty."""
     rng = np.random.default_rng(500)

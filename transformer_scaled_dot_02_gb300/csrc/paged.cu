@@ -417,16 +417,24 @@ struct Walk {
 // one piece's, but publishing the last piece and asking for all others' takes 2 to
 // 3 us.  One sequence of 26595 positions, 69 new tokens of 2 heads of 64 (52
 // pieces of 18 KB a head) takes 17 us in slices and took 27 as a tree of radix 4.
-// At 7 pieces of 64 KB (2 chunks of 485 and 1 tokens, 20 heads of 128) the last one
-// alone takes 66 us, slices 79: there every SM merges at once, and slices read
-// every piece once more.
+// Of 8 pieces of 64 KB (32 tokens over 8192 positions, 16 / 4 heads of 128) the last
+// run alone takes 23.8 us, slices 22.1; of 3 of 128 KB (3
+// chunks of 200 tokens, 8 / 1 heads of 256) 28.8 and 33.2.  In a cut by weight,
+// where every SM merges at once, 5 to 7 of 64 KB (2 chunks of 992 and 188 tokens, 20
+// / 4 heads of 128) take 66.0 and 66.1 us, 4 69.1 in slices; of up to 16 narrow ones
+// (single tokens, 32 / 8 heads of 128) 12.6 us, in slices 14.8.
+//
 // A slicer waits for pieces of later runs too, and those need not be running
 // (with another kernel on the GPU): it waits so long and then leaves its slice
 // to the unit's last run, whose own wait is for earlier ones alone.  A slicer's
 // STATE says what became of its slice: kOpen while it waits, kTaken, kLeft.
-constexpr int kTogether = 8, kTogetherNarrow = 16;   // pieces that the last run merges alone, at most
+// pieces that the last run merges alone, at most
+constexpr int kTogether = 8, kTogetherPieces = 4, kTogetherNarrow = 16;
 constexpr int kSliceVectors = 16;          // of a slice, at least
-constexpr long long kPatience = 1 << 17;   // clock cycles, about 65 us: runs end within a few of each other
+#ifndef SDPA_TEST_PATIENCE
+#define SDPA_TEST_PATIENCE (1 << 17)       // (a test leaves slices at once)
+#endif
+constexpr long long kPatience = SDPA_TEST_PATIENCE;   // clock cycles, about 65 us: runs end within a few of each other
 enum State : unsigned long long { kOpen, kTaken, kLeft };
 
 __device__ __forceinline__ unsigned long long load_acquire(const unsigned long long* x) {
@@ -453,14 +461,6 @@ __device__ __forceinline__ void set_flag(unsigned long long* flag, unsigned long
 
 // 2^(m - sub), 0 for a piece that saw nothing
 __device__ __forceinline__ float weight(float m, float sub) { return ex2_approx(m - sub); }
-
-__device__ __forceinline__ void add_weighed(float4& acc, float& sum, const float4& v, float l, float f) {
-  sum += l * f;
-  acc.x += v.x * f;
-  acc.y += v.y * f;
-  acc.z += v.z * f;
-  acc.w += v.w * f;
-}
 
 // --------------------------------------------------------------------- split
 template <int D>
@@ -519,14 +519,15 @@ struct PCfg {
   static_assert(kBoxes * (kBN / kPagedMinPage) <= 32, "a lane of the producer warp for each box of a tile's parts");
 };
 
-// Four columns of row rw of a tile into the output (row0: the tile's first token,
-// head0: the group's first head).
+// Where row rw of a tile begins in the output (row0: the tile's first token, head0:
+// the group's first head), and four columns into the output.
 template <int D>
-__device__ __forceinline__ void write_out(const PagedParams& p, int row0, int head0, int rw, int col, const float4& v,
-                                          float inv) {
+__device__ __forceinline__ long long out_begin(const PagedParams& p, int row0, int head0, int rw) {
   const int tok = rw / p.group;
-  *reinterpret_cast<uint2*>(p.out + (static_cast<long long>(row0 + tok) * p.h + head0 + rw - tok * p.group) * D + col) =
-      make_uint2(pack_bf16x2(v.x * inv, v.y * inv), pack_bf16x2(v.z * inv, v.w * inv));
+  return (static_cast<long long>(row0 + tok) * p.h + head0 + rw - tok * p.group) * D;
+}
+__device__ __forceinline__ void write_four(uint16_t* at, const float4& v, float f) {
+  *reinterpret_cast<uint2*>(at) = make_uint2(pack_bf16x2(v.x * f, v.y * f), pack_bf16x2(v.z * f, v.w * f));
 }
 
 // Where the parts of a unit are: piece j of `of` (this run's) is run cta.
@@ -557,12 +558,13 @@ __device__ __forceinline__ void time_out(const AbortState& ab) {
 }
 
 // Slice k of a unit's pieces, merged into the output: rows block k % row_blocks,
-// columns block k / row_blocks.  `ring`: kMergeBytes of idle memory.
+// columns block k / row_blocks.  `ring`: kMergeBytes of idle memory.  There is one
+// warp on each of the SM's schedulers here, so every instruction's latency shows:
+// the rows' weights are worked out first, places move on without divisions.
 template <int D>
 __device__ __forceinline__ bool merge_slice(const PagedParams& p, const Pieces& u, uint8_t* ring, int k, int row_blocks,
                                             int col_blocks, Meeting& meet) {
-  const int lane = threadIdx.x & 31, quarter = threadIdx.x >> 5;
-  const int rows = u.rows, of = u.of;
+  const int tid = threadIdx.x, rows = u.rows, of = u.of;
   auto slot = [&](int i) { return p.slots + static_cast<long long>(u.place(p, i)) * p.slot_bytes; };
   const int rb = k % row_blocks, cb = k / row_blocks;
   const int r_begin = rb * rows / row_blocks, r_end = (rb + 1) * rows / row_blocks;
@@ -574,61 +576,95 @@ __device__ __forceinline__ bool merge_slice(const PagedParams& p, const Pieces& 
   const int most_cols = min(c_end - c_begin, (room / most_rows - 8) / 16);
   float4* o = reinterpret_cast<float4*>(ring);
   float4* part_o = reinterpret_cast<float4*>(ring + kRoom);
-  float2* part_ml = reinterpret_cast<float2*>(part_o + kBlockM);
+  long long* begin = reinterpret_cast<long long*>(part_o + kBlockM);   // of the rows in the output
   for (int r0 = r_begin; r0 < r_end; r0 += most_rows) {
     for (int c0 = c_begin; c0 < c_end; c0 += most_cols) {
       const int nr = min(most_rows, r_end - r0), nc = min(most_cols, c_end - c0), nv = nr * nc;
       float2* ml = reinterpret_cast<float2*>(o + of * nv);
       if ((r0 > r_begin || c0 > c_begin) && !meet()) return false;
-      for (int v = lane; v < nv; v += 32) {                  // a warp takes every fourth piece
-        const int c = v / nr;
-        const int at = ((c0 + c) * rows + r0 + v - c * nr) * 16;
+      // a thread takes vectors of every piece, or if there are few a warp takes
+      // those of every fourth piece
+      const bool many = nv >= kBlockM;
+      const int v0 = many ? tid : tid & 31, step = many ? kBlockM : 32;
+      const int i0 = many ? 0 : tid >> 5, i_step = many ? 1 : 4;
+      const int dc = step / nr, dr = step - dc * nr;
+      int c = v0 / nr, r = v0 - c * nr;
+      for (int v = v0; v < nv; v += step) {
+        const int at = ((c0 + c) * rows + r0 + r) * 16;
 #pragma unroll 4
-        for (int i = quarter; i < of; i += 4) cp_async16(o + i * nv + v, slot(i) + at);
+        for (int i = i0; i < of; i += i_step) cp_async16(o + i * nv + v, slot(i) + at);
+        c += dc;
+        r += dr;
+        if (r >= nr) {
+          r -= nr;
+          ++c;
+        }
       }
 #pragma unroll 4
-      for (int x = threadIdx.x; x < of * nr; x += kBlockM) {
+      for (int x = tid; x < of * nr; x += kBlockM) {
         const int i = x / nr;
         ml[x] = __ldcg(reinterpret_cast<const float2*>(slot(i) + rows * D * 4) + r0 + x - i * nr);
       }
+      if (tid < nr) begin[tid] = out_begin<D>(p, u.row0, u.head0, r0 + tid);
       cp_async_wait<0>();
       if (!meet()) return false;
-      // `parts` threads for a vector, each summing every parts'th piece
-      const int parts = max(1, kBlockM / nv);
-      for (int x = threadIdx.x; x < nv * parts; x += kBlockM) {
-        const int part = x / nv, v = x - part * nv, rw = v % nr;
-        float top = -INFINITY;
-#pragma unroll 4
-        for (int i = part; i < of; i += parts) top = fmaxf(top, ml[i * nr + rw].x);
-        const float base = top == -INFINITY ? 0.f : top;
+      // what each piece weighs in each row, in the place of m: 2^(m - M) / l of all;
+      // `lanes` lanes for a row
+      int lanes = 32;
+      while (lanes * nr > kBlockM) lanes >>= 1;
+      const int row = tid / lanes;
+      float top = -INFINITY, sum = 0.f;
+      if (row < nr)
+        for (int i = tid & (lanes - 1); i < of; i += lanes) top = fmaxf(top, ml[i * nr + row].x);
+      for (int x = lanes >> 1; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+      const float base = top == -INFINITY ? 0.f : top;
+      if (row < nr)
+        for (int i = tid & (lanes - 1); i < of; i += lanes) sum += ml[i * nr + row].y * weight(ml[i * nr + row].x, base);
+      for (int x = lanes >> 1; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+      const float inv = sum > 0.f ? 1.f / sum : 0.f;
+      if (row < nr)
+        for (int i = tid & (lanes - 1); i < of; i += lanes) ml[i * nr + row].x = weight(ml[i * nr + row].x, base) * inv;
+      if (!meet()) return false;
+      // the sums; `parts` threads for a vector, each summing every parts'th piece
+      auto sum_of = [&](int v, int rw, int from, int by) {
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        float sum = 0.f;
 #pragma unroll 4
-        for (int i = part; i < of; i += parts) {
-          const float2 mi = ml[i * nr + rw];
-          add_weighed(acc, sum, o[i * nv + v], mi.y, weight(mi.x, base));
+        for (int i = from; i < of; i += by) {
+          const float4 x = o[i * nv + v];
+          const float f = ml[i * nr + rw].x;
+          acc.x = fmaf(x.x, f, acc.x);
+          acc.y = fmaf(x.y, f, acc.y);
+          acc.z = fmaf(x.z, f, acc.z);
+          acc.w = fmaf(x.w, f, acc.w);
         }
-        if (parts == 1) {
-          write_out<D>(p, u.row0, u.head0, r0 + rw, (c0 + v / nr) * 4, acc, sum > 0.f ? 1.f / sum : 0.f);
-        } else {
-          part_o[x] = acc;
-          part_ml[x] = make_float2(top, sum);
-        }
-      }
-      if (parts > 1) {
-        if (!meet()) return false;
-        const int v = threadIdx.x;
-        if (v < nv) {
-          float top = -INFINITY;
-          for (int i = 0; i < parts; ++i) top = fmaxf(top, part_ml[i * nv + v].x);
-          const float base = top == -INFINITY ? 0.f : top;
-          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-          float sum = 0.f;
-          for (int i = 0; i < parts; ++i) {
-            const float2 mi = part_ml[i * nv + v];
-            add_weighed(acc, sum, part_o[i * nv + v], mi.y, weight(mi.x, base));
+        return acc;
+      };
+      if (many) {
+        c = v0 / nr;
+        r = v0 - c * nr;
+        for (int v = v0; v < nv; v += kBlockM) {
+          write_four(p.out + begin[r] + (c0 + c) * 4, sum_of(v, r, 0, 1), 1.f);
+          c += dc;
+          r += dr;
+          if (r >= nr) {
+            r -= nr;
+            ++c;
           }
-          write_out<D>(p, u.row0, u.head0, r0 + v % nr, (c0 + v / nr) * 4, acc, sum > 0.f ? 1.f / sum : 0.f);
+        }
+      } else {
+        const int parts = kBlockM / nv, part = tid / nv, v = tid - part * nv;
+        if (part < parts) part_o[tid] = sum_of(v, v % nr, part, parts);
+        if (!meet()) return false;
+        if (part == 0) {
+          float4 acc = part_o[v];
+          for (int i = 1; i < parts; ++i) {
+            const float4 x = part_o[i * nv + v];
+            acc.x += x.x;
+            acc.y += x.y;
+            acc.z += x.z;
+            acc.w += x.w;
+          }
+          write_four(p.out + begin[v % nr] + (c0 + v / nr) * 4, acc, 1.f);
         }
       }
     }
@@ -1007,7 +1043,7 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
           of = cut.run_of(begin + w.w.of(w.tiles) - 1) - first + 1;
         }
       }
-      const bool sliced = of > (narrow ? kTogetherNarrow : kTogether), publishes = open_above || sliced;
+      const bool sliced = of > (narrow ? kTogetherNarrow : cut.scheme == kPieces ? kTogetherPieces : kTogether), publishes = open_above || sliced;
       const int sources = publishes ? 0 : of - 1;            // the runs before this one, merged here
       const Pieces unit{rows, w.q.start + token0, w.hk * p.group, cta, j, of, sliced};
       const int place = unit.place(p, j);                    // this piece's slot
@@ -1184,7 +1220,7 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
               v.z += o.z;
               v.w += o.w;
             }
-            if (whole) write_out<D>(p, unit.row0, unit.head0, x % rows, c0 + x / rows * 4, v, xinv[x % rows]);
+            if (whole) write_four(p.out + out_begin<D>(p, unit.row0, unit.head0, x % rows) + c0 + x / rows * 4, v, xinv[x % rows]);
             else reinterpret_cast<float4*>(own)[c0 / 4 * rows + x] = v;
           }
         }
@@ -1235,7 +1271,7 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
                 reinterpret_cast<float4*>(slot(cta))[x] = acc;
                 if (x < rows) ml_of(slot(cta))[rw] = ml_row;
               } else {
-                write_out<D>(p, unit.row0, unit.head0, rw, x / rows * 4, acc, sum > 0.f ? 1.f / sum : 0.f);
+                write_four(p.out + out_begin<D>(p, unit.row0, unit.head0, rw) + x / rows * 4, acc, sum > 0.f ? 1.f / sum : 0.f);
               }
             }
             if (further) {
