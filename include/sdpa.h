@@ -265,8 +265,8 @@ sdpa_status sdpa_decode(const void* q, const void* k, const void* v, void* out, 
  *     q_stride, k_stride, v_stride elements apart (multiples of 8, at least
  *     the row itself), so the three may be columns of one projection's output
  *   q_out [n_tokens, h, d]  bf16, device, written, dense: the rotated queries.
- *     It may be q itself when q_stride == h * d.  q and q_out may both be NULL
- *     to append alone.
+ *     It may be q itself when q_stride == h * d; else it must not overlap the
+ *     other rows.  q and q_out may both be NULL to append alone.
  *   rope_freqs  device fp32 [d_rot / 2]: radians per position.  With angle
  *     t = position * rope_freqs[j], the pair (a, b) becomes
  *     (a cos t - b sin t, b cos t + a sin t); angles are exact to about 1e-6

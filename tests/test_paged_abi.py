@@ -44,7 +44,7 @@ def _append(lib, **kw):
 
 
 def _forward(lib, **kw):
-    a = dict(SHAPE, q=A, kp=A, vp=A, out=A, ws=A, ws_bytes=1 << 40, qs=512, scale=0.0)
+    a = dict(SHAPE, q=A, kp=A, vp=A, out=2 * A, ws=A, ws_bytes=1 << 40, qs=512, scale=0.0)
     a.update(kw)
     return lib.sdpa_paged_forward(a["q"], a["kp"], a["vp"], a["out"], a["ws"], a["ws_bytes"], a["b"], a["t"],
                                   a["h"], a["h_kv"], a["d"], a["page"], a["n_pages"], a["per_seq"], a["table"],
@@ -92,8 +92,15 @@ def test_append_argument_checks(lib):
     assert _append(lib, freqs=A + 2) == INVALID
     # in place only where the rows are dense
     assert _append(lib, q=A, q_out=A, qs=768) == INVALID
+    # rotated queries on the rows of another operand, or partly on their own
+    far = 16 * A
+    assert _append(lib, q=far, k=A, v=far, q_out=A) == INVALID
+    assert _append(lib, q=far, k=far, v=A, q_out=A + 64) == INVALID
+    assert _append(lib, q=A, k=far, v=far, q_out=A + 1024) == INVALID
     if not _gpu_visible():
-        assert _append(lib, q=A, q_out=A, qs=512) == NODEV
+        assert _append(lib, q=A, k=far, v=far, q_out=A, qs=512) == NODEV
+        assert _append(lib, q=A, k=far, v=far, q_out=A + 5 * 1024, qs=512) == NODEV
+        assert _forward(lib, out=A + 5 * 1024) == NODEV
 
 
 def test_forward_argument_checks(lib):
@@ -103,6 +110,10 @@ def test_forward_argument_checks(lib):
     assert _forward(lib, out=MIS) == INVALID
     assert _forward(lib, qs=504) == INVALID
     assert _forward(lib, qs=516) == UNSUPPORTED
+    # the output must not lie on the queries: 5 rows of 1024 bytes
+    for out in (A, A + 1024, A + 4 * 1024, A - 16, A - 4 * 1024):
+        assert _forward(lib, out=out) == INVALID, out
+    assert _forward(lib, out=A + 5 * 1024, scale=-1.0) == INVALID
     for scale in (-1.0, float("nan"), float("inf")):
         assert _forward(lib, scale=scale) == INVALID
     need = sd.sdpa_paged_workspace_size(3, 5, 8, 2, 64, 16, 12)

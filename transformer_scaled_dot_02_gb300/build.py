@@ -43,12 +43,13 @@ def _flags() -> list[str]:
                    "-I", CSRC, "--expt-relaxed-constexpr"]
 
 
-def _bind_command(nvcc: str, out: str) -> list[str] | None:
-    """Compiles and links the extension; None without torch."""
+def _torch_dir() -> str | None:
     spec = importlib.util.find_spec("torch")
-    if spec is None or spec.origin is None:
-        return None
-    torch = os.path.dirname(spec.origin)
+    return os.path.dirname(spec.origin) if spec is not None and spec.origin is not None else None
+
+
+def _bind_command(nvcc: str, torch: str, out: str) -> list[str]:
+    """Compiles and links the extension against the torch in this folder."""
     cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc))), "include")
     return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-I", INCLUDE,
             "-isystem", os.path.join(torch, "include"), "-isystem", cuda, "-I", sysconfig.get_paths()["include"],
@@ -85,8 +86,10 @@ def build(force: bool = False, verbose: bool = False) -> str:
 
     bind_tmp = BIND + ".tmp%d" % os.getpid()
     bind = None
-    if force or _stale(BIND, [BIND_SOURCE, os.path.join(INCLUDE, "sdpa.h"), __file__]):
-        bind = _bind_command(nvcc, bind_tmp)
+    torch = _torch_dir()
+    if torch and (force or _stale(BIND, [BIND_SOURCE, os.path.join(INCLUDE, "sdpa.h"), __file__,
+                                         os.path.join(torch, "version.py")])):
+        bind = _bind_command(nvcc, torch, bind_tmp)
     commands = jobs + ([bind] if bind else [])
     if commands:
         with cf.ThreadPoolExecutor(max_workers=len(commands)) as ex:

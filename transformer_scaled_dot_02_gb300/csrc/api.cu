@@ -469,6 +469,13 @@ unsigned long long paged_call_number() {
   return z != 0 ? z : 1;
 }
 
+// Do packed rows (n of `row` bf16, `stride` apart) and n dense rows of out share
+// memory?  (Strided rows count with what lies between them.)
+bool rows_overlap(const void* rows, long long row, long long stride, const void* out, long long out_row, long long n) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(rows), b = reinterpret_cast<uintptr_t>(out);
+  return n > 0 && a < b + 2ull * n * out_row && b < a + 2ull * ((n - 1) * stride + row);
+}
+
 // Bytes of a workspace slot: fp32 O and two statistics a row.
 int paged_slot_bytes(int n_tokens, int group, int d) {
   const long long rows = std::min(128ll, 1ll * n_tokens * group);
@@ -820,6 +827,10 @@ sdpa_status sdpa_paged_append(const void* q, const void* k, const void* v, void*
   if (d_rot % 16 != 0 || k_stride % 8 != 0 || v_stride % 8 != 0 || k_stride > most || v_stride > most ||
       (q != nullptr && (q_stride % 8 != 0 || q_stride > most)))
     return SDPA_ERR_UNSUPPORTED;
+  if (q != nullptr && ((q != q_out && rows_overlap(q, q_row, q_stride, q_out, q_row, n_tokens)) ||
+                       rows_overlap(k, kv_row, k_stride, q_out, q_row, n_tokens) ||
+                       rows_overlap(v, kv_row, v_stride, q_out, q_row, n_tokens)))
+    return SDPA_ERR_INVALID_ARG;
   unsigned* status = nullptr;
   st = current_device(&status);
   if (st != SDPA_OK) return st;
@@ -886,6 +897,7 @@ sdpa_status sdpa_paged_forward(const void* q, const void* k_pages, const void* v
   if (st != SDPA_OK) return st;
   if (!std::isfinite(scale) || scale < 0.f || q_stride < 1ll * h * d) return SDPA_ERR_INVALID_ARG;
   if (q_stride % 8 != 0 || q_stride >= (1ll << 38)) return SDPA_ERR_UNSUPPORTED;
+  if (rows_overlap(q, 1ll * h * d, q_stride, out, 1ll * h * d, n_tokens)) return SDPA_ERR_INVALID_ARG;
   const size_t need = sdpa_paged_workspace_size(b, n_tokens, h, h_kv, d, page_size, pages_per_seq);
   if (need > 0 && (workspace == nullptr || !aligned16(workspace) || ws_bytes < need))
     return SDPA_ERR_WORKSPACE;
