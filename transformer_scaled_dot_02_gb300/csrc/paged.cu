@@ -769,6 +769,12 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
     fence_mbar_init();
   }
   if (warp == kMmaWarp) tmem_alloc(tmem_slot, C::kTmemCols);
+  if (threadIdx.x == kProducerWarp * 32) {
+    tma_prefetch_desc(&p.tm_q);
+    tma_prefetch_desc(&p.tm_q_narrow);
+    tma_prefetch_desc(&p.tm_k);
+    tma_prefetch_desc(&p.tm_v);
+  }
   tc_fence_before();
   griddep_launch_dependents();
   griddep_wait();
@@ -800,12 +806,6 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
     const int part = tile_parts == 1 ? 0 : lane_kv / C::kBoxes, col = tile_parts == 1 ? 0 : lane_kv % C::kBoxes;
     const bool copies = (tile_parts == 1 ? lane_kv == 0 : part < tile_parts) && (!C::kJoint || lane < 16);
     const uint32_t dst = static_cast<uint32_t>(col * C::kKVBox + (part << box_shift) * C::kRowBytes);
-    if (lane == 0) {
-      tma_prefetch_desc(&p.tm_q);
-      tma_prefetch_desc(&p.tm_q_narrow);
-      tma_prefetch_desc(&p.tm_k);
-      tma_prefetch_desc(&p.tm_v);
-    }
     Walk w;
     int u0 = 0, pieces = 0, k_issued = 0, v_issued = 0;
     bool go = true;
