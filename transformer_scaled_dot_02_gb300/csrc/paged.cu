@@ -110,9 +110,12 @@ enum Scheme { kWeighed, kPieces };
 // with one, 15.3 with eight; 128 tokens over 4096 positions of 4 key-value heads
 // of 64 (32 KB) 18.4 us with eight, 20.3 with four, 19.2 with sixteen; 200 tokens over
 // 8192 positions of 4 key-value heads of 128 (64 KB) 29.9 us with sixteen, 32.3
-// with twelve, 31.7 with 24.
-constexpr int kSmallPiece = 8 << 10, kMiddlePiece = 32 << 10;
-constexpr int kSmallPieceTiles = 4, kMiddlePieceTiles = 8, kLargePieceTiles = 16;
+// with twelve, 31.7 with 24.  Pieces of up to 4 KB have two where the walk is short,
+// but none is cut whose key tiles take less than a merge, six of up to 64 columns
+// or four wider ones: single tokens over 500 positions take 8.8 us so and 9.8 with
+// four (8 heads of 64), 9.6 and 11.6 (32 / 8 heads of 128), over 300 8.0 us uncut, 8.7 cut.
+constexpr int kTinyPiece = 4 << 10, kSmallPiece = 8 << 10, kMiddlePiece = 32 << 10;
+constexpr int kShortWalk = 32;
 
 __device__ __forceinline__ int tile_rows(const PagedParams& p, const Seq& q, int r) {
   return min(p.tile_tokens, q.n - r * p.tile_tokens) * p.group;
@@ -120,9 +123,10 @@ __device__ __forceinline__ int tile_rows(const PagedParams& p, const Seq& q, int
 // The pieces that a walk of `tiles` is worth with these rows.
 __device__ __forceinline__ int pieces_of(const PagedParams& p, int rows, int tiles) {
   const int bytes = rows * p.row_bytes;
-  return bytes <= kSmallPiece    ? (tiles + kSmallPieceTiles - 1) / kSmallPieceTiles
-         : bytes <= kMiddlePiece ? (tiles + kMiddlePieceTiles - 1) / kMiddlePieceTiles
-                                 : (tiles + kLargePieceTiles - 1) / kLargePieceTiles;
+  const int shift = bytes <= kSmallPiece ? (bytes <= kTinyPiece && tiles <= kShortWalk ? 1 : 2)
+                                         : (bytes <= kMiddlePiece ? 3 : 4);
+  if (tiles <= (shift == 1 ? (p.row_bytes <= 256 ? 6 : 4) : 1 << shift)) return 1;
+  return (tiles + (1 << shift) - 1) >> shift;
 }
 // Pieces of each full row tile of a sequence that has more than one: those of
 // the longest walk, or as many as there are key tiles.
