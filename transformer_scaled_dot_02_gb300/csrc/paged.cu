@@ -241,13 +241,15 @@ struct Cut {
 };
 
 // The whole block: how the work is cut, and the place where run c ends.
-// Returns false (everywhere) when there is no such run.
+// Returns false (everywhere) when there is no such run.  Up to 32 sequences every
+// warp looks at all of them for itself, and no thread waits for another warp.
 template <int D>
 __device__ bool find_place(const PagedParams& p, ScheduleShared* sh, int c, int max_ctas, Cut* cut,
                            Place* at, Seq* seq) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int per = (p.b + kThreads - 1) / kThreads;
-  const int s0 = min(tid * per, p.b), s1 = min(s0 + per, p.b);
+  const bool alone = p.b <= 32;
+  const int per = alone ? 1 : (p.b + kThreads - 1) / kThreads;
+  const int s0 = min((alone ? lane : tid) * per, p.b), s1 = min(s0 + per, p.b);
   Work mine = {0, 0}, one = {0, 0};                          // one: a head of the last sequence
   Seq q;
   for (int s = s0; s < s1; ++s) {
@@ -272,14 +274,18 @@ __device__ bool find_place(const PagedParams& p, ScheduleShared* sh, int c, int 
     const Work o = {__shfl_up_sync(0xffffffffu, incl.pieces, x), __shfl_up_sync(0xffffffffu, incl.cost, x)};
     if (lane >= x) incl.add(o);
   }
-  if (lane == 31) sh->warp_sum[warp] = incl;
-  __syncthreads();
-  Work sum = {0, 0}, before = {incl.pieces - mine.pieces, incl.cost - mine.cost};
+  Work sum = {__shfl_sync(0xffffffffu, incl.pieces, 31), __shfl_sync(0xffffffffu, incl.cost, 31)};
+  Work before = {incl.pieces - mine.pieces, incl.cost - mine.cost};
+  if (!alone) {
+    if (lane == 31) sh->warp_sum[warp] = incl;
+    __syncthreads();
+    sum = {0, 0};
 #pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) {
-    const Work v = sh->warp_sum[w];
-    if (w < warp) before.add(v);
-    sum.add(v);
+    for (int w = 0; w < kThreads / 32; ++w) {
+      const Work v = sh->warp_sum[w];
+      if (w < warp) before.add(v);
+      sum.add(v);
+    }
   }
   // (there are no more pieces than key tiles: no run is shorter than a key tile)
   const Scheme scheme = sum.pieces <= max_ctas ? kPieces : kWeighed;
@@ -288,33 +294,50 @@ __device__ bool find_place(const PagedParams& p, ScheduleShared* sh, int c, int 
   const long long own = mine.of(scheme), excl = before.of(scheme);
   *cut = Cut(sum.of(scheme), n, max_ctas, p.ctas_magic, scheme);
   const long long x = cut->begin(c + 1) - 1;                 // its last item
-  if (own > 0 && excl <= x && x < excl + own) {
-    long long rem = x - excl, head = one.of(scheme);
-    Place pl;
-    pl.s = s0;
-    if (per > 1) {
-      for (pl.s = s0; pl.s < s1; ++pl.s) {
-        q = load_seq(p, pl.s);
-        head = cost_before(p, q, q.tiles, scheme);
-        if (rem < head * p.h_kv) break;
-        rem -= head * p.h_kv;
-      }
+  const bool here = own > 0 && excl <= x && x < excl + own;
+  long long rem = x - excl, head = one.of(scheme);
+  Place pl;
+  pl.s = s0;
+  if (here && per > 1) {
+    for (pl.s = s0; pl.s < s1; ++pl.s) {
+      q = load_seq(p, pl.s);
+      head = cost_before(p, q, q.tiles, scheme);
+      if (rem < head * p.h_kv) break;
+      rem -= head * p.h_kv;
     }
+  }
+  if (alone) {
+    const int from = __ffs(__ballot_sync(0xffffffffu, here)) - 1;
+    pl.s = from;
+    rem = __shfl_sync(0xffffffffu, rem, from);
+    head = __shfl_sync(0xffffffffu, head, from);
+    q.start = __shfl_sync(0xffffffffu, q.start, from);
+    q.n = __shfl_sync(0xffffffffu, q.n, from);
+    q.len = __shfl_sync(0xffffffffu, q.len, from);
+    q.tiles = __shfl_sync(0xffffffffu, q.tiles, from);
+  }
+  if (alone || here) {
     pl.hk = static_cast<int>(divide(rem, head));
     rem -= pl.hk * head;
     pl.r = 0;
     pl.item = rem + 1;                                       // for a single row tile
-    sh->at = pl;
-    sh->rem = rem;
-    sh->q = q;
   }
-  __syncthreads();
-  *at = sh->at;
-  *seq = sh->q;
+  if (!alone) {
+    if (here) {
+      sh->at = pl;
+      sh->rem = rem;
+      sh->q = q;
+    }
+    __syncthreads();
+    pl = sh->at;
+    rem = sh->rem;
+    q = sh->q;
+  }
+  *at = pl;
+  *seq = q;
   if (seq->tiles > 1) {
     // the last row tile that begins at or before rem: 32 probes a round (every
     // warp does it for itself)
-    const long long rem = sh->rem;
     int lo = 0, hi = seq->tiles;
     long long before_lo = 0;
     while (hi - lo > 1) {
@@ -335,7 +358,7 @@ __device__ bool find_place(const PagedParams& p, ScheduleShared* sh, int c, int 
     at->pieces = pieces;
     at->kt0 = i - 1;
     at->kt1 = i;
-    if (pieces != tiles) {                                   // (a piece has up to 12: in 32 bits)
+    if (pieces != tiles) {                                   // (a piece has up to 16: in 32 bits)
       at->kt0 = (i - 1) * tiles / pieces;
       at->kt1 = i * tiles / pieces;
     }
@@ -500,14 +523,13 @@ struct PCfg {
   static_assert(4 * kNarrowRows * 16 * 4 <= kXBytes, "quarters");
   static constexpr int kXmlOff = kXOff + kXBytes;            // the quarters' (m, l)
   // merging: the idle K and V stages hold a wide piece's O, or with the exchange
-  // memory behind them three of a narrow tile's, or of every piece a vector and
+  // memory behind them two of a narrow tile's, or of every piece a vector and
   // its (m, l) beside what the threads that share a vector exchange
   static constexpr int kMergeBytes = 2 * kRing * kKVBytes + kXBytes;
   static constexpr int kPartBytes = kBlockM * (16 + 8);
   static_assert(2 * kRing * kKVBytes >= kBlockM * D * 4 && kMergeBytes >= 2 * kNarrowRows * (D * 4 + 8) &&
                     kMergeBytes - kPartBytes >= kPagedMaxRuns * (16 + 8), "pieces");
-  static constexpr int kXinvOff = kXmlOff + 4 * kQuarter * 8;   // 1 / l of their sum
-  static constexpr int kBarOff = kXinvOff + kNarrowRows * 4;
+  static constexpr int kBarOff = kXmlOff + 4 * kQuarter * 8;
   // q_full, q_empty, k_full[R], v_full[R], s_full[R], o_full[R], p_full[2], o_last, o_free,
   // merge, drain
   static constexpr int kNumBars = 2 + 4 * kRing + 2 + 4;
@@ -781,13 +803,13 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
   }
   tc_fence_before();
   griddep_launch_dependents();
+  __syncthreads();                                           // the set-up above, for all
   griddep_wait();
 
   Cut cut(0, 1, 0, 0, kWeighed);
   Place last;
   Seq last_seq;
   const int cta = static_cast<int>(blockIdx.x);
-  // (its barriers also stand between the set-up above and the roles below)
   const bool any = find_place<D>(p, &sched, cta, static_cast<int>(gridDim.x), &cut, &last, &last_seq);
   const long long run = any ? cut.begin(cta + 1) - cut.begin(cta) : 0;
   tc_fence_after();
@@ -1159,30 +1181,12 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
         ok = mbar_wait_warp(o_last, static_cast<uint32_t>(pieces) & 1u, ab);
         if (!ok) break;
         tc_fence_after();
-        // ---- sum the quarters: (m, l) first, then as many columns at a time
-        // as the exchange memory holds of the rows there are
+        // ---- sum the quarters: (m, l) and as many columns at a time as the
+        // exchange memory holds of the rows there are (at the end of the run the
+        // idle K and V stages serve, behind the place of the own piece)
         float2* xml = reinterpret_cast<float2*>(smem + C::kXmlOff);
-        float* xinv = reinterpret_cast<float*>(smem + C::kXinvOff);
         xml[quarter * kQuarter + lane] = make_float2(m_used, l);
-        if (!(ok = meet())) break;
-        float mm = m_used, ll = 0.f;
-#pragma unroll
-        for (int y = 0; y < 4; ++y) mm = fmaxf(mm, xml[y * kQuarter + lane].x);
-        const float sub = mm == -INFINITY ? 0.f : mm;
-#pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          const float2 ml = xml[y * kQuarter + lane];
-          ll += ml.y * weight(ml.x, sub);
-        }
-        const float f = weight(m_used, sub);
-        // own piece: where it is kept while it is not whole
-        uint8_t* own = publishes ? slot(place) : ring;
-        if (valid && quarter == 0) {
-          if (!whole) ml_of(own)[row] = make_float2(mm, ll);
-          xinv[row] = ll > 0.f ? 1.f / ll : 0.f;
-        }
-        // (at the end of the run the idle K and V stages serve, behind the place
-        // of the own piece)
+        uint8_t* own = publishes ? slot(place) : ring;       // where the piece is kept while it is not whole
         const bool at_end = w.off <= 0;
         float4* lay = reinterpret_cast<float4*>(at_end ? ring + piece_bytes : smem + C::kXOff);
         const int room = at_end ? C::kMergeBytes - piece_bytes : C::kXBytes;
@@ -1202,8 +1206,8 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
 #pragma unroll
               for (int e = 0; e < kWidth / 4; ++e)
                 lay[(quarter * (cols / 4) + c / 4 + e) * rows + row] =
-                    make_float4(__uint_as_float(o[e * 4]) * f, __uint_as_float(o[e * 4 + 1]) * f,
-                                __uint_as_float(o[e * 4 + 2]) * f, __uint_as_float(o[e * 4 + 3]) * f);
+                    make_float4(__uint_as_float(o[e * 4]), __uint_as_float(o[e * 4 + 1]),
+                                __uint_as_float(o[e * 4 + 2]), __uint_as_float(o[e * 4 + 3]));
             }
           };
           if (cols == 16) {
@@ -1215,17 +1219,34 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
           if (!(ok = meet())) break;
           const int items = rows * (cols / 4);
           for (int x = threadIdx.x; x < items; x += kBlockM) {
-            float4 v = lay[x];
+            const int rw = x % rows;
+            float2 ml[4];
+            float4 v[4];
 #pragma unroll
-            for (int y = 1; y < 4; ++y) {
-              const float4 o = lay[y * items + x];
-              v.x += o.x;
-              v.y += o.y;
-              v.z += o.z;
-              v.w += o.w;
+            for (int y = 0; y < 4; ++y) {
+              ml[y] = xml[y * kQuarter + rw];
+              v[y] = lay[y * items + x];
             }
-            if (whole) write_four(p.out + out_begin<D>(p, unit.row0, unit.head0, x % rows) + c0 + x / rows * 4, v, xinv[x % rows]);
-            else reinterpret_cast<float4*>(own)[c0 / 4 * rows + x] = v;
+            const float mm = fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x));
+            const float sub = mm == -INFINITY ? 0.f : mm;
+            float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+            float ll = 0.f;
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              const float f = weight(ml[y].x, sub);
+              ll += ml[y].y * f;
+              sum.x += v[y].x * f;
+              sum.y += v[y].y * f;
+              sum.z += v[y].z * f;
+              sum.w += v[y].w * f;
+            }
+            if (whole) {
+              write_four(p.out + out_begin<D>(p, unit.row0, unit.head0, rw) + c0 + x / rows * 4, sum,
+                         ll > 0.f ? 1.f / ll : 0.f);
+            } else {
+              reinterpret_cast<float4*>(own)[c0 / 4 * rows + x] = sum;
+              if (c0 == 0 && x < rows) ml_of(own)[x] = make_float2(mm, ll);
+            }
           }
         }
         if (!ok) break;
