@@ -253,7 +253,7 @@ sdpa_status sdpa_decode(const void* q, const void* k, const void* v, void* out, 
  * graph follows their values.  Head shapes: d in {16, 32, 64, 128, 256},
  * h = group * h_kv with group <= 128 (query head x reads key-value head
  * x / group), page_size a power of two of at least 8, pages_per_seq *
- * page_size < 2^30; else SDPA_ERR_UNSUPPORTED.
+ * page_size < 2^30, h_kv * page_size < 2^31; else SDPA_ERR_UNSUPPORTED.
  * With n_tokens == 0 nothing is enqueued, and the row pointers may be NULL.
  * A page number outside [0, n_pages) is never followed: the append skips that
  * token's key and value, the attention takes the page as zeros, and

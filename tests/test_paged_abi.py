@@ -69,6 +69,7 @@ def test_shared_argument_checks(lib, call):
     assert call(lib, h=129, h_kv=1, qs=129 * 64) == UNSUPPORTED
     assert call(lib, per_seq=1 << 26) == UNSUPPORTED          # 2^30 positions
     assert call(lib, t=(1 << 24) + 1) == UNSUPPORTED
+    assert call(lib, h=64, h_kv=64, d=16, qs=1024, page=1 << 25, per_seq=1, n_pages=1) == UNSUPPORTED
     assert call(lib, n_pages=1 << 30) == UNSUPPORTED
 
 

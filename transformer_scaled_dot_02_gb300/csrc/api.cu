@@ -123,23 +123,20 @@ bool make_map_4d(CUtensorMap* map, const void* base, int d, int n, int h, int b,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// 5-D bf16 map over cache pages [n_pages][h_kv][page][d], a row's columns in
-// blocks of min(d, 64): (columns, rows, blocks, heads, pages).  A box is a key
-// tile's rows of every block; of pages smaller than that, a page's rows of
-// one block.  Pages past n_pages read as zeros.
+// 5-D bf16 map over the pages [n_pages][h_kv][page][d], rows in groups of eight,
+// columns in blocks of min(d, 64): (columns, rows of a group, blocks, groups of all
+// heads, pages).  A box is a key tile's rows or, if that is less, a page's of a
+// head.  Pages past n_pages read as zeros.
 bool make_map_pages(CUtensorMap* map, const void* base, int d, int page, int h_kv, int n_pages) {
   auto enc = encode_fn();
   if (enc == nullptr) return false;
   const int cols = d < 64 ? d : 64;
-  const cuuint64_t dims[5] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(page),
-                              static_cast<cuuint64_t>(d / cols), static_cast<cuuint64_t>(h_kv),
-                              static_cast<cuuint64_t>(n_pages)};
+  const cuuint64_t dims[5] = {static_cast<cuuint64_t>(cols), 8, static_cast<cuuint64_t>(d / cols),
+                              static_cast<cuuint64_t>(h_kv) * (page / 8), static_cast<cuuint64_t>(n_pages)};
   const cuuint64_t row = static_cast<cuuint64_t>(d) * 2;
-  const cuuint64_t strides[4] = {row, static_cast<cuuint64_t>(cols) * 2, row * page, row * page * h_kv};
-  const bool whole = page >= sdpa::kPagedKeyTile;
-  const cuuint32_t box[5] = {static_cast<cuuint32_t>(cols),
-                             static_cast<cuuint32_t>(whole ? sdpa::kPagedKeyTile : page),
-                             static_cast<cuuint32_t>(whole ? d / cols : 1), 1, 1};
+  const cuuint64_t strides[4] = {row, static_cast<cuuint64_t>(cols) * 2, row * 8, row * page * h_kv};
+  const cuuint32_t box[5] = {static_cast<cuuint32_t>(cols), 8, static_cast<cuuint32_t>(d / cols),
+                             static_cast<cuuint32_t>(std::min(page, sdpa::kPagedKeyTile) / 8), 1};
   const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
   const CUtensorMapSwizzle swz = d >= 64 ? CU_TENSOR_MAP_SWIZZLE_128B
                                          : (d == 32 ? CU_TENSOR_MAP_SWIZZLE_64B
@@ -417,8 +414,9 @@ sdpa_status check_paged_args(const void* k_pages, const void* v_pages, int b, in
       (page_size & (page_size - 1)) != 0 || 1ll * pages_per_seq * page_size >= (1ll << 30) ||
       n_tokens > (1 << 24) || b > (1 << 24) || h > 65536)
     return SDPA_ERR_UNSUPPORTED;
-  // the largest tensor-map stride (bytes from page to page) and the whole cache
-  if (1ll * h_kv * page_size * d * 2 >= (1ll << 40) || n_pages >= (1 << 30) ||
+  // the largest tensor-map coordinate and stride (bytes from page to page), and the
+  // whole cache
+  if (1ll * h_kv * page_size >= (1ll << 31) || 1ll * h_kv * page_size * d * 2 >= (1ll << 40) || n_pages >= (1 << 30) ||
       1ll * h_kv * page_size * d > (1ll << 40) / n_pages)
     return SDPA_ERR_UNSUPPORTED;
   return SDPA_OK;

@@ -106,9 +106,7 @@ cudaError_t launch_sdpa_decode(const DecodeParams& p, int d_k, int d_v, cudaStre
 struct PagedParams {
   CUtensorMap tm_q;           // 3-D (d, h, n_tokens) map, boxes of min(d, 64) x group x tile_tokens
   CUtensorMap tm_q_narrow;    // the same with boxes of 16 / group tokens (tm_q for groups over 16)
-  CUtensorMap tm_k, tm_v;     // 5-D (64 columns, page rows, d / 64, h_kv, n_pages) maps; boxes of
-                              // kPagedKeyTile rows of every column block, or of a smaller page's
-                              // rows of one
+  CUtensorMap tm_k, tm_v;     // 5-D (64 columns, 8 rows, d / 64, h_kv x page / 8, n_pages) maps
   uint16_t* out;              // bf16 [n_tokens][h][d]
   // workspace (split_ctas > 1)
   uint8_t* slots;             // [slots][slot_bytes]: a published piece's O, then its (m, l)

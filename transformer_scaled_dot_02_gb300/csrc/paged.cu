@@ -533,6 +533,13 @@ struct PCfg {
   // q_full, q_empty, k_full[R], v_full[R], s_full[R], o_full[R], p_full[2], o_last, o_free,
   // merge, drain
   static constexpr int kNumBars = 2 + 4 * kRing + 2 + 4;
+  // A tile of K or V lies as [8 rows][column block][row of the eight]: groups of eight
+  // rows are equally far apart, as the operands' descriptors want them, however
+  // many copies the tile came in, one for each page that it spans: a copy costs its
+  // issue (100 clk and more) before its bytes, and copying each column block of a
+  // page by itself took 136 us instead of QQ for 4 chunks of 512 tokens behind 7680
+  // positions (heads of 128, pages of 16).
+  static constexpr int kGroupBytes = kBoxes * kSBO;
   static constexpr int kSmemBytes = kBarOff + kNumBars * 8 + 16 + 1024;
   static constexpr uint32_t kOCol = 2 * kBN;
   static constexpr uint32_t kTmemCols = kOCol + D <= 256 ? 256u : 512u;
@@ -540,9 +547,10 @@ struct PCfg {
   static constexpr uint32_t kIdescS = idesc_bf16(kBlockM, kBN, false, false);
   static constexpr uint32_t kIdescPV = idesc_bf16(kBlockM, D, false, true);
   static constexpr uint32_t kDescHi = (kSBO >> 4) | (1u << 14) | (kLayout << 29);
+  static constexpr uint32_t kDescHiKV = (kGroupBytes >> 4) | (1u << 14) | (kLayout << 29);
   static_assert(kSmemBytes * kMinBlocks <= 232448 - 1024 * kMinBlocks, "CTAs per SM");
   static_assert(kKOff % 1024 == 0 && kVOff % 1024 == 0 && kKVBox % 1024 == 0, "alignment");
-  static_assert(kBoxes * (kBN / kPagedMinPage) <= 32, "a lane of the producer warp for each box of a tile's parts");
+  static_assert(kBN / kPagedMinPage <= 8 && kPagedMinPage % 8 == 0, "a lane of the producer warp for each copy");
 };
 
 // Where row rw of a tile begins in the output (row0: the tile's first token, head0:
@@ -817,21 +825,17 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
 
   if (run > 0 && warp == kProducerWarp) {
     // ---------------------------------------------------------- producer
-    // A tile of 64 keys that lies in one page is one copy of all its column
-    // boxes.  Smaller pages are `parts` of a tile: lane part * kBoxes + c
-    // copies column box c of its part, all lanes at once (one lane doing them
-    // one after the other took 270 clk for each).  A lane reads the page of its
-    // part two tiles ahead and looks at it only when it uses it: waiting for
-    // each read took 700 clk a tile.
+    // Pages smaller than a tile are `parts` of it, each copied by a lane, all at
+    // once (one lane doing them one after the other took 270 clk for each).  A
+    // lane reads the page of its part two tiles ahead and looks at it only when it
+    // uses it: waiting for each read took 700 clk a tile.
     const int box_shift = min(p.page_shift, kBNShift);
-    const int box_rows = 1 << box_shift, tile_parts = kBN >> box_shift;
+    const int box_rows = 1 << box_shift;
     const int row_mask = (1 << p.page_shift) - 1;
     // (together: lanes 0 - 7 copy K, lanes 8 - 15 V)
-    static_assert(!C::kJoint || C::kBoxes * (kBN / kPagedMinPage) <= 8, "lanes");
-    const int lane_kv = C::kJoint ? lane & 7 : lane;
-    const int part = tile_parts == 1 ? 0 : lane_kv / C::kBoxes, col = tile_parts == 1 ? 0 : lane_kv % C::kBoxes;
-    const bool copies = (tile_parts == 1 ? lane_kv == 0 : part < tile_parts) && (!C::kJoint || lane < 16);
-    const uint32_t dst = static_cast<uint32_t>(col * C::kKVBox + (part << box_shift) * C::kRowBytes);
+    const int part = C::kJoint ? lane & 7 : lane;
+    const bool copies = part << box_shift < kBN && (!C::kJoint || lane < 16);
+    const uint32_t dst = static_cast<uint32_t>((part << box_shift) * C::kRowBytes * C::kBoxes);
     Walk w;
     int u0 = 0, pieces = 0, k_issued = 0, v_issued = 0;
     bool go = true;
@@ -845,10 +849,9 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
       auto holds = [&](int i) { return copies && i < n && key_lane + i * kBN < w.q.len; };
       auto page_of = [&](int i) -> int { return holds(i) ? pages[(key_lane + i * kBN) >> p.page_shift] : 0; };
       auto load = [&](const CUtensorMap* map, uint64_t* bar, uint8_t* stage, int i, int page) {
-        const int key = (kt0 + i) * kBN;
-        const int parts = min(tile_parts, (w.q.len - key + box_rows - 1) >> box_shift);
+        const int rows = min(kBN, (w.q.len - (kt0 + i) * kBN + box_rows - 1) >> box_shift << box_shift);
         if (lane == 0)
-          mbar_arrive_expect_tx(bar, static_cast<uint32_t>(parts << box_shift) *
+          mbar_arrive_expect_tx(bar, static_cast<uint32_t>(rows) *
                                          (C::kRowBytes * C::kBoxes * (C::kJoint ? 2 : 1)));
         __syncwarp();
         if (holds(i)) {
@@ -857,7 +860,8 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
             atomicOr(p.status, kStatusBadPage);
             page = p.n_pages;
           }
-          tma_load_5d(map, bar, stage + dst, 0, (key_lane + i * kBN) & row_mask, col, w.hk, page);
+          tma_load_5d(map, bar, stage + dst, 0, 0, 0,
+                      (w.hk << (p.page_shift - 3)) + (((key_lane + i * kBN) & row_mask) >> 3), page);
         }
       };
       int page_v = page_of(0), page_k = page_v, page_n = page_of(1);
@@ -921,8 +925,8 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
       for (int k = 0; k < D / 16; ++k) {
         constexpr int kS = C::kStepsPerRow;
         mma_bf16_ss_warp(d, q_lo + static_cast<uint32_t>(((k / kS) * C::kQBox + (k % kS) * 32) >> 4),
-                         C::kDescHi, b0 + static_cast<uint32_t>(((k / kS) * C::kKVBox + (k % kS) * 32) >> 4),
-                         C::kDescHi, C::kIdescS, k > 0 ? 1u : 0u);
+                         C::kDescHi, b0 + static_cast<uint32_t>(((k / kS) * C::kSBO + (k % kS) * 32) >> 4),
+                         C::kDescHiKV, C::kIdescS, k > 0 ? 1u : 0u);
       }
 #ifdef SDPA_TEST_WITHHOLD_FIRST_S_COMMIT
       // (test builds only, never in libsdpa.so: the first score tile of a CTA
@@ -934,11 +938,11 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
     };
     auto issue_pv = [&](int u, bool accumulate) {
       const uint32_t pa = tmem + static_cast<uint32_t>((u & 1) * kBN);
-      const uint32_t b0 = lo(smem_base + C::kVOff + (u % R) * C::kKVBytes, C::kKVBox);
+      const uint32_t b0 = lo(smem_base + C::kVOff + (u % R) * C::kKVBytes, C::kSBO);
 #pragma unroll
       for (int k = 0; k < kBN / 16; ++k)
         mma_bf16_ts_warp(tmem + C::kOCol, pa + static_cast<uint32_t>(k * 8),
-                         b0 + static_cast<uint32_t>((k * 16 * C::kRowBytes) >> 4), C::kDescHi, C::kIdescPV,
+                         b0 + static_cast<uint32_t>((k * 2 * C::kGroupBytes) >> 4), C::kDescHiKV, C::kIdescPV,
                          (accumulate || k > 0) ? 1u : 0u);
     };
     Walk w;
@@ -995,10 +999,12 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
       uint8_t* v = smem + C::kVOff + (u % R) * C::kKVBytes;
       const int keep = w.q.len - key0;                       // in [1, kBN)
       constexpr int kPerRow = C::kRowBytes / 16;
-      for (int x = threadIdx.x; x < (kBN - keep) * kPerRow; x += kBlockM)
+      for (int x = threadIdx.x; x < (kBN - keep) * kPerRow; x += kBlockM) {
+        const int r = keep + x / kPerRow;
+        uint8_t* at = v + (r >> 3) * C::kGroupBytes + (r & 7) * C::kRowBytes + x % kPerRow * 16;
 #pragma unroll
-        for (int c = 0; c < C::kBoxes; ++c)
-          *reinterpret_cast<uint4*>(v + c * C::kKVBox + keep * C::kRowBytes + x * 16) = make_uint4(0, 0, 0, 0);
+        for (int c = 0; c < C::kBoxes; ++c) *reinterpret_cast<uint4*>(at + c * C::kSBO) = make_uint4(0, 0, 0, 0);
+      }
       fence_proxy_async_smem();
       return true;
     };
