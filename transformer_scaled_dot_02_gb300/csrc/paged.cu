@@ -537,7 +537,7 @@ struct PCfg {
   // rows are equally far apart, as the operands' descriptors want them, however
   // many copies the tile came in, one for each page that it spans: a copy costs its
   // issue (100 clk and more) before its bytes, and copying each column block of a
-  // page by itself took 136 us instead of QQ for 4 chunks of 512 tokens behind 7680
+  // page by itself took 136 us instead of 112 for 4 chunks of 512 tokens behind 7680
   // positions (heads of 128, pages of 16).
   static constexpr int kGroupBytes = kBoxes * kSBO;
   static constexpr int kSmemBytes = kBarOff + kNumBars * 8 + 16 + 1024;
