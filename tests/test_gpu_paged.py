@@ -624,6 +624,36 @@ def test_two_streams_with_a_workspace_each():
             assert torch.equal(_raw(o), _raw(want))
 
 
+def test_slices_beside_other_work():
+    """Units merged by several runs on two streams at once, while matrix products
+    on a third hold SMs: runs wait for runs that may not have begun."""
+    import torch
+    rng = np.random.default_rng(804)
+    jobs = []
+    for new, lens, h, h_kv, d in (([69], [26595], 2, 2, 64), ([1, 1], [70000, 300], 16, 4, 64)):
+        cache = pu.Cache(rng, lens, h_kv, d, 64)
+        dense = [[_bf16(rng, (n, h_kv, d)) for n in lens] for _ in range(2)]
+        kp, vp = (dev(cache.pages_of(x, 0.0)) for x in dense)
+        q = dev(_bf16(rng, (sum(new), h, d)))
+        args = (q, kp, vp, dev_int(cache.table), dev_int(pu.starts_of(new)), dev_int(cache.lens))
+        want = sd.paged_attention(*args)
+        jobs.append((args, want, sd.paged_workspace(q, kp, args[3]), torch.cuda.Stream(), []))
+    a = torch.randn(4096, 4096, dtype=torch.bfloat16, device="cuda")
+    c = torch.empty_like(a)
+    third = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(60):
+        with torch.cuda.stream(third):
+            torch.mm(a, a, out=c)
+        for args, _, ws, stream, outs in jobs:
+            outs.append(sd.paged_attention(*args, workspace=ws, stream=stream))
+    torch.cuda.synchronize()
+    sd.sdpa_device_check()
+    for _, want, _, _, outs in jobs:
+        for out in outs:
+            assert torch.equal(_raw(out), _raw(want))
+
+
 def test_inputs_written_just_before_the_call():
     """Lengths, tables and queries written by kernels of the same stream right
     before each call."""
