@@ -906,6 +906,7 @@ sdpa_status sdpa_paged_forward(const void* q, const void* k_pages, const void* v
   sdpa::PagedParams p;
   p.group = h / h_kv;
   p.tile_tokens = 128 / p.group;
+  p.group_magic = ((1u << 16) + p.group - 1) / p.group;
   paged_steps(&p);
   if (!make_map_rows(&p.tm_q, q, d, h, n_tokens, q_stride, p.group, p.tile_tokens) ||
       !make_map_rows(&p.tm_q_narrow, q, d, h, n_tokens, q_stride, p.group,

@@ -119,6 +119,7 @@ struct PagedParams {
   unsigned* status;
   int b, n_tokens, h, h_kv;
   int group, tile_tokens;     // h / h_kv; tokens per row tile, t = 128 / group
+  unsigned group_magic;       // ceil(2^16 / group)
   // t = 2^log_step t', 2^log_step the largest power of two that divides t and the
   // key tile, P = kPagedKeyTile / 2^log_step: t' 's inverse modulo P, and the sums
   // of the first k of 0, t', 2 t', .. modulo P

@@ -117,6 +117,11 @@ enum Scheme { kWeighed, kPieces };
 constexpr int kTinyPiece = 4 << 10, kSmallPiece = 8 << 10, kMiddlePiece = 32 << 10;
 constexpr int kShortWalk = 32;
 
+// The token that row `row` of a tile belongs to, row / group: rows are below 128, so
+// the product's error stays below 2^16.
+__device__ __forceinline__ int token_of(const PagedParams& p, int row) {
+  return static_cast<int>(static_cast<unsigned>(row) * p.group_magic >> 16);
+}
 __device__ __forceinline__ int tile_rows(const PagedParams& p, const Seq& q, int r) {
   return min(p.tile_tokens, q.n - r * p.tile_tokens) * p.group;
 }
@@ -557,7 +562,7 @@ struct PCfg {
 // the group's first head), and four columns into the output.
 template <int D>
 __device__ __forceinline__ long long out_begin(const PagedParams& p, int row0, int head0, int rw) {
-  const int tok = rw / p.group;
+  const int tok = token_of(p, rw);
   return (static_cast<long long>(row0 + tok) * p.h + head0 + rw - tok * p.group) * D;
 }
 __device__ __forceinline__ void write_four(uint16_t* at, const float4& v, float f) {
@@ -1053,7 +1058,7 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
       const int rows = w.rows;
       const bool narrow = rows <= kNarrowRows;
       const int row = narrow ? lane : quarter * 32 + lane;   // row of the tile
-      const int token = row / p.group, head = row % p.group;
+      const int token = token_of(p, row), head = row - token * p.group;
       const int token0 = w.r * p.tile_tokens;
       const bool valid = row < rows;
       const int pos0 = w.q.len - w.q.n + token0;             // position of the tile's first row
@@ -1187,6 +1192,9 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
         ok = mbar_wait_warp(o_last, static_cast<uint32_t>(pieces) & 1u, ab);
         if (!ok) break;
         tc_fence_after();
+        // x / rows, for the at most 16 rows and 1024 vectors of a narrow piece
+        const unsigned rows_magic = ((1u << 16) + rows - 1) / rows;
+        auto column_of = [&](int x) { return static_cast<int>(static_cast<unsigned>(x) * rows_magic >> 16); };
         // ---- sum the quarters: (m, l) and as many columns at a time as the
         // exchange memory holds of the rows there are (at the end of the run the
         // idle K and V stages serve, behind the place of the own piece)
@@ -1225,7 +1233,7 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
           if (!(ok = meet())) break;
           const int items = rows * (cols / 4);
           for (int x = threadIdx.x; x < items; x += kBlockM) {
-            const int rw = x % rows;
+            const int col = column_of(x), rw = x - col * rows;
             float2 ml[4];
             float4 v[4];
 #pragma unroll
@@ -1247,7 +1255,7 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
               sum.w += v[y].w * f;
             }
             if (whole) {
-              write_four(p.out + out_begin<D>(p, unit.row0, unit.head0, rw) + c0 + x / rows * 4, sum,
+              write_four(p.out + out_begin<D>(p, unit.row0, unit.head0, rw) + c0 + col * 4, sum,
                          ll > 0.f ? 1.f / ll : 0.f);
             } else {
               reinterpret_cast<float4*>(own)[c0 / 4 * rows + x] = sum;
@@ -1274,7 +1282,7 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
             if (!(ok = meet())) break;
             float2 ml_row = make_float2(0.f, 0.f);
             for (int x = threadIdx.x; x < rows * (D / 4); x += kBlockM) {
-              const int rw = x % rows;
+              const int col = column_of(x), rw = x - col * rows;
               float4 acc = reinterpret_cast<float4*>(ring)[x];
               const float2 ml = ml_of(ring)[rw];
               float top = ml.x;
@@ -1302,7 +1310,7 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
                 reinterpret_cast<float4*>(slot(cta))[x] = acc;
                 if (x < rows) ml_of(slot(cta))[rw] = ml_row;
               } else {
-                write_four(p.out + out_begin<D>(p, unit.row0, unit.head0, rw) + x / rows * 4, acc, sum > 0.f ? 1.f / sum : 0.f);
+                write_four(p.out + out_begin<D>(p, unit.row0, unit.head0, rw) + col * 4, acc, sum > 0.f ? 1.f / sum : 0.f);
               }
             }
             if (further) {
@@ -1442,7 +1450,7 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
           uint16_t* dst[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const int rr = quarter * 32 + r0 + 8 * k, tok = rr / p.group;
+            const int rr = quarter * 32 + r0 + 8 * k, tok = token_of(p, rr);
             dst[k] = p.out + (static_cast<long long>(w.q.start + token0 + tok) * p.h + w.hk * p.group + rr -
                               tok * p.group) * D + piece * 8;
           }
