@@ -232,9 +232,9 @@ struct Cut {
   long long each, longer;                                    // longer: items in the longer runs
   int over;
   Scheme scheme;
-  // `magic`: ceil(2^64 / max_ctas), for the usual number of runs
-  __device__ Cut(long long work, int ctas, int max_ctas, unsigned long long magic, Scheme how) : scheme(how) {
-    each = ctas == max_ctas && ctas > 1 ? static_cast<long long>(__umul64hi(work, magic)) : divide(work, ctas);
+  // kPieces: a run for each item.  `magic`: ceil(2^64 / ctas).
+  __device__ Cut(long long work, int ctas, unsigned long long magic, Scheme how) : scheme(how) {
+    each = how == kPieces ? 1 : ctas > 1 ? static_cast<long long>(__umul64hi(work, magic)) : work;
     over = static_cast<int>(work - each * ctas);
     longer = over * (each + 1);
   }
@@ -297,7 +297,7 @@ __device__ bool find_place(const PagedParams& p, ScheduleShared* sh, int c, int 
   const int n = scheme == kPieces ? static_cast<int>(sum.pieces) : max_ctas;
   if (c >= n) return false;
   const long long own = mine.of(scheme), excl = before.of(scheme);
-  *cut = Cut(sum.of(scheme), n, max_ctas, p.ctas_magic, scheme);
+  *cut = Cut(sum.of(scheme), n, p.ctas_magic, scheme);
   const long long x = cut->begin(c + 1) - 1;                 // its last item
   const bool here = own > 0 && excl <= x && x < excl + own;
   long long rem = x - excl, head = one.of(scheme);
@@ -819,7 +819,7 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
   __syncthreads();                                           // the set-up above, for all
   griddep_wait();
 
-  Cut cut(0, 1, 0, 0, kWeighed);
+  Cut cut(0, 1, 0, kWeighed);
   Place last;
   Seq last_seq;
   const int cta = static_cast<int>(blockIdx.x);
