@@ -11,11 +11,12 @@
 // sdpa_paged_split<D>: a UNIT is (sequence, key-value head, row tile); the
 // rows of a tile are tile_tokens tokens x the group's heads (at most 128), so
 // one walk over the keys serves every query head of the group.  A unit's walk
-// is its visible keys in tiles of 64; all units laid end to end, each as long
-// as it is expected to take, are cut into equal runs, one per CTA, so that one
-// long sequence, many short ones and any mixture load the SMs alike.  The cut
-// is worked out on the device from the lengths, so a captured launch follows
-// them.
+// is its visible keys in tiles of 64.  Where the GPU has a CTA for each piece
+// that the units are worth cutting into, a CTA's run is one piece; else all
+// units laid end to end, each as long as it is expected to take, are cut into
+// equal runs, so that one long sequence, many short ones and any mixture load
+// the SMs alike.  The cut is worked out on the device from the lengths, so a
+// captured launch follows them.
 //
 // A CTA works its run from the end to the beginning.  If the run ends inside
 // a unit, that piece comes first and its (O, m, l) is published in the
