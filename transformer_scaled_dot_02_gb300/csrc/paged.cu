@@ -816,8 +816,10 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
     tma_prefetch_desc(&p.tm_v);
   }
   tc_fence_before();
-  griddep_launch_dependents();
   __syncthreads();                                           // the set-up above, for all
+  // not before the block has met: the next kernel's block could be given this
+  // one's tensor memory, and then wait for this grid, which waits for the memory
+  griddep_launch_dependents();
   griddep_wait();
 
   Cut cut(0, 1, 0, kWeighed);
