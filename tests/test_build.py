@@ -1,0 +1,56 @@
+"""The build on the CPU: the library is built whatever becomes of the paged
+helpers' extension.  (In a folder of its own, with a source of one line.)"""
+import ctypes
+import os
+
+import pytest
+
+from transformer_scaled_dot_02_gb300 import build as sd_build
+
+
+@pytest.fixture
+def tree(tmp_path, monkeypatch):
+    (tmp_path / "one.cu").write_text('extern "C" int one() { return 1; }\n')
+    (tmp_path / "bind.cpp").write_text("int two() { return 2; }\n")
+    for name, value in (("SOURCES", ["one.cu"]), ("HEADERS", []), ("CSRC", str(tmp_path)),
+                        ("BUILD_DIR", str(tmp_path / "_build")), ("LIB", str(tmp_path / "libone.so")),
+                        ("BIND", str(tmp_path / os.path.basename(sd_build.BIND))),
+                        ("BIND_SOURCE", str(tmp_path / "bind.cpp"))):
+        monkeypatch.setattr(sd_build, name, value)
+    return tmp_path
+
+
+@pytest.fixture
+def torch_dir():
+    torch = sd_build._torch_dir()
+    if torch is None:
+        pytest.skip("no torch for CUDA")
+    return torch
+
+
+@pytest.mark.parametrize("why", ["source", "compiler"])
+def test_the_library_is_built_where_the_extension_is_not(tree, torch_dir, why, monkeypatch, capfd):
+    if why == "source":
+        (tree / "bind.cpp").write_text("#error no\n")
+    else:
+        monkeypatch.setenv("CXX", str(tree / "no_such_compiler"))
+    open(sd_build.BIND, "w").write("an older one")
+    os.utime(sd_build.BIND, (1, 1))
+    sd_build.build()
+    assert ctypes.CDLL(sd_build.LIB).one() == 1
+    assert not os.path.exists(sd_build.BIND)
+    assert "extension was not built" in capfd.readouterr().err
+
+
+def test_without_a_torch_the_library_alone_is_built(tree, monkeypatch):
+    monkeypatch.setattr(sd_build, "_torch_dir", lambda: None)
+    sd_build.build()
+    assert ctypes.CDLL(sd_build.LIB).one() == 1 and not os.path.exists(sd_build.BIND)
+
+
+def test_a_torch_without_cuda_counts_as_none(tmp_path, monkeypatch):
+    (tmp_path / "torch").mkdir()
+    (tmp_path / "torch" / "__init__.py").write_text("")
+    spec = type("spec", (), {"origin": str(tmp_path / "torch" / "__init__.py")})
+    monkeypatch.setattr(sd_build.importlib.util, "find_spec", lambda name: spec)
+    assert sd_build._torch_dir() is None

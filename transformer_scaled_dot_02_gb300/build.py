@@ -3,7 +3,9 @@ CPython extension _bind.so with the host compiler.
 
 Each CUDA translation unit is compiled in parallel, then linked into one
 shared library with the CUDA runtime linked statically.  The extension is
-built against the installed torch (where there is none, the library alone is).
+built against the installed torch.  The library does not depend on it: without
+a torch for CUDA the library alone is built, and an extension that does not
+compile is reported, and left out.
 Usage:
     python -m transformer_scaled_dot_02_gb300.build [--force]
 """
@@ -44,8 +46,12 @@ def _flags() -> list[str]:
 
 
 def _torch_dir() -> str | None:
+    """The folder of an installed torch for CUDA."""
     spec = importlib.util.find_spec("torch")
-    return os.path.dirname(spec.origin) if spec is not None and spec.origin is not None else None
+    if spec is None or spec.origin is None:
+        return None
+    torch = os.path.dirname(spec.origin)
+    return torch if os.path.exists(os.path.join(torch, "lib", "libc10_cuda.so")) else None
 
 
 def _bind_command(nvcc: str, torch: str, out: str) -> list[str]:
@@ -84,22 +90,27 @@ def build(force: bool = False, verbose: bool = False) -> str:
         if verbose and (r.stdout or r.stderr):
             sys.stderr.write(r.stdout + r.stderr)
 
+    # the extension compiles beside the library's sources, and fails by itself
     bind_tmp = BIND + ".tmp%d" % os.getpid()
-    bind = None
     torch = _torch_dir()
-    if torch and (force or _stale(BIND, [BIND_SOURCE, os.path.join(INCLUDE, "sdpa.h"), __file__,
-                                         os.path.join(torch, "version.py")])):
-        bind = _bind_command(nvcc, torch, bind_tmp)
-    commands = jobs + ([bind] if bind else [])
-    if commands:
-        with cf.ThreadPoolExecutor(max_workers=len(commands)) as ex:
-            list(ex.map(run, commands))
-    if bind:
-        os.replace(bind_tmp, BIND)
+    bind = torch and (force or _stale(BIND, [BIND_SOURCE, os.path.join(INCLUDE, "sdpa.h"), __file__,
+                                             os.path.join(torch, "version.py")]))
+    with cf.ThreadPoolExecutor(max_workers=len(jobs) + 1) as ex:
+        binding = ex.submit(run, _bind_command(nvcc, torch, bind_tmp)) if bind else None
+        list(ex.map(run, jobs))
     if force or jobs or _stale(LIB, objs):
         tmp = LIB + ".tmp%d" % os.getpid()
         run([nvcc] + ARCH + ["-shared", "-cudart", "static", "-o", tmp] + objs)
         os.replace(tmp, LIB)
+    if binding is not None:
+        try:
+            binding.result()
+            os.replace(bind_tmp, BIND)
+        except (RuntimeError, OSError) as e:
+            # (one of older sources must not be taken for it)
+            if os.path.exists(BIND):
+                os.remove(BIND)
+            sys.stderr.write("the paged helpers' extension was not built: %s\n" % e)
     return LIB
 
 
