@@ -54,3 +54,31 @@ def test_a_torch_without_cuda_counts_as_none(tmp_path, monkeypatch):
     spec = type("spec", (), {"origin": str(tmp_path / "torch" / "__init__.py")})
     monkeypatch.setattr(sd_build.importlib.util, "find_spec", lambda name: spec)
     assert sd_build._torch_dir() is None
+
+
+def test_the_extension_follows_the_interpreter_and_the_torch(tree, torch_dir, monkeypatch):
+    import sysconfig
+    assert sd_build.BIND.endswith(sysconfig.get_config_var("EXT_SUFFIX"))
+
+    def rebuilt():
+        before = os.stat(sd_build.BIND).st_ino if os.path.exists(sd_build.BIND) else None
+        sd_build.build()
+        return os.stat(sd_build.BIND).st_ino != before
+
+    assert rebuilt() and not rebuilt()
+    monkeypatch.setattr(sd_build, "_torch_version", lambda torch: "0.0.1")
+    assert rebuilt() and not rebuilt()          # another torch, though its files are the older ones
+    os.remove(sd_build._bind_stamp())
+    assert rebuilt() and not rebuilt()
+
+
+def test_an_extension_of_another_torch_is_not_used(torch_dir, monkeypatch):
+    import torch
+    import transformer_scaled_dot_02_gb300 as sd
+    sd_build.build()
+    monkeypatch.setattr(sd, "_bind_module", None)
+    assert sd._paged().torch_version == str(torch.__version__)
+    monkeypatch.setattr(sd, "_bind_module", None)
+    monkeypatch.setattr(torch, "__version__", "0.0.1")
+    with pytest.raises(ImportError, match="built against torch"):
+        sd._paged()

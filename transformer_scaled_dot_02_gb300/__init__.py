@@ -6,11 +6,12 @@ and only marshal arguments: every step of the computation runs in the CUDA
 kernels of libsdpa.so.  Tensor arguments may be torch tensors (their
 ``data_ptr()`` is passed) or raw device addresses as ints.  ``stream`` defaults
 to PyTorch's current CUDA stream.  The paged helpers check and pass their
-tensors through a small extension, _bind.so (csrc/bind.cpp): a call takes 3 us
+tensors through a small extension, _bind (csrc/bind.cpp): a call takes 3 us
 so, 10 us in Python and ctypes.
 
-There is no fallback: if libsdpa.so (or, for the paged helpers, _bind.so) is
-missing or fails to load, importing the functions raises, and every call returns the library's status as an exception.
+There is no fallback: if libsdpa.so (or, for the paged helpers, _bind) is
+missing, fails to load or was built against another torch, the first call
+raises, and every call returns the library's status as an exception.
 
 The library picks kernels and tile sizes from the shapes;
 ``sdpa_set_kernel_choice`` (or the ``kernel_choice`` context manager) pins
@@ -269,12 +270,16 @@ def _paged():
     entry points (csrc/bind.cpp)."""
     global _bind_module
     if _bind_module is None:
-        import torch  # noqa: F401 (its libraries resolve the extension's symbols)
+        import torch   # (its libraries resolve the extension's symbols)
         lib = load_library()
         try:
             from . import _bind as module
         except ImportError as e:
-            raise ImportError("_bind.so not built; run transformer_scaled_dot_02_gb300.build") from e
+            raise ImportError("_bind not built; run transformer_scaled_dot_02_gb300.build") from e
+        built = getattr(module, "torch_version", None)
+        if built != str(torch.__version__):
+            raise ImportError("_bind was built against torch %s, not %s; run transformer_scaled_dot_02_gb300.build"
+                              % (built, torch.__version__))
         address = lambda f: ctypes.cast(f, ctypes.c_void_p).value
         module.bind(address(lib.sdpa_paged_append), address(lib.sdpa_paged_forward))
         _bind_module = module

@@ -1,11 +1,12 @@
 """Builds libsdpa.so in-tree with nvcc for sm_103a, and the paged helpers'
-CPython extension _bind.so with the host compiler.
+CPython extension _bind with the host compiler.
 
 Each CUDA translation unit is compiled in parallel, then linked into one
 shared library with the CUDA runtime linked statically.  The extension is
 built against the installed torch.  The library does not depend on it: without
 a torch for CUDA the library alone is built, and an extension that does not
-compile is reported, and left out.
+compile is reported, and left out.  Its name holds the interpreter's tag, and
+it is built again when the torch that it was built against changes.
 Usage:
     python -m transformer_scaled_dot_02_gb300.build [--force]
 """
@@ -14,6 +15,7 @@ from __future__ import annotations
 import concurrent.futures as cf
 import importlib.util
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -25,7 +27,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libsdpa.so")
-BIND = os.path.join(HERE, "_bind.so")
+BIND = os.path.join(HERE, "_bind" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 BIND_SOURCE = os.path.join(CSRC, "bind.cpp")
 SOURCES = ["api.cu", "sdpa_tc.cu", "sdpa_one_tile.cu", "sdpa_bwd.cu", "sdpa_f32.cu", "gemm_tc.cu",
            "decode.cu", "mha_noalloc.cu", "sdpa_bwd_wide.cu", "paged.cu"]
@@ -54,10 +56,36 @@ def _torch_dir() -> str | None:
     return torch if os.path.exists(os.path.join(torch, "lib", "libc10_cuda.so")) else None
 
 
+def _torch_version(torch: str) -> str:
+    """What torch.__version__ will be."""
+    with open(os.path.join(torch, "version.py")) as f:
+        return re.search(r"""^__version__\s*=\s*['"]([^'"]+)""", f.read(), re.M).group(1)
+
+
+def _fits(torch: str) -> str:
+    """What an extension built now fits: this interpreter, this torch."""
+    return "%s\n%s\n%s\n" % (os.path.basename(BIND), torch, _torch_version(torch))
+
+
+def _bind_stamp() -> str:
+    return os.path.join(BUILD_DIR, os.path.basename(BIND) + ".fits")
+
+
+def _bind_stale(torch: str) -> bool:
+    if _stale(BIND, [BIND_SOURCE, os.path.join(INCLUDE, "sdpa.h"), __file__]):
+        return True
+    try:
+        with open(_bind_stamp()) as f:
+            return f.read() != _fits(torch)
+    except OSError:
+        return True
+
+
 def _bind_command(nvcc: str, torch: str, out: str) -> list[str]:
     """Compiles and links the extension against the torch in this folder."""
     cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc))), "include")
     return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-I", INCLUDE,
+            '-DSDPA_TORCH_VERSION="%s"' % _torch_version(torch),
             "-isystem", os.path.join(torch, "include"), "-isystem", cuda, "-I", sysconfig.get_paths()["include"],
             BIND_SOURCE, "-o", out, "-L", os.path.join(torch, "lib"),
             "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
@@ -93,8 +121,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     # the extension compiles beside the library's sources, and fails by itself
     bind_tmp = BIND + ".tmp%d" % os.getpid()
     torch = _torch_dir()
-    bind = torch and (force or _stale(BIND, [BIND_SOURCE, os.path.join(INCLUDE, "sdpa.h"), __file__,
-                                             os.path.join(torch, "version.py")]))
+    bind = torch and (force or _bind_stale(torch))
     with cf.ThreadPoolExecutor(max_workers=len(jobs) + 1) as ex:
         binding = ex.submit(run, _bind_command(nvcc, torch, bind_tmp)) if bind else None
         list(ex.map(run, jobs))
@@ -106,6 +133,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
         try:
             binding.result()
             os.replace(bind_tmp, BIND)
+            with open(_bind_stamp(), "w") as f:
+                f.write(_fits(torch))
         except (RuntimeError, OSError) as e:
             # (one of older sources must not be taken for it)
             if os.path.exists(BIND):

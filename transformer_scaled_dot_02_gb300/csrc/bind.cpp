@@ -247,4 +247,12 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_bind", "Argument handling of the 
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__bind() { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__bind() {
+  PyObject* m = PyModule_Create(&module);
+  // the torch that this was compiled against: Python compares it with its own
+  if (m != nullptr && PyModule_AddStringConstant(m, "torch_version", SDPA_TORCH_VERSION) < 0) {
+    Py_DECREF(m);
+    return nullptr;
+  }
+  return m;
+}
