@@ -468,6 +468,13 @@ constexpr int kSliceVectors = 8;           // of a slice, at least (152 pieces o
 #define SDPA_TEST_PATIENCE (1 << 17)       // (a test leaves slices at once)
 #endif
 constexpr long long kPatience = SDPA_TEST_PATIENCE;   // clock cycles, about 65 us: runs end within a few of each other
+// The last run waits for the others' pieces as long as a CTA's warps wait for one
+// another, and longer by what its run takes: an item, a quarter of a key tile, takes
+// about 450 clock cycles.
+#ifndef SDPA_TEST_ITEM_CYCLES
+#define SDPA_TEST_ITEM_CYCLES 4096         // (a test waits longer)
+#endif
+constexpr long long kItemCycles = SDPA_TEST_ITEM_CYCLES;
 enum State : unsigned long long { kOpen, kTaken, kLeft };
 
 __device__ __forceinline__ unsigned long long load_acquire(const unsigned long long* x) {
@@ -586,9 +593,17 @@ struct Meeting {
   uint64_t* bar;
   int met;
   AbortState ab;
-  __device__ __forceinline__ bool operator()() {
+  __device__ __forceinline__ bool operator()() { return within<kWaitLimitCycles>(); }
+  // Where some of them come from a wait for other runs, which has a limit of its
+  // own: when that is over the abort flag ends the others' wait here too.  (A limit
+  // worked out here would cost registers in the loops: 8 bytes spilled at d = 128.)
+  __device__ __forceinline__ bool after_waits() { return within<(kWaitLimitCycles << 10)>(); }
+
+ private:
+  template <long long kLimit>
+  __device__ __forceinline__ bool within() {
     mbar_arrive(bar);
-    return mbar_wait_warp(bar, static_cast<uint32_t>(met++) & 1u, ab);
+    return mbar_wait_warp(bar, static_cast<uint32_t>(met++) & 1u, ab, kLimit);
   }
 };
 
@@ -734,7 +749,7 @@ __device__ __forceinline__ int merge_slices(const PagedParams& p, const Pieces& 
     if (final) time_out(ab);
     else left[0] = 1;
   }
-  if (!meet() || *ab.flag != 0) return -1;
+  if (!meet.after_waits() || *ab.flag != 0) return -1;
   const bool taken = left[0] == 0;
   if (threadIdx.x == 0)
     asm volatile("st.release.gpu.global.u64 [%0], %1;" ::"l"(p.states + u.cta),
@@ -750,7 +765,7 @@ __device__ __forceinline__ int merge_slices(const PagedParams& p, const Pieces& 
         if (!wait_word(p.states + first + x, [](unsigned long long v) { return v != kOpen; }, limit, ab)) time_out(ab);
         else if (load_acquire(p.states + first + x) == kLeft) left[1] = 1;
       }
-      if (!meet() || *ab.flag != 0) return -1;
+      if (!meet.after_waits() || *ab.flag != 0) return -1;
       for (int x = threadIdx.x; x < u.of; x += kBlockM) p.flags[u.place(p, x)] = 0;
       if (left[1] == 0) return meet.met;
       k = -1;
@@ -1096,11 +1111,17 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
       uint8_t* ring = smem + C::kKOff;
       // The slot is written: its flag, released after everybody's writes.
       auto publish = [&]() -> bool {
+#ifdef SDPA_TEST_LATE_PUBLISH
+        // (test builds only, never in libsdpa.so: a piece that is all of its run,
+        // and not the unit's last, is published this many clock cycles late)
+        if (open_above && w.off <= 0)
+          for (const long long t0 = clock64(); clock64() - t0 < SDPA_TEST_LATE_PUBLISH;) {}
+#endif
         if (!meet()) return false;
         if (threadIdx.x == 0) set_flag(p.flags + place, p.call);
         return true;
       };
-      const long long patience = kWaitLimitCycles + 4096 * run;   // a run's items take well below 4096 each
+      const long long patience = kWaitLimitCycles + kItemCycles * run;
       // What this run merges alone has been published.
       auto wait_sources = [&]() -> bool {
         bool got = true;
@@ -1110,7 +1131,7 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
           if (got) *flag = 0;
           else time_out(ab);
         }
-        return __all_sync(0xffffffffu, got) && meet();
+        return __all_sync(0xffffffffu, got) && meet.after_waits();
       };
       // O columns [c kOChunk, +kOChunk) of this row, normalised into the output
       auto store = [&](int c, const uint32_t (&o)[C::kOChunk], float inv_l) {

@@ -11,7 +11,10 @@ namespace sdpa {
 
 // A bounded wait gives up after this many SM clock cycles (about one second
 // at the GB300's clocks); nothing in a healthy kernel waits that long.
-constexpr long long kWaitLimitCycles = 2000000000ll;
+#ifndef SDPA_TEST_WAIT_LIMIT
+#define SDPA_TEST_WAIT_LIMIT 2000000000ll   // (a test waits less)
+#endif
+constexpr long long kWaitLimitCycles = SDPA_TEST_WAIT_LIMIT;
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
@@ -62,14 +65,15 @@ struct AbortState {
 
 // Waits for the phase with parity `parity` of `bar` to complete.  Returns
 // false (and raises the CTA's abort flag and the global error bit) when the
-// wait exceeds kWaitLimitCycles, or when another role already aborted.
-__device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, const AbortState& ab) {
+// wait exceeds `limit` clock cycles, or when another role already aborted.
+__device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, const AbortState& ab,
+                                          long long limit = kWaitLimitCycles) {
   if (mbar_try_wait(bar, parity)) return true;
   const long long t0 = clock64();
   while (true) {
     if (mbar_try_wait(bar, parity)) return true;
     if (*ab.flag) return false;
-    if (clock64() - t0 > kWaitLimitCycles) {
+    if (clock64() - t0 > limit) {
       *ab.flag = 1;
       atomicOr(ab.status, kStatusTimeout);
       return false;
@@ -88,8 +92,9 @@ __device__ __forceinline__ bool mbar_wait_drain(uint64_t* bar, uint32_t parity) 
 }
 
 // Warp-uniform wait: every lane waits, the warp continues only if all did.
-__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, const AbortState& ab) {
-  const bool ok = mbar_wait(bar, parity, ab);
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, const AbortState& ab,
+                                               long long limit = kWaitLimitCycles) {
+  const bool ok = mbar_wait(bar, parity, ab, limit);
   return __all_sync(0xffffffffu, ok);
 }
 
