@@ -1330,9 +1330,6 @@ __global__ void __launch_bounds__(kThreads, PCfg<D>::kMinBlocks)
               if (x < rows) ml_row = make_float2(top, sum);
               if (further) {
                 reinterpret_cast<float4*>(ring)[x] = acc;
-              } else if (open_above) {
-                reinterpret_cast<float4*>(slot(cta))[x] = acc;
-                if (x < rows) ml_of(slot(cta))[rw] = ml_row;
               } else {
                 write_four(p.out + out_begin<D>(p, unit.row0, unit.head0, rw) + col * 4, acc, sum > 0.f ? 1.f / sum : 0.f);
               }
