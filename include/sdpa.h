@@ -270,8 +270,9 @@ sdpa_status sdpa_decode(const void* q, const void* k, const void* v, void* out, 
  *   rope_freqs  device fp32 [d_rot / 2]: radians per position.  With angle
  *     t = position * rope_freqs[j], the pair (a, b) becomes
  *     (a cos t - b sin t, b cos t + a sin t); angles are exact to 1.3e-6 at
- *     any position while they are below 2^48.  Pair j is columns j and j + d_rot / 2, or 2 j and
- *     2 j + 1 with interleaved != 0; columns from d_rot on stay as they are.
+ *     any position while they are below 2^48.  Pair j is columns j and
+ *     j + d_rot / 2, or 2 j and 2 j + 1 with interleaved != 0; columns from
+ *     d_rot on stay as they are.
  *   d_rot  a multiple of 16, 0 <= d_rot <= d; 0 copies (rope_freqs may be NULL)
  * Arithmetic is fp32, rounded once to bf16.  A token at a negative position
  * (more new tokens than the length) is rotated but not stored.  Two tokens
