@@ -266,7 +266,7 @@ _bind_module = None
 
 
 def _paged():
-    """The extension that checks the paged helpers' tensors and calls the two
+    """The extension that checks the paged helpers' tensors and calls the
     entry points (csrc/bind.cpp)."""
     global _bind_module
     if _bind_module is None:
@@ -281,7 +281,8 @@ def _paged():
             raise ImportError("_bind was built against torch %s, not %s; run transformer_scaled_dot_02_gb300.build"
                               % (built, torch.__version__))
         address = lambda f: ctypes.cast(f, ctypes.c_void_p).value
-        module.bind(address(lib.sdpa_paged_append), address(lib.sdpa_paged_forward))
+        module.bind(address(lib.sdpa_paged_append), address(lib.sdpa_paged_forward),
+                    address(lib.sdpa_paged_workspace_size))
         _bind_module = module
     return _bind_module
 
@@ -323,8 +324,6 @@ def paged_attention(q, k_pages, v_pages, page_table, q_starts, kv_lengths, scale
     if stream is not None:
         with _on_stream(stream):
             return paged_attention(q, k_pages, v_pages, page_table, q_starts, kv_lengths, scale, out, workspace)
-    if workspace is None:
-        workspace = paged_workspace(q, k_pages, page_table)
     done = (_bind_module or _paged()).forward(q, k_pages, v_pages, page_table, q_starts, kv_lengths, scale, out,
                                              workspace)
     if type(done) is int:

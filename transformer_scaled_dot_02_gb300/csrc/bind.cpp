@@ -25,6 +25,7 @@ namespace {
 
 decltype(&sdpa_paged_append) append_entry = nullptr;
 decltype(&sdpa_paged_forward) forward_entry = nullptr;
+decltype(&sdpa_paged_workspace_size) workspace_entry = nullptr;
 
 constexpr int kInvalid = SDPA_ERR_INVALID_ARG;
 
@@ -179,7 +180,8 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// forward(q, k_pages, v_pages, page_table, q_starts, kv_lengths, scale, out, workspace)
+// forward(q, k_pages, v_pages, page_table, q_starts, kv_lengths, scale, out, workspace);
+// a workspace that is not given is allocated once the tensors have been checked
 PyObject* forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (!counted("forward", n, 9, forward_entry != nullptr)) return nullptr;
   return guarded([&]() -> PyObject* {
@@ -194,7 +196,7 @@ PyObject* forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int64_t t = q.size(0), h = q.size(1);
     long long q_stride, out_stride;
     if (t > INT32_MAX || h > INT32_MAX || !check_rows(q, t, h, c, &q_stride)) return status_object(kInvalid);
-    at::Tensor made;
+    at::Tensor made, made_ws;
     void *out_ptr, *ws = nullptr;
     if (a[7] == Py_None) {
       made = at::empty({t, h, c.d}, q.options());
@@ -212,6 +214,12 @@ PyObject* forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
       if (!plain(*w, w->scalar_type(), c.device) || !w->is_contiguous()) return status_object(kInvalid);
       ws = w->data_ptr();
       ws_bytes = w->nbytes();
+    } else {
+      ws_bytes = workspace_entry(c.b, static_cast<int>(t), static_cast<int>(h), c.h_kv, c.d, c.page, c.per_seq);
+      if (ws_bytes > 0) {
+        made_ws = at::empty({static_cast<int64_t>(ws_bytes)}, q.options().dtype(at::kByte));
+        ws = made_ws.data_ptr();
+      }
     }
     const void* q_ptr = q.const_data_ptr();
     void* stream = c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(c.device)).stream();
@@ -226,13 +234,15 @@ PyObject* forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// bind(append, forward): the addresses of sdpa_paged_append and sdpa_paged_forward
+// bind(append, forward, workspace): the addresses of sdpa_paged_append,
+// sdpa_paged_forward and sdpa_paged_workspace_size
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  if (!counted("bind", n, 2, true)) return nullptr;
-  void *x = PyLong_AsVoidPtr(a[0]), *y = PyLong_AsVoidPtr(a[1]);
+  if (!counted("bind", n, 3, true)) return nullptr;
+  void *x = PyLong_AsVoidPtr(a[0]), *y = PyLong_AsVoidPtr(a[1]), *z = PyLong_AsVoidPtr(a[2]);
   if (PyErr_Occurred()) return nullptr;
   append_entry = reinterpret_cast<decltype(append_entry)>(x);
   forward_entry = reinterpret_cast<decltype(forward_entry)>(y);
+  workspace_entry = reinterpret_cast<decltype(workspace_entry)>(z);
   Py_RETURN_NONE;
 }
 
