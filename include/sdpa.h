@@ -276,7 +276,9 @@ sdpa_status sdpa_decode(const void* q, const void* k, const void* v, void* out, 
  *   d_rot  a multiple of 16, 0 <= d_rot <= d; 0 copies (rope_freqs may be NULL)
  * Arithmetic is fp32, rounded once to bf16.  A token at a negative position
  * (more new tokens than the length) is rotated but not stored.  Two tokens
- * that the tables send to one place race.
+ * that the tables send to one place race, and so do pages of keys and values
+ * that overlap, or rows that lie in pages which the call writes (the Python
+ * helper refuses overlapping pages).
  */
 sdpa_status sdpa_paged_append(const void* q, const void* k, const void* v, void* q_out,
                               void* k_pages, void* v_pages, int b, int n_tokens, int h, int h_kv,

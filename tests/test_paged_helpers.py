@@ -70,3 +70,20 @@ def test_a_workspace_is_made_where_one_is_needed():
         want, bound = pu.attention(host(q), *dense, [0, 1], [16 * per_seq])
         assert np.all(np.abs(host(sd.paged_attention(*args)) - want) <= bound)
     sd.sdpa_device_check()
+
+
+@pytest.mark.gpu
+def test_keys_and_values_in_one_place_are_refused_by_the_append_alone():
+    rows, pages, _, table, ints, lens = _tensors("cuda")
+    starts, lens = ints + torch.tensor([0, 1], dtype=torch.int32, device="cuda"), lens + 5
+    both = torch.zeros(5, 2, 16, 64, dtype=torch.bfloat16, device="cuda")
+    for kp, vp in ((pages, pages), (both[:4], both[1:]), (both[1:], both[:4])):
+        with pytest.raises(sd.SdpaError) as e:
+            sd.paged_append(rows, rows, rows, kp, vp, table, starts, lens)
+        assert e.value.status == 1
+        assert torch.all(sd.paged_attention(rows, kp, vp, table, starts, lens) == 0)
+    kp, vp = torch.zeros(2, 4, 2, 16, 64, dtype=torch.bfloat16, device="cuda")     # side by side is well
+    sd.paged_append(rows, rows + 1, rows + 2, kp, vp, table, starts, lens)
+    assert kp[0, :, 4].eq(1).all() and vp[0, :, 4].eq(2).all()
+    assert kp.sum() == 128 and vp.sum() == 256
+    sd.sdpa_device_check()

@@ -16,6 +16,7 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <cstdint>
 #include <exception>
 #include <new>
 
@@ -82,6 +83,13 @@ bool check_cache(const at::Tensor& k, const at::Tensor& v, const at::Tensor& tab
   return true;
 }
 
+// Do the keys' and the values' pages share memory?  The attention may read them so,
+// the append would store both to one place.
+bool pages_overlap(const at::Tensor& k, const at::Tensor& v) {
+  const auto a = reinterpret_cast<uintptr_t>(k.const_data_ptr()), b = reinterpret_cast<uintptr_t>(v.const_data_ptr());
+  return a < b + v.nbytes() && b < a + k.nbytes();
+}
+
 // Packed rows [n_tokens, heads, d] whose heads are dense; the stride from token
 // to token (a single token's says nothing).
 bool check_rows(const at::Tensor& x, int64_t n_tokens, int64_t heads, const Cache& c, long long* stride) {
@@ -128,7 +136,8 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
       if ((x[i] = tensor_of(a[i])) == nullptr) return nullptr;
     const at::Tensor &k = *x[1], &v = *x[2];
     Cache c;
-    if (!check_cache(*x[3], *x[4], *x[5], *x[6], *x[7], &c) || k.dim() != 3) return status_object(kInvalid);
+    if (!check_cache(*x[3], *x[4], *x[5], *x[6], *x[7], &c) || k.dim() != 3 || pages_overlap(*x[3], *x[4]))
+      return status_object(kInvalid);
     const int64_t t = k.size(0);
     long long q_stride = 0, k_stride, v_stride, out_stride;
     if (t > INT32_MAX || !check_rows(k, t, c.h_kv, c, &k_stride) || !check_rows(v, t, c.h_kv, c, &v_stride))
