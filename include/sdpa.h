@@ -304,6 +304,10 @@ sdpa_status sdpa_paged_append(const void* q, const void* k, const void* v, void*
  *       each.  The size depends on the current device's SM count: ask on the
  *       device the call runs on.  After SDPA_ERR_DEVICE_TIMEOUT, clear it before
  *       a captured call uses it again.
+ * Parts of a long walk are computed by several blocks and joined by the one of
+ * the highest index, which waits for the others.  A GPU that did not start a
+ * launch's blocks in the order of their index (CUDA promises none) could leave
+ * it waiting for blocks that cannot start: SDPA_ERR_DEVICE_TIMEOUT.
  * Scores, softmax statistics and sums are fp32; the softmax weights enter the
  * products with the values rounded to bf16.  Cache rows past a sequence's
  * length may hold anything; those below it must be finite.

@@ -23,8 +23,9 @@
 // workspace; if it begins inside a unit, that piece comes last, and the CTA
 // merges the pieces that the runs before it published:
 //   O = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s, M = max_s m_s.
-// So a CTA waits for CTAs of lower index only, which are dispatched before it:
-// the waits end however few CTAs run at a time.  Units cut into many pieces are
+// So a CTA waits for CTAs of lower index only.  GPUs start a launch's CTAs in the
+// order of their index, which CUDA does not promise: with it the waits end however
+// few CTAs run at a time, without it they run out and are reported.  Units cut into many pieces are
 // merged in slices by several CTAs, which wait for one another, but not for long
 // (see merge).  The pieces merge in an order fixed by the cut, so results repeat
 // bit by bit.
@@ -92,9 +93,11 @@ __device__ __forceinline__ int walk_tiles(int keys) { return max(1, (keys + kBN 
 
 // What a unit is expected to take: `start` (loading Q, storing O) and 2^log_tile
 // for each key tile, in quarters of a key tile.  From least squares over the
-// CTAs' times on GB300: two prompts of 8192 tokens (16 heads of 128) take 4.4 us
-// a walk and 0.94 us a wide key tile, 16 x 4 drafted tokens (64 wide) 2.4 us
-// and 0.67 us a narrow one.  Counting key tiles alone, the CTAs with a prompt's
+// CTAs' times of two calls on GB300: two prompts of 8192 tokens (16 heads of 128) take
+// 4.4 us a walk and 0.94 us a wide key tile, 16 x 4 drafted tokens (64 wide) 2.4 us
+// and 0.67 us a narrow one.  So a start is worth 18 or 14 quarters; wide and narrow
+// key tiles, and those of all head and page sizes, count alike, and a cut piece's
+// publication and merge are left out.  Counting key tiles alone, the CTAs with a prompt's
 // shortest walks finished 20 % after the others (514 us instead of 396).
 struct Weight {
   int start, log_tile;
