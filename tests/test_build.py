@@ -28,12 +28,16 @@ def torch_dir():
     return torch
 
 
-@pytest.mark.parametrize("why", ["source", "compiler"])
+@pytest.mark.parametrize("why", ["source", "compiler", "version"])
 def test_the_library_is_built_where_the_extension_is_not(tree, torch_dir, why, monkeypatch, capfd):
     if why == "source":
         (tree / "bind.cpp").write_text("#error no\n")
-    else:
+    elif why == "compiler":
         monkeypatch.setenv("CXX", str(tree / "no_such_compiler"))
+    else:
+        real = open
+        monkeypatch.setattr("builtins.open", lambda path, *a, **k: real(
+            str(tree / "one.cu") if str(path) == os.path.join(torch_dir, "version.py") else path, *a, **k))
     open(sd_build.BIND, "w").write("an older one")
     os.utime(sd_build.BIND, (1, 1))
     sd_build.build()

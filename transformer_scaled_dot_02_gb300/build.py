@@ -59,7 +59,10 @@ def _torch_dir() -> str | None:
 def _torch_version(torch: str) -> str:
     """What torch.__version__ will be."""
     with open(os.path.join(torch, "version.py")) as f:
-        return re.search(r"""^__version__\s*=\s*['"]([^'"]+)""", f.read(), re.M).group(1)
+        found = re.search(r"""^__version__\s*=\s*['"]([^'"]+)""", f.read(), re.M)
+    if found is None:
+        raise RuntimeError("no version in %s" % os.path.join(torch, "version.py"))
+    return found.group(1)
 
 
 def _fits(torch: str) -> str:
@@ -77,7 +80,7 @@ def _bind_stale(torch: str) -> bool:
     try:
         with open(_bind_stamp()) as f:
             return f.read() != _fits(torch)
-    except OSError:
+    except (RuntimeError, OSError):
         return True
 
 
@@ -119,11 +122,11 @@ def build(force: bool = False, verbose: bool = False) -> str:
             sys.stderr.write(r.stdout + r.stderr)
 
     # the extension compiles beside the library's sources, and fails by itself
-    bind_tmp = BIND + ".tmp%d" % os.getpid()
+    bind_tmp = os.path.join(BUILD_DIR, os.path.basename(BIND) + ".tmp%d" % os.getpid())
     torch = _torch_dir()
     bind = torch and (force or _bind_stale(torch))
     with cf.ThreadPoolExecutor(max_workers=len(jobs) + 1) as ex:
-        binding = ex.submit(run, _bind_command(nvcc, torch, bind_tmp)) if bind else None
+        binding = ex.submit(lambda: run(_bind_command(nvcc, torch, bind_tmp))) if bind else None
         list(ex.map(run, jobs))
     if force or jobs or _stale(LIB, objs):
         tmp = LIB + ".tmp%d" % os.getpid()
