@@ -323,6 +323,77 @@ sdpa_status sdpa_paged_forward(const void* q, const void* k_pages, const void* v
                                void* stream);
 
 /*
+ * The paged cache held in 4 bits: 4.5 bits a value instead of 16, so that a
+ * cache holds 3.5 times the positions and a step reads as many fewer bytes.
+ * Page tables, lengths, packed rows, head shapes, limits and the report of bad
+ * pages are those of the bf16 cache above, but for the pages:
+ *   k_pages, v_pages [n_pages, h_kv, page_size, 9 d / 16] bytes, device;
+ *     page_size a power of two of at least 16 (else SDPA_ERR_UNSUPPORTED)
+ * A row is held in blocks of 16 columns.  With the unit u = 2^exp, a block is
+ *   s   = e4m3(max_i |x_i| / (6 u))   nearest, ties to even, at most 448
+ *   c_i = e2m1(x_i / (s u))           0, 0.5, 1, 1.5, 2, 3, 4, 6 and a sign;
+ *                                     nearest, ties to even; 0 where s is 0
+ * and stands for c_i s u, exactly a bf16 number.  A page of one key-value head
+ * is its rows' codes (d / 2 bytes a row, columns 2 i and 2 i + 1 in the low and
+ * the high half of byte i, the sign the highest of a code's four bits), then its
+ * rows' scales (d / 16 bytes a row).  k_exp and v_exp (-32 .. 32, else
+ * SDPA_ERR_UNSUPPORTED) are the exponents of keys and values: the same for every
+ * call on a cache.  Scales reach from 2^-9 to 448 with full precision from
+ * 2^-6 on, so 2^exp is best a hundredth to a tenth of the largest values.
+ *
+ * sdpa_paged4_append is sdpa_paged_append into such a cache: queries are rotated
+ * and rounded to bf16, keys are rotated and quantised from the rotation itself,
+ * as if worked out exactly where the nearest scale or code is in doubt.  Rows
+ * must be finite: infinities count as the largest number, of a NaN only that
+ * something finite is stored.  Pages that overlap each other, the rows or q_out
+ * return SDPA_ERR_INVALID_ARG.
+ */
+sdpa_status sdpa_paged4_append(const void* q, const void* k, const void* v, void* q_out,
+                               void* k_pages, void* v_pages, int b, int n_tokens, int h, int h_kv,
+                               int d, int page_size, int n_pages, int pages_per_seq,
+                               const int32_t* page_table, const int32_t* q_starts,
+                               const int32_t* kv_lengths, long long q_stride, long long k_stride,
+                               long long v_stride, const float* rope_freqs, int d_rot,
+                               int interleaved, int k_exp, int v_exp, void* stream);
+
+/*
+ * The cache read back: row i of the n rows [q_starts[s], q_starts[s+1]) is
+ * position kv_lengths[s] - n + i of sequence s, as what its codes stand for.
+ *   k_out, v_out [n_tokens, h_kv, d] bf16, device, written, dense (must overlap
+ *     neither each other nor the pages); zeros for a row at a negative position
+ *     and for a page outside the cache, rows of no sequence stay as they were
+ */
+sdpa_status sdpa_paged4_read(const void* k_pages, const void* v_pages, void* k_out, void* v_out,
+                             int b, int n_tokens, int h_kv, int d, int page_size, int n_pages,
+                             int pages_per_seq, const int32_t* page_table, const int32_t* q_starts,
+                             const int32_t* kv_lengths, int k_exp, int v_exp, void* stream);
+
+/*
+ * sdpa_paged_forward over the cache in 4 bits, with an optional window.
+ *   window  0: the token at position p sees keys j <= p.  Else it sees the last
+ *           `window` of them, p - window < j, and the first `sinks`, j < sinks
+ *   sinks   first positions that stay visible behind the window (>= 0)
+ * A page that holds no visible position is not looked at: its table entry may
+ * be anything, and its memory another sequence's.
+ *   workspace: as sdpa_paged_forward's, of sdpa_paged4_workspace_size(...) bytes.
+ *     A call that failed or timed out leaves counts in it: clear it before a
+ *     captured call uses it again.
+ * Scores and softmax statistics are fp32; queries enter the products as fp16
+ * scaled by a power of two for each row (elements down to 2^-27 of the row's
+ * largest keep every bit), keys and values as what the codes stand for, and the
+ * softmax weights rounded to fp16.  No block waits for another.
+ */
+size_t sdpa_paged4_workspace_size(int b, int n_tokens, int h, int h_kv, int d, int page_size,
+                                  int pages_per_seq);
+
+sdpa_status sdpa_paged4_forward(const void* q, const void* k_pages, const void* v_pages, void* out,
+                                void* workspace, size_t ws_bytes, int b, int n_tokens, int h,
+                                int h_kv, int d, int page_size, int n_pages, int pages_per_seq,
+                                const int32_t* page_table, const int32_t* q_starts,
+                                const int32_t* kv_lengths, long long q_stride, float scale,
+                                int k_exp, int v_exp, int window, int sinks, void* stream);
+
+/*
  * Bytes of device workspace mha_forward needs: the projected Q [b*n_q, h*d_k],
  * K [b*n_k, h*d_k], V [b*n_k, h*d_v] and the concatenated heads
  * [b*n_q, h*d_v], bf16, each rounded up to 256 bytes.  Returns 0 for

@@ -37,7 +37,8 @@ STATUS_NAMES = {0: "SDPA_OK", 1: "SDPA_ERR_INVALID_ARG", 2: "SDPA_ERR_UNSUPPORTE
 EXPORTS = ("sdpa_forward", "sdpa_forward_restricted", "sdpa_forward_lse", "sdpa_forward_host",
            "sdpa_backward_workspace_size", "sdpa_backward", "sdpa_forward_f32",
            "sdpa_decode_workspace_size", "sdpa_decode", "sdpa_paged_append",
-           "sdpa_paged_workspace_size", "sdpa_paged_forward", "mha_workspace_size",
+           "sdpa_paged_workspace_size", "sdpa_paged_forward", "sdpa_paged4_append",
+           "sdpa_paged4_read", "sdpa_paged4_workspace_size", "sdpa_paged4_forward", "mha_workspace_size",
            "mha_forward",
            "mha_forward_noalloc", "linear_forward", "sdpa_set_kernel_choice", "sdpa_device_check",
            "sdpa_status_string")
@@ -93,6 +94,15 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
     lib.sdpa_paged_workspace_size.restype = SZ
     lib.sdpa_paged_forward.argtypes = [P, P, P, P, P, SZ, I, I, I, I, I, I, I, I, P, P, P, L, F, P]
     lib.sdpa_paged_forward.restype = I
+    lib.sdpa_paged4_append.argtypes = [P, P, P, P, P, P, I, I, I, I, I, I, I, I, P, P, P, L, L, L, P, I,
+                                       I, I, I, P]
+    lib.sdpa_paged4_append.restype = I
+    lib.sdpa_paged4_read.argtypes = [P, P, P, P, I, I, I, I, I, I, I, P, P, P, I, I, P]
+    lib.sdpa_paged4_read.restype = I
+    lib.sdpa_paged4_workspace_size.argtypes = [I, I, I, I, I, I, I]
+    lib.sdpa_paged4_workspace_size.restype = SZ
+    lib.sdpa_paged4_forward.argtypes = [P, P, P, P, P, SZ, I, I, I, I, I, I, I, I, P, P, P, L, F, I, I, I, I, P]
+    lib.sdpa_paged4_forward.restype = I
     lib.mha_workspace_size.argtypes = [I, I, I, I, I, I]
     lib.mha_workspace_size.restype = SZ
     lib.mha_forward.argtypes = [P, P, P, P, P, P, P, P, SZ, I, I, I, I, I, I, I, I, P, F, P]
@@ -262,6 +272,43 @@ def sdpa_paged_forward(q, k_pages, v_pages, out, workspace, ws_bytes, b, n_token
         _addr(kv_lengths), q_stride, float(scale), _stream(stream)), "sdpa_paged_forward")
 
 
+def sdpa_paged4_append(q, k, v, q_out, k_pages, v_pages, b, n_tokens, h, h_kv, d, page_size, n_pages,
+                       pages_per_seq, page_table, q_starts, kv_lengths, q_stride, k_stride, v_stride,
+                       rope_freqs=None, d_rot=0, interleaved=False, k_exp=0, v_exp=0, stream=None) -> None:
+    """sdpa_paged_append into a cache held in 4 bits (see include/sdpa.h)."""
+    _check(load_library().sdpa_paged4_append(
+        _addr(q), _addr(k), _addr(v), _addr(q_out), _addr(k_pages), _addr(v_pages), b, n_tokens, h,
+        h_kv, d, page_size, n_pages, pages_per_seq, _addr(page_table), _addr(q_starts),
+        _addr(kv_lengths), q_stride, k_stride, v_stride, _addr(rope_freqs), d_rot, int(interleaved),
+        k_exp, v_exp, _stream(stream)), "sdpa_paged4_append")
+
+
+def sdpa_paged4_read(k_pages, v_pages, k_out, v_out, b, n_tokens, h_kv, d, page_size, n_pages, pages_per_seq,
+                     page_table, q_starts, kv_lengths, k_exp=0, v_exp=0, stream=None) -> None:
+    """Rows of a cache held in 4 bits back as bf16 (see include/sdpa.h)."""
+    _check(load_library().sdpa_paged4_read(
+        _addr(k_pages), _addr(v_pages), _addr(k_out), _addr(v_out), b, n_tokens, h_kv, d, page_size,
+        n_pages, pages_per_seq, _addr(page_table), _addr(q_starts), _addr(kv_lengths), k_exp, v_exp,
+        _stream(stream)), "sdpa_paged4_read")
+
+
+def sdpa_paged4_workspace_size(b, n_tokens, h, h_kv, d, page_size, pages_per_seq) -> int:
+    return int(load_library().sdpa_paged4_workspace_size(b, n_tokens, h, h_kv, d, page_size,
+                                                         pages_per_seq))
+
+
+def sdpa_paged4_forward(q, k_pages, v_pages, out, workspace, ws_bytes, b, n_tokens, h, h_kv, d, page_size,
+                        n_pages, pages_per_seq, page_table, q_starts, kv_lengths, q_stride, scale=0.0,
+                        k_exp=0, v_exp=0, window=0, sinks=0, stream=None) -> None:
+    """Attention of packed new tokens over a paged cache held in 4 bits, all of
+    it or a window and the first positions (see include/sdpa.h)."""
+    _check(load_library().sdpa_paged4_forward(
+        _addr(q), _addr(k_pages), _addr(v_pages), _addr(out), _addr(workspace), int(ws_bytes), b,
+        n_tokens, h, h_kv, d, page_size, n_pages, pages_per_seq, _addr(page_table), _addr(q_starts),
+        _addr(kv_lengths), q_stride, float(scale), k_exp, v_exp, window, sinks, _stream(stream)),
+        "sdpa_paged4_forward")
+
+
 _bind_module = None
 
 
@@ -282,7 +329,9 @@ def _paged():
                               % (built, torch.__version__))
         address = lambda f: ctypes.cast(f, ctypes.c_void_p).value
         module.bind(address(lib.sdpa_paged_append), address(lib.sdpa_paged_forward),
-                    address(lib.sdpa_paged_workspace_size))
+                    address(lib.sdpa_paged_workspace_size), address(lib.sdpa_paged4_append),
+                    address(lib.sdpa_paged4_read), address(lib.sdpa_paged4_forward),
+                    address(lib.sdpa_paged4_workspace_size))
         _bind_module = module
     return _bind_module
 
@@ -328,6 +377,69 @@ def paged_attention(q, k_pages, v_pages, page_table, q_starts, kv_lengths, scale
                                              workspace)
     if type(done) is int:
         raise SdpaError(done, "paged_attention")
+    return done
+
+
+def paged4_pages(n_pages, h_kv, page_size, d, device="cuda"):
+    """Allocates with torch the pages of keys, or of values, of a cache held in
+    4 bits: bytes [n_pages, h_kv, page_size, 9 d / 16], zeros."""
+    import torch
+    if d % 16 != 0:
+        raise SdpaError(1, "paged4_pages")
+    return torch.zeros((n_pages, h_kv, page_size, 9 * d // 16), dtype=torch.uint8, device=device)
+
+
+def paged4_append(q, k, v, k_pages, v_pages, page_table, q_starts, kv_lengths, rope_freqs=None,
+                  interleaved=False, k_exp=0, v_exp=0, q_out=None, stream=None):
+    """paged_append into a cache held in 4 bits (paged4_pages), in units of
+    2^k_exp and 2^v_exp.  Returns the rotated queries; q = None appends alone."""
+    if stream is not None:
+        with _on_stream(stream):
+            return paged4_append(q, k, v, k_pages, v_pages, page_table, q_starts, kv_lengths, rope_freqs,
+                                 interleaved, k_exp, v_exp, q_out)
+    done = (_bind_module or _paged()).append4(q, k, v, k_pages, v_pages, page_table, q_starts, kv_lengths, rope_freqs,
+                                             interleaved, k_exp, v_exp, q_out)
+    if type(done) is int:
+        raise SdpaError(done, "paged4_append")
+    return done
+
+
+def paged4_read(k_pages, v_pages, page_table, q_starts, kv_lengths, k_out, v_out, k_exp=0, v_exp=0, stream=None):
+    """Reads positions of a cache held in 4 bits back into bf16 tensors k_out,
+    v_out [t,h_kv,d]: rows [q_starts[s], q_starts[s+1]) are the last positions
+    of sequence s.  Returns (k_out, v_out)."""
+    if stream is not None:
+        with _on_stream(stream):
+            return paged4_read(k_pages, v_pages, page_table, q_starts, kv_lengths, k_out, v_out, k_exp, v_exp)
+    done = (_bind_module or _paged()).read4(k_pages, v_pages, page_table, q_starts, kv_lengths, k_out, v_out, k_exp,
+                                           v_exp)
+    if done != 0:
+        raise SdpaError(done, "paged4_read")
+    return k_out, v_out
+
+
+def paged4_workspace(q, k_pages, page_table):
+    """Allocates with torch the workspace of paged4_attention for these shapes
+    (None where it needs none), to be kept as that of paged_attention."""
+    import torch
+    n_pages, h_kv, page, _ = k_pages.shape
+    need = sdpa_paged4_workspace_size(page_table.shape[0], q.shape[0], q.shape[1], h_kv, q.shape[2], page,
+                                      page_table.shape[1])
+    return torch.empty(need, dtype=torch.uint8, device=q.device) if need > 0 else None
+
+
+def paged4_attention(q, k_pages, v_pages, page_table, q_starts, kv_lengths, scale=0.0, k_exp=0, v_exp=0, window=0,
+                     sinks=0, out=None, workspace=None, stream=None):
+    """paged_attention over a cache held in 4 bits.  With window > 0 a token
+    sees the last `window` positions up to its own and the first `sinks`."""
+    if stream is not None:
+        with _on_stream(stream):
+            return paged4_attention(q, k_pages, v_pages, page_table, q_starts, kv_lengths, scale, k_exp, v_exp, window,
+                                    sinks, out, workspace)
+    done = (_bind_module or _paged()).forward4(q, k_pages, v_pages, page_table, q_starts, kv_lengths, scale, k_exp,
+                                              v_exp, window, sinks, out, workspace)
+    if type(done) is int:
+        raise SdpaError(done, "paged4_attention")
     return done
 
 

@@ -5,6 +5,7 @@
 #include <algorithm>
 #include <atomic>
 #include <chrono>
+#include <climits>
 #include <cmath>
 #include <cstdint>
 #include <mutex>
@@ -480,6 +481,47 @@ int paged_slot_bytes(int n_tokens, int group, int d) {
   return static_cast<int>(round256(static_cast<size_t>(rows) * (d * 4 + 8) + 8));
 }
 
+// Do [a, a + n) and [b, b + m) share memory?
+bool bytes_overlap(const void* a, unsigned long long n, const void* b, unsigned long long m) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return n > 0 && m > 0 && x < y + m && y < x + n;
+}
+
+// ------------------------------------------------- the paged cache in 4 bits
+constexpr int kPaged4MaxExp = 32;
+
+// Rules beside check_paged_args': pages whose parts are aligned, units.
+sdpa_status check_paged4_args(const void* k_pages, const void* v_pages, int b, int n_tokens, int h,
+                              int h_kv, int d, int page_size, int n_pages, int pages_per_seq,
+                              const int32_t* page_table, const int32_t* q_starts,
+                              const int32_t* kv_lengths, int k_exp, int v_exp) {
+  const sdpa_status st = check_paged_args(k_pages, v_pages, b, n_tokens, h, h_kv, d, page_size, n_pages,
+                                          pages_per_seq, page_table, q_starts, kv_lengths);
+  if (st != SDPA_OK) return st;
+  auto in_range = [](int exp) { return exp >= -kPaged4MaxExp && exp <= kPaged4MaxExp; };
+  if (page_size < sdpa::kPaged4MinPage || !in_range(k_exp) || !in_range(v_exp)) return SDPA_ERR_UNSUPPORTED;
+  return SDPA_OK;
+}
+
+unsigned long long paged4_cache_bytes(int n_pages, int h_kv, int page_size, int d) {
+  return static_cast<unsigned long long>(n_pages) * h_kv * page_size * (9 * d / 16);
+}
+
+// Runs that the attention's work is cut into: every CTA that the GPU holds at a
+// time, or as many as there could ever be work for.
+int paged4_runs(int b, int n_tokens, int h_kv, int group, int d, long long max_len) {
+  const int rows = sdpa::paged4_rows(group, n_tokens, b);
+  const long long units = (1ll * n_tokens * group / rows + std::min(b, n_tokens)) * h_kv;
+  const long long most = std::min<long long>(sdpa::kPaged4MaxRuns,
+                                             1ll * sdpa::paged4_resident_ctas(d, rows) * sdpa::device_sm_count());
+  return static_cast<int>(std::max(1ll, std::min(most, sdpa::paged4_most_runs(units, max_len))));
+}
+
+// Bytes of a workspace slot: fp32 O, and two statistics a row twice.
+int paged4_slot_bytes(int group, int n_tokens, int b, int d) {
+  return static_cast<int>(round256(static_cast<size_t>(sdpa::paged4_rows(group, n_tokens, b)) * (d * 4 + 16)));
+}
+
 }  // namespace
 
 namespace sdpa {
@@ -939,6 +981,203 @@ sdpa_status sdpa_paged_forward(const void* q, const void* k_pages, const void* v
   p.scale_log2 = effective_scale(scale, d) * 1.4426950408889634f;
   return sdpa::launch_sdpa_paged(p, d, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SDPA_OK
                                                                                           : SDPA_ERR_CUDA;
+}
+
+sdpa_status sdpa_paged4_append(const void* q, const void* k, const void* v, void* q_out,
+                               void* k_pages, void* v_pages, int b, int n_tokens, int h, int h_kv,
+                               int d, int page_size, int n_pages, int pages_per_seq,
+                               const int32_t* page_table, const int32_t* q_starts,
+                               const int32_t* kv_lengths, long long q_stride, long long k_stride,
+                               long long v_stride, const float* rope_freqs, int d_rot,
+                               int interleaved, int k_exp, int v_exp, void* stream) {
+  // an empty tensor of rows has no address
+  if (n_tokens != 0 && (k == nullptr || v == nullptr || (q == nullptr) != (q_out == nullptr)))
+    return SDPA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out))
+    return SDPA_ERR_INVALID_ARG;
+  sdpa_status st = check_paged4_args(k_pages, v_pages, b, n_tokens, h, h_kv, d, page_size, n_pages,
+                                     pages_per_seq, page_table, q_starts, kv_lengths, k_exp, v_exp);
+  if (st != SDPA_OK) return st;
+  const long long kv_row = 1ll * h_kv * d, q_row = 1ll * h * d;
+  if (d_rot < 0 || d_rot > d || k_stride < kv_row || v_stride < kv_row ||
+      (q != nullptr && q_stride < q_row) || (d_rot > 0 && rope_freqs == nullptr) ||
+      (reinterpret_cast<uintptr_t>(rope_freqs) & 3u) != 0 || (q != nullptr && q == q_out && q_stride != q_row))
+    return SDPA_ERR_INVALID_ARG;
+  const long long most = 1ll << 38;
+  if (d_rot % 16 != 0 || k_stride % 8 != 0 || v_stride % 8 != 0 || k_stride > most || v_stride > most ||
+      (q != nullptr && (q_stride % 8 != 0 || q_stride > most)))
+    return SDPA_ERR_UNSUPPORTED;
+  if (q != nullptr && ((q != q_out && rows_overlap(q, q_row, q_stride, q_out, q_row, n_tokens)) ||
+                       rows_overlap(k, kv_row, k_stride, q_out, q_row, n_tokens) ||
+                       rows_overlap(v, kv_row, v_stride, q_out, q_row, n_tokens)))
+    return SDPA_ERR_INVALID_ARG;
+  const unsigned long long cache = paged4_cache_bytes(n_pages, h_kv, page_size, d);
+  if (bytes_overlap(k_pages, cache, v_pages, cache)) return SDPA_ERR_INVALID_ARG;
+  if (n_tokens > 0) {
+    const unsigned long long k_span = 2ull * ((n_tokens - 1) * k_stride + kv_row);
+    const unsigned long long v_span = 2ull * ((n_tokens - 1) * v_stride + kv_row);
+    const unsigned long long q_span = q != nullptr ? 2ull * ((n_tokens - 1) * q_stride + q_row) : 0;
+    const unsigned long long out_span = q != nullptr ? 2ull * n_tokens * q_row : 0;
+    for (const void* pages : {k_pages, v_pages})
+      if (bytes_overlap(k, k_span, pages, cache) || bytes_overlap(v, v_span, pages, cache) ||
+          bytes_overlap(q, q_span, pages, cache) || bytes_overlap(q_out, out_span, pages, cache))
+        return SDPA_ERR_INVALID_ARG;
+  }
+  unsigned* status = nullptr;
+  st = current_device(&status);
+  if (st != SDPA_OK) return st;
+  if (n_tokens == 0) return SDPA_OK;
+  sdpa::Paged4AppendParams p;
+  p.q = static_cast<const uint16_t*>(q);
+  p.k = static_cast<const uint16_t*>(k);
+  p.v = static_cast<const uint16_t*>(v);
+  p.q_out = static_cast<uint16_t*>(q_out);
+  p.k_pages = static_cast<uint8_t*>(k_pages);
+  p.v_pages = static_cast<uint8_t*>(v_pages);
+  p.freqs = rope_freqs;
+  p.page_table = page_table;
+  p.q_starts = q_starts;
+  p.kv_lengths = kv_lengths;
+  p.status = status;
+  p.q_stride = q_stride;
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  p.b = b;
+  p.n_tokens = n_tokens;
+  p.h = h;
+  p.h_kv = h_kv;
+  p.d = d;
+  p.d_rot = d_rot;
+  p.interleaved = interleaved != 0;
+  p.log_blocks = log2_of(d / 16);
+  // x / items as the high word of x * magic: exact while x (magic items - 2^32)
+  // < 2^32, and x is below a block's tokens (at most 8) times items
+  const unsigned long long items = static_cast<unsigned long long>(h + 2 * h_kv) * (d / 16);
+  p.items_magic = items > 1 && 8 * items * items < (1ull << 32)
+                      ? static_cast<unsigned>(((1ull << 32) + items - 1) / items)
+                      : 0;
+  p.page_shift = log2_of(page_size);
+  p.n_pages = n_pages;
+  p.pages_per_seq = pages_per_seq;
+  p.k_unit = std::ldexp(1.f, -k_exp);
+  p.v_unit = std::ldexp(1.f, -v_exp);
+  return sdpa::launch_sdpa_paged4_append(p, static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? SDPA_OK
+             : SDPA_ERR_CUDA;
+}
+
+sdpa_status sdpa_paged4_read(const void* k_pages, const void* v_pages, void* k_out, void* v_out,
+                             int b, int n_tokens, int h_kv, int d, int page_size, int n_pages,
+                             int pages_per_seq, const int32_t* page_table, const int32_t* q_starts,
+                             const int32_t* kv_lengths, int k_exp, int v_exp, void* stream) {
+  if (n_tokens != 0 && (k_out == nullptr || v_out == nullptr)) return SDPA_ERR_INVALID_ARG;
+  if (!aligned16(k_out) || !aligned16(v_out)) return SDPA_ERR_INVALID_ARG;
+  sdpa_status st = check_paged4_args(k_pages, v_pages, b, n_tokens, h_kv, h_kv, d, page_size, n_pages,
+                                     pages_per_seq, page_table, q_starts, kv_lengths, k_exp, v_exp);
+  if (st != SDPA_OK) return st;
+  const unsigned long long cache = paged4_cache_bytes(n_pages, h_kv, page_size, d);
+  const unsigned long long rows = 2ull * n_tokens * h_kv * d;
+  if (bytes_overlap(k_out, rows, v_out, rows)) return SDPA_ERR_INVALID_ARG;
+  for (const void* pages : {k_pages, v_pages})
+    if (bytes_overlap(k_out, rows, pages, cache) || bytes_overlap(v_out, rows, pages, cache))
+      return SDPA_ERR_INVALID_ARG;
+  unsigned* status = nullptr;
+  st = current_device(&status);
+  if (st != SDPA_OK) return st;
+  if (n_tokens == 0) return SDPA_OK;
+  sdpa::Paged4ReadParams p;
+  p.k_pages = static_cast<const uint8_t*>(k_pages);
+  p.v_pages = static_cast<const uint8_t*>(v_pages);
+  p.k = static_cast<uint16_t*>(k_out);
+  p.v = static_cast<uint16_t*>(v_out);
+  p.page_table = page_table;
+  p.q_starts = q_starts;
+  p.kv_lengths = kv_lengths;
+  p.status = status;
+  p.b = b;
+  p.n_tokens = n_tokens;
+  p.h_kv = h_kv;
+  p.d = d;
+  p.log_items = log2_of(d / 8);
+  // (as for the append; a block has up to 16 tokens)
+  const unsigned long long items = 2ull * h_kv * (d / 8);
+  p.items_magic = 16 * items * items < (1ull << 32) ? static_cast<unsigned>(((1ull << 32) + items - 1) / items) : 0;
+  p.page_shift = log2_of(page_size);
+  p.n_pages = n_pages;
+  p.pages_per_seq = pages_per_seq;
+  p.k_unit = std::ldexp(1.f, k_exp);
+  p.v_unit = std::ldexp(1.f, v_exp);
+  return sdpa::launch_sdpa_paged4_read(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SDPA_OK
+                                                                                            : SDPA_ERR_CUDA;
+}
+
+size_t sdpa_paged4_workspace_size(int b, int n_tokens, int h, int h_kv, int d, int page_size,
+                                  int pages_per_seq) {
+  if (b < 1 || n_tokens < 1 || h < 1 || h_kv < 1 || h % h_kv != 0 || h / h_kv > 128 || page_size < 1 ||
+      pages_per_seq < 1 || !sdpa::paged_supports(d))
+    return 0;
+  const int group = h / h_kv;
+  const size_t runs = paged4_runs(b, n_tokens, h_kv, group, d, 1ll * pages_per_seq * page_size);
+  if (runs == 1) return 0;
+  return 2 * runs * paged4_slot_bytes(group, n_tokens, b, d) + round256(3 * runs * 8);
+}
+
+sdpa_status sdpa_paged4_forward(const void* q, const void* k_pages, const void* v_pages, void* out,
+                                void* workspace, size_t ws_bytes, int b, int n_tokens, int h,
+                                int h_kv, int d, int page_size, int n_pages, int pages_per_seq,
+                                const int32_t* page_table, const int32_t* q_starts,
+                                const int32_t* kv_lengths, long long q_stride, float scale,
+                                int k_exp, int v_exp, int window, int sinks, void* stream) {
+  if (n_tokens != 0 && (q == nullptr || out == nullptr)) return SDPA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(out)) return SDPA_ERR_INVALID_ARG;
+  sdpa_status st = check_paged4_args(k_pages, v_pages, b, n_tokens, h, h_kv, d, page_size, n_pages,
+                                     pages_per_seq, page_table, q_starts, kv_lengths, k_exp, v_exp);
+  if (st != SDPA_OK) return st;
+  if (!std::isfinite(scale) || scale < 0.f || q_stride < 1ll * h * d || window < 0 || sinks < 0)
+    return SDPA_ERR_INVALID_ARG;
+  if (q_stride % 8 != 0 || q_stride >= (1ll << 38)) return SDPA_ERR_UNSUPPORTED;
+  if (rows_overlap(q, 1ll * h * d, q_stride, out, 1ll * h * d, n_tokens)) return SDPA_ERR_INVALID_ARG;
+  const unsigned long long cache = paged4_cache_bytes(n_pages, h_kv, page_size, d);
+  for (const void* pages : {k_pages, v_pages})
+    if (bytes_overlap(out, 2ull * n_tokens * h * d, pages, cache)) return SDPA_ERR_INVALID_ARG;
+  const size_t need = sdpa_paged4_workspace_size(b, n_tokens, h, h_kv, d, page_size, pages_per_seq);
+  if (need > 0 && (workspace == nullptr || !aligned16(workspace) || ws_bytes < need))
+    return SDPA_ERR_WORKSPACE;
+  unsigned* status = nullptr;
+  st = current_device(&status);
+  if (st != SDPA_OK) return st;
+  if (n_tokens == 0) return SDPA_OK;
+  sdpa::Paged4Params p;
+  p.q = static_cast<const uint16_t*>(q);
+  p.out = static_cast<uint16_t*>(out);
+  p.k_pages = static_cast<const uint8_t*>(k_pages);
+  p.v_pages = static_cast<const uint8_t*>(v_pages);
+  p.page_table = page_table;
+  p.q_starts = q_starts;
+  p.kv_lengths = kv_lengths;
+  p.status = status;
+  p.q_stride = q_stride;
+  p.b = b;
+  p.n_tokens = n_tokens;
+  p.h = h;
+  p.h_kv = h_kv;
+  p.group = h / h_kv;
+  p.page_shift = log2_of(page_size);
+  p.n_pages = n_pages;
+  p.pages_per_seq = pages_per_seq;
+  p.runs = paged4_runs(b, n_tokens, h_kv, p.group, d, 1ll * pages_per_seq * page_size);
+  p.slot_bytes = paged4_slot_bytes(p.group, n_tokens, b, d);
+  p.slots = need > 0 ? static_cast<uint8_t*>(workspace) : nullptr;
+  p.counts = need > 0 ? reinterpret_cast<unsigned long long*>(p.slots + 2ll * p.runs * p.slot_bytes) : nullptr;
+  p.call = paged_call_number() & ~0xffffull;
+  // (positions stay below 2^30)
+  p.window = window == 0 || window >= (1 << 30) ? INT_MAX : window;
+  p.sinks = std::min(sinks, 1 << 30);
+  p.scale_log2 = effective_scale(scale, d) * 1.4426950408889634f;
+  p.k_unit = std::ldexp(1.f, k_exp);
+  p.v_unit = std::ldexp(1.f, v_exp);
+  return sdpa::launch_sdpa_paged4(p, d, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SDPA_OK
+                                                                                           : SDPA_ERR_CUDA;
 }
 
 size_t mha_workspace_size(int b, int n_q, int n_k, int h, int d_k, int d_v) {

@@ -156,6 +156,63 @@ struct PagedAppendParams {
 };
 cudaError_t launch_sdpa_paged_append(const PagedAppendParams& p, cudaStream_t stream);
 
+// The paged cache in 4 bits (paged4.cu, paged4_attn.cu).  A page of one
+// key-value head is page_bytes long: the rows' codes (d / 2 bytes each), then
+// their scales (d / 16 bytes each).
+struct Paged4AppendParams {
+  const uint16_t *q, *k, *v;  // rows of n_tokens tokens, strides in elements (q may be null)
+  uint16_t* q_out;
+  uint8_t *k_pages, *v_pages;
+  const float* freqs;         // [d_rot / 2] radians per position
+  const int32_t *page_table, *q_starts, *kv_lengths;
+  unsigned* status;
+  long long q_stride, k_stride, v_stride;
+  int b, n_tokens, h, h_kv, d, d_rot, interleaved;
+  int log_blocks;             // of d / 16
+  unsigned items_magic;       // ceil(2^32 / ((h + 2 h_kv) d / 16)), 0 if that is too large to divide by
+  int page_shift, n_pages, pages_per_seq;
+  float k_unit, v_unit;       // 2^-exp
+};
+cudaError_t launch_sdpa_paged4_append(const Paged4AppendParams& p, cudaStream_t stream);
+
+// Rows of the cache back as bf16.
+struct Paged4ReadParams {
+  const uint8_t *k_pages, *v_pages;
+  uint16_t *k, *v;            // [n_tokens, h_kv, d]
+  const int32_t *page_table, *q_starts, *kv_lengths;
+  unsigned* status;
+  int b, n_tokens, h_kv, d;
+  int log_items;              // of d / 8
+  unsigned items_magic;       // ceil(2^32 / (2 h_kv d / 8)), 0 if that is too large to divide by
+  int page_shift, n_pages, pages_per_seq;
+  float k_unit, v_unit;       // 2^exp
+};
+cudaError_t launch_sdpa_paged4_read(const Paged4ReadParams& p, cudaStream_t stream);
+
+// Attention of packed new tokens over the cache in 4 bits.
+struct Paged4Params {
+  const uint16_t* q;          // [n_tokens, h, d], rows q_stride elements apart
+  uint16_t* out;              // [n_tokens, h, d]
+  const uint8_t *k_pages, *v_pages;
+  const int32_t *page_table, *q_starts, *kv_lengths;
+  unsigned* status;
+  uint8_t* slots;             // what a run publishes: two slots a run
+  unsigned long long* counts; // pieces published: [2 runs] of a group (by slot), [runs] groups of a unit
+  unsigned long long call;    // this call's number, the low 16 bits clear
+  long long q_stride;
+  int b, n_tokens, h, h_kv, group;
+  int page_shift, n_pages, pages_per_seq;
+  int runs, slot_bytes;
+  int window, sinks;          // window: keys p - window + 1 .. p (INT_MAX: all)
+  float scale_log2, k_unit, v_unit;   // scale log2(e); 2^exp
+};
+constexpr int kPaged4MinPage = 16;
+constexpr int kPaged4MaxRuns = 2 * 160;
+int paged4_rows(int group, int n_tokens, int b);       // rows of a row tile
+int paged4_resident_ctas(int d, int rows);             // CTAs that share an SM
+long long paged4_most_runs(long long units, long long max_len);   // that this much work is cut into
+cudaError_t launch_sdpa_paged4(const Paged4Params& p, int d, cudaStream_t stream);
+
 // Gradients of attention (bf16 BHSD tensors, fp32 accumulation).
 struct SdpaBwdParams {
   CUtensorMap tm_q, tm_k, tm_v, tm_do;   // 4-D (d, n, h, b) bf16 maps; d = d_k for Q, K

@@ -1,0 +1,92 @@
+// What the kernels that write and read paged caches share: the rotation's
+// angles and the place of a packed row.
+#pragma once
+
+#include <climits>
+#include <cstdint>
+
+#include "kernels.h"
+
+namespace sdpa {
+
+// cos and sin of pos * freq.  The angle in turns is formed from products whose
+// rounding errors are kept (fma): the position in two parts of at most 19 bits,
+// freq / 2 pi as a sum of three floats, good to 2^-70 of itself.  Whole turns are
+// dropped after each sum of two parts of at most half a turn, which rounds off by
+// 2^-25 at most; there are six such sums and a last one, so that the fraction is good
+// to 7 2^-25 = 2.1e-7 of a turn, 1.3e-6 rad, while the angle is below 2^48.  (Against
+// exact arithmetic, 300000 angles of positions up to 2^30 and frequencies up to 1e5
+// were off by 4.6e-7 rad at most.)
+__device__ __forceinline__ float2 cos_sin(int pos, float freq) {
+  // 1 / (2 pi) = 0.15915494309189533576888376..., rounded to fp32, then what that left, twice
+  constexpr float kInvTwoPi0 = 0x1.45f306p-3f, kInvTwoPi1 = 0x1.b9391p-28f, kInvTwoPi2 = 0x1.529fc2p-54f;
+  const float th = freq * kInvTwoPi0, e0 = fmaf(freq, kInvTwoPi0, -th);
+  const float p1 = freq * kInvTwoPi1, e1 = fmaf(freq, kInvTwoPi1, -p1);
+  const float tm = e0 + p1, back = tm - e0;
+  const float tl = (e0 - (tm - back)) + (p1 - back) + fmaf(freq, kInvTwoPi2, e1);
+  float t = 0.f, rest = 0.f;
+  auto add = [&](float part) {
+    const float x = t + (part - rintf(part));
+    t = x - rintf(x);
+  };
+  auto add_product = [&](float x) {
+    const float a = x * th, b = x * tm;
+    add(a);
+    add(fmaf(x, th, -a));
+    add(b);
+    rest += fmaf(x, tl, fmaf(x, tm, -b));
+  };
+  add_product(static_cast<float>(pos >> 12) * 4096.f);
+  add_product(static_cast<float>(pos & 4095));
+  add(rest);
+  float2 r;
+  sincospif(2.f * t, &r.y, &r.x);
+  return r;
+}
+
+__device__ __forceinline__ float2 unpack_bf16x2(uint32_t u) {
+  return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+}
+
+// Sequence of packed row t: the last s with q_starts[s] <= t, found by a warp
+// with 32 probes a round.  Returns -1 for a row outside every sequence.
+template <class Params>
+__device__ __forceinline__ int find_seq(const Params& p, int t, int lane) {
+  int lo = 0, hi = p.b + 1;                                   // q_starts[0 .. b]
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) / 32;
+    const int probe = lo + lane * step;
+    const bool le = probe < hi && p.q_starts[probe] <= t;
+    const uint32_t votes = __ballot_sync(0xffffffffu, le);
+    if (votes == 0) return -1;                                // before the first sequence
+    lo += (31 - __clz(votes)) * step;
+    hi = min(hi, lo + step);
+  }
+  return lo < p.b ? lo : -1;
+}
+
+// Where packed row t lies: its position (INT_MIN: no sequence's row) and the
+// page row of its first head, page * h_kv * P + position % P (-1: none; a page
+// number outside the cache is reported).  One warp, every lane.
+struct RowPlace {
+  int pos;
+  long long row;
+};
+template <class Params>
+__device__ __forceinline__ RowPlace place_of_row(const Params& p, int t, int lane) {
+  RowPlace r{INT_MIN, -1};
+  const int s = find_seq(p, t, lane);
+  const int end = s >= 0 ? min(p.q_starts[s + 1], p.n_tokens) : 0;
+  if (t >= end) return r;
+  const int len = min(max(p.kv_lengths[s], 0), p.pages_per_seq << p.page_shift);
+  r.pos = len - end + t;
+  if (r.pos < 0) return r;
+  const int page = p.page_table[static_cast<long long>(s) * p.pages_per_seq + (r.pos >> p.page_shift)];
+  if (page >= 0 && page < p.n_pages)
+    r.row = (static_cast<long long>(page) * p.h_kv << p.page_shift) + (r.pos & ((1 << p.page_shift) - 1));
+  else if (lane == 0)
+    atomicOr(p.status, kStatusBadPage);
+  return r;
+}
+
+}  // namespace sdpa
