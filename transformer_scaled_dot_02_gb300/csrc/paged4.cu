@@ -58,41 +58,40 @@ __device__ __forceinline__ float e4m3_value(uint32_t byte) {
 //
 // The rotation is in fp32 with angles good to 1.3e-6.  Where that leaves open
 // which scale or code is the nearest, some element of a block lies within kSlack
-// of a border between two (about one block in 6000): the block is worked out
+// of a border between two (about one block in 3000): the block is worked out
 // again in 64 bits, so that the cache holds what the definition says.
 // Of |a| + |b|: the angle, cos and sin's own rounding, and three roundings of products and sum.
 constexpr float kSlack = 1.8e-6f;
 
-// Block `col` of key row `row` at position pos, in 64 bits.
+// Columns col .. col + 15 of key row `row` at position pos, in 64 bits, by all
+// lanes of a warp: a lane for each column, as a sine in 64 bits takes 2 us (one
+// lane for the 16 took 30 us, ten times a short call).
 __device__ __noinline__ void block_in_64_bits(const Paged4AppendParams& p, const uint16_t* row, int col, int pos,
-                                              uint2* codes, uint32_t* scale) {
+                                              int lane, uint2* codes, uint32_t* scale) {
   const int half = p.d_rot / 2;
-  const double unit = p.k_unit;
   auto value = [&](int x) { return static_cast<double>(__uint_as_float(static_cast<uint32_t>(row[x]) << 16)); };
-  double y[16], top = 0.0;
-  for (int i = 0; i < 16; ++i) {
-    const int x = col + i;
-    const int pair = p.interleaved ? x / 2 : (x < half ? x : x - half);
-    const bool second = p.interleaved ? (x & 1) : x >= half;
-    const double own = value(x), other = value(p.interleaved ? x ^ 1 : (second ? x - half : x + half));
-    double s, c;
-    sincos(static_cast<double>(pos) * static_cast<double>(p.freqs[pair]), &s, &c);
-    y[i] = (second ? own * c + other * s : own * c - other * s) * unit;
-    top = fmax(top, fabs(y[i]));
-  }
+  const int i = lane & 15, x = col + i;
+  const int pair = p.interleaved ? x / 2 : (x < half ? x : x - half);
+  const bool second = p.interleaved ? (x & 1) : x >= half;
+  const double own = value(x), other = value(p.interleaved ? x ^ 1 : (second ? x - half : x + half));
+  double sn, cs;
+  sincos(static_cast<double>(pos) * static_cast<double>(p.freqs[pair]), &sn, &cs);
+  const double y = (second ? own * cs + other * sn : own * cs - other * sn) * static_cast<double>(p.k_unit);
+  double top = fabs(y);
+#pragma unroll
+  for (int z = 8; z > 0; z >>= 1) top = fmax(top, __shfl_xor_sync(0xffffffffu, top, z));
   // rounded to a float that is odd where it is not exact, a second rounding is as if it were the first
-  auto odd = [](double x) {
-    const float f = __double2float_rz(x);
-    return static_cast<double>(f) != x && isfinite(f) ? __uint_as_float(__float_as_uint(f) | 1u) : f;
+  auto odd = [](double v) {
+    const float f = __double2float_rz(v);
+    return static_cast<double>(f) != v && isfinite(f) ? __uint_as_float(__float_as_uint(f) | 1u) : f;
   };
   const uint32_t s8 = e4m3x2(odd(fmin(top / 6.0, 448.0)), 0.f) & 0xff;
-  const double s = e4m3_value(s8);
-  uint32_t w[2] = {0, 0};
-  for (int i = 0; i < 16 && s > 0.0; ++i) {
-    const uint32_t c = e2m1x2(odd(fmin(fabs(y[i]) / s, 8.0)), 0.f) & 7u;
-    w[i >> 3] |= (c | (y[i] < 0.0 ? 8u : 0u)) << (4 * (i & 7));
-  }
-  *codes = make_uint2(w[0], w[1]);
+  const float s = e4m3_value(s8);
+  uint32_t c = s > 0.f ? e2m1x2(odd(fmin(fabs(y) / static_cast<double>(s), 8.0)), 0.f) & 7u : 0u;
+  c = (c | (y < 0.0 ? 8u : 0u)) << (4 * (i & 7));
+#pragma unroll
+  for (int z = 1; z < 8; z <<= 1) c |= __shfl_xor_sync(0xffffffffu, c, z);
+  *codes = make_uint2(__shfl_sync(0xffffffffu, c, 0), __shfl_sync(0xffffffffu, c, 8));
   *scale = s8;
 }
 
@@ -204,14 +203,24 @@ __global__ void __launch_bounds__(kThreads, kBlocks) sdpa_paged4_append_kernel(c
     if (t0 + i < p.n_tokens && pos_of[i] != INT_MIN) angles[x] = cos_sin(pos_of[i], p.freqs[x - i * half]);
   }
   __syncthreads();
-  for (int x = threadIdx.x; x < all; x += kThreads) {
-    if (x != static_cast<int>(threadIdx.x)) load(x);
-    const Item it = item_of(x);
-    if (pos_of[it.token] == INT_MIN) continue;
+  // stores a key's or value's block
+  auto store = [&](const Item& it, uint2 codes, uint32_t scale) {
+    // row_of: page h_kv P + r for page row r of head 0
+    const long long row = row_of[it.token];
+    const int r = static_cast<int>(row & page_rows_mask), hk = it.head - p.h;
+    const bool is_k = hk < p.h_kv;
+    uint8_t* page = (is_k ? p.k_pages : p.v_pages) +
+                    ((row >> p.page_shift) + (is_k ? hk : hk - p.h_kv)) * (static_cast<long long>(9 * p.d / 16) << p.page_shift);
+    *reinterpret_cast<uint2*>(page + r * (p.d / 2) + it.c * 8) = codes;
+    page[(p.d / 2 << p.page_shift) + (r << p.log_blocks) + it.c] = static_cast<uint8_t>(scale);
+  };
+  // Does an item; true: its block has to be worked out in 64 bits.
+  auto work = [&](const Item& it) -> bool {
+    if (pos_of[it.token] == INT_MIN) return false;
     const float4* turn = reinterpret_cast<const float4*>(angles + it.token * half);   // (cos, sin) of two pairs
     const uint32_t ua[4] = {a.x, a.y, a.z, a.w}, ub[4] = {b.x, b.y, b.z, b.w};
     if (it.head < p.h) {
-      if (p.q == nullptr) continue;
+      if (p.q == nullptr) return false;
       uint16_t* dst = p.q_out + (static_cast<long long>(t0 + it.token) * p.h + it.head) * p.d;
       uint32_t ra[4], rb[4];
 #pragma unroll
@@ -234,13 +243,10 @@ __global__ void __launch_bounds__(kThreads, kBlocks) sdpa_paged4_append_kernel(c
       }
       *reinterpret_cast<uint4*>(dst + it.c0) = make_uint4(ra[0], ra[1], ra[2], ra[3]);
       *reinterpret_cast<uint4*>(dst + it.c1) = make_uint4(rb[0], rb[1], rb[2], rb[3]);
-      continue;
+      return false;
     }
-    const long long row = row_of[it.token];
-    if (row < 0) continue;
-    const int hk = it.head - p.h;
-    const bool is_k = hk < p.h_kv;
-    const float unit = is_k ? p.k_unit : p.v_unit;
+    if (row_of[it.token] < 0) return false;
+    const float unit = it.head < p.h + p.h_kv ? p.k_unit : p.v_unit;
     float y[16];
     uint2 codes;
     uint32_t scale;
@@ -278,8 +284,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) sdpa_paged4_append_kernel(c
           }
         }
       }
-      if (!quantise<true>(y, off * kSlack * unit, &codes, &scale))
-        block_in_64_bits(p, source(it), it.c * 16, pos_of[it.token], &codes, &scale);
+      if (!quantise<true>(y, off * kSlack * unit, &codes, &scale)) return true;
     } else {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
@@ -291,12 +296,21 @@ __global__ void __launch_bounds__(kThreads, kBlocks) sdpa_paged4_append_kernel(c
       }
       quantise<false>(y, 0.f, &codes, &scale);
     }
-    // row = page h_kv P + r: page row r of head hk
-    const int r = static_cast<int>(row & page_rows_mask);
-    uint8_t* page = (is_k ? p.k_pages : p.v_pages) +
-                    ((row >> p.page_shift) + (is_k ? hk : hk - p.h_kv)) * (static_cast<long long>(9 * p.d / 16) << p.page_shift);
-    *reinterpret_cast<uint2*>(page + r * (p.d / 2) + it.c * 8) = codes;
-    page[(p.d / 2 << p.page_shift) + (r << p.log_blocks) + it.c] = static_cast<uint8_t>(scale);
+    store(it, codes, scale);
+    return false;
+  };
+  for (int x0 = warp * 32; x0 < all; x0 += kThreads) {
+    const int x = x0 + lane;
+    if (x0 != warp * 32) load(x);
+    const Item it = item_of(min(x, all - 1));
+    const bool open = x < all && work(it);
+    for (uint32_t left = __ballot_sync(0xffffffffu, open); left != 0; left &= left - 1) {
+      const Item its = item_of(x0 + __ffs(left) - 1);
+      uint2 codes;
+      uint32_t scale;
+      block_in_64_bits(p, source(its), its.c * 16, pos_of[its.token], lane, &codes, &scale);
+      if (lane == 0) store(its, codes, scale);
+    }
   }
 }
 
