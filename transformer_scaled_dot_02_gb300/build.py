@@ -31,7 +31,7 @@ BIND = os.path.join(HERE, "_bind" + (sysconfig.get_config_var("EXT_SUFFIX") or "
 BIND_SOURCE = os.path.join(CSRC, "bind.cpp")
 SOURCES = ["api.cu", "sdpa_tc.cu", "sdpa_one_tile.cu", "sdpa_bwd.cu", "sdpa_f32.cu", "gemm_tc.cu",
            "decode.cu", "mha_noalloc.cu", "sdpa_bwd_wide.cu", "paged.cu",
-           "paged4.cu", "paged4_attn.cu"]
+           "paged4.cu", "paged4_attn.cu", "paged4_wide.cu"]
 HEADERS = ["kernels.h", "paged.cuh", "ptx.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

@@ -507,19 +507,39 @@ unsigned long long paged4_cache_bytes(int n_pages, int h_kv, int page_size, int 
   return static_cast<unsigned long long>(n_pages) * h_kv * page_size * (9 * d / 16);
 }
 
-// Runs that the attention's work is cut into: every CTA that the GPU holds at a
-// time, or as many as there could ever be work for.
-int paged4_runs(int b, int n_tokens, int h_kv, int group, int d, long long max_len) {
-  const int rows = sdpa::paged4_rows(group, n_tokens, b);
-  const long long units = (1ll * n_tokens * group / rows + std::min(b, n_tokens)) * h_kv;
-  const long long most = std::min<long long>(sdpa::kPaged4MaxRuns,
-                                             1ll * sdpa::paged4_resident_ctas(d, rows) * sdpa::device_sm_count());
-  return static_cast<int>(std::max(1ll, std::min(most, sdpa::paged4_most_runs(units, max_len))));
-}
+// How a call's attention is divided: the few-rows kernel alone, or with it the
+// kernel for sequences of many rows.  `runs`: that the work is cut into, every CTA
+// that the GPU holds at a time or as many as there could ever be work for.
+struct Paged4Division {
+  bool wide;
+  int few_runs, wide_runs;
+  size_t few_slot, wide_slot;              // bytes: fp32 O, and two statistics a row
 
-// Bytes of a workspace slot: fp32 O, and two statistics a row twice.
-int paged4_slot_bytes(int group, int n_tokens, int b, int d) {
-  return static_cast<int>(round256(static_cast<size_t>(sdpa::paged4_rows(group, n_tokens, b)) * (d * 4 + 16)));
+  size_t few_bytes() const { return few_runs > 1 ? 2 * few_runs * few_slot + round256(3ull * few_runs * 8) : 0; }
+  size_t wide_bytes() const { return wide_runs > 1 ? 2 * wide_runs * wide_slot + round256(2ull * wide_runs * 8) : 0; }
+};
+Paged4Division paged4_divide(int b, int n_tokens, int h_kv, int group, int d, long long max_len) {
+  Paged4Division v;
+  const long long all_rows = 1ll * n_tokens * group;
+  const int rows = sdpa::paged4_rows(group, n_tokens, b);
+  auto runs = [](long long most, long long work) { return static_cast<int>(std::max(1ll, std::min(most, work))); };
+  const long long units = (all_rows / rows + std::min(b, n_tokens)) * h_kv;
+  v.few_runs = runs(std::min(sdpa::kPaged4MaxRuns, sdpa::paged4_resident_ctas(d, rows) * sdpa::device_sm_count()),
+                    sdpa::paged4_most_runs(units, max_len));
+  v.few_slot = round256(static_cast<size_t>(rows) * (d * 4 + 8));
+  // as many tokens as sequences: single tokens, in all likelihood, and the few-rows
+  // kernel takes whatever there is
+  v.wide = n_tokens > b && all_rows > sdpa::kPaged4FewRows;
+  v.wide_runs = 0;
+  v.wide_slot = 0;
+  if (v.wide) {
+    const int wide_rows = sdpa::paged4_wide_rows(d);
+    const long long wide_units = (all_rows / wide_rows + std::min(b, n_tokens)) * h_kv;
+    v.wide_runs = runs(std::min(sdpa::kPaged4WideMaxRuns, sdpa::device_sm_count()),
+                       sdpa::paged4_wide_most_runs(wide_units, max_len));
+    v.wide_slot = round256(static_cast<size_t>(wide_rows) * (d * 4 + 8));
+  }
+  return v;
 }
 
 }  // namespace
@@ -1116,10 +1136,8 @@ size_t sdpa_paged4_workspace_size(int b, int n_tokens, int h, int h_kv, int d, i
   if (b < 1 || n_tokens < 1 || h < 1 || h_kv < 1 || h % h_kv != 0 || h / h_kv > 128 || page_size < 1 ||
       pages_per_seq < 1 || !sdpa::paged_supports(d))
     return 0;
-  const int group = h / h_kv;
-  const size_t runs = paged4_runs(b, n_tokens, h_kv, group, d, 1ll * pages_per_seq * page_size);
-  if (runs == 1) return 0;
-  return 2 * runs * paged4_slot_bytes(group, n_tokens, b, d) + round256(3 * runs * 8);
+  const Paged4Division v = paged4_divide(b, n_tokens, h_kv, h / h_kv, d, 1ll * pages_per_seq * page_size);
+  return v.few_bytes() + v.wide_bytes();
 }
 
 sdpa_status sdpa_paged4_forward(const void* q, const void* k_pages, const void* v_pages, void* out,
@@ -1165,19 +1183,29 @@ sdpa_status sdpa_paged4_forward(const void* q, const void* k_pages, const void* 
   p.page_shift = log2_of(page_size);
   p.n_pages = n_pages;
   p.pages_per_seq = pages_per_seq;
-  p.runs = paged4_runs(b, n_tokens, h_kv, p.group, d, 1ll * pages_per_seq * page_size);
-  p.slot_bytes = paged4_slot_bytes(p.group, n_tokens, b, d);
-  p.slots = need > 0 ? static_cast<uint8_t*>(workspace) : nullptr;
-  p.counts = need > 0 ? reinterpret_cast<unsigned long long*>(p.slots + 2ll * p.runs * p.slot_bytes) : nullptr;
+  const Paged4Division v = paged4_divide(b, n_tokens, h_kv, p.group, d, 1ll * pages_per_seq * page_size);
+  auto set_work = [&](int runs, size_t slot, uint8_t* at) {
+    p.runs = runs;
+    p.slot_bytes = static_cast<int>(slot);
+    p.slots = at;
+    p.counts = reinterpret_cast<unsigned long long*>(at + 2 * runs * slot);
+  };
+  set_work(v.few_runs, v.few_slot, static_cast<uint8_t*>(workspace));
+  p.few_rows = v.wide ? sdpa::kPaged4FewRows : INT_MAX;
   p.call = paged_call_number() & ~0xffffull;
+  p.page_bytes = 9ll * d / 16 * page_size;
+  p.page_stride = h_kv * p.page_bytes;
   // (positions stay below 2^30)
   p.window = window == 0 || window >= (1 << 30) ? INT_MAX : window;
   p.sinks = std::min(sinks, 1 << 30);
   p.scale_log2 = effective_scale(scale, d) * 1.4426950408889634f;
   p.k_unit = std::ldexp(1.f, k_exp);
   p.v_unit = std::ldexp(1.f, v_exp);
-  return sdpa::launch_sdpa_paged4(p, d, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SDPA_OK
-                                                                                           : SDPA_ERR_CUDA;
+  if (sdpa::launch_sdpa_paged4(p, d, static_cast<cudaStream_t>(stream)) != cudaSuccess) return SDPA_ERR_CUDA;
+  if (!v.wide) return SDPA_OK;
+  set_work(v.wide_runs, v.wide_slot, static_cast<uint8_t*>(workspace) + v.few_bytes());
+  return sdpa::launch_sdpa_paged4_wide(p, d, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SDPA_OK
+                                                                                                : SDPA_ERR_CUDA;
 }
 
 size_t mha_workspace_size(int b, int n_q, int n_k, int h, int d_k, int d_v) {

@@ -203,15 +203,23 @@ struct Paged4Params {
   int b, n_tokens, h, h_kv, group;
   int page_shift, n_pages, pages_per_seq;
   int runs, slot_bytes;
+  long long page_bytes, page_stride;  // of one key-value head, of all of them
+  int few_rows;               // rows of a head (new tokens x group) of a sequence that is the few-rows kernel's, at most
   int window, sinks;          // window: keys p - window + 1 .. p (INT_MAX: all)
   float scale_log2, k_unit, v_unit;   // scale log2(e); 2^exp
 };
 constexpr int kPaged4MinPage = 16;
-constexpr int kPaged4MaxRuns = 2 * 160;
+constexpr int kPaged4MaxRuns = 3 * 160;
 int paged4_rows(int group, int n_tokens, int b);       // rows of a row tile
 int paged4_resident_ctas(int d, int rows);             // CTAs that share an SM
 long long paged4_most_runs(long long units, long long max_len);   // that this much work is cut into
 cudaError_t launch_sdpa_paged4(const Paged4Params& p, int d, cudaStream_t stream);
+// The kernel for the other sequences: p.slots, p.counts, p.runs and p.slot_bytes are its own.
+constexpr int kPaged4FewRows = 16;
+constexpr int kPaged4WideMaxRuns = 160;
+int paged4_wide_rows(int d);                           // rows of a row tile
+long long paged4_wide_most_runs(long long units, long long max_len);
+cudaError_t launch_sdpa_paged4_wide(const Paged4Params& p, int d, cudaStream_t stream);
 
 // Gradients of attention (bf16 BHSD tensors, fp32 accumulation).
 struct SdpaBwdParams {

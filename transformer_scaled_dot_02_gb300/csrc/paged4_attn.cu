@@ -11,9 +11,13 @@
 // so that results repeat bit by bit and no run waits for another:
 //   O = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s, M = max_s m_s.
 //
-// Every warp takes key tiles of its own (every kWarps'th of a piece), with a
-// ring of bulk copies ahead of it, and keeps O, m and l of its own until the
-// piece ends.  A step for single tokens is bound by reading the cache, so what
+// Every warp takes key tiles of its own (every kWarps'th of a piece), copies them
+// some tiles ahead into a ring of its own and keeps O, m and l of its own until
+// the piece ends.  CTAs are small, so that others on the SM work while one's
+// warps meet.  The copies are cp.async, 16 bytes a lane, 9 instructions a tile at
+// d = 128: as bulk copies, four for the codes and scales of K and V, a tile took
+// the SM's copy engine 600 clock cycles (41 us instead of @@ for 32 sequences of
+// 4096 to 8192 positions).  A step for single tokens is bound by reading the cache, so what
 // counts is that few instructions stand between a byte and its products.  They
 // are mma.sync on registers: tcgen05 takes its operands from shared memory (or A
 // from tensor memory), where the expanded numbers, 4 bytes for each byte of the
@@ -33,6 +37,7 @@
 #include <algorithm>
 #include <atomic>
 #include <climits>
+#include <type_traits>
 
 #include "kernels.h"
 #include "ptx.cuh"
@@ -40,16 +45,21 @@
 namespace sdpa {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kKeys = 32;                  // per tile
 constexpr int kKeysShift = 5;
-constexpr int kStages = 2;                 // tiles of a warp's ring
 constexpr float kRescaleThreshold = 8.0f;  // log2 units, as in the other forward kernels
 // What a unit costs beside its key tiles, in key tiles.
 constexpr int kStart = 8;
 constexpr int kMinRun = 16;                // items of a run, at least
-constexpr int kRadix = 16;                 // pieces that one run merges
+// How the work is cut.  kPieces: every unit into pieces of its own, a run for each,
+// where that many runs fit the GPU; a walk of up to kWhole key tiles is one piece,
+// a longer one has pieces of about kPiece.  kItems: into
+// equal runs.
+enum Scheme { kItems, kPieces };
+constexpr int kWhole = 12, kPiece = 8;
+constexpr int kTogether = 16;              // pieces that one run merges, at most (more in two steps)
 
 // ------------------------------------------------------------------ schedule
 struct Seq {
@@ -60,7 +70,6 @@ struct Seq {
 // tiles [0, head), then those from `first` on.
 struct Tiles {
   int head, first, count;
-  __device__ __forceinline__ int at(int i) const { return i < head ? i : first + i - head; }
 };
 
 template <int R>
@@ -74,7 +83,8 @@ struct Plan {
     q.start = min(max(p.q_starts[s], 0), p.n_tokens);
     q.n = min(max(p.q_starts[s + 1], q.start), p.n_tokens) - q.start;
     q.len = min(max(p.kv_lengths[s], 0), cap);
-    q.tiles = static_cast<int>((1ll * q.n * p.group + R - 1) / R);
+    const long long rows = 1ll * q.n * p.group;
+    q.tiles = rows <= p.few_rows ? static_cast<int>((rows + R - 1) / R) : 0;
     return q;
   }
   __device__ __forceinline__ Tiles walk(int lo, int hi) const {
@@ -90,100 +100,203 @@ struct Plan {
     return t;
   }
   // positions of the first and the last row of a row tile
-  __device__ __forceinline__ int first_pos(const Seq& q, int r) const { return q.len - q.n + r * R / p.group; }
-  __device__ __forceinline__ int last_pos(const Seq& q, int r) const {
-    return q.len - q.n + static_cast<int>((min((r + 1ll) * R, 1ll * q.n * p.group) - 1) / p.group);
+  // (rows of a head: up to 2^31, as unsigned numbers; one tile of rows, the usual case, needs no division)
+  __device__ __forceinline__ int first_pos(const Seq& q, int r) const {
+    return q.len - q.n + (r == 0 ? 0 : static_cast<int>(static_cast<unsigned>(r) * R / static_cast<unsigned>(p.group)));
   }
-  // items of a unit: no walk of the sequence is longer
-  __device__ __forceinline__ long long cost(const Seq& q) const {
-    if (q.len <= 0) return kStart;
+  __device__ __forceinline__ int last_pos(const Seq& q, int r) const {
+    if (r + 1 == q.tiles) return q.len - 1;
+    return q.len - q.n + static_cast<int>((static_cast<unsigned>(r + 1) * R - 1u) / static_cast<unsigned>(p.group));
+  }
+  // key tiles that no walk of the sequence is longer than
+  __device__ __forceinline__ int most_tiles(const Seq& q) const {
+    if (q.len <= 0) return 0;
     int tiles = ((q.len - 1) >> kKeysShift) + 1;
     if (p.window < INT_MAX) {
       const long long span = 1ll * p.window + R / p.group + 1;
       tiles = static_cast<int>(min(1ll * tiles, (span >> kKeysShift) + 2 + ((min(p.sinks, q.len) + kKeys - 1) >> kKeysShift)));
     }
-    return kStart + tiles;
+    return tiles;
+  }
+  __device__ __forceinline__ int pieces(int tiles) const { return tiles <= kWhole ? 1 : (tiles + kPiece - 1) / kPiece; }
+  // items of a unit
+  __device__ __forceinline__ int cost(const Seq& q, Scheme scheme) const {
+    return scheme == kPieces ? pieces(most_tiles(q)) : kStart + most_tiles(q);
   }
 };
 
-struct Place {
+// Most counts fit 32 bits, where a division costs a tenth of one in 64.
+__device__ __forceinline__ long long divide(long long a, long long b) {
+  if (((a | b) >> 32) == 0) return static_cast<unsigned>(a) / static_cast<unsigned>(b);
+  return a / b;
+}
+
+// A run's place: a unit and the piece of it that is the run's.
+struct Unit {
+  Seq q;
   int s, hk, r;
   long long begin;                         // the unit's first item
-  Seq q;
-};
-
-struct ScheduleShared {
-  long long warp_sum[kWarps];
-  Place at;
+  Tiles tiles;
+  int kt0, kt1;                            // the piece, of tiles.count key tiles
+  int first_run, of;                       // the unit's pieces are those of runs first_run .. first_run + of - 1
+  int first_pos, hi_pos;                   // positions of the first and the last row
+  int first_row, rows;                     // of the sequence's rows for this head (no rows: no further unit)
 };
 
 // The runs: [begin(c), begin(c + 1)) of all items.
 struct Cut {
   long long each;
   int over, runs;
-  __device__ void set(long long work, int most) {
+  Scheme scheme;
+  __device__ void set(long long work, int most, Scheme how) {
+    scheme = how;
+    if (how == kPieces) {
+      runs = static_cast<int>(work);
+      each = 1;
+      over = 0;
+      return;
+    }
     runs = static_cast<int>(min(static_cast<long long>(most), max(1ll, work / kMinRun)));
-    each = work / runs;
+    each = divide(work, runs);
     over = static_cast<int>(work - each * runs);
   }
   __device__ long long begin(int c) const { return each * c + min(c, over); }
   __device__ int run_of(long long x) const {
     const long long longer = over * (each + 1);
-    return static_cast<int>(x < longer ? x / (each + 1) : over + (x - longer) / each);
+    return static_cast<int>(x < longer ? divide(x, each + 1) : over + divide(x - longer, each));
   }
 };
 
+// The piece of run c of the unit *u.
+template <int R>
+__device__ __forceinline__ void set_piece(const Plan<R>& plan, const Cut& cut, int c, Unit* u) {
+  const Paged4Params& p = plan.p;
+  const long long x0 = cut.begin(c), x1 = cut.begin(c + 1);
+  u->first_pos = plan.first_pos(u->q, u->r);
+  u->hi_pos = plan.last_pos(u->q, u->r);
+  const Tiles tiles = plan.walk(u->first_pos, u->hi_pos);
+  u->tiles = tiles;
+  u->first_row = u->r * R;
+  u->rows = static_cast<int>(min(1ll * R, 1ll * u->q.n * p.group - u->first_row));
+  u->kt0 = u->kt1 = 0;
+  u->first_run = c;
+  u->of = 1;
+  if (cut.scheme == kPieces) {
+    // (as many as the sequence's longest walk is worth: this one may have fewer key tiles)
+    const int j = static_cast<int>(x0 - u->begin);
+    u->of = min(plan.cost(u->q, kPieces), max(tiles.count, 1));
+    u->first_run = c - j;
+    if (j < u->of) {
+      u->kt0 = static_cast<int>(divide(1ll * j * tiles.count, u->of));
+      u->kt1 = static_cast<int>(divide((j + 1ll) * tiles.count, u->of));
+    }
+  } else {
+    const long long items0 = u->begin + kStart;              // the first key tile's item
+    u->kt0 = static_cast<int>(min(1ll * tiles.count, max(0ll, x0 - items0)));
+    u->kt1 = static_cast<int>(min(1ll * tiles.count, max(0ll, x1 - items0)));
+    if (u->kt1 > u->kt0 && u->kt1 - u->kt0 < tiles.count) {
+      u->first_run = cut.run_of(items0);
+      u->of = cut.run_of(items0 + tiles.count - 1) - u->first_run + 1;
+    }
+  }
+}
+
 // The whole block: the cut, and the unit in which run c begins.  Returns false
 // when there is no such run.
+struct Schedule {
+  long long items[kWarps], pieces[kWarps];
+  Cut cut;
+};
+
 template <int R>
-__device__ bool find_place(const Plan<R>& plan, ScheduleShared* sh, int c, Cut* cut, Place* at) {
+__device__ bool find_place(const Plan<R>& plan, Schedule* sh, Unit* first, int c) {
   const Paged4Params& p = plan.p;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int per = (p.b + kThreads - 1) / kThreads;
   const int s0 = min(tid * per, p.b), s1 = min(s0 + per, p.b);
-  long long mine = 0;
+  long long items = 0, pieces = 0;
+  Seq q;
   for (int s = s0; s < s1; ++s) {
-    const Seq q = plan.seq(s);
-    mine += plan.cost(q) * q.tiles * p.h_kv;
+    q = plan.seq(s);
+    const int tiles = plan.most_tiles(q);
+    const long long units = 1ll * q.tiles * p.h_kv;
+    items += (kStart + tiles) * units;
+    pieces += plan.pieces(tiles) * units;
   }
-  long long incl = mine;
+  long long items_to = items, pieces_to = pieces;            // of the threads up to this one
 #pragma unroll
   for (int x = 1; x < 32; x <<= 1) {
-    const long long o = __shfl_up_sync(0xffffffffu, incl, x);
-    if (lane >= x) incl += o;
+    const long long i = __shfl_up_sync(0xffffffffu, items_to, x), n = __shfl_up_sync(0xffffffffu, pieces_to, x);
+    if (lane >= x) {
+      items_to += i;
+      pieces_to += n;
+    }
   }
-  if (lane == 31) sh->warp_sum[warp] = incl;
-  if (tid == 0) sh->at.begin = LLONG_MAX;                    // (no unit, should the lengths change meanwhile)
+  if (lane == 31) {
+    sh->items[warp] = items_to;
+    sh->pieces[warp] = pieces_to;
+  }
+  if (tid == 0) first->begin = LLONG_MAX;                    // (no unit, should the lengths change meanwhile)
   __syncthreads();
-  long long before = incl - mine, sum = 0;
+  long long all_items = 0, all_pieces = 0;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) {
-    const long long v = sh->warp_sum[w];
-    if (w < warp) before += v;
-    sum += v;
+    if (w == warp) {
+      items_to += all_items;
+      pieces_to += all_pieces;
+    }
+    all_items += sh->items[w];
+    all_pieces += sh->pieces[w];
   }
-  if (sum == 0) return false;
-  cut->set(sum, p.runs);
-  if (c >= cut->runs) return false;
-  const long long x = cut->begin(c);
+  if (all_items == 0) return false;
+  const Scheme scheme = all_pieces <= p.runs ? kPieces : kItems;
+  Cut cut;
+  cut.set(scheme == kPieces ? all_pieces : all_items, p.runs, scheme);
+  if (c >= cut.runs) return false;
+  const long long x = cut.begin(c);
+  if (tid == 0) sh->cut = cut;
+  const long long mine = scheme == kPieces ? pieces : items;
+  long long before = (scheme == kPieces ? pieces_to : items_to) - mine;
   if (mine > 0 && before <= x && x < before + mine) {
-    Place pl;
-    for (pl.s = s0; pl.s < s1; ++pl.s) {
-      pl.q = plan.seq(pl.s);
-      const long long unit = plan.cost(pl.q), all = unit * pl.q.tiles * p.h_kv;
+    for (int s = s0; s < s1; ++s) {
+      if (per > 1) q = plan.seq(s);
+      const int unit = plan.cost(q, scheme);
+      const long long all = 1ll * unit * q.tiles * p.h_kv;
       if (x < before + all) {
-        const long long i = (x - before) / unit;
-        pl.hk = static_cast<int>(i / pl.q.tiles);
-        pl.r = static_cast<int>(i - 1ll * pl.hk * pl.q.tiles);
-        pl.begin = before + i * unit;
-        sh->at = pl;
+        const long long i = divide(x - before, unit);
+        Unit u;
+        u.q = q;
+        u.s = s;
+        u.hk = static_cast<int>(divide(i, q.tiles));
+        u.r = static_cast<int>(i - 1ll * u.hk * q.tiles);
+        u.begin = before + i * unit;
+        set_piece(plan, cut, c, &u);
+        *first = u;
         break;
       }
       before += all;
     }
   }
   __syncthreads();
-  *at = sh->at;
+  return true;
+}
+
+// One thread: the unit after *u, false if there is none of run c's.
+template <int R>
+__device__ __noinline__ bool next_unit(const Plan<R>& plan, const Cut& cut, int c, Unit* u) {
+  u->begin += plan.cost(u->q, cut.scheme);
+  if (u->begin >= cut.begin(c + 1)) return false;
+  if (++u->r == u->q.tiles) {
+    u->r = 0;
+    if (++u->hk == plan.p.h_kv) {
+      u->hk = 0;
+      do {
+        if (++u->s >= plan.p.b) return false;
+        u->q = plan.seq(u->s);
+      } while (u->q.tiles == 0);
+    }
+  }
+  set_piece(plan, cut, c, u);
   return true;
 }
 
@@ -254,6 +367,10 @@ __device__ __forceinline__ void load_bytes(const uint8_t* at, uint32_t (&w)[N < 
 
 template <int D, int NT>
 struct NCfg {
+  // CTAs on an SM: with 168 registers a thread nothing is spilled in the loop for up
+  // to 128 columns (of rows of 8), with 255 for twice as many
+  static constexpr int kCtas = D * NT <= 128 ? 3 : 2;
+  static constexpr int kStages = D * NT <= 128 ? 3 : D == 128 ? 3 : 2;   // tiles of a warp's ring
   static constexpr int kRows = 8 * NT;
   static constexpr int kCodes = kKeys * D / 2, kScales = kKeys * D / 16;
   static constexpr int kHalf = kCodes + kScales;             // K or V of a tile
@@ -264,12 +381,14 @@ struct NCfg {
   static constexpr int kPassCols = D / kPasses;
   static constexpr int kExchange = kWarps * kRows * kPassCols * 4;
   static constexpr int kMlOff = kRing + kExchange;
-  static constexpr int kQOff = kMlOff + kWarps * kRows * 8;
-  static constexpr int kBarOff = kQOff;
-  static constexpr int kSmemBytes = kBarOff + kWarps * kStages * 8 + 16;
-  static constexpr int kCtas = D * NT <= 128 ? 2 : 1;
-  static_assert(kTile % 16 == 0 && kHalf % 16 == 0, "bulk copies");
+  static constexpr int kSmemBytes = kMlOff + kWarps * kRows * 8;
+  static_assert(kSmemBytes * kCtas <= 232448 - 1024 * kCtas, "CTAs per SM");
 };
+
+// Copies 16 bytes, or zeros.
+__device__ __forceinline__ void cp_async16_or_zeros(uint32_t dst, const uint8_t* src, bool get) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(get ? 16 : 0) : "memory");
+}
 
 template <int D, int NT>
 __global__ void __launch_bounds__(kThreads, NCfg<D, NT>::kCtas) sdpa_paged4_few(const __grid_constant__ Paged4Params p) {
@@ -277,124 +396,155 @@ __global__ void __launch_bounds__(kThreads, NCfg<D, NT>::kCtas) sdpa_paged4_few(
   constexpr int R = C::kRows;
   constexpr int KS = D / 16;                                 // steps of 16 columns
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ ScheduleShared sched;
-  __shared__ int last_one;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kBarOff);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + kWarps * kStages);
-  const AbortState ab{abort_flag, p.status};
+  __shared__ Schedule sched;
+  __shared__ Unit at;                                        // (what is wanted at the ends of pieces only is no register's)
+  __shared__ int last_one, more;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-  uint64_t* full = bars + warp * kStages;
-  uint8_t* ring = smem + warp * kStages * C::kTile;
-  if (tid < kWarps * kStages) mbar_init(bars + tid, 1);
-  if (tid == 0) {
-    *abort_flag = 0;
-    fence_mbar_init();
-  }
-  __syncthreads();
-  griddep_launch_dependents();
+  uint8_t* ring = smem + warp * C::kStages * C::kTile;
+  // With a second kernel for the other sequences, which begins beside this one, the
+  // kernel before has to be over first.
+  if (p.few_rows == INT_MAX) griddep_launch_dependents();
   griddep_wait();
+  if (p.few_rows != INT_MAX) griddep_launch_dependents();
 
   const Plan<R> plan(p);
-  Cut cut;
-  Place at;
   const int cta = static_cast<int>(blockIdx.x);
-  if (!find_place<R>(plan, &sched, cta, &cut, &at)) return;
-  const long long x0 = cut.begin(cta), x1 = cut.begin(cta + 1);
+  if (!find_place<R>(plan, &sched, &at, cta) || at.begin == LLONG_MAX) return;
 
-  const int box_shift = min(p.page_shift, kKeysShift);       // rows of a page in a tile
-  const long long page_bytes = static_cast<long long>(9 * D / 16) << p.page_shift;
-  const int page_mask = (1 << p.page_shift) - 1;
+  const bool windowed = p.window < INT_MAX;
   auto slot = [&](int i) { return p.slots + static_cast<long long>(i) * p.slot_bytes; };
-
-  int used = 0, issued = 0;                                  // tiles that this warp has consumed, asked for
-  bool ok = true;
-  while (at.begin < x1) {
-    const long long unit_items = plan.cost(at.q);
-    const int first_pos = plan.first_pos(at.q, at.r), hi_pos = plan.last_pos(at.q, at.r);
-    const int lo_pos = max(first_pos, 0);
-    const Tiles tiles = plan.walk(lo_pos, hi_pos);
-    const long long items0 = at.begin + kStart;              // the first key tile's item
-    // this run's key tiles of the unit
-    const int kt0 = static_cast<int>(min(1ll * tiles.count, max(0ll, x0 - items0)));
-    const int kt1 = static_cast<int>(min(1ll * tiles.count, max(0ll, x1 - items0)));
-    const int first_row = at.r * R, rows = static_cast<int>(min(1ll * R, 1ll * at.q.n * p.group - first_row));
+  // A word that counts published pieces: this call's number and the count.  Every
+  // run that has a piece puts the number there long before the piece is done, so
+  // that counting is one addition (counting from whatever was there took a
+  // compare-and-swap for each of the pieces that come at once, 13 us for 16).
+  auto open_count = [&](unsigned long long* count) {
+    unsigned long long old = 0, seen;
+    while ((seen = atomicCAS(count, old, p.call)) != old && (seen & ~0xffffull) != p.call) old = seen;
+  };
+  while (true) {
+    const int rows = at.rows, first_row = at.first_row;
     // where row x's output begins
     auto out_of = [&](int x) {
       const int token = (first_row + x) / p.group, head = first_row + x - token * p.group;
       return p.out + (static_cast<long long>(at.q.start + token) * p.h + at.hk * p.group + head) * D;
     };
-    if (tiles.count == 0 && at.begin >= x0) {
+    if (at.tiles.count == 0 && at.begin >= sched.cut.begin(cta)) {
       // nothing to see: rows of zeros
       for (int x = tid; x < rows * (D / 4); x += kThreads)
         *reinterpret_cast<uint2*>(out_of(x / (D / 4)) + x % (D / 4) * 4) = make_uint2(0u, 0u);
     }
-    if (kt1 > kt0) {
-      const int32_t* pages = p.page_table + static_cast<long long>(at.s) * p.pages_per_seq;
-      const int mine = kt0 + warp < kt1 ? (kt1 - kt0 - warp + kWarps - 1) / kWarps : 0;
-      // ---- copies: lane x & 3 of a page's part takes K's codes, K's scales, V's, V's
-      const int part = lane >> 2, what = lane & 3;
-      const bool copies = part << box_shift < kKeys;
-      const uint32_t part_bytes = static_cast<uint32_t>((what & 1 ? D / 16 : D / 2) << box_shift);
-      auto page_of = [&](int i) -> int {
-        if (!copies || i >= mine) return -2;
-        const int key = (tiles.at(kt0 + warp + i * kWarps) << kKeysShift) + (part << box_shift);
-        // a page of which no row sees anything is not looked at
-        const int end = key + (1 << box_shift) - 1;
-        if (key > hi_pos || (p.window < INT_MAX && key >= p.sinks && end <= lo_pos - p.window)) return -2;
-        const int page = pages[key >> p.page_shift];
-        if (page >= 0 && page < p.n_pages) return page;
-        atomicOr(p.status, kStatusBadPage);
-        return -1;
+    if (at.kt1 > at.kt0) {
+      const int mine = (at.kt1 - at.kt0 - warp + kWarps - 1) / kWarps;   // tiles of this warp
+      const int hi_pos = at.hi_pos;
+      const int hidden = windowed ? max(at.first_pos, 0) - p.window : -1;   // up to here nobody sees what is no sink
+      auto key_of = [&](int i) {                             // of tile i
+        const int kt = at.kt0 + warp + i * kWarps;
+        return (kt < at.tiles.head ? kt : kt + at.tiles.first - at.tiles.head) << kKeysShift;
       };
-      auto issue = [&](int i, int page) {
-        if (i >= mine) return;
-        issued = used + i + 1;
-        const int st = (used + i) % kStages;
-        uint8_t* stage = ring + st * C::kTile;
-        const int key = (tiles.at(kt0 + warp + i * kWarps) << kKeysShift) + (part << box_shift);
-        const bool get = copies && page >= 0;
-        uint8_t* dst = stage + (what >> 1) * C::kHalf + (what & 1 ? C::kCodes + (part << box_shift) * (D / 16)
-                                                                  : (part << box_shift) * (D / 2));
-        const uint32_t bytes = __reduce_add_sync(0xffffffffu, get ? part_bytes : 0u);
-        if (lane == 0) mbar_arrive_expect_tx(full + st, bytes);
-        if (copies && page == -1 && (what & 1)) {
-          // a page outside the cache: scales of zero
-          for (uint32_t x = 0; x < part_bytes; x += 4) *reinterpret_cast<uint32_t*>(dst + x) = 0u;
-          fence_proxy_async_smem();
-        }
-        __syncwarp();
-        if (get) {
-          const uint8_t* src = (what >> 1 ? p.v_pages : p.k_pages) +
-                               (static_cast<long long>(page) * p.h_kv + at.hk) * page_bytes;
-          const int r = key & page_mask;
-          src += what & 1 ? (static_cast<long long>(D / 2) << p.page_shift) + r * (D / 16) : static_cast<long long>(r) * (D / 2);
-          tma_load_1d(dst, src, part_bytes, full + st);
-        }
+      // pieces in groups, those of a group merged first where there are many
+      auto radix_of = [&]() {
+        int radix = at.of;
+        if (radix > kTogether)
+          for (radix = 4; radix * radix < at.of;) ++radix;
+        return radix;
       };
-      int page_next = page_of(0);
-#pragma unroll
-      for (int i = 0; i < kStages - 1; ++i) {
-        const int page = page_next;
-        page_next = page_of(i + 1);
-        issue(i, page);
-      }
+      auto place = [&](int i) { return 2 * (at.first_run + i) + (i == 0 ? 1 : 0); };   // of piece i
       // ---- Q: row 8 nt + g, columns [t D / 4, + D / 4)
-      uint32_t qf[KS][NT][2];
-      float sc[NT][2];                                       // of columns 2 t, 2 t + 1: score to log2 units
-      int pos[NT][2];                                        // their positions (-1: no row)
+      uint2 raw[NT][KS];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         const int x = nt * 8 + g;
-        const bool valid = x < rows;
-        const int token = (first_row + (valid ? x : 0)) / p.group, head = first_row + (valid ? x : 0) - token * p.group;
+        const int token = (first_row + (x < rows ? x : 0)) / p.group;
+        const int head = first_row + (x < rows ? x : 0) - token * p.group;
         const uint2* src = reinterpret_cast<const uint2*>(
             p.q + static_cast<long long>(at.q.start + token) * p.q_stride + (at.hk * p.group + head) * D + t * (D / 4));
-        uint2 raw[KS];
+#pragma unroll
+        for (int k = 0; k < KS; ++k) raw[nt][k] = x < rows ? src[k] : make_uint2(0u, 0u);
+      }
+      // ---- copies.  A lane holds the page of one of this warp's next 32 tiles (of rows
+      // 0 .. 15 and 16 .. 31 of it, with pages of 16): -1 where nothing is copied.
+      const int32_t* pages = p.page_table + static_cast<long long>(at.s) * p.pages_per_seq;
+      int page0 = -1, page1 = -1;
+      auto page_at = [&](int key) -> int {
+        // a page of which no row sees anything is not looked at
+        if (key > hi_pos || (key + min(1 << p.page_shift, kKeys) - 1 <= hidden && key >= p.sinks)) return -1;
+        const int page = pages[key >> p.page_shift];
+        if (page >= 0 && page < p.n_pages) return page;
+        // one outside the cache is reported and read as zeros
+        atomicOr(p.status, kStatusBadPage);
+        return -1;
+      };
+      auto ask = [&](int i) {                                // for tiles i .. i + 31
+        page0 = page1 = -1;
+        if (i + lane < mine) {
+          const int key = key_of(i + lane);
+          page0 = page_at(key);
+          if (p.page_shift < kKeysShift) page1 = page_at(key + 16);
+        }
+        __syncwarp();
+      };
+      const uint32_t dst_lane = smem_u32(ring) + lane * 16;
+      const uint8_t *k_head = p.k_pages + at.hk * p.page_bytes, *v_head = p.v_pages + at.hk * p.page_bytes;
+      auto issue = [&](int i) {
+        if (i < mine) {
+          if ((i & 31) == 0 && i > 0) ask(i);
+          const uint32_t dst = dst_lane + i % C::kStages * C::kTile;
+          auto copy = [&](uint32_t to, const uint8_t* from, auto chunks, bool get) {
+            constexpr int n = decltype(chunks)::value;       // of 16 bytes
+#pragma unroll
+            for (int y = 0; y < n; y += 32)
+              if (n >= 32 || lane < n) cp_async16_or_zeros(to + y * 16, from + y * 16, get);
+          };
+          // (the scales of K and V by one instruction where 32 lanes do)
+          auto rows = [&](auto share, int page, int r, uint32_t codes_to, uint32_t scales_to) {
+            constexpr int n = decltype(share)::value;         // of the tile's rows, one in n
+            std::integral_constant<int, C::kCodes / 16 / n> codes;
+            std::integral_constant<int, C::kScales / 16 / n> scales;
+            const bool get = page >= 0;
+            const long long off = get ? page * p.page_stride : 0;
+            const uint8_t *k = k_head + off + lane * 16, *v = v_head + off + lane * 16;
+            const int at_codes = r * (D / 2), at_scales = r * (D / 16);
+            copy(dst + codes_to, k + at_codes, codes, get);
+            copy(dst + C::kHalf + codes_to, v + at_codes, codes, get);
+            const long long skip = (static_cast<long long>(D / 2) << p.page_shift) + at_scales;
+            if constexpr (scales <= 16) {
+              const bool second = lane >= 16;
+              const uint8_t* from = (second ? v - 256 : k) + skip;
+              if ((lane & 15) < scales)
+                cp_async16_or_zeros(dst + C::kCodes + scales_to + (second ? C::kHalf - 256 : 0), from, get);
+            } else {
+              copy(dst + C::kCodes + scales_to, k + skip, scales, get);
+              copy(dst + C::kHalf + C::kCodes + scales_to, v + skip, scales, get);
+            }
+          };
+          const int first = __shfl_sync(0xffffffffu, page0, i & 31);
+          if (p.page_shift >= kKeysShift) {
+            rows(std::integral_constant<int, 1>{}, first, key_of(i) & ((1 << p.page_shift) - 1), 0, 0);
+          } else {
+            const int second = __shfl_sync(0xffffffffu, page1, i & 31);
+            rows(std::integral_constant<int, 2>{}, first, 0, 0, 0);
+            rows(std::integral_constant<int, 2>{}, second, 0, C::kCodes / 2, C::kScales / 2);
+          }
+        }
+        cp_async_commit();
+      };
+      ask(0);
+#pragma unroll
+      for (int i = 0; i < C::kStages - 1; ++i) issue(i);
+      if (at.of > 1 && tid == kThreads - 1) {
+        const int radix = radix_of();
+        open_count(p.counts + place((cta - at.first_run) / radix * radix));
+        if (radix < at.of) open_count(p.counts + 2 * p.runs + at.first_run);
+      }
+      uint32_t qf[KS][NT][2];
+      float sc[NT][2];                                       // of columns 2 t, 2 t + 1: score to log2 units
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
         uint32_t top = 0;
 #pragma unroll
         for (int k = 0; k < KS; ++k) {
-          raw[k] = valid ? src[k] : make_uint2(0u, 0u);
-          top = max(max(top, max(raw[k].x & 0x7fffu, raw[k].y & 0x7fffu)), max(raw[k].x >> 16 & 0x7fffu, raw[k].y >> 16 & 0x7fffu));
+          const uint2 v = raw[nt][k];
+          top = max(max(top, max(v.x & 0x7fffu, v.y & 0x7fffu)), max(v.x >> 16 & 0x7fffu, v.y >> 16 & 0x7fffu));
         }
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
@@ -404,15 +554,13 @@ __global__ void __launch_bounds__(kThreads, NCfg<D, NT>::kCtas) sdpa_paged4_few(
         const float back = __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
 #pragma unroll
         for (int k = 0; k < KS; ++k) {
-          qf[k][nt][0] = pack_f16x2(__uint_as_float(raw[k].x << 16) * f, __uint_as_float(raw[k].x & 0xffff0000u) * f);
-          qf[k][nt][1] = pack_f16x2(__uint_as_float(raw[k].y << 16) * f, __uint_as_float(raw[k].y & 0xffff0000u) * f);
+          const uint2 v = raw[nt][k];
+          qf[k][nt][0] = pack_f16x2(__uint_as_float(v.x << 16) * f, __uint_as_float(v.x & 0xffff0000u) * f);
+          qf[k][nt][1] = pack_f16x2(__uint_as_float(v.y << 16) * f, __uint_as_float(v.y & 0xffff0000u) * f);
         }
-        const int row_pos = valid ? at.q.len - at.q.n + token : -1;
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          sc[nt][c] = __shfl_sync(0xffffffffu, back, (2 * t + c) * 4) * p.k_unit * p.scale_log2;
-          pos[nt][c] = __shfl_sync(0xffffffffu, row_pos, (2 * t + c) * 4);
-        }
+        for (int c = 0; c < 2; ++c)   // (never 0, which a masked score of -infinity would make a NaN)
+          sc[nt][c] = fmaxf(__shfl_sync(0xffffffffu, back, (2 * t + c) * 4) * p.k_unit * p.scale_log2, 1e-37f);
       }
       float o[KS][NT][4], m[NT][2], l[NT][2];
 #pragma unroll
@@ -429,136 +577,134 @@ __global__ void __launch_bounds__(kThreads, NCfg<D, NT>::kCtas) sdpa_paged4_few(
           l[nt][c] = 0.f;
         }
 
-      for (int i = 0; i < mine && ok; ++i) {
-        {
-          const int page = page_next;
-          page_next = page_of(i + kStages);
-          __syncwarp();                                      // (the stage has been read by all lanes)
-          issue(i + kStages - 1, page);
-        }
-        const int st = (used + i) % kStages;
-        ok = mbar_wait_warp(full + st, static_cast<uint32_t>((used + i) / kStages) & 1u, ab);
-        if (!ok) break;
-        const uint8_t* ks = ring + st * C::kTile;
-        const uint8_t* vs = ks + C::kHalf;
-        const int key0 = tiles.at(kt0 + warp + i * kWarps) << kKeysShift;
-        const bool edge = key0 + kKeys - 1 > first_pos || (p.window < INT_MAX && key0 <= hi_pos - p.window);
-        // ---- scores
-        float s[2][NT][4];
+      for (int i = 0; i < mine; ++i) {
+        cp_async_wait<C::kStages - 2>();
+        __syncwarp();                                        // (for all lanes; and the stage before has been read)
+        issue(i + C::kStages - 1);
+        uint8_t* ks = ring + i % C::kStages * C::kTile;
+        const int key0 = key_of(i);
+        const bool edge = key0 + kKeys - 1 > at.first_pos || (windowed && key0 <= hi_pos - p.window);
+        if (edge) {
+          // what no row sees may be anything: its weight is zero, but zero times a NaN
+          // is not, so its scales are cleared (a lane for each key)
+          const int j = key0 + lane;
+          if (j > hi_pos || (j <= hidden && j >= p.sinks)) {
 #pragma unroll
-        for (int mb = 0; mb < 2; ++mb) {
-          constexpr int kB = D / 8, kW = kB < 4 ? 1 : kB / 4;   // bytes, words of a lane's columns
-          uint32_t w[2][kW], sw[2];
-          constexpr int kSB = D >= 64 ? D / 64 : 1;             // scales of a lane's columns
-#pragma unroll
-          for (int hh = 0; hh < 2; ++hh) {
-            const int row = mb * 16 + hh * 8 + g;
-            load_bytes<kB>(ks + row * (D / 2) + t * kB, w[hh]);
-            uint32_t sb[1];
-            load_bytes<kSB>(ks + C::kCodes + row * (D / 16) + (D >= 64 ? t * kSB : t * D / 64), sb);
-            sw[hh] = sb[0];
+            for (int x = 0; x < D / 16; ++x) ks[C::kHalf + C::kCodes + lane * (D / 16) + x] = 0;
           }
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) s[mb][nt][e] = 0.f;
-#pragma unroll
-          for (int wi = 0; wi < kW; ++wi) {
-            uint32_t a[2][4];
+          __syncwarp();
+        }
+        const uint8_t* vs = ks + C::kHalf;
+#pragma unroll 2
+        for (int half = 0; half < 2; ++half, ks += 16 * (D / 2), vs += 16 * (D / 2)) {
+          // ---- scores of keys g and g + 8 in rows 2 t, 2 t + 1
+          float s[NT][4];
+          {
+            constexpr int kB = D / 8, kW = kB < 4 ? 1 : kB / 4;   // bytes, words of a lane's columns
+            constexpr int kSB = D >= 64 ? D / 64 : 1;             // scales of a lane's columns
+            const uint8_t* scales = ks + C::kCodes - half * (16 * (D / 2 - D / 16)) + (D >= 64 ? t * kSB : t * D / 64);
+            uint32_t w[2][kW], sw[2];
 #pragma unroll
             for (int hh = 0; hh < 2; ++hh) {
-              expand4(w[hh][wi], a[hh]);
-              // columns t D / 4 + 8 wi ..: block wi / 2 of the lane's
-              const uint32_t b = sw[hh] >> (8 * (wi / 2)) & 0xffu;
-              const uint32_t sc2 = scales_f16x2(b | b << 8);
-#pragma unroll
-              for (int e = 0; e < 4; ++e) a[hh][e] = mul_f16x2(a[hh][e], sc2);
+              const int row = hh * 8 + g;
+              load_bytes<kB>(ks + row * (D / 2) + t * kB, w[hh]);
+              uint32_t sb[1];
+              load_bytes<kSB>(scales + row * (D / 16), sb);
+              sw[hh] = sb[0];
             }
-            constexpr int kSteps = kB < 4 ? 1 : 2;
 #pragma unroll
-            for (int e = 0; e < kSteps; ++e)
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
-                mma_f16(s[mb][nt], a[0][2 * e], a[1][2 * e], a[0][2 * e + 1], a[1][2 * e + 1], qf[wi * 2 + e][nt][0],
-                        qf[wi * 2 + e][nt][1]);
-          }
-        }
-        if (edge) {
+              for (int e = 0; e < 4; ++e) s[nt][e] = 0.f;
 #pragma unroll
-          for (int mb = 0; mb < 2; ++mb)
+            for (int wi = 0; wi < kW; ++wi) {
+              uint32_t a[2][4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int j = key0 + mb * 16 + (e >> 1) * 8 + g;
+              for (int hh = 0; hh < 2; ++hh) {
+                expand4(w[hh][wi], a[hh]);
+                // columns t D / 4 + 8 wi ..: block wi / 2 of the lane's
+                const uint32_t sc2 = scales_f16x2(__byte_perm(sw[hh], 0, 0x11 * (wi / 2)));
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt) {
-                const int pp = pos[nt][e & 1];
-                if (j > pp || (j <= pp - p.window && j >= p.sinks)) s[mb][nt][e] = -INFINITY;
+                for (int e = 0; e < 4; ++e) a[hh][e] = mul_f16x2(a[hh][e], sc2);
               }
+              constexpr int kSteps = kB < 4 ? 1 : 2;
+#pragma unroll
+              for (int e = 0; e < kSteps; ++e)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+                  mma_f16(s[nt], a[0][2 * e], a[1][2 * e], a[0][2 * e + 1], a[1][2 * e + 1], qf[wi * 2 + e][nt][0],
+                          qf[wi * 2 + e][nt][1]);
             }
-        }
-        // ---- the running maxima: they move when one grew by more than the threshold
-        bool need = false;
-        float top[NT][2];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            top[nt][c] = fmaxf(fmaxf(s[0][nt][c], s[0][nt][2 + c]), fmaxf(s[1][nt][c], s[1][nt][2 + c])) * sc[nt][c];
-            need |= top[nt][c] > m[nt][c] + kRescaleThreshold;
           }
-        if (__any_sync(0xffffffffu, need)) {
+          if (edge) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                const int x = nt * 8 + 2 * t + c;            // this row's position (-1: no row)
+                const int pp = x < rows ? at.q.len - at.q.n + (first_row + x) / p.group : -1;
+#pragma unroll
+                for (int hh = 0; hh < 2; ++hh) {
+                  const int j = key0 + half * 16 + hh * 8 + g;
+                  if (j > pp || (j <= pp - p.window && j >= p.sinks)) s[nt][2 * hh + c] = -INFINITY;
+                }
+              }
+          }
+          // ---- the running maxima: they move when one grew by more than the threshold
+          bool need = false;
+          float top[NT][2];
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-              float x = top[nt][c];
-#pragma unroll
-              for (int y = 4; y < 32; y <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, y));
-              x = fmaxf(x, m[nt][c]);
-              const float f = x == -INFINITY ? 1.f : ex2_approx(m[nt][c] - x);
-              m[nt][c] = x;
-              l[nt][c] *= f;
-#pragma unroll
-              for (int k = 0; k < KS; ++k) {
-                o[k][nt][c] *= f;
-                o[k][nt][2 + c] *= f;
-              }
+              top[nt][c] = fmaxf(s[nt][c], s[nt][2 + c]) * sc[nt][c];
+              need |= top[nt][c] > m[nt][c] + kRescaleThreshold;
             }
-        }
-        // ---- weights, turned so that a lane holds two keys of a row
-        uint32_t pb[2][NT][2];
+          if (__any_sync(0xffffffffu, need)) {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const float m0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0], m1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int mb = 0; mb < 2; ++mb)
+              for (int c = 0; c < 2; ++c) {
+                float x = top[nt][c];
+#pragma unroll
+                for (int y = 4; y < 32; y <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, y));
+                x = fmaxf(x, m[nt][c]);
+                const float f = x == -INFINITY ? 1.f : ex2_approx(m[nt][c] - x);
+                m[nt][c] = x;
+                l[nt][c] *= f;
+#pragma unroll
+                for (int k = 0; k < KS; ++k) {
+                  o[k][nt][c] *= f;
+                  o[k][nt][2 + c] *= f;
+                }
+              }
+          }
+          // ---- weights, turned so that a lane holds two keys of a row
+          uint32_t pb[NT][2];
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const float m0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0], m1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
 #pragma unroll
             for (int hh = 0; hh < 2; ++hh) {
-              const float p0 = ex2_approx(fmaf(s[mb][nt][2 * hh], sc[nt][0], -m0));
-              const float p1 = ex2_approx(fmaf(s[mb][nt][2 * hh + 1], sc[nt][1], -m1));
+              const float p0 = ex2_approx(fmaf(s[nt][2 * hh], sc[nt][0], -m0));
+              const float p1 = ex2_approx(fmaf(s[nt][2 * hh + 1], sc[nt][1], -m1));
               l[nt][0] += p0;
               l[nt][1] += p1;
-              pb[mb][nt][hh] = transpose8x8(pack_f16x2(p0, p1));
+              pb[nt][hh] = transpose8x8(pack_f16x2(p0, p1));
             }
-        }
-        // ---- O^T += V^T P
-#pragma unroll
-        for (int mb = 0; mb < 2; ++mb) {
+          }
+          // ---- O^T += V^T P: keys 2 t, 2 t + 1, 2 t + 8, 2 t + 9
           constexpr int kB = D / 16, kW = kB < 4 ? 1 : kB / 4;
           constexpr int kSB = D >= 128 ? D / 128 : 1;
-          uint32_t w[4][kW], sw[4];                          // keys 2 t, 2 t + 1, 2 t + 8, 2 t + 9
+          const uint8_t* scales = vs + C::kCodes - half * (16 * (D / 2 - D / 16)) + (D >= 128 ? g * kSB : g * D / 128);
+          uint32_t w[4][kW], sw[4];
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
-            const int row = mb * 16 + 2 * t + (x & 1) + (x >> 1) * 8;
+            const int row = 2 * t + (x & 1) + (x >> 1) * 8;
             load_bytes<kB>(vs + row * (D / 2) + g * kB, w[x]);
             uint32_t sb[1];
-            load_bytes<kSB>(vs + C::kCodes + row * (D / 16) + (D >= 128 ? g * kSB : g * D / 128), sb);
+            load_bytes<kSB>(scales + row * (D / 16), sb);
             sw[x] = sb[0];
-            if (edge) {
-              // what no row sees may be anything: its weight is zero, zero times a NaN is not
-              const int j = key0 + row;
-              if (j > hi_pos || (p.window < INT_MAX && j <= lo_pos - p.window && j >= p.sinks)) sw[x] = 0;
-            }
           }
 #pragma unroll
           for (int wi = 0; wi < kW; ++wi) {
@@ -569,7 +715,7 @@ __global__ void __launch_bounds__(kThreads, NCfg<D, NT>::kCtas) sdpa_paged4_few(
               expand4((w0 & 0x0f0f0f0fu) | (w1 << 4 & 0xf0f0f0f0u), a[2 * y]);
               expand4((w0 >> 4 & 0x0f0f0f0fu) | (w1 & 0xf0f0f0f0u), a[2 * y + 1]);
               const int blk = wi / 2;                         // 8 columns a word
-              const uint32_t sc2 = scales_f16x2((sw[2 * y] >> (8 * blk) & 0xffu) | (sw[2 * y + 1] >> (8 * blk) & 0xffu) << 8);
+              const uint32_t sc2 = scales_f16x2(__byte_perm(sw[2 * y], sw[2 * y + 1], blk | (4 + blk) << 4));
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
                 a[2 * y][e] = mul_f16x2(a[2 * y][e], sc2);
@@ -580,11 +726,11 @@ __global__ void __launch_bounds__(kThreads, NCfg<D, NT>::kCtas) sdpa_paged4_few(
             for (int e = 0; e < (kB < 4 ? kB : 4); ++e)
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt)
-                mma_f16(o[wi * 4 + e][nt], a[0][e], a[1][e], a[2][e], a[3][e], pb[mb][nt][0], pb[mb][nt][1]);
+                mma_f16(o[wi * 4 + e][nt], a[0][e], a[1][e], a[2][e], a[3][e], pb[nt][0], pb[nt][1]);
           }
         }
       }
-      used += mine;
+      cp_async_wait<0>();                                    // (groups without copies)
       // ---- the piece's end: the warps' (O, m, l) are merged
       float2* ml = reinterpret_cast<float2*>(smem + C::kMlOff);
 #pragma unroll
@@ -595,11 +741,9 @@ __global__ void __launch_bounds__(kThreads, NCfg<D, NT>::kCtas) sdpa_paged4_few(
           for (int y = 4; y < 32; y <<= 1) l[nt][c] += __shfl_xor_sync(0xffffffffu, l[nt][c], y);
           if (g == 0) ml[warp * R + nt * 8 + 2 * t + c] = make_float2(m[nt][c], l[nt][c]);
         }
-      const int first_run = cut.run_of(items0), last_run = cut.run_of(items0 + tiles.count - 1);
-      const bool whole = first_run == last_run;
-      const int of = last_run - first_run + 1;
+      const bool whole = at.of == 1;
       float* xo = reinterpret_cast<float*>(smem + C::kRing);
-      uint8_t* own = whole ? nullptr : slot(2 * cta + (cta == first_run ? 1 : 0));
+      uint8_t* own = whole ? nullptr : slot(2 * cta + (cta == at.first_run ? 1 : 0));
       constexpr int kPC = C::kPassCols, kPer = kPC / 8;      // columns of a lane group g in a pass
 #pragma unroll
       for (int pass = 0; pass < C::kPasses; ++pass) {
@@ -612,11 +756,7 @@ __global__ void __launch_bounds__(kThreads, NCfg<D, NT>::kCtas) sdpa_paged4_few(
             for (int c = 0; c < 2; ++c)
               *reinterpret_cast<float2*>(xo + (warp * R + nt * 8 + 2 * t + c) * kPC + g * kPer + 2 * k) =
                   make_float2(o[pass * (KS / C::kPasses) + k][nt][c], o[pass * (KS / C::kPasses) + k][nt][2 + c]);
-        // (also the decision whether to go on, the same for all)
-        if (__syncthreads_or(!ok)) {
-          ok = false;
-          break;
-        }
+        __syncthreads();
         constexpr int kVec = kPer % 4 == 0 ? 4 : 2;          // columns that lie together
         for (int x = tid; x < rows * (kPC / kVec); x += kThreads) {
           const int row = x / (kPC / kVec), c0 = x % (kPC / kVec) * kVec;
@@ -658,103 +798,83 @@ __global__ void __launch_bounds__(kThreads, NCfg<D, NT>::kCtas) sdpa_paged4_few(
           }
         }
       }
-      if (!ok) break;
       if (!whole) {
         // ---- published; the last of a group of pieces merges it, the last
         // group's all groups
-        const int j = cta - first_run, group = j / kRadix, groups = (of + kRadix - 1) / kRadix;
-        auto place = [&](int i) { return 2 * (first_run + i) + (i == 0 ? 1 : 0); };   // of piece i
-        // counts `count` up and tells everybody whether this was the last of `all`
+        const int radix = radix_of(), of = at.of;
+        const int group = (cta - at.first_run) / radix, groups = (of + radix - 1) / radix;
+        // counts up and tells everybody whether this was the last of `all`
         auto arrive = [&](unsigned long long* count, int all) -> bool {
           __threadfence();
           __syncthreads();
           if (tid == 0) {
-            unsigned long long old = __ldcg(count), seen;
-            while (true) {
-              const unsigned long long base = (old & ~0xffffull) == p.call ? old : p.call;
-              const bool last = static_cast<int>(base & 0xffff) + 1 >= all;
-              seen = atomicCAS(count, old, last ? 0ull : base + 1);
-              if (seen == old) {
-                last_one = last;
-                break;
-              }
-              old = seen;
-            }
+            last_one = static_cast<int>(atomicAdd(count, 1ull) & 0xffff) + 1 == all;
+            if (last_one) *count = 0;
             __threadfence();
           }
           __syncthreads();
           return last_one != 0;
         };
-        // pieces i0, i0 + step, .. of n, into the output or piece i0's place
+        // pieces i0, i0 + step, .. of n, into the output or piece i0's place.  All
+        // statistics come in at once, then kAhead pieces at a time.
         auto merge = [&](int i0, int step, int n, bool final) {
+          constexpr int kAhead = 16;
+          float2* stats = reinterpret_cast<float2*>(smem + C::kRing);   // [piece][row]
+          for (int x = tid; x < n * R; x += kThreads)
+            if (x % R < rows)
+              stats[x] = __ldcg(reinterpret_cast<const float2*>(slot(place(i0 + x / R * step)) + R * D * 4) + x % R);
+          __syncthreads();
           for (int x = tid; x < rows * (D / 4); x += kThreads) {
             const int row = x / (D / 4), col = x % (D / 4) * 4;
-            float mm = -INFINITY;
-            for (int i = 0; i < n; ++i)
-              mm = fmaxf(mm, __ldcg(reinterpret_cast<const float2*>(slot(place(i0 + i * step)) + R * D * 4) + row).x);
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f), v[kAhead];
+            float mm = -INFINITY, ll = 0.f;
+            auto ask = [&](int i1) {
+#pragma unroll
+              for (int e = 0; e < kAhead; ++e)
+                if (i1 + e < n)
+                  v[e] = __ldcg(reinterpret_cast<const float4*>(slot(place(i0 + (i1 + e) * step))) + x);
+            };
+            ask(0);
+            for (int i = 0; i < n; ++i) mm = fmaxf(mm, stats[i * R + row].x);
             const float sub = mm == -INFINITY ? 0.f : mm;
-            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-            float ll = 0.f;
-#pragma unroll 4
-            for (int i = 0; i < n; ++i) {
-              const uint8_t* src = slot(place(i0 + i * step));
-              const float2 one = __ldcg(reinterpret_cast<const float2*>(src + R * D * 4) + row);
-              const float4 v = __ldcg(reinterpret_cast<const float4*>(src) + row * (D / 4) + col / 4);
-              const float f = weight(one.x, sub);
-              ll = fmaf(one.y, f, ll);
-              acc.x = fmaf(v.x, f, acc.x);
-              acc.y = fmaf(v.y, f, acc.y);
-              acc.z = fmaf(v.z, f, acc.z);
-              acc.w = fmaf(v.w, f, acc.w);
+            for (int i1 = 0; i1 < n; i1 += kAhead) {
+              if (i1 > 0) ask(i1);
+#pragma unroll
+              for (int e = 0; e < kAhead; ++e) {
+                if (i1 + e >= n) continue;
+                const float2 one = stats[(i1 + e) * R + row];
+                const float f = weight(one.x, sub);
+                ll = fmaf(one.y, f, ll);
+                acc.x = fmaf(v[e].x, f, acc.x);
+                acc.y = fmaf(v[e].y, f, acc.y);
+                acc.z = fmaf(v[e].z, f, acc.z);
+                acc.w = fmaf(v[e].w, f, acc.w);
+              }
             }
             if (final) {
               const float f = ll > 0.f ? p.v_unit / ll : 0.f;
               *reinterpret_cast<uint2*>(out_of(row) + col) =
                   make_uint2(pack_bf16x2(acc.x * f, acc.y * f), pack_bf16x2(acc.z * f, acc.w * f));
             } else {
-              // (this thread alone reads and writes these columns; the statistics are
-              // in a place of their own, behind those that others still read)
+              // (this thread alone reads and writes these columns)
               uint8_t* dst = slot(place(i0));
-              reinterpret_cast<float4*>(dst)[row * (D / 4) + col / 4] = acc;
-              if (col == 0) reinterpret_cast<float2*>(dst + R * D * 4)[R + row] = make_float2(mm, ll);
+              reinterpret_cast<float4*>(dst)[x] = acc;
+              if (col == 0) reinterpret_cast<float2*>(dst + R * D * 4)[row] = make_float2(mm, ll);
             }
           }
         };
-        if (groups == 1) {
-          if (arrive(p.counts + place(0), of)) merge(0, 1, of, true);
-        } else {
-          const int i0 = group * kRadix, n = min(kRadix, of - i0);
-          if (arrive(p.counts + place(i0), n)) {
-            merge(i0, 1, n, false);
-            __syncthreads();
-            // the merged statistics take the piece's place
-            if (tid < rows) {
-              float2* at_ml = reinterpret_cast<float2*>(slot(place(i0)) + R * D * 4);
-              at_ml[tid] = at_ml[R + tid];
-            }
-            if (arrive(p.counts + 2 * p.runs + first_run, groups)) merge(0, kRadix, groups, true);
-          }
+        const int i0 = group * radix, n = min(radix, of - i0);
+        if (arrive(p.counts + place(i0), n)) {
+          merge(i0, 1, n, groups == 1);
+          if (groups > 1 && arrive(p.counts + 2 * p.runs + at.first_run, groups)) merge(0, radix, groups, true);
         }
       }
-      __syncthreads();                                       // (the exchange memory has been read)
     }
-    // ---- the next unit
-    at.begin += unit_items;
-    if (++at.r == at.q.tiles) {
-      at.r = 0;
-      if (++at.hk == p.h_kv) {
-        at.hk = 0;
-        do {
-          if (++at.s == p.b) break;
-          at.q = plan.seq(at.s);
-        } while (at.q.n == 0);
-        if (at.s == p.b) break;
-      }
-    }
+    __syncthreads();                                         // (the unit and the exchange memory have been read)
+    if (tid == 0) more = next_unit<R>(plan, sched.cut, cta, &at);
+    __syncthreads();
+    if (more == 0) break;
   }
-  // let every copy land before the CTA can exit (a wait may have run out above)
-  for (int u = max(0, issued - kStages); u < issued; ++u)
-    mbar_wait_drain(full + u % kStages, static_cast<uint32_t>(u / kStages) & 1u);
 }
 
 template <int D, int NT>
@@ -785,7 +905,7 @@ int paged4_rows(int group, int n_tokens, int b) {
   return 1ll * group * n_tokens <= 8ll * b ? 8 : 16;
 }
 
-int paged4_resident_ctas(int d, int rows) { return d * rows <= 1024 ? 2 : 1; }
+int paged4_resident_ctas(int d, int rows) { return d * rows <= 1024 ? 3 : 2; }
 
 long long paged4_most_runs(long long units, long long max_len) {
   return std::max(1ll, units * (kStart + max_len / kKeys + 2) / kMinRun);
