@@ -390,6 +390,68 @@ __device__ __forceinline__ void cp_async16_or_zeros(uint32_t dst, const uint8_t*
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(get ? 16 : 0) : "memory");
 }
 
+// Where row x of a unit begins in the output.
+template <int D>
+__device__ __forceinline__ uint16_t* out_row(const Paged4Params& p, const Unit& at, int x) {
+  const int row = at.first_row + x, token = row / p.group;
+  return p.out + (static_cast<long long>(at.q.start + token) * p.h + at.hk * p.group + row - token * p.group) * D;
+}
+
+// The slot of piece i of a unit.  A run has two: for the unit in which it ends, and
+// for the one in which it begins.
+__device__ __forceinline__ int slot_of(const Unit& at, int i) { return 2 * (at.first_run + i) + (i == 0 ? 1 : 0); }
+
+// The whole block: pieces i0, i0 + step, .. (n of them) merged into the output, or
+// into piece i0's slot.  All statistics come in at once, then kAhead pieces at a time.
+// (A function of its own, or its registers cost the loop over the keys some.)
+template <int D, int R>
+__device__ __noinline__ void merge_pieces(const Paged4Params& p, const Unit& at, float2* stats, int i0, int step, int n,
+                                          bool final) {
+  constexpr int kAhead = 16;
+  const int rows = at.rows;
+  auto slot = [&](int i) { return p.slots + static_cast<long long>(slot_of(at, i0 + i * step)) * p.slot_bytes; };
+  for (int x = threadIdx.x; x < n * R; x += kThreads)        // [piece][row]
+    if (x % R < rows) stats[x] = __ldcg(reinterpret_cast<const float2*>(slot(x / R) + R * D * 4) + x % R);
+  __syncthreads();
+  for (int x = threadIdx.x; x < rows * (D / 4); x += kThreads) {
+    const int row = x / (D / 4), col = x % (D / 4) * 4;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f), v[kAhead];
+    float mm = -INFINITY, ll = 0.f;
+    auto ask = [&](int i1) {
+#pragma unroll
+      for (int e = 0; e < kAhead; ++e)
+        if (i1 + e < n) v[e] = __ldcg(reinterpret_cast<const float4*>(slot(i1 + e)) + x);
+    };
+    ask(0);
+    for (int i = 0; i < n; ++i) mm = fmaxf(mm, stats[i * R + row].x);
+    const float sub = mm == -INFINITY ? 0.f : mm;
+    for (int i1 = 0; i1 < n; i1 += kAhead) {
+      if (i1 > 0) ask(i1);
+#pragma unroll
+      for (int e = 0; e < kAhead; ++e) {
+        if (i1 + e >= n) continue;
+        const float2 one = stats[(i1 + e) * R + row];
+        const float f = weight(one.x, sub);
+        ll = fmaf(one.y, f, ll);
+        acc.x = fmaf(v[e].x, f, acc.x);
+        acc.y = fmaf(v[e].y, f, acc.y);
+        acc.z = fmaf(v[e].z, f, acc.z);
+        acc.w = fmaf(v[e].w, f, acc.w);
+      }
+    }
+    if (final) {
+      const float f = ll > 0.f ? p.v_unit / ll : 0.f;
+      *reinterpret_cast<uint2*>(out_row<D>(p, at, row) + col) =
+          make_uint2(pack_bf16x2(acc.x * f, acc.y * f), pack_bf16x2(acc.z * f, acc.w * f));
+    } else {
+      // (this thread alone reads and writes these columns)
+      uint8_t* dst = slot(0);
+      reinterpret_cast<float4*>(dst)[x] = acc;
+      if (col == 0) reinterpret_cast<float2*>(dst + R * D * 4)[row] = make_float2(mm, ll);
+    }
+  }
+}
+
 template <int D, int NT>
 __global__ void __launch_bounds__(kThreads, NCfg<D, NT>::kCtas) sdpa_paged4_few(const __grid_constant__ Paged4Params p) {
   using C = NCfg<D, NT>;
@@ -412,7 +474,6 @@ __global__ void __launch_bounds__(kThreads, NCfg<D, NT>::kCtas) sdpa_paged4_few(
   if (!find_place<R>(plan, &sched, &at, cta) || at.begin == LLONG_MAX) return;
 
   const bool windowed = p.window < INT_MAX;
-  auto slot = [&](int i) { return p.slots + static_cast<long long>(i) * p.slot_bytes; };
   // A word that counts published pieces: this call's number and the count.  Every
   // run that has a piece puts the number there long before the piece is done, so
   // that counting is one addition (counting from whatever was there took a
@@ -423,11 +484,7 @@ __global__ void __launch_bounds__(kThreads, NCfg<D, NT>::kCtas) sdpa_paged4_few(
   };
   while (true) {
     const int rows = at.rows, first_row = at.first_row;
-    // where row x's output begins
-    auto out_of = [&](int x) {
-      const int token = (first_row + x) / p.group, head = first_row + x - token * p.group;
-      return p.out + (static_cast<long long>(at.q.start + token) * p.h + at.hk * p.group + head) * D;
-    };
+    auto out_of = [&](int x) { return out_row<D>(p, at, x); };
     if (at.tiles.count == 0 && at.begin >= sched.cut.begin(cta)) {
       // nothing to see: rows of zeros
       for (int x = tid; x < rows * (D / 4); x += kThreads)
@@ -448,7 +505,6 @@ __global__ void __launch_bounds__(kThreads, NCfg<D, NT>::kCtas) sdpa_paged4_few(
           for (radix = 4; radix * radix < at.of;) ++radix;
         return radix;
       };
-      auto place = [&](int i) { return 2 * (at.first_run + i) + (i == 0 ? 1 : 0); };   // of piece i
       // ---- Q: row 8 nt + g, columns [t D / 4, + D / 4)
       uint2 raw[NT][KS];
 #pragma unroll
@@ -533,7 +589,7 @@ __global__ void __launch_bounds__(kThreads, NCfg<D, NT>::kCtas) sdpa_paged4_few(
       for (int i = 0; i < C::kStages - 1; ++i) issue(i);
       if (at.of > 1 && tid == kThreads - 1) {
         const int radix = radix_of();
-        open_count(p.counts + place((cta - at.first_run) / radix * radix));
+        open_count(p.counts + slot_of(at, (cta - at.first_run) / radix * radix));
         if (radix < at.of) open_count(p.counts + 2 * p.runs + at.first_run);
       }
       uint32_t qf[KS][NT][2];
@@ -743,7 +799,7 @@ __global__ void __launch_bounds__(kThreads, NCfg<D, NT>::kCtas) sdpa_paged4_few(
         }
       const bool whole = at.of == 1;
       float* xo = reinterpret_cast<float*>(smem + C::kRing);
-      uint8_t* own = whole ? nullptr : slot(2 * cta + (cta == at.first_run ? 1 : 0));
+      uint8_t* own = whole ? nullptr : p.slots + static_cast<long long>(slot_of(at, cta - at.first_run)) * p.slot_bytes;
       constexpr int kPC = C::kPassCols, kPer = kPC / 8;      // columns of a lane group g in a pass
 #pragma unroll
       for (int pass = 0; pass < C::kPasses; ++pass) {
@@ -815,58 +871,12 @@ __global__ void __launch_bounds__(kThreads, NCfg<D, NT>::kCtas) sdpa_paged4_few(
           __syncthreads();
           return last_one != 0;
         };
-        // pieces i0, i0 + step, .. of n, into the output or piece i0's place.  All
-        // statistics come in at once, then kAhead pieces at a time.
-        auto merge = [&](int i0, int step, int n, bool final) {
-          constexpr int kAhead = 16;
-          float2* stats = reinterpret_cast<float2*>(smem + C::kRing);   // [piece][row]
-          for (int x = tid; x < n * R; x += kThreads)
-            if (x % R < rows)
-              stats[x] = __ldcg(reinterpret_cast<const float2*>(slot(place(i0 + x / R * step)) + R * D * 4) + x % R);
-          __syncthreads();
-          for (int x = tid; x < rows * (D / 4); x += kThreads) {
-            const int row = x / (D / 4), col = x % (D / 4) * 4;
-            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f), v[kAhead];
-            float mm = -INFINITY, ll = 0.f;
-            auto ask = [&](int i1) {
-#pragma unroll
-              for (int e = 0; e < kAhead; ++e)
-                if (i1 + e < n)
-                  v[e] = __ldcg(reinterpret_cast<const float4*>(slot(place(i0 + (i1 + e) * step))) + x);
-            };
-            ask(0);
-            for (int i = 0; i < n; ++i) mm = fmaxf(mm, stats[i * R + row].x);
-            const float sub = mm == -INFINITY ? 0.f : mm;
-            for (int i1 = 0; i1 < n; i1 += kAhead) {
-              if (i1 > 0) ask(i1);
-#pragma unroll
-              for (int e = 0; e < kAhead; ++e) {
-                if (i1 + e >= n) continue;
-                const float2 one = stats[(i1 + e) * R + row];
-                const float f = weight(one.x, sub);
-                ll = fmaf(one.y, f, ll);
-                acc.x = fmaf(v[e].x, f, acc.x);
-                acc.y = fmaf(v[e].y, f, acc.y);
-                acc.z = fmaf(v[e].z, f, acc.z);
-                acc.w = fmaf(v[e].w, f, acc.w);
-              }
-            }
-            if (final) {
-              const float f = ll > 0.f ? p.v_unit / ll : 0.f;
-              *reinterpret_cast<uint2*>(out_of(row) + col) =
-                  make_uint2(pack_bf16x2(acc.x * f, acc.y * f), pack_bf16x2(acc.z * f, acc.w * f));
-            } else {
-              // (this thread alone reads and writes these columns)
-              uint8_t* dst = slot(place(i0));
-              reinterpret_cast<float4*>(dst)[x] = acc;
-              if (col == 0) reinterpret_cast<float2*>(dst + R * D * 4)[row] = make_float2(mm, ll);
-            }
-          }
-        };
         const int i0 = group * radix, n = min(radix, of - i0);
-        if (arrive(p.counts + place(i0), n)) {
-          merge(i0, 1, n, groups == 1);
-          if (groups > 1 && arrive(p.counts + 2 * p.runs + at.first_run, groups)) merge(0, radix, groups, true);
+        if (arrive(p.counts + slot_of(at, i0), n)) {
+          float2* stats = reinterpret_cast<float2*>(smem + C::kRing);   // (the exchange memory)
+          merge_pieces<D, R>(p, at, stats, i0, 1, n, groups == 1);
+          if (groups > 1 && arrive(p.counts + 2 * p.runs + at.first_run, groups))
+            merge_pieces<D, R>(p, at, stats, 0, radix, groups, true);
         }
       }
     }
