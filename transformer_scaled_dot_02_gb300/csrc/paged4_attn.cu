@@ -51,7 +51,10 @@ constexpr int kKeys = 32;                  // per tile
 constexpr int kKeysShift = 5;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units, as in the other forward kernels
 // What a unit costs beside its key tiles, in key tiles.
-constexpr int kStart = 8;
+#ifndef KSTART
+#define KSTART 20
+#endif
+constexpr int kStart = KSTART;
 constexpr int kMinRun = 16;                // items of a run, at least
 // How the work is cut.  kPieces: every unit into pieces of its own, a run for each,
 // where that many runs fit the GPU; a walk of up to kWhole key tiles is one piece,
@@ -211,9 +214,11 @@ struct Schedule {
 template <int R>
 __device__ bool find_place(const Plan<R>& plan, Schedule* sh, Unit* first, int c) {
   const Paged4Params& p = plan.p;
+  // (up to 32 sequences every warp looks at all of them, and none waits for another)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int per = (p.b + kThreads - 1) / kThreads;
-  const int s0 = min(tid * per, p.b), s1 = min(s0 + per, p.b);
+  const bool alone = p.b <= 32;
+  const int per = alone ? 1 : (p.b + kThreads - 1) / kThreads;
+  const int s0 = min((alone ? lane : tid) * per, p.b), s1 = min(s0 + per, p.b);
   long long items = 0, pieces = 0;
   Seq q;
   for (int s = s0; s < s1; ++s) {
@@ -232,21 +237,24 @@ __device__ bool find_place(const Plan<R>& plan, Schedule* sh, Unit* first, int c
       pieces_to += n;
     }
   }
-  if (lane == 31) {
-    sh->items[warp] = items_to;
-    sh->pieces[warp] = pieces_to;
-  }
+  long long all_items = __shfl_sync(0xffffffffu, items_to, 31), all_pieces = __shfl_sync(0xffffffffu, pieces_to, 31);
   if (tid == 0) first->begin = LLONG_MAX;                    // (no unit, should the lengths change meanwhile)
-  __syncthreads();
-  long long all_items = 0, all_pieces = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    if (w == warp) {
-      items_to += all_items;
-      pieces_to += all_pieces;
+  if (!alone) {
+    if (lane == 31) {
+      sh->items[warp] = items_to;
+      sh->pieces[warp] = pieces_to;
     }
-    all_items += sh->items[w];
-    all_pieces += sh->pieces[w];
+    __syncthreads();
+    all_items = all_pieces = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      if (w == warp) {
+        items_to += all_items;
+        pieces_to += all_pieces;
+      }
+      all_items += sh->items[w];
+      all_pieces += sh->pieces[w];
+    }
   }
   if (all_items == 0) return false;
   const Scheme scheme = all_pieces <= p.runs ? kPieces : kItems;
@@ -257,7 +265,7 @@ __device__ bool find_place(const Plan<R>& plan, Schedule* sh, Unit* first, int c
   if (tid == 0) sh->cut = cut;
   const long long mine = scheme == kPieces ? pieces : items;
   long long before = (scheme == kPieces ? pieces_to : items_to) - mine;
-  if (mine > 0 && before <= x && x < before + mine) {
+  if (mine > 0 && before <= x && x < before + mine && (!alone || warp == 0)) {
     for (int s = s0; s < s1; ++s) {
       if (per > 1) q = plan.seq(s);
       const int unit = plan.cost(q, scheme);
@@ -402,52 +410,74 @@ __device__ __forceinline__ uint16_t* out_row(const Paged4Params& p, const Unit& 
 __device__ __forceinline__ int slot_of(const Unit& at, int i) { return 2 * (at.first_run + i) + (i == 0 ? 1 : 0); }
 
 // The whole block: pieces i0, i0 + step, .. (n of them) merged into the output, or
-// into piece i0's slot.  All statistics come in at once, then kAhead pieces at a time.
-// (A function of its own, or its registers cost the loop over the keys some.)
+// into piece i0's slot.  A thread takes kVectors vectors of four columns, kAhead
+// pieces at a time, the first asked for together with the statistics.  (A function of
+// its own, or its registers cost the loop over the keys some.)
 template <int D, int R>
 __device__ __noinline__ void merge_pieces(const Paged4Params& p, const Unit& at, float2* stats, int i0, int step, int n,
                                           bool final) {
-  constexpr int kAhead = 16;
-  const int rows = at.rows;
+  constexpr int kAhead = 8, kVectors = R * (D / 4) >= 2 * kThreads ? 2 : 1;
+  const int rows = at.rows, all = rows * (D / 4);
   auto slot = [&](int i) { return p.slots + static_cast<long long>(slot_of(at, i0 + i * step)) * p.slot_bytes; };
-  for (int x = threadIdx.x; x < n * R; x += kThreads)        // [piece][row]
-    if (x % R < rows) stats[x] = __ldcg(reinterpret_cast<const float2*>(slot(x / R) + R * D * 4) + x % R);
-  __syncthreads();
-  for (int x = threadIdx.x; x < rows * (D / 4); x += kThreads) {
-    const int row = x / (D / 4), col = x % (D / 4) * 4;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f), v[kAhead];
-    float mm = -INFINITY, ll = 0.f;
+  for (int x0 = threadIdx.x; x0 < (all + kThreads - 1) / kThreads * kThreads; x0 += kVectors * kThreads) {
+    float4 acc[kVectors], v[kVectors][kAhead];
+    float mm[kVectors], ll[kVectors];
+    int row[kVectors];
     auto ask = [&](int i1) {
 #pragma unroll
       for (int e = 0; e < kAhead; ++e)
-        if (i1 + e < n) v[e] = __ldcg(reinterpret_cast<const float4*>(slot(i1 + e)) + x);
+#pragma unroll
+        for (int y = 0; y < kVectors; ++y)
+          if (i1 + e < n && x0 + y * kThreads < all)
+            v[y][e] = __ldcg(reinterpret_cast<const float4*>(slot(i1 + e)) + x0 + y * kThreads);
     };
     ask(0);
-    for (int i = 0; i < n; ++i) mm = fmaxf(mm, stats[i * R + row].x);
-    const float sub = mm == -INFINITY ? 0.f : mm;
+    if (x0 == static_cast<int>(threadIdx.x)) {
+      for (int x = threadIdx.x; x < n * R; x += kThreads)    // [piece][row]
+        if (x % R < rows) stats[x] = __ldcg(reinterpret_cast<const float2*>(slot(x / R) + R * D * 4) + x % R);
+      __syncthreads();
+    }
+#pragma unroll
+    for (int y = 0; y < kVectors; ++y) {
+      row[y] = min((x0 + y * kThreads) / (D / 4), rows - 1);
+      acc[y] = make_float4(0.f, 0.f, 0.f, 0.f);
+      mm[y] = -INFINITY;
+      ll[y] = 0.f;
+    }
+    for (int i = 0; i < n; ++i)
+#pragma unroll
+      for (int y = 0; y < kVectors; ++y) mm[y] = fmaxf(mm[y], stats[i * R + row[y]].x);
     for (int i1 = 0; i1 < n; i1 += kAhead) {
       if (i1 > 0) ask(i1);
 #pragma unroll
       for (int e = 0; e < kAhead; ++e) {
         if (i1 + e >= n) continue;
-        const float2 one = stats[(i1 + e) * R + row];
-        const float f = weight(one.x, sub);
-        ll = fmaf(one.y, f, ll);
-        acc.x = fmaf(v[e].x, f, acc.x);
-        acc.y = fmaf(v[e].y, f, acc.y);
-        acc.z = fmaf(v[e].z, f, acc.z);
-        acc.w = fmaf(v[e].w, f, acc.w);
+#pragma unroll
+        for (int y = 0; y < kVectors; ++y) {
+          const float2 one = stats[(i1 + e) * R + row[y]];
+          const float f = weight(one.x, mm[y] == -INFINITY ? 0.f : mm[y]);
+          ll[y] = fmaf(one.y, f, ll[y]);
+          acc[y].x = fmaf(v[y][e].x, f, acc[y].x);
+          acc[y].y = fmaf(v[y][e].y, f, acc[y].y);
+          acc[y].z = fmaf(v[y][e].z, f, acc[y].z);
+          acc[y].w = fmaf(v[y][e].w, f, acc[y].w);
+        }
       }
     }
-    if (final) {
-      const float f = ll > 0.f ? p.v_unit / ll : 0.f;
-      *reinterpret_cast<uint2*>(out_row<D>(p, at, row) + col) =
-          make_uint2(pack_bf16x2(acc.x * f, acc.y * f), pack_bf16x2(acc.z * f, acc.w * f));
-    } else {
-      // (this thread alone reads and writes these columns)
-      uint8_t* dst = slot(0);
-      reinterpret_cast<float4*>(dst)[x] = acc;
-      if (col == 0) reinterpret_cast<float2*>(dst + R * D * 4)[row] = make_float2(mm, ll);
+#pragma unroll
+    for (int y = 0; y < kVectors; ++y) {
+      const int x = x0 + y * kThreads, col = x % (D / 4) * 4;
+      if (x >= all) continue;
+      if (final) {
+        const float f = ll[y] > 0.f ? p.v_unit / ll[y] : 0.f;
+        *reinterpret_cast<uint2*>(out_row<D>(p, at, row[y]) + col) =
+            make_uint2(pack_bf16x2(acc[y].x * f, acc[y].y * f), pack_bf16x2(acc[y].z * f, acc[y].w * f));
+      } else {
+        // (this thread alone reads and writes these columns)
+        uint8_t* dst = slot(0);
+        reinterpret_cast<float4*>(dst)[x] = acc[y];
+        if (col == 0) reinterpret_cast<float2*>(dst + R * D * 4)[row[y]] = make_float2(mm[y], ll[y]);
+      }
     }
   }
 }
@@ -865,8 +895,8 @@ __global__ void __launch_bounds__(kThreads, NCfg<D, NT>::kCtas) sdpa_paged4_few(
           __syncthreads();
           if (tid == 0) {
             last_one = static_cast<int>(atomicAdd(count, 1ull) & 0xffff) + 1 == all;
-            if (last_one) *count = 0;
             __threadfence();
+            if (last_one) *count = 0;
           }
           __syncthreads();
           return last_one != 0;

@@ -10,8 +10,8 @@
 // is published as fp32 (O, m, l), and the run that publishes the last piece merges
 // them in the order of their keys: results repeat bit by bit, no run waits for another.
 //
-// Roles: four warps expand K and V, codes and scales to fp16 (exact), into shared
-// memory as the tensor core's swizzled operands; one issues the products
+// Roles: two warps copy K's and V's pages as they are held; four expand codes and
+// scales to fp16 (exact) into the tensor core's swizzled operands; one issues the products
 // (tcgen05.mma, kind::f16: S = Q K^T into tensor memory, O += P V with P from
 // there); four for each 128 rows do the softmax, a row a thread; one works out the
 // units.  Queries are scaled by a power of two for each row to fit fp16, the softmax
@@ -30,12 +30,10 @@
 namespace sdpa {
 namespace {
 
-constexpr int kBN = 64;                    // keys of a tile
-constexpr int kBNShift = 6;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units, as in the other forward kernels
 // What a unit costs beside its keys (loading Q, storing O), in keys.
 constexpr int kStartKeys = 512;
-constexpr int kMinRunTiles = 8;            // key tiles of a run, at least
+constexpr int kMinRunKeys = 512;           // of a run, at least
 
 // ------------------------------------------------------------------ schedule
 struct Seq {
@@ -45,8 +43,9 @@ struct Seq {
 // Items are keys x group.  A unit is start items and then those of the keys that its
 // last row sees, were the tile full: group (len - n) + (r + 1) R, or what a window
 // holds of them.  So the sum over row tiles has a closed form.
-template <int R>
+template <int R, int kBNShift>
 struct Plan {
+  static constexpr int kBN = 1 << kBNShift;                  // keys of a tile
   const Paged4Params& p;
   __device__ explicit Plan(const Paged4Params& params) : p(params) {}
   __device__ __forceinline__ Seq seq(int s) const {
@@ -95,6 +94,11 @@ struct Unit {
   int first_pos, hi_pos;                   // positions of the first and the last row
   int first_row, rows;                     // of the sequence's rows for this head (no rows: no further unit)
   bool zeros;                              // nothing to see, and this run's
+  // which key tile the piece's tile i is
+  __device__ __forceinline__ int tile(int i) const {
+    const int kt = kt0 + i;
+    return kt < tiles.head ? kt : kt + tiles.first - tiles.head;
+  }
 };
 
 // The runs: [begin(c), begin(c + 1)) of all items.
@@ -108,9 +112,10 @@ struct Cut {
   }
 };
 
-template <int R>
-__device__ void set_piece(const Plan<R>& plan, const Cut& cut, int c, Unit* u) {
+template <int R, int S>
+__device__ void set_piece(const Plan<R, S>& plan, const Cut& cut, int c, Unit* u) {
   const Paged4Params& p = plan.p;
+  constexpr int kBN = 1 << S;
   const Seq& q = u->q;
   const long long rows = 1ll * q.n * p.group, row0 = 1ll * u->r * R;
   u->first_row = static_cast<int>(row0);
@@ -120,10 +125,10 @@ __device__ void set_piece(const Plan<R>& plan, const Cut& cut, int c, Unit* u) {
   Tiles t{0, 0, 0};
   if (u->hi_pos >= 0) {
     if (p.window < INT_MAX) {
-      t.first = max(max(u->first_pos, 0) - p.window + 1, 0) >> kBNShift;
-      t.head = min((min(p.sinks, u->hi_pos + 1) + kBN - 1) >> kBNShift, t.first);
+      t.first = max(max(u->first_pos, 0) - p.window + 1, 0) >> S;
+      t.head = min((min(p.sinks, u->hi_pos + 1) + kBN - 1) >> S, t.first);
     }
-    t.count = t.head + (u->hi_pos >> kBNShift) - t.first + 1;
+    t.count = t.head + (u->hi_pos >> S) - t.first + 1;
   }
   u->tiles = t;
   // Key tiles before item y of the unit, in proportion; all of them at once where a tile
@@ -157,8 +162,8 @@ struct Schedule {
 
 // The whole block: the cut, and the unit in which run c begins.  Returns false
 // when there is no such run.
-template <int R>
-__device__ bool find_place(const Plan<R>& plan, Schedule* sh, Unit* first, int c) {
+template <int R, int S>
+__device__ bool find_place(const Plan<R, S>& plan, Schedule* sh, Unit* first, int c) {
   const Paged4Params& p = plan.p;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, threads = blockDim.x;
   const int per = (p.b + threads - 1) / threads;
@@ -184,7 +189,7 @@ __device__ bool find_place(const Plan<R>& plan, Schedule* sh, Unit* first, int c
   }
   if (all == 0) return false;
   Cut cut;
-  const long long least = 1ll * kMinRunTiles * kBN * p.group;
+  const long long least = 1ll * kMinRunKeys * p.group;
   cut.runs = static_cast<int>(min(static_cast<long long>(p.runs), max(1ll, all / least)));
   cut.each = all / cut.runs;
   cut.over = static_cast<int>(all - cut.each * cut.runs);
@@ -222,8 +227,8 @@ __device__ bool find_place(const Plan<R>& plan, Schedule* sh, Unit* first, int c
 }
 
 // One thread: the unit after *u, false if there is none of run c's.
-template <int R>
-__device__ __forceinline__ bool next_unit(const Plan<R>& plan, const Cut& cut, int c, Unit* u) {
+template <int R, int S>
+__device__ __forceinline__ bool next_unit(const Plan<R, S>& plan, const Cut& cut, int c, Unit* u) {
   u->begin += plan.cost(u->q, u->r);
   if (u->begin >= cut.begin(c + 1)) return false;
   if (++u->r == u->q.tiles) {
@@ -263,6 +268,14 @@ __device__ __forceinline__ uint4 expand8(uint32_t w, uint32_t scale2) {
   for (int i = 0; i < 4; ++i) asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(r[i]) : "r"(scale2));
   return make_uint4(r[0], r[1], r[2], r[3]);
 }
+// Copies 16 bytes, or zeros.
+__device__ __forceinline__ void cp_async16_or_zeros(uint32_t dst, const uint8_t* src, bool get) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(get ? 16 : 0) : "memory");
+}
+// This thread's arrival on `bar` once the copies that it has asked for are done.
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
 // Instruction descriptor, kind::f16: fp16 A and B (formats 0), fp32 D.
 constexpr uint32_t idesc_f16(int M, int N, bool b_mn_major) {
   return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | ((static_cast<uint32_t>(N) >> 3) << 17) |
@@ -273,6 +286,12 @@ __device__ __forceinline__ float weight(float m, float sub) { return ex2_approx(
 template <int D>
 struct WCfg {
   static constexpr int kSub = D <= 128 ? 2 : 1;              // 128 rows each
+  // Keys of a tile and score buffers: with two times 128 rows one's softmax runs beside
+  // the other's products, and a tile of 128 keys costs the tensor core 2048 clock cycles
+  // (d = 128) where two of 64 cost 2560, as a product of 64 columns is bound by reading A.
+  static constexpr int kBNShift = kSub == 2 ? 7 : 6, kBN = 1 << kBNShift, kBufs = kSub == 2 ? 1 : 2;
+  // P is handed over in parts, O += P V of the first beginning while the others are worked out
+  static constexpr int kParts = kSub == 2 ? 4 : 1, kPartKeys = kBN / kParts;
   static constexpr int kRows = 128 * kSub;
   static constexpr int kSoftmaxWarps = 4 * kSub;
   static constexpr int kExpandWarp = kSoftmaxWarps;          // the first of four
@@ -290,20 +309,25 @@ struct WCfg {
   static constexpr int kKVBytes = kBN * D * 2;               // a tile of K or of V
   // a tile lies as [8 rows][column block][row of the eight]
   static constexpr int kGroupBytes = kBoxes * kSBO;
-  static constexpr int kRing = D <= 64 ? 4 : (D == 128 ? 3 : 2);
+  static constexpr int kRing = D <= 64 ? 3 : 2;
   static constexpr int kKOff = kSub * kQBytes;
   static constexpr int kVOff = kKOff + kRing * kKVBytes;
-  static constexpr int kTurnOff = kVOff + kRing * kKVBytes;  // rows on their way to the output
+  // A tile as it is held, on its way to be expanded: K's codes and scales, V's
+  static constexpr int kCodes = kBN * D / 2, kScales = kBN * D / 16;
+  static constexpr int kRawOff = kVOff + kRing * kKVBytes;
+  static constexpr int kRawHalf = kCodes + kScales;
+  static constexpr int kBarOff = kRawOff + 2 * kRawHalf;
+  // rows on their way to the output lie over Q, where they fit
   static constexpr int kTurnRow = 64 + 16;
   static constexpr int kTurnSlot = 32 * kTurnRow;
-  static constexpr int kBarOff = kTurnOff + kSoftmaxWarps * kTurnSlot;
-  // q_full, o_full, o_last, o_free [2]; s_full, p_full [2][2]; k_full, v_full, k_empty, v_empty [R];
-  // ready, done [2]; meet, drain
-  static constexpr int kNumBars = 8 + 8 + 4 * kRing + 4 + 2;
+  static constexpr bool kTurns = 4 * kTurnSlot <= kQBytes;
+  // q_full, o_full, o_last, o_free, s_full [2]; p_full [2][4]; k_full, v_full, k_empty, v_empty [R];
+  // ready, done [2]; meet, drain; raw_full, raw_empty [2]
+  static constexpr int kNumBars = 10 + 8 + 4 * kRing + 4 + 2 + 4;
   static constexpr int kSmemBytes = kBarOff + kNumBars * 8 + 16 + 1024;
   static constexpr int kOChunk = D < 32 ? D : 32;
-  static constexpr uint32_t kSubCols = 2 * kBN + (D < 32 ? 32 : D);
-  static constexpr uint32_t kOCol = 2 * kBN;
+  static constexpr uint32_t kSubCols = 128 + (D < 32 ? 32 : D);
+  static constexpr uint32_t kOCol = 128;
   static constexpr uint32_t kTmemCols = 512;
   static_assert(kSub * kSubCols <= kTmemCols, "tensor memory");
   static_assert(kSmemBytes <= 232448 - 1024, "shared memory");
@@ -313,14 +337,124 @@ struct WCfg {
   static constexpr uint32_t kDescHi = (kSBO >> 4) | (1u << 14) | (kLayout << 29);
   static constexpr uint32_t kDescHiKV = (kGroupBytes >> 4) | (1u << 14) | (kLayout << 29);
   // registers a thread: the launch's 128 (kSub == 2) are split
-  static constexpr int kSoftmaxRegs = 160, kExpandRegs = 96, kRestRegs = 96;
+  static constexpr int kSoftmaxRegs = 176, kExpandRegs = 96, kRestRegs = 64;
   static_assert(kSub == 1 || 2 * kSoftmaxRegs + kExpandRegs + kRestRegs <= 512, "registers");
 };
+
+// The slot of piece i of a unit.  A run has two: for the unit in which it ends, and
+// for the one in which it begins.
+__device__ __forceinline__ int slot_of(const Unit& at, int i) { return 2 * (at.first_run + i) + (i == 0 ? 1 : 0); }
+
+// O columns [c kOChunk, + kOChunk) of a warp's rows (`rows` of the 32), a lane for each,
+// times f into the output: turned through shared memory, four lanes write 64 bytes of a row.
+template <int D>
+__device__ __forceinline__ void store_rows(uint8_t* turn, uint16_t* out, int rows, int c,
+                                           const uint32_t (&o)[WCfg<D>::kOChunk], float f) {
+  using C = WCfg<D>;
+  const int lane = threadIdx.x & 31;
+  if constexpr (!C::kTurns) {
+    if (lane < rows)
+      for (int e = 0; e < C::kOChunk / 2; ++e)
+        reinterpret_cast<uint32_t*>(out)[c * (C::kOChunk / 2) + e] =
+            pack_bf16x2(__uint_as_float(o[2 * e]) * f, __uint_as_float(o[2 * e + 1]) * f);
+  } else {
+    uint4* mine = reinterpret_cast<uint4*>(turn + lane * C::kTurnRow);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      mine[e] = make_uint4(pack_bf16x2(__uint_as_float(o[e * 8 + 0]) * f, __uint_as_float(o[e * 8 + 1]) * f),
+                           pack_bf16x2(__uint_as_float(o[e * 8 + 2]) * f, __uint_as_float(o[e * 8 + 3]) * f),
+                           pack_bf16x2(__uint_as_float(o[e * 8 + 4]) * f, __uint_as_float(o[e * 8 + 5]) * f),
+                           pack_bf16x2(__uint_as_float(o[e * 8 + 6]) * f, __uint_as_float(o[e * 8 + 7]) * f));
+    __syncwarp();
+#pragma unroll
+    for (int y = 0; y < 4; ++y) {
+      const int x = (lane >> 2) + 8 * y;                     // row of this warp (its lane knows where it goes)
+      const long long at_out = __shfl_sync(0xffffffffu, reinterpret_cast<long long>(out), x);
+      const uint4 v = *reinterpret_cast<const uint4*>(turn + x * C::kTurnRow + (lane & 3) * 16);
+      if (x < rows) *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(at_out) + c * 32 + (lane & 3) * 8) = v;
+    }
+    __syncwarp();
+  }
+}
+
+// A warp's rows of all pieces of a unit, in their order, into the output: a lane for
+// each row, the next piece's columns under way while one's are summed.  (A function
+// of its own, or its registers cost the loop over the keys some.)
+template <int D>
+__device__ __noinline__ void merge_rows(const Paged4Params& p, const Unit& at, uint8_t* turn, uint16_t* out, int rows,
+                                        int row) {
+  using C = WCfg<D>;
+  constexpr int kVec = C::kOChunk / 4;
+  const int of = at.of, steps = D / C::kOChunk * of;
+  const int rw = min(row, at.rows - 1);
+  auto slot = [&](int i) { return p.slots + static_cast<long long>(slot_of(at, i)) * p.slot_bytes; };
+  auto ml_of = [&](int i) { return __ldcg(reinterpret_cast<const float2*>(slot(i) + C::kRows * D * 4) + rw); };
+  float4 acc[kVec], v[2][kVec];
+  float2 ml[2];
+  auto fetch = [&](int c, int i, float4 (&x)[kVec], float2& m) {
+    m = ml_of(i);
+    const float4* src = reinterpret_cast<const float4*>(slot(i)) + rw;
+#pragma unroll
+    for (int e = 0; e < kVec; ++e) x[e] = __ldcg(src + (c * kVec + e) * C::kRows);
+  };
+  int fc = 0, fi = 0;                                        // of the step that is asked for
+  auto next = [&]() {
+    if (++fi == of) {
+      fi = 0;
+      ++fc;
+    }
+  };
+  fetch(fc, fi, v[0], ml[0]);
+  next();
+  float mm = -INFINITY, sum = 0.f;
+#pragma unroll 4
+  for (int i = 0; i < of; ++i) mm = fmaxf(mm, ml_of(i).x);
+  const float base = mm == -INFINITY ? 0.f : mm;
+#pragma unroll 4
+  for (int i = 0; i < of; ++i) {
+    const float2 one = ml_of(i);
+    sum = fmaf(one.y, weight(one.x, base), sum);
+  }
+  const float f = sum > 0.f ? p.v_unit / sum : 0.f;
+  int c = 0, i = 0;                                          // of the step that is summed
+  auto sum_up = [&](const float4 (&x)[kVec], const float2& m) {
+    const float g = weight(m.x, base);
+#pragma unroll
+    for (int e = 0; e < kVec; ++e) {
+      if (i == 0) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+      acc[e].x = fmaf(x[e].x, g, acc[e].x);
+      acc[e].y = fmaf(x[e].y, g, acc[e].y);
+      acc[e].z = fmaf(x[e].z, g, acc[e].z);
+      acc[e].w = fmaf(x[e].w, g, acc[e].w);
+    }
+    if (++i < of) return;
+    uint32_t o[C::kOChunk];
+#pragma unroll
+    for (int e = 0; e < kVec; ++e) {
+      o[4 * e] = __float_as_uint(acc[e].x);
+      o[4 * e + 1] = __float_as_uint(acc[e].y);
+      o[4 * e + 2] = __float_as_uint(acc[e].z);
+      o[4 * e + 3] = __float_as_uint(acc[e].w);
+    }
+    store_rows<D>(turn, out, rows, c, o, f);
+    i = 0;
+    ++c;
+  };
+#pragma unroll 1
+  for (int x = 0; x < steps; x += 2) {
+    if (x + 1 < steps) fetch(fc, fi, v[1], ml[1]);
+    next();
+    sum_up(v[0], ml[0]);
+    if (x + 2 < steps) fetch(fc, fi, v[0], ml[0]);
+    next();
+    if (x + 1 < steps) sum_up(v[1], ml[1]);
+  }
+}
 
 template <int D>
 __global__ void __launch_bounds__(WCfg<D>::kThreads, 1) sdpa_paged4_many(const __grid_constant__ Paged4Params p) {
   using C = WCfg<D>;
-  constexpr int R = C::kRing;
+  constexpr int R = C::kRing, kBN = C::kBN, kBNShift = C::kBNShift;
   extern __shared__ uint8_t smem_raw[];
   __shared__ Schedule sched;
   __shared__ Unit units[2];
@@ -332,9 +466,9 @@ __global__ void __launch_bounds__(WCfg<D>::kThreads, 1) sdpa_paged4_many(const _
   uint64_t* o_full = q_full + 2;
   uint64_t* o_last = o_full + 2;           // once a piece, after its last O += P V
   uint64_t* o_free = o_last + 2;           // once a piece, when the softmax warps have read O
-  uint64_t* s_full = o_free + 2;           // [sub][buffer]
-  uint64_t* p_full = s_full + 4;
-  uint64_t* k_full = p_full + 4;
+  uint64_t* s_full = o_free + 2;           // [sub], or [buffer]
+  uint64_t* p_full = s_full + 2;           // [sub][part], or [buffer]
+  uint64_t* k_full = p_full + 8;
   uint64_t* v_full = k_full + R;
   uint64_t* k_empty = v_full + R;
   uint64_t* v_empty = k_empty + R;
@@ -342,7 +476,9 @@ __global__ void __launch_bounds__(WCfg<D>::kThreads, 1) sdpa_paged4_many(const _
   uint64_t* done = ready + 2;
   uint64_t* meet_bar = done + 2;
   uint64_t* drain = meet_bar + 1;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  uint64_t* raw_full = drain + 1;          // K, V
+  uint64_t* raw_empty = raw_full + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(raw_empty + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const AbortState ab{abort_flag, p.status};
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -354,17 +490,19 @@ __global__ void __launch_bounds__(WCfg<D>::kThreads, 1) sdpa_paged4_many(const _
       mbar_init(o_last + i, 1);
       mbar_init(o_free + i, 128);
       mbar_init(ready + i, 1);
-      mbar_init(done + i, C::kSoftmaxWarps + 4 + 1);
+      mbar_init(done + i, C::kSoftmaxWarps + 4 + 1 + 2);
     }
-    for (int i = 0; i < 4; ++i) {
-      mbar_init(s_full + i, 1);
-      mbar_init(p_full + i, 128);
-    }
+    for (int i = 0; i < 2; ++i) mbar_init(s_full + i, 1);
+    for (int i = 0; i < 8; ++i) mbar_init(p_full + i, 128);
     for (int i = 0; i < R; ++i) {
       mbar_init(k_full + i, 128);
       mbar_init(v_full + i, 128);
       mbar_init(k_empty + i, 1);
       mbar_init(v_empty + i, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(raw_full + i, 32);
+      mbar_init(raw_empty + i, 4);
     }
     mbar_init(meet_bar, C::kSoftmaxWarps);
     mbar_init(drain, 1);
@@ -380,9 +518,9 @@ __global__ void __launch_bounds__(WCfg<D>::kThreads, 1) sdpa_paged4_many(const _
   // The kernel before is the one for the other sequences: it began when the one before
   // it was over, and is waited for at the end only.
 
-  const Plan<C::kRows> plan(p);
+  const Plan<C::kRows, kBNShift> plan(p);
   const int cta = static_cast<int>(blockIdx.x);
-  const bool any = find_place<C::kRows>(plan, &sched, &units[0], cta) && units[0].begin != LLONG_MAX;
+  const bool any = find_place(plan, &sched, &units[0], cta) && units[0].begin != LLONG_MAX;
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
@@ -393,7 +531,6 @@ __global__ void __launch_bounds__(WCfg<D>::kThreads, 1) sdpa_paged4_many(const _
     const int row = sub * 128 + quarter * 32 + lane;         // of the row tile
     const uint32_t lane_base = tmem + sub * C::kSubCols + (static_cast<uint32_t>(quarter * 32) << 16);
     const bool windowed = p.window < INT_MAX;
-    auto slot = [&](int i) { return p.slots + static_cast<long long>(i) * p.slot_bytes; };
     auto open_count = [&](unsigned long long* count) {       // (see the few-rows kernel)
       unsigned long long old = 0, seen;
       while ((seen = atomicCAS(count, old, p.call)) != old && (seen & ~0xffffull) != p.call) old = seen;
@@ -427,8 +564,9 @@ __global__ void __launch_bounds__(WCfg<D>::kThreads, 1) sdpa_paged4_many(const _
         if (active) {
           // ---- Q: this row, scaled by a power of two, as fp16 (its last scores are done with the one before)
           const uint4* src = reinterpret_cast<const uint4*>(p.q + static_cast<long long>(at.q.start + token) * p.q_stride + head * D);
+          // (twice, eight loads at a time: the second time from L1)
           uint32_t top = 0;
-#pragma unroll 4
+#pragma unroll 8
           for (int c = 0; c < D / 8; ++c) {
             const uint4 v = valid ? src[c] : make_uint4(0, 0, 0, 0);
             const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -459,23 +597,24 @@ __global__ void __launch_bounds__(WCfg<D>::kThreads, 1) sdpa_paged4_many(const _
           const float2 sc2 = make_float2(sc, sc);
           // ---- key tiles
           for (int i = 0; i < n; ++i, ++u) {
-            const int buf = u & 1;
+            // (two buffers: tile u's phases come every second tile)
+            const int buf = C::kBufs == 2 ? u & 1 : 0;
+            const uint32_t phase = static_cast<uint32_t>(C::kBufs == 2 ? u >> 1 : u) & 1u;
             const uint32_t s_col = static_cast<uint32_t>(buf * kBN);
-            int key0 = at.kt0 + i;
-            if (key0 >= at.tiles.head) key0 += at.tiles.first - at.tiles.head;
-            key0 <<= kBNShift;
-            ok = mbar_wait_warp(s_full + sub * 2 + buf, static_cast<uint32_t>(u >> 1) & 1u, ab);
+            uint64_t* p_bar = p_full + (C::kBufs == 2 ? buf : sub * C::kParts);
+            const int key0 = at.tile(i) << kBNShift;
+            ok = mbar_wait_warp(s_full + (C::kBufs == 2 ? buf : sub), phase, ab);
             if (!ok) break;
             tc_fence_after();
             if (busy) {
               float s[kBN];
               {
-                uint32_t sr[2][32];
-                tmem_ld32(lane_base + s_col, sr[0]);
-                tmem_ld32(lane_base + s_col + 32, sr[1]);
+                uint32_t sr[kBN / 32][32];
+#pragma unroll
+                for (int c = 0; c < kBN / 32; ++c) tmem_ld32(lane_base + s_col + c * 32, sr[c]);
                 tmem_ld_wait();
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
+                for (int c = 0; c < kBN / 32; ++c) {
                   reg_fence(sr[c]);
 #pragma unroll
                   for (int e = 0; e < 32; ++e) s[c * 32 + e] = __uint_as_float(sr[c][e]);
@@ -488,14 +627,14 @@ __global__ void __launch_bounds__(WCfg<D>::kThreads, 1) sdpa_paged4_many(const _
                 for (int c = 0; c < kBN; ++c)
                   if (c > hi_c || (c <= lo_c && c >= sink_c)) s[c] = -INFINITY;
               }
-              float mx4[4];
+              float mx8[8];
 #pragma unroll
-              for (int x = 0; x < 4; ++x) mx4[x] = s[x];
+              for (int x = 0; x < 8; ++x) mx8[x] = s[x];
 #pragma unroll
-              for (int c = 4; c < kBN; c += 8)
+              for (int c = 8; c < kBN; c += 16)
 #pragma unroll
-                for (int x = 0; x < 4; ++x) mx4[x] = fmax3(mx4[x], s[c + x], c + 4 + x < kBN ? s[c + 4 + x] : s[c + x]);
-              const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
+                for (int x = 0; x < 8; ++x) mx8[x] = fmax3(mx8[x], s[c + x], c + 8 + x < kBN ? s[c + 8 + x] : s[c + x]);
+              const float mx = fmax3(fmax3(mx8[0], mx8[1], mx8[2]), fmax3(mx8[3], mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7]));
               // the running maximum moves when it grew by more than the threshold
               const float m_new = fmaxf(m_used, mx * sc);
               float alpha = 1.f;
@@ -510,12 +649,25 @@ __global__ void __launch_bounds__(WCfg<D>::kThreads, 1) sdpa_paged4_many(const _
                   m_used = m_new;
                   l *= alpha;
                 }
-                if (rescale) {
-                  // (until O += P V of the tile before is done: of the one before that it is, its
-                  // product was issued before these scores', and the next needs this tile's P)
-                  ok = mbar_wait_warp(o_full + sub, static_cast<uint32_t>(u - 1) & 1u, ab);
+              }
+              if (rescale) {
+                // With one buffer these scores were issued behind O += P V of the tile before, which
+                // is done then; with two it is waited for (of the one before that it is done, and
+                // the next needs this tile's P).
+                if constexpr (C::kBufs == 2) {
+                  ok = mbar_wait_warp(o_full, static_cast<uint32_t>(u - 1) & 1u, ab);
                   if (!ok) break;
                   tc_fence_after();
+                }
+#pragma unroll 1
+                for (int c = 0; c < D / 16; ++c) {           // (rare)
+                  uint32_t o[16];
+                  tmem_ld_chunk(lane_base + C::kOCol + c * 16, o);
+                  tmem_ld_wait();
+                  reg_fence(o);
+#pragma unroll
+                  for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                  tmem_st_chunk(lane_base + C::kOCol + c * 16, o);
                 }
               }
               const float m_sub = m_used == -INFINITY ? 0.f : m_used;
@@ -523,33 +675,32 @@ __global__ void __launch_bounds__(WCfg<D>::kThreads, 1) sdpa_paged4_many(const _
               float2 acc[4];
 #pragma unroll
               for (int x = 0; x < 4; ++x) acc[x] = make_float2(0.f, 0.f);
-              uint32_t pk[kBN / 2];
 #pragma unroll
-              for (int e = 0; e < kBN / 2; ++e) {
-                const float2 x = __ffma2_rn(make_float2(s[2 * e], s[2 * e + 1]), sc2, neg2);
-                const float2 pe = make_float2(ex2_approx(x.x), ex2_approx(x.y));
-                acc[e & 3] = __fadd2_rn(acc[e & 3], pe);
-                pk[e] = pack_f16x2(pe.x, pe.y);
-              }
-              tmem_st32(lane_base + s_col, pk);
-              const float2 a = __fadd2_rn(__fadd2_rn(acc[0], acc[1]), __fadd2_rn(acc[2], acc[3]));
-              if (rescale) {
+              for (int y = 0; y < C::kParts; ++y) {
+                uint32_t pk[C::kPartKeys / 2];
 #pragma unroll
-                for (int c = 0; c < D / C::kOChunk; ++c) {
-                  uint32_t o[C::kOChunk];
-                  tmem_ld_chunk(lane_base + C::kOCol + c * C::kOChunk, o);
-                  tmem_ld_wait();
-                  reg_fence(o);
-#pragma unroll
-                  for (int e = 0; e < C::kOChunk; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-                  tmem_st_chunk(lane_base + C::kOCol + c * C::kOChunk, o);
+                for (int e = 0; e < C::kPartKeys / 2; ++e) {
+                  const int c = y * C::kPartKeys + 2 * e;
+                  const float2 x = __ffma2_rn(make_float2(s[c], s[c + 1]), sc2, neg2);
+                  const float2 pe = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+                  acc[e & 3] = __fadd2_rn(acc[e & 3], pe);
+                  pk[e] = pack_f16x2(pe.x, pe.y);
+                }
+                tmem_st_chunk(lane_base + s_col + y * (C::kPartKeys / 2), pk);
+                if (y + 1 < C::kParts) {
+                  tmem_st_wait();
+                  tc_fence_before();
+                  mbar_arrive(p_bar + y);
                 }
               }
+              const float2 a = __fadd2_rn(__fadd2_rn(acc[0], acc[1]), __fadd2_rn(acc[2], acc[3]));
               l += a.x + a.y;
               tmem_st_wait();
+            } else {
+              for (int y = 0; y + 1 < C::kParts; ++y) mbar_arrive(p_bar + y);
             }
             tc_fence_before();
-            mbar_arrive(p_full + sub * 2 + buf);
+            mbar_arrive(p_bar + C::kParts - 1);
           }
           if (!ok) break;
           // (a barrier of its own: o_full may still be two tiles behind)
@@ -559,8 +710,7 @@ __global__ void __launch_bounds__(WCfg<D>::kThreads, 1) sdpa_paged4_many(const _
         }
         // ---- the piece's end.  Slots: O as [D / 4][rows] vectors of four columns, (m, l) as [rows].
         const bool whole = at.of == 1;
-        auto place = [&](int i) { return 2 * (at.first_run + i) + (i == 0 ? 1 : 0); };   // of piece i
-        uint8_t* own = slot(whole ? 0 : place(cta - at.first_run));
+        uint8_t* own = p.slots + static_cast<long long>(whole ? 0 : slot_of(at, cta - at.first_run)) * p.slot_bytes;
         float ll = l;
         // O columns [c kOChunk, + kOChunk) of this row
         auto load_o = [&](int c, uint32_t (&o)[C::kOChunk]) {
@@ -569,36 +719,8 @@ __global__ void __launch_bounds__(WCfg<D>::kThreads, 1) sdpa_paged4_many(const _
           tmem_ld_wait();
           reg_fence(o);
         };
-        // ... normalised into the output: four lanes write 64 bytes of a row
-        auto store_out = [&](int c, const uint32_t (&o)[C::kOChunk], float f) {
-          if constexpr (D < 32) {
-            if (valid)
-              for (int e = 0; e < C::kOChunk / 2; ++e)
-                reinterpret_cast<uint32_t*>(out)[c * (C::kOChunk / 2) + e] =
-                    pack_bf16x2(__uint_as_float(o[2 * e]) * f, __uint_as_float(o[2 * e + 1]) * f);
-          } else {
-            uint8_t* turn = smem + C::kTurnOff + warp * C::kTurnSlot;
-            uint4* mine = reinterpret_cast<uint4*>(turn + lane * C::kTurnRow);
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              mine[e] = make_uint4(
-                  pack_bf16x2(__uint_as_float(o[e * 8 + 0]) * f, __uint_as_float(o[e * 8 + 1]) * f),
-                  pack_bf16x2(__uint_as_float(o[e * 8 + 2]) * f, __uint_as_float(o[e * 8 + 3]) * f),
-                  pack_bf16x2(__uint_as_float(o[e * 8 + 4]) * f, __uint_as_float(o[e * 8 + 5]) * f),
-                  pack_bf16x2(__uint_as_float(o[e * 8 + 6]) * f, __uint_as_float(o[e * 8 + 7]) * f));
-            __syncwarp();
-#pragma unroll
-            for (int y = 0; y < 4; ++y) {
-              const int x = (lane >> 2) + 8 * y;             // row of this warp
-              // (its output row: the lane that holds it knows)
-              const long long at_out = __shfl_sync(0xffffffffu, reinterpret_cast<long long>(out), x);
-              const uint4 v = *reinterpret_cast<const uint4*>(turn + x * C::kTurnRow + (lane & 3) * 16);
-              if (sub * 128 + quarter * 32 + x < rows)
-                *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(at_out) + c * 32 + (lane & 3) * 8) = v;
-            }
-            __syncwarp();
-          }
-        };
+        uint8_t* turn = smem + sub * C::kQBytes + quarter * C::kTurnSlot;   // (the products are done with Q)
+        const int rows_here = rows - (sub * 128 + quarter * 32);
         if (busy && active) {
           const float f = ll > 0.f ? p.v_unit / ll : 0.f;
 #pragma unroll 1
@@ -606,7 +728,7 @@ __global__ void __launch_bounds__(WCfg<D>::kThreads, 1) sdpa_paged4_many(const _
             uint32_t o[C::kOChunk];
             load_o(c, o);
             if (whole) {
-              store_out(c, o, f);
+              store_rows<D>(turn, out, rows_here, c, o, f);
             } else if (valid) {
               float4* dst = reinterpret_cast<float4*>(own) + row;
 #pragma unroll
@@ -623,7 +745,7 @@ __global__ void __launch_bounds__(WCfg<D>::kThreads, 1) sdpa_paged4_many(const _
           mbar_arrive(o_free + sub);
         }
         if (!whole) {
-          unsigned long long* count = p.counts + place(0);
+          unsigned long long* count = p.counts + slot_of(at, 0);
           __threadfence();
           if (!(ok = meet())) break;
           if (tid == 0) {
@@ -633,55 +755,7 @@ __global__ void __launch_bounds__(WCfg<D>::kThreads, 1) sdpa_paged4_many(const _
             __threadfence();
           }
           if (!(ok = meet())) break;
-          if (last_one != 0 && busy) {
-            // this row of all pieces, in their order
-            const int of = at.of;
-            const int rw = valid ? row : rows - 1;
-            auto ml_of = [&](int i) {
-              return __ldcg(reinterpret_cast<const float2*>(slot(place(i)) + C::kRows * D * 4) + rw);
-            };
-            float mm = -INFINITY, sum = 0.f;
-#pragma unroll 4
-            for (int i = 0; i < of; ++i) mm = fmaxf(mm, ml_of(i).x);
-            const float base = mm == -INFINITY ? 0.f : mm;
-#pragma unroll 4
-            for (int i = 0; i < of; ++i) {
-              const float2 one = ml_of(i);
-              sum = fmaf(one.y, weight(one.x, base), sum);
-            }
-            const float f = sum > 0.f ? p.v_unit / sum : 0.f;
-#pragma unroll 1
-            for (int c = 0; c < D / C::kOChunk; ++c) {
-              constexpr int kVec = C::kOChunk / 4;
-              float4 acc[kVec];
-#pragma unroll
-              for (int e = 0; e < kVec; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
-              for (int i = 0; i < of; ++i) {
-                const float4* src = reinterpret_cast<const float4*>(slot(place(i))) + rw;
-                float4 v[kVec];
-#pragma unroll
-                for (int e = 0; e < kVec; ++e) v[e] = __ldcg(src + (c * kVec + e) * C::kRows);
-                const float g = weight(ml_of(i).x, base);
-#pragma unroll
-                for (int e = 0; e < kVec; ++e) {
-                  acc[e].x = fmaf(v[e].x, g, acc[e].x);
-                  acc[e].y = fmaf(v[e].y, g, acc[e].y);
-                  acc[e].z = fmaf(v[e].z, g, acc[e].z);
-                  acc[e].w = fmaf(v[e].w, g, acc[e].w);
-                }
-              }
-              uint32_t o[C::kOChunk];
-#pragma unroll
-              for (int e = 0; e < kVec; ++e) {
-                o[4 * e] = __float_as_uint(acc[e].x);
-                o[4 * e + 1] = __float_as_uint(acc[e].y);
-                o[4 * e + 2] = __float_as_uint(acc[e].z);
-                o[4 * e + 3] = __float_as_uint(acc[e].w);
-              }
-              store_out(c, o, f);
-            }
-          }
+          if (last_one != 0 && busy) merge_rows<D>(p, at, turn, out, rows_here, row);
           // (last_one has been read)
           if (!(ok = meet())) break;
         }
@@ -692,16 +766,18 @@ __global__ void __launch_bounds__(WCfg<D>::kThreads, 1) sdpa_paged4_many(const _
   } else if (any && warp < C::kMmaWarp) {
     // -------------------------------------------------------------- expand
     if constexpr (C::kSub == 2) regs_decrease<C::kExpandRegs>();
+    // (Loops are short for the instruction cache's sake, which all roles share: with two
+    // tiles' loads and products unrolled every role waited for instructions, and 4 chunks of
+    // 512 tokens behind 7680 positions took 250 us instead of @@.)
     const int tid_e = tid - C::kExpandWarp * 32;
-    // An item is 32 columns of a row (16 at d = 16): 16 bytes of codes, two scales.
-    constexpr int kCols = D < 32 ? 16 : 32, kPerRow = D / kCols, kAll = kBN * kPerRow;
-    constexpr int kItems = (kAll + 127) / 128;
-    struct Raw {
-      uint4 codes;
-      uint32_t scales;
-    };
-    Raw kr[kItems], vr[kItems];
-    int page[kItems];                                        // of the next tile's items
+    // A thread expands blocks of 16 columns: the same place in every kStep-th row.
+    constexpr int kBlocks = D / 16, kStep = 128 / kBlocks, kTimes = kBN / kStep;
+    static_assert(kStep % 8 == 0 && kBN % kStep == 0, "the swizzle is the same in all of a thread's rows");
+    const int row0 = tid_e / kBlocks, chunk = 2 * (tid_e % kBlocks);
+    constexpr int kRowChunks = C::kRowBytes / 16;
+    const int at_row = (row0 >> 3) * C::kGroupBytes + (chunk / kRowChunks) * C::kSBO;
+    const int dst0 = at_row + swizzle_offset<C::kRowBytes>(row0 & 7, chunk % kRowChunks);
+    const int dst1 = at_row + swizzle_offset<C::kRowBytes>(row0 & 7, chunk % kRowChunks + 1);
     int u = 0;
     bool ok = true;
     for (int k = 0; ok; ++k) {
@@ -709,87 +785,42 @@ __global__ void __launch_bounds__(WCfg<D>::kThreads, 1) sdpa_paged4_many(const _
       if (!ok) break;
       const Unit& at = units[k & 1];
       if (at.rows == 0) break;
-      const int n = at.kt1 - at.kt0, kt0 = at.kt0, head = at.tiles.head, skip = at.tiles.first - head;
-      const int hi_pos = at.hi_pos, hidden = p.window < INT_MAX ? max(at.first_pos, 0) - p.window : -1;
-      const int32_t* pages = p.page_table + static_cast<long long>(at.s) * p.pages_per_seq;
-      const uint8_t *k_head = p.k_pages + at.hk * p.page_bytes, *v_head = p.v_pages + at.hk * p.page_bytes;
-      auto key_of = [&](int i, int j) {
-        const int kt = kt0 + i;
-        return ((kt < head ? kt : kt + skip) << kBNShift) + (tid_e + 128 * j) / kPerRow;
-      };
-      // a position that no row sees is not looked at, and zero
-      auto seen = [&](int key) { return key <= hi_pos && (key > hidden || key < p.sinks); };
-      auto ask = [&](int i) {
-        if (i >= n) return;
-#pragma unroll
-        for (int j = 0; j < kItems; ++j) {
-          const int key = key_of(i, j);
-          page[j] = tid_e + 128 * j < kAll && seen(key) ? pages[key >> p.page_shift] : 0;
-        }
-      };
-      auto load = [&](int i) {
-        if (i >= n) return;
-#pragma unroll
-        for (int j = 0; j < kItems; ++j) {
-          const int key = key_of(i, j), part = (tid_e + 128 * j) % kPerRow;
-          kr[j].codes = vr[j].codes = make_uint4(0, 0, 0, 0);
-          kr[j].scales = vr[j].scales = 0;
-          if (tid_e + 128 * j >= kAll || !seen(key)) continue;
-          if (page[j] < 0 || page[j] >= p.n_pages) {
-            atomicOr(p.status, kStatusBadPage);              // and zeros
-            continue;
+      const int n = at.kt1 - at.kt0, hi_pos = at.hi_pos;
+      const int hidden = p.window < INT_MAX ? max(at.first_pos, 0) - p.window : -1;
+#pragma unroll 1
+      for (int i = 0; i < n && ok; ++i, ++u) {
+        const int st = u % R, key0 = at.tile(i) << kBNShift;
+        const bool edge = key0 + kBN - 1 > hi_pos || key0 <= hidden;
+#pragma unroll 1
+        for (int y = 0; y < 2; ++y) {                        // K, V
+          ok = mbar_wait_warp(raw_full + y, static_cast<uint32_t>(u) & 1u, ab) &&
+               (u < R || mbar_wait_warp((y == 0 ? k_empty : v_empty) + st, static_cast<uint32_t>(u / R - 1) & 1u, ab));
+          if (!ok) break;
+          uint8_t* raw = smem + C::kRawOff + y * C::kRawHalf;
+          uint8_t* scales = raw + C::kCodes + tid_e;
+          if (edge) {
+            // what no row sees may be anything: its scale could be a NaN
+            for (int x = 0; x < kTimes; ++x) {
+              const int key = key0 + row0 + x * kStep;
+              if (key > hi_pos || (key <= hidden && key >= p.sinks)) scales[x * 128] = 0;
+            }
           }
-          const int r = key & ((1 << p.page_shift) - 1);
-          const long long off = page[j] * p.page_stride;
-          const long long codes = off + static_cast<long long>(r) * (D / 2) + part * (kCols / 2);
-          const long long scales = off + (static_cast<long long>(D / 2) << p.page_shift) + r * (D / 16) + part * (kCols / 16);
-          if constexpr (kCols == 32) {
-            kr[j].codes = __ldcg(reinterpret_cast<const uint4*>(k_head + codes));
-            vr[j].codes = __ldcg(reinterpret_cast<const uint4*>(v_head + codes));
-            kr[j].scales = __ldcg(reinterpret_cast<const uint16_t*>(k_head + scales));
-            vr[j].scales = __ldcg(reinterpret_cast<const uint16_t*>(v_head + scales));
-          } else {
-            const uint2 a = __ldcg(reinterpret_cast<const uint2*>(k_head + codes));
-            const uint2 b = __ldcg(reinterpret_cast<const uint2*>(v_head + codes));
-            kr[j].codes = make_uint4(a.x, a.y, 0, 0);
-            vr[j].codes = make_uint4(b.x, b.y, 0, 0);
-            kr[j].scales = __ldcg(k_head + scales);
-            vr[j].scales = __ldcg(v_head + scales);
-          }
-        }
-      };
-      auto store = [&](const Raw (&raw)[kItems], uint8_t* stage) {
+          uint8_t* stage = smem + (y == 0 ? C::kKOff : C::kVOff) + st * C::kKVBytes;
 #pragma unroll
-        for (int j = 0; j < kItems; ++j) {
-          if (tid_e + 128 * j >= kAll) continue;
-          const int row = (tid_e + 128 * j) / kPerRow, part = (tid_e + 128 * j) % kPerRow;
-          const uint32_t w[4] = {raw[j].codes.x, raw[j].codes.y, raw[j].codes.z, raw[j].codes.w};
-          uint8_t* dst = stage + (row >> 3) * C::kGroupBytes;
-#pragma unroll
-          for (int e = 0; e < kCols / 8; ++e) {
-            constexpr int kChunks = C::kRowBytes / 16;
-            const int c = part * (kCols / 8) + e;
-            *reinterpret_cast<uint4*>(dst + (c / kChunks) * C::kSBO + swizzle_offset<C::kRowBytes>(row & 7, c % kChunks)) =
-                expand8(w[e], scale_f16x2(raw[j].scales >> (8 * (e / 2)) & 0xffu));
+          for (int x = 0; x < kTimes; ++x) {
+            const uint2 w = *reinterpret_cast<const uint2*>(raw + tid_e * 8 + x * (128 * 8));
+            const uint32_t sc2 = scale_f16x2(scales[x * 128]);
+            uint8_t* dst = stage + x * (kStep / 8 * C::kGroupBytes);
+            *reinterpret_cast<uint4*>(dst + dst0) = expand8(w.x, sc2);
+            *reinterpret_cast<uint4*>(dst + dst1) = expand8(w.y, sc2);
           }
+          fence_proxy_async_smem();
+          mbar_arrive((y == 0 ? k_full : v_full) + st);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(raw_empty + y);
         }
-        fence_proxy_async_smem();
-      };
-      ask(0);
-      load(0);
-      ask(1);
-      for (int i = 0; i < n; ++i, ++u) {
-        const int st = u % R;
-        const uint32_t phase = static_cast<uint32_t>(u / R - 1) & 1u;
-        if (u >= R && !(ok = mbar_wait_warp(k_empty + st, phase, ab))) break;
-        store(kr, smem + C::kKOff + st * C::kKVBytes);
-        mbar_arrive(k_full + st);
-        if (u >= R && !(ok = mbar_wait_warp(v_empty + st, phase, ab))) break;
-        store(vr, smem + C::kVOff + st * C::kKVBytes);
-        mbar_arrive(v_full + st);
-        load(i + 1);
-        ask(i + 2);
       }
+      if (!ok) break;
       __syncwarp();
       if (lane == 0) mbar_arrive(done + (k & 1));
     }
@@ -798,8 +829,10 @@ __global__ void __launch_bounds__(WCfg<D>::kThreads, 1) sdpa_paged4_many(const _
     if (warp == C::kMmaWarp) {
       // ---------------------------------------------------------- products
       auto lo = [](uint32_t addr, uint32_t lbo) { return (addr >> 4) | ((lbo >> 4) << 16); };
+      // scores of tile u (us: of the sub's)
       auto issue_s = [&](int sub, int u, int us) {
-        const uint32_t d = tmem + sub * C::kSubCols + static_cast<uint32_t>((us & 1) * kBN);
+        const int buf = C::kBufs == 2 ? us & 1 : 0;
+        const uint32_t d = tmem + sub * C::kSubCols + static_cast<uint32_t>(buf * kBN);
         const uint32_t a0 = lo(smem_base + sub * C::kQBytes, 16), b0 = lo(smem_base + C::kKOff + (u % R) * C::kKVBytes, 16);
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
@@ -808,19 +841,32 @@ __global__ void __launch_bounds__(WCfg<D>::kThreads, 1) sdpa_paged4_many(const _
                            b0 + static_cast<uint32_t>(((k / kS) * C::kSBO + (k % kS) * 32) >> 4), C::kDescHiKV, C::kIdescS,
                            k > 0 ? 1u : 0u);
         }
-        mma_commit_warp(s_full + sub * 2 + (us & 1));
+        mma_commit_warp(s_full + (C::kBufs == 2 ? buf : sub));
       };
-      auto issue_pv = [&](int sub, int u, int us, bool accumulate) {
-        const uint32_t pa = tmem + sub * C::kSubCols + static_cast<uint32_t>((us & 1) * kBN);
+      // O += P V of tile u, as P's parts come
+      auto issue_pv = [&](int sub, int u, int us, bool accumulate) -> bool {
+        const int buf = C::kBufs == 2 ? us & 1 : 0;
+        const uint32_t phase = static_cast<uint32_t>(C::kBufs == 2 ? us >> 1 : us) & 1u;
+        const uint32_t pa = tmem + sub * C::kSubCols + static_cast<uint32_t>(buf * kBN);
         const uint32_t b0 = lo(smem_base + C::kVOff + (u % R) * C::kKVBytes, C::kSBO);
+        constexpr int kSteps = C::kPartKeys / 16;
+        bool ok = true;
 #pragma unroll
-        for (int k = 0; k < kBN / 16; ++k)
-          mma_bf16_ts_warp(tmem + sub * C::kSubCols + C::kOCol, pa + static_cast<uint32_t>(k * 8),
-                           b0 + static_cast<uint32_t>((k * 2 * C::kGroupBytes) >> 4), C::kDescHiKV, C::kIdescPV,
-                           (accumulate || k > 0) ? 1u : 0u);
-        mma_commit_warp(o_full + sub);
+        for (int y = 0; y < C::kParts; ++y) {
+          if (!ok) continue;
+          ok = mbar_wait_warp(p_full + (C::kBufs == 2 ? buf : sub * C::kParts + y), phase, ab);
+          if (!ok) continue;
+          tc_fence_after();
+#pragma unroll
+          for (int k = y * kSteps; k < (y + 1) * kSteps; ++k)
+            mma_bf16_ts_warp(tmem + sub * C::kSubCols + C::kOCol, pa + static_cast<uint32_t>(k * 8),
+                             b0 + static_cast<uint32_t>((k * 2 * C::kGroupBytes) >> 4), C::kDescHiKV, C::kIdescPV,
+                             (accumulate || k > 0) ? 1u : 0u);
+        }
+        if (C::kBufs == 2 && ok) mma_commit_warp(o_full);
+        return ok;
       };
-      int u = 0, us[2] = {0, 0}, pieces[2] = {0, 0};
+      int u = 0, us0 = 0, us1 = 0, pieces0 = 0, pieces1 = 0;
       bool ok = true;
       for (int k = 0; ok; ++k) {
         ok = mbar_wait_warp(ready + (k & 1), static_cast<uint32_t>(k >> 1) & 1u, ab);
@@ -831,56 +877,124 @@ __global__ void __launch_bounds__(WCfg<D>::kThreads, 1) sdpa_paged4_many(const _
           const int subs = rows > 128 ? 2 : 1;
           auto k_ready = [&](int v) { return mbar_wait_warp(k_full + v % R, static_cast<uint32_t>(v / R) & 1u, ab); };
           if (!(ok = k_ready(u))) break;
-#pragma unroll
-          for (int sub = 0; sub < C::kSub; ++sub) {
-            if (sub >= subs || !ok) continue;
-            ok = mbar_wait_warp(q_full + sub, static_cast<uint32_t>(pieces[sub]) & 1u, ab);
-            if (!ok) continue;
+#pragma unroll 1
+          for (int sub = 0; sub < subs && ok; ++sub) {
+            ok = mbar_wait_warp(q_full + sub, static_cast<uint32_t>(sub == 0 ? pieces0 : pieces1) & 1u, ab);
+            if (!ok) break;
             tc_fence_after();
-            issue_s(sub, u, us[sub]);
+            issue_s(sub, u, sub == 0 ? us0 : us1);
           }
           if (!ok) break;
           mma_commit_warp(k_empty + u % R);
+#pragma unroll 1
           for (int i = 0; i < n && ok; ++i, ++u) {
-            if (i + 1 < n && !(ok = k_ready(u + 1))) break;
+            if (C::kBufs == 2 && i + 1 < n && !(ok = k_ready(u + 1))) break;
             if (!(ok = mbar_wait_warp(v_full + u % R, static_cast<uint32_t>(u / R) & 1u, ab))) break;
-#pragma unroll
-            for (int sub = 0; sub < C::kSub; ++sub) {
-              if (sub >= subs || !ok) continue;
+#pragma unroll 1
+            for (int sub = 0; sub < subs; ++sub) {
+              const int us = sub == 0 ? us0 : us1, pieces = sub == 0 ? pieces0 : pieces1;
               tc_fence_after();
-              // S of the next tile into the buffer of P of the one before: its O += P V was issued before
-              if (i + 1 < n) {
-                issue_s(sub, u + 1, us[sub] + 1);
+              // With two buffers the next scores go ahead of this tile's O += P V (into the buffer
+              // of the P before: its product was issued before), with one behind it, into P's place.
+              auto next_s = [&]() {
+                if (i + 1 >= n) return;
+                issue_s(sub, u + 1, us + 1);
                 if (sub + 1 == subs) mma_commit_warp(k_empty + (u + 1) % R);
-              }
+              };
+              if (C::kBufs == 2) next_s();
               // O of the piece before has been read out
-              if (i == 0 && pieces[sub] > 0) {
-                ok = mbar_wait_warp(o_free + sub, static_cast<uint32_t>(pieces[sub] - 1) & 1u, ab);
-                if (!ok) continue;
+              if (i == 0 && pieces > 0) {
+                ok = mbar_wait_warp(o_free + sub, static_cast<uint32_t>(pieces - 1) & 1u, ab);
+                if (!ok) break;
               }
-              ok = mbar_wait_warp(p_full + sub * 2 + (us[sub] & 1), static_cast<uint32_t>(us[sub] >> 1) & 1u, ab);
-              if (!ok) continue;
-              tc_fence_after();
-              issue_pv(sub, u, us[sub], i > 0);
+              if (!(ok = issue_pv(sub, u, us, i > 0))) break;
               if (i + 1 == n) mma_commit_warp(o_last + sub);
-              ++us[sub];
+              if (sub + 1 == subs) mma_commit_warp(v_empty + u % R);
+              if (C::kBufs == 1) {
+                if (sub == 0 && i + 1 < n && !(ok = k_ready(u + 1))) break;
+                tc_fence_after();
+                next_s();
+              }
+              if (sub == 0) ++us0;
+              else ++us1;
             }
-            if (ok) mma_commit_warp(v_empty + u % R);
           }
           if (!ok) break;
-          ++pieces[0];
-          if (subs > 1) ++pieces[1];
+          ++pieces0;
+          if (subs > 1) ++pieces1;
         }
         if (lane == 0) mbar_arrive(done + (k & 1));
       }
       mma_commit_warp(drain);
       mbar_wait_drain(drain, 0);
+    } else if (warp > C::kUnitWarp) {
+      // ------------------------------------------------------------- copies
+      // One warp K's, one V's, 16 bytes a lane, by 16 rows: they are one page's.  A lane
+      // looks up the page of one of a tile's 16 rows, a tile ahead of their copies.
+      const int y = warp - C::kUnitWarp - 1;
+      constexpr int kGroups = kBN / 16, kChunks = D / 2, kScaleChunks = D / 16;   // of 16 rows
+      int u = 0;
+      bool ok = true;
+      for (int k = 0; ok; ++k) {
+        ok = mbar_wait_warp(ready + (k & 1), static_cast<uint32_t>(k >> 1) & 1u, ab);
+        if (!ok) break;
+        const Unit& at = units[k & 1];
+        if (at.rows == 0) break;
+        const int n = at.kt1 - at.kt0, hi_pos = at.hi_pos;
+        const int hidden = p.window < INT_MAX ? max(at.first_pos, 0) - p.window : -1;
+        const int32_t* pages = p.page_table + static_cast<long long>(at.s) * p.pages_per_seq;
+        const uint8_t* from = (y == 0 ? p.k_pages : p.v_pages) + at.hk * p.page_bytes + lane * 16;
+        // what no row sees is not looked at (-1: zeros are copied)
+        auto ask = [&](int i) -> int {
+          const int key = (at.tile(i) << kBNShift) + lane * 16;
+          const bool seen = i < n && lane < kGroups && key <= hi_pos && (key + 15 > hidden || key < p.sinks);
+          return seen ? pages[key >> p.page_shift] : -1;
+        };
+        int page = ask(0), shown = page;
+#pragma unroll 1
+        for (int i = 0; i < n; ++i, ++u) {
+          const int next = ask(i + 1);
+          const int key0 = at.tile(i) << kBNShift;
+          shown = page;
+          if (page >= p.n_pages || page < -1) {
+            atomicOr(p.status, kStatusBadPage);              // and zeros
+            shown = -1;
+          } else if (page == -1 && lane < kGroups) {
+            // (-1 in the table is a bad page too, if it was asked for)
+            const int key = key0 + lane * 16;
+            if (key <= hi_pos && (key + 15 > hidden || key < p.sinks)) atomicOr(p.status, kStatusBadPage);
+          }
+          __syncwarp();
+          ok = u == 0 || mbar_wait_warp(raw_empty + y, static_cast<uint32_t>(u - 1) & 1u, ab);
+          if (!ok) break;
+          const uint32_t dst = smem_base + C::kRawOff + y * C::kRawHalf + lane * 16;
+#pragma unroll 2
+          for (int g = 0; g < kGroups; ++g) {
+            const int pg = __shfl_sync(0xffffffffu, shown, g);
+            const int r = (key0 + g * 16) & ((1 << p.page_shift) - 1);
+            const uint8_t* src = from + (pg >= 0 ? pg * p.page_stride : 0);
+            const uint8_t* codes = src + static_cast<long long>(r) * (D / 2);
+#pragma unroll
+            for (int c = 0; c < kChunks; c += 32)
+              if (kChunks >= 32 || lane < kChunks) cp_async16_or_zeros(dst + g * (8 * D) + c * 16, codes + c * 16, pg >= 0);
+            if (lane < kScaleChunks)
+              cp_async16_or_zeros(dst + C::kCodes + g * D, src + (static_cast<long long>(D / 2) << p.page_shift) + r * (D / 16),
+                                  pg >= 0);
+          }
+          cp_async_arrive(raw_full + y);
+          page = next;
+        }
+        if (!ok) break;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(done + (k & 1));
+      }
+      cp_async_wait<0>();                                    // (a wait may have run out above)
     } else if (warp == C::kUnitWarp && lane == 0) {
       // ------------------------------------------------------------- units
       mbar_arrive(ready);
       Unit next = units[0];
       for (int k = 1;; ++k) {
-        const bool more = next_unit<C::kRows>(plan, sched.cut, cta, &next);
+        const bool more = next_unit(plan, sched.cut, cta, &next);
         if (k > 1 && !mbar_wait(done + (k & 1), static_cast<uint32_t>((k >> 1) - 1) & 1u, ab)) break;
         if (!more) next.rows = 0;
         units[k & 1] = next;
@@ -923,7 +1037,7 @@ cudaError_t launch_wide_impl(const Paged4Params& p, cudaStream_t stream) {
 int paged4_wide_rows(int d) { return d <= 128 ? 256 : 128; }
 
 long long paged4_wide_most_runs(long long units, long long max_len) {
-  return std::max(1ll, units * (kStartKeys + max_len + kBN) / (kMinRunTiles * kBN));
+  return std::max(1ll, units * (kStartKeys + max_len + 128) / kMinRunKeys);
 }
 
 cudaError_t launch_sdpa_paged4_wide(const Paged4Params& p, int d, cudaStream_t stream) {
