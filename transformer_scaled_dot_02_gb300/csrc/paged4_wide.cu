@@ -4,22 +4,28 @@
 //
 // sdpa_paged4_many<D>: a UNIT is (sequence, key-value head, row tile), a row being
 // a new token's query head of the group; a row tile has kSub times 128 rows, so that
-// a key tile of 64 is expanded once for all of them.  All units' walks laid end to
-// end are cut into equal runs, one for each CTA (one on an SM), by the keys that
-// the rows see; the cut is worked out on the device.  A piece of a unit that is cut
-// is published as fp32 (O, m, l), and the run that publishes the last piece merges
-// them in the order of their keys: results repeat bit by bit, no run waits for another.
+// a key tile is expanded once for all of them.  All units' walks laid end to end are
+// cut into equal runs, one for each CTA (one on an SM), by the keys that the rows
+// see; the cut is worked out on the device.  A piece of a unit that is cut is
+// published as fp32 (O, m, l), and the run that publishes the last piece merges them
+// in the order of their keys: results repeat bit by bit, no run waits for another.
 //
-// Roles: two warps copy K's and V's pages as they are held; four expand codes and
-// scales to fp16 (exact) into the tensor core's swizzled operands; one issues the products
-// (tcgen05.mma, kind::f16: S = Q K^T into tensor memory, O += P V with P from
-// there); four for each 128 rows do the softmax, a row a thread; one works out the
-// units.  Queries are scaled by a power of two for each row to fit fp16, the softmax
-// weights are rounded to fp16 (2^-12).
+// Roles: two warps copy K's and V's pages as they are held (cp.async, 16 bytes a
+// lane), the first works out the units too; four expand codes and scales to fp16
+// (exact) into the tensor core's swizzled operands; one for each 128 rows issues the
+// products (tcgen05.mma, kind::f16: S = Q K^T into tensor memory, O += P V with P
+// from there); four for each 128 rows do the softmax, a row a thread.  Queries are
+// scaled by a power of two for each row to fit fp16, the softmax weights are rounded
+// to fp16 (2^-12: bf16's 2^-9 would cost a third of the result's own half step).
 //
-// What bounds it: the products of a key tile take 1024 clock cycles of the tensor
-// core for 256 rows of 128 columns; beside them an SM issues about 760 instructions
-// (a warp's) to expand the tile and 2600 for its softmax, 840 cycles' worth.
+// What bounds it: a key tile (128 keys, 256 rows, d = 128) takes 2048 clock cycles of
+// the tensor core, 1.0 us, and 2.0 us here: the softmax of a row (128 exponentials on
+// the unit that four warps share, maximum, sum, tensor memory to registers and back)
+// takes 0.95 us from S to P, and what the two halves of the rows overlap of it with the
+// other's products is 1.0 us.  The rest is a run's beginning (place, Q, the first tile:
+// 10 us) and its end (pieces out and merged: 15 us).  4 chunks of 512 tokens behind
+// 7680 positions (32 query heads, 8 of keys, d = 128): 136 us, the products' rate a
+// half of the peak; 814 us in the few-rows kernel.
 #include <algorithm>
 #include <atomic>
 #include <climits>
@@ -39,6 +45,12 @@ constexpr int kMinRunKeys = 512;           // of a run, at least
 struct Seq {
   int start, n, len, tiles;                // tiles: row tiles
 };
+
+// Most counts fit 32 bits, where a division costs a tenth of one in 64.
+__device__ __forceinline__ long long divide(long long a, long long b) {
+  if (((a | b) >> 32) == 0) return static_cast<unsigned>(a) / static_cast<unsigned>(b);
+  return a / b;
+}
 
 // Items are keys x group.  A unit is start items and then those of the keys that its
 // last row sees, were the tile full: group (len - n) + (r + 1) R, or what a window
@@ -65,7 +77,7 @@ struct Plan {
   // row tiles that see no more than a window holds
   __device__ __forceinline__ long long growing(const Seq& q, long long a) const {
     const long long m = most() - a;
-    return m <= 0 ? 0 : min(static_cast<long long>(q.tiles), m / R);
+    return m <= 0 ? 0 : min(static_cast<long long>(q.tiles), m / R);   // (R: a power of two)
   }
   __device__ __forceinline__ long long base(const Seq& q) const { return 1ll * max(q.len - q.n, 0) * p.group; }
   __device__ __forceinline__ long long cost(const Seq& q, int r) const {
@@ -108,7 +120,7 @@ struct Cut {
   __device__ long long begin(int c) const { return each * c + min(c, over); }
   __device__ int run_of(long long x) const {
     const long long longer = over * (each + 1);
-    return static_cast<int>(x < longer ? x / (each + 1) : over + (x - longer) / each);
+    return static_cast<int>(x < longer ? divide(x, each + 1) : over + divide(x - longer, each));
   }
 };
 
@@ -120,8 +132,8 @@ __device__ void set_piece(const Plan<R, S>& plan, const Cut& cut, int c, Unit* u
   const long long rows = 1ll * q.n * p.group, row0 = 1ll * u->r * R;
   u->first_row = static_cast<int>(row0);
   u->rows = static_cast<int>(min(static_cast<long long>(R), rows - row0));
-  u->first_pos = q.len - q.n + static_cast<int>(row0 / p.group);
-  u->hi_pos = q.len - q.n + static_cast<int>((row0 + u->rows - 1) / p.group);
+  u->first_pos = q.len - q.n + static_cast<int>(divide(row0, p.group));
+  u->hi_pos = q.len - q.n + static_cast<int>(divide(row0 + u->rows - 1, p.group));
   Tiles t{0, 0, 0};
   if (u->hi_pos >= 0) {
     if (p.window < INT_MAX) {
@@ -137,7 +149,7 @@ __device__ void set_piece(const Plan<R, S>& plan, const Cut& cut, int c, Unit* u
   const bool single = items > t.count * cut.each;
   auto tile_at = [&](long long y) -> int {
     y -= plan.start();
-    return y <= 0 ? 0 : single ? t.count : static_cast<int>(min(static_cast<long long>(t.count), y * t.count / items));
+    return y <= 0 ? 0 : single ? t.count : static_cast<int>(min(static_cast<long long>(t.count), divide(y * t.count, items)));
   };
   const long long y0 = cut.begin(c) - u->begin, y1 = cut.begin(c + 1) - u->begin;
   u->kt0 = tile_at(y0);
@@ -190,8 +202,8 @@ __device__ bool find_place(const Plan<R, S>& plan, Schedule* sh, Unit* first, in
   if (all == 0) return false;
   Cut cut;
   const long long least = 1ll * kMinRunKeys * p.group;
-  cut.runs = static_cast<int>(min(static_cast<long long>(p.runs), max(1ll, all / least)));
-  cut.each = all / cut.runs;
+  cut.runs = static_cast<int>(min(static_cast<long long>(p.runs), max(1ll, divide(all, least))));
+  cut.each = divide(all, cut.runs);
   cut.over = static_cast<int>(all - cut.each * cut.runs);
   if (c >= cut.runs) return false;
   if (tid == 0) sh->cut = cut;
@@ -205,7 +217,7 @@ __device__ bool find_place(const Plan<R, S>& plan, Schedule* sh, Unit* first, in
         Unit u;
         u.q = q;
         u.s = s;
-        u.hk = static_cast<int>((x - before) / head);
+        u.hk = static_cast<int>(divide(x - before, head));
         before += u.hk * head;
         int lo = 0, hi = q.tiles;                            // the last row tile that begins at or before x
         while (hi - lo > 1) {
@@ -290,13 +302,11 @@ struct WCfg {
   // the other's products, and a tile of 128 keys costs the tensor core 2048 clock cycles
   // (d = 128) where two of 64 cost 2560, as a product of 64 columns is bound by reading A.
   static constexpr int kBNShift = kSub == 2 ? 7 : 6, kBN = 1 << kBNShift, kBufs = kSub == 2 ? 1 : 2;
-  // P is handed over in parts, O += P V of the first beginning while the others are worked out
-  static constexpr int kParts = kSub == 2 ? 4 : 1, kPartKeys = kBN / kParts;
   static constexpr int kRows = 128 * kSub;
   static constexpr int kSoftmaxWarps = 4 * kSub;
   static constexpr int kExpandWarp = kSoftmaxWarps;          // the first of four
-  static constexpr int kMmaWarp = kExpandWarp + 4;
-  static constexpr int kUnitWarp = kMmaWarp + 1;
+  static constexpr int kMmaWarp = kExpandWarp + 4;           // one for each 128 rows
+  static constexpr int kCopyWarp = kMmaWarp + 2;             // K's, and V's; K's works out the units too
   static constexpr int kThreads = 32 * (kMmaWarp + 4);       // whole warpgroups, for the registers' split
   static constexpr int kBoxCols = D < 64 ? D : 64;
   static constexpr int kBoxes = D / kBoxCols;
@@ -316,14 +326,15 @@ struct WCfg {
   static constexpr int kCodes = kBN * D / 2, kScales = kBN * D / 16;
   static constexpr int kRawOff = kVOff + kRing * kKVBytes;
   static constexpr int kRawHalf = kCodes + kScales;
-  static constexpr int kBarOff = kRawOff + 2 * kRawHalf;
+  static constexpr int kRawSlots = D == 256 ? 2 : 3;         // halves (K or V of a tile) under way, in turn
+  static constexpr int kBarOff = kRawOff + kRawSlots * kRawHalf;
   // rows on their way to the output lie over Q, where they fit
   static constexpr int kTurnRow = 64 + 16;
   static constexpr int kTurnSlot = 32 * kTurnRow;
   static constexpr bool kTurns = 4 * kTurnSlot <= kQBytes;
-  // q_full, o_full, o_last, o_free, s_full [2]; p_full [2][4]; k_full, v_full, k_empty, v_empty [R];
-  // ready, done [2]; meet, drain; raw_full, raw_empty [2]
-  static constexpr int kNumBars = 10 + 8 + 4 * kRing + 4 + 2 + 4;
+  // q_full, o_full, o_last, o_free, s_full, p_full [2]; k_full, v_full, k_empty, v_empty [R];
+  // ready, done [2]; meet, drain; raw_full, raw_empty [3]; turn [2]
+  static constexpr int kNumBars = 12 + 4 * kRing + 4 + 2 + 6 + 2;
   static constexpr int kSmemBytes = kBarOff + kNumBars * 8 + 16 + 1024;
   static constexpr int kOChunk = D < 32 ? D : 32;
   static constexpr uint32_t kSubCols = 128 + (D < 32 ? 32 : D);
@@ -385,14 +396,14 @@ __device__ __noinline__ void merge_rows(const Paged4Params& p, const Unit& at, u
                                         int row) {
   using C = WCfg<D>;
   constexpr int kVec = C::kOChunk / 4;
-  const int of = at.of, steps = D / C::kOChunk * of;
+  const int of = at.of;
   const int rw = min(row, at.rows - 1);
   auto slot = [&](int i) { return p.slots + static_cast<long long>(slot_of(at, i)) * p.slot_bytes; };
   auto ml_of = [&](int i) { return __ldcg(reinterpret_cast<const float2*>(slot(i) + C::kRows * D * 4) + rw); };
   float4 acc[kVec], v[2][kVec];
   float2 ml[2];
-  auto fetch = [&](int c, int i, float4 (&x)[kVec], float2& m) {
-    m = ml_of(i);
+  auto fetch = [&](int c, int i, float4 (&x)[kVec], float2& w) {
+    w = ml_of(i);
     const float4* src = reinterpret_cast<const float4*>(slot(i)) + rw;
 #pragma unroll
     for (int e = 0; e < kVec; ++e) x[e] = __ldcg(src + (c * kVec + e) * C::kRows);
@@ -417,8 +428,8 @@ __device__ __noinline__ void merge_rows(const Paged4Params& p, const Unit& at, u
   }
   const float f = sum > 0.f ? p.v_unit / sum : 0.f;
   int c = 0, i = 0;                                          // of the step that is summed
-  auto sum_up = [&](const float4 (&x)[kVec], const float2& m) {
-    const float g = weight(m.x, base);
+  auto sum_up = [&](const float4 (&x)[kVec], const float2& w) {
+    const float g = weight(w.x, base);
 #pragma unroll
     for (int e = 0; e < kVec; ++e) {
       if (i == 0) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -440,6 +451,7 @@ __device__ __noinline__ void merge_rows(const Paged4Params& p, const Unit& at, u
     i = 0;
     ++c;
   };
+  const int steps = D / C::kOChunk * of;
 #pragma unroll 1
   for (int x = 0; x < steps; x += 2) {
     if (x + 1 < steps) fetch(fc, fi, v[1], ml[1]);
@@ -467,8 +479,8 @@ __global__ void __launch_bounds__(WCfg<D>::kThreads, 1) sdpa_paged4_many(const _
   uint64_t* o_last = o_full + 2;           // once a piece, after its last O += P V
   uint64_t* o_free = o_last + 2;           // once a piece, when the softmax warps have read O
   uint64_t* s_full = o_free + 2;           // [sub], or [buffer]
-  uint64_t* p_full = s_full + 2;           // [sub][part], or [buffer]
-  uint64_t* k_full = p_full + 8;
+  uint64_t* p_full = s_full + 2;
+  uint64_t* k_full = p_full + 2;
   uint64_t* v_full = k_full + R;
   uint64_t* k_empty = v_full + R;
   uint64_t* v_empty = k_empty + R;
@@ -476,9 +488,10 @@ __global__ void __launch_bounds__(WCfg<D>::kThreads, 1) sdpa_paged4_many(const _
   uint64_t* done = ready + 2;
   uint64_t* meet_bar = done + 2;
   uint64_t* drain = meet_bar + 1;
-  uint64_t* raw_full = drain + 1;          // K, V
-  uint64_t* raw_empty = raw_full + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(raw_empty + 2);
+  uint64_t* raw_full = drain + 1;          // half 2 u + y, y = 0 for K and 1 for V of tile u, is in slot (2 u + y) % kRawSlots
+  uint64_t* raw_empty = raw_full + 3;
+  uint64_t* turn = raw_empty + 3;          // of the warps that issue products
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(turn + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const AbortState ab{abort_flag, p.status};
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -490,22 +503,25 @@ __global__ void __launch_bounds__(WCfg<D>::kThreads, 1) sdpa_paged4_many(const _
       mbar_init(o_last + i, 1);
       mbar_init(o_free + i, 128);
       mbar_init(ready + i, 1);
-      mbar_init(done + i, C::kSoftmaxWarps + 4 + 1 + 2);
+      mbar_init(turn + i, 1);
+      mbar_init(done + i, C::kSoftmaxWarps + 4 + C::kSub + 2);
     }
-    for (int i = 0; i < 2; ++i) mbar_init(s_full + i, 1);
-    for (int i = 0; i < 8; ++i) mbar_init(p_full + i, 128);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(s_full + i, 1);
+      mbar_init(p_full + i, 128);
+    }
     for (int i = 0; i < R; ++i) {
       mbar_init(k_full + i, 128);
       mbar_init(v_full + i, 128);
-      mbar_init(k_empty + i, 1);
-      mbar_init(v_empty + i, 1);
+      mbar_init(k_empty + i, C::kSub);
+      mbar_init(v_empty + i, C::kSub);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 3; ++i) {
       mbar_init(raw_full + i, 32);
       mbar_init(raw_empty + i, 4);
     }
     mbar_init(meet_bar, C::kSoftmaxWarps);
-    mbar_init(drain, 1);
+    mbar_init(drain, C::kSub);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -562,38 +578,56 @@ __global__ void __launch_bounds__(WCfg<D>::kThreads, 1) sdpa_paged4_many(const _
         const int pos = valid ? at.q.len - at.q.n + token : -1;
         float m_used = -INFINITY, l = 0.f, sc = 0.f;
         if (active) {
-          // ---- Q: this row, scaled by a power of two, as fp16 (its last scores are done with the one before)
-          const uint4* src = reinterpret_cast<const uint4*>(p.q + static_cast<long long>(at.q.start + token) * p.q_stride + head * D);
-          // (twice, eight loads at a time: the second time from L1)
-          uint32_t top = 0;
-#pragma unroll 8
-          for (int c = 0; c < D / 8; ++c) {
-            const uint4 v = valid ? src[c] : make_uint4(0, 0, 0, 0);
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) top = max(top, max(w[e] & 0x7fffu, w[e] >> 16 & 0x7fffu));
-          }
-          const int ex = static_cast<int>(top >> 7);         // biased; rows of zeros, infinities and NaN stay
-          const int up = top == 0 || ex == 255 ? 0 : max(-120, min(120, 13 + 127 - ex));
-          const float f = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
-          // (never 0, which a masked score of -infinity would make a NaN)
-          sc = fmaxf(__uint_as_float(static_cast<uint32_t>(127 - up) << 23) * p.k_unit * p.scale_log2, 1e-37f);
+          // ---- Q: rows scaled by powers of two, as fp16 (the last scores are done with the ones before);
+          // kLanes lanes read a row (rows apart by thread touch 32 lines with each load: 7 us)
+          const long long mine = reinterpret_cast<long long>(p.q + static_cast<long long>(at.q.start + token) * p.q_stride + head * D);
+          constexpr int kLanes = D / 8, kRowsAtOnce = 32 / kLanes, kLoads = 32 / kRowsAtOnce;
           uint8_t* q_smem = smem + sub * C::kQBytes;
-          const int r = quarter * 32 + lane;
-#pragma unroll 4
-          for (int c = 0; c < D / 8; ++c) {
-            const uint4 v = valid ? src[c] : make_uint4(0, 0, 0, 0);
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-            uint32_t h[4];
+          const int row0 = sub * 128 + quarter * 32;
+          float back = 1.f;
+#pragma unroll 1
+          for (int x0 = 0; x0 < kLoads; x0 += 4) {
+            uint4 v[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              h[e] = pack_f16x2(__uint_as_float(w[e] << 16) * f, __uint_as_float(w[e] & 0xffff0000u) * f);
-            constexpr int kChunks = C::kRowBytes / 16;
-            *reinterpret_cast<uint4*>(q_smem + (c / kChunks) * C::kQBox + swizzle_offset<C::kRowBytes>(r, c % kChunks)) =
-                make_uint4(h[0], h[1], h[2], h[3]);
+            for (int x = 0; x < 4; ++x) {
+              const int r = ((x0 + x) * kRowsAtOnce + lane / kLanes) & 31;
+              const long long src = __shfl_sync(0xffffffffu, mine, r);
+              v[x] = make_uint4(0, 0, 0, 0);
+              if (row0 + r < rows && x0 + x < kLoads) v[x] = reinterpret_cast<const uint4*>(src)[lane % kLanes];
+            }
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              if (x0 + x >= kLoads) continue;
+              const int r = (x0 + x) * kRowsAtOnce + lane / kLanes;
+              const uint32_t w[4] = {v[x].x, v[x].y, v[x].z, v[x].w};
+              uint32_t top = 0;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) top = max(top, max(w[e] & 0x7fffu, w[e] >> 16 & 0x7fffu));
+#pragma unroll
+              for (int y = 1; y < kLanes; y <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, y));
+              const int ex = static_cast<int>(top >> 7);     // biased; rows of zeros, infinities and NaN stay
+              const int up = top == 0 || ex == 255 ? 0 : max(-120, min(120, 13 + 127 - ex));
+              const float f = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
+              uint32_t h[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                h[e] = pack_f16x2(__uint_as_float(w[e] << 16) * f, __uint_as_float(w[e] & 0xffff0000u) * f);
+              constexpr int kChunks = C::kRowBytes / 16;
+              const int c = lane % kLanes;
+              *reinterpret_cast<uint4*>(q_smem + (c / kChunks) * C::kQBox +
+                                        swizzle_offset<C::kRowBytes>(quarter * 32 + r, c % kChunks)) =
+                  make_uint4(h[0], h[1], h[2], h[3]);
+              // 2^-up to the lane whose row it is
+              const float b = __shfl_sync(0xffffffffu, __uint_as_float(static_cast<uint32_t>(127 - up) << 23),
+                                          (lane % kRowsAtOnce) * kLanes);
+              if (lane / kRowsAtOnce == x0 + x) back = b;
+            }
           }
+          // (never 0, which a masked score of -infinity would make a NaN)
+          sc = fmaxf(back * p.k_unit * p.scale_log2, 1e-37f);
           fence_proxy_async_smem();
           mbar_arrive(q_full + sub);
+          if (at.of > 1 && tid == 0) open_count(p.counts + slot_of(at, 0));
           const float2 sc2 = make_float2(sc, sc);
           // ---- key tiles
           for (int i = 0; i < n; ++i, ++u) {
@@ -601,9 +635,9 @@ __global__ void __launch_bounds__(WCfg<D>::kThreads, 1) sdpa_paged4_many(const _
             const int buf = C::kBufs == 2 ? u & 1 : 0;
             const uint32_t phase = static_cast<uint32_t>(C::kBufs == 2 ? u >> 1 : u) & 1u;
             const uint32_t s_col = static_cast<uint32_t>(buf * kBN);
-            uint64_t* p_bar = p_full + (C::kBufs == 2 ? buf : sub * C::kParts);
+            const int bar = C::kBufs == 2 ? buf : sub;       // of s_full and p_full
             const int key0 = at.tile(i) << kBNShift;
-            ok = mbar_wait_warp(s_full + (C::kBufs == 2 ? buf : sub), phase, ab);
+            ok = mbar_wait_warp(s_full + bar, phase, ab);
             if (!ok) break;
             tc_fence_after();
             if (busy) {
@@ -675,32 +709,28 @@ __global__ void __launch_bounds__(WCfg<D>::kThreads, 1) sdpa_paged4_many(const _
               float2 acc[4];
 #pragma unroll
               for (int x = 0; x < 4; ++x) acc[x] = make_float2(0.f, 0.f);
+              // (P is handed over whole: in two or four parts the warps that issue the products
+              // wait for each, 143 and 160 us instead of 140 for 4 chunks of 512 tokens behind
+              // 7680 positions)
 #pragma unroll
-              for (int y = 0; y < C::kParts; ++y) {
-                uint32_t pk[C::kPartKeys / 2];
+              for (int y = 0; y < kBN / 32; ++y) {
+                uint32_t pk[16];
 #pragma unroll
-                for (int e = 0; e < C::kPartKeys / 2; ++e) {
-                  const int c = y * C::kPartKeys + 2 * e;
+                for (int e = 0; e < 16; ++e) {
+                  const int c = y * 32 + 2 * e;
                   const float2 x = __ffma2_rn(make_float2(s[c], s[c + 1]), sc2, neg2);
                   const float2 pe = make_float2(ex2_approx(x.x), ex2_approx(x.y));
                   acc[e & 3] = __fadd2_rn(acc[e & 3], pe);
                   pk[e] = pack_f16x2(pe.x, pe.y);
                 }
-                tmem_st_chunk(lane_base + s_col + y * (C::kPartKeys / 2), pk);
-                if (y + 1 < C::kParts) {
-                  tmem_st_wait();
-                  tc_fence_before();
-                  mbar_arrive(p_bar + y);
-                }
+                tmem_st16(lane_base + s_col + y * 16, pk);
               }
               const float2 a = __fadd2_rn(__fadd2_rn(acc[0], acc[1]), __fadd2_rn(acc[2], acc[3]));
               l += a.x + a.y;
               tmem_st_wait();
-            } else {
-              for (int y = 0; y + 1 < C::kParts; ++y) mbar_arrive(p_bar + y);
             }
             tc_fence_before();
-            mbar_arrive(p_bar + C::kParts - 1);
+            mbar_arrive(p_full + bar);
           }
           if (!ok) break;
           // (a barrier of its own: o_full may still be two tiles behind)
@@ -749,13 +779,13 @@ __global__ void __launch_bounds__(WCfg<D>::kThreads, 1) sdpa_paged4_many(const _
           __threadfence();
           if (!(ok = meet())) break;
           if (tid == 0) {
-            open_count(count);
             last_one = static_cast<int>(atomicAdd(count, 1ull) & 0xffff) + 1 == at.of;
-            if (last_one) *count = 0;
             __threadfence();
+            if (last_one) *count = 0;
           }
           if (!(ok = meet())) break;
-          if (last_one != 0 && busy) merge_rows<D>(p, at, turn, out, rows_here, row);
+          if (last_one != 0 && busy && active)
+            merge_rows<D>(p, at, turn, out, rows_here, row);
           // (last_one has been read)
           if (!(ok = meet())) break;
         }
@@ -768,7 +798,7 @@ __global__ void __launch_bounds__(WCfg<D>::kThreads, 1) sdpa_paged4_many(const _
     if constexpr (C::kSub == 2) regs_decrease<C::kExpandRegs>();
     // (Loops are short for the instruction cache's sake, which all roles share: with two
     // tiles' loads and products unrolled every role waited for instructions, and 4 chunks of
-    // 512 tokens behind 7680 positions took 250 us instead of @@.)
+    // 512 tokens behind 7680 positions took 250 us instead of 160.)
     const int tid_e = tid - C::kExpandWarp * 32;
     // A thread expands blocks of 16 columns: the same place in every kStep-th row.
     constexpr int kBlocks = D / 16, kStep = 128 / kBlocks, kTimes = kBN / kStep;
@@ -793,10 +823,11 @@ __global__ void __launch_bounds__(WCfg<D>::kThreads, 1) sdpa_paged4_many(const _
         const bool edge = key0 + kBN - 1 > hi_pos || key0 <= hidden;
 #pragma unroll 1
         for (int y = 0; y < 2; ++y) {                        // K, V
-          ok = mbar_wait_warp(raw_full + y, static_cast<uint32_t>(u) & 1u, ab) &&
+          const int half = 2 * u + y, slot = half % C::kRawSlots;
+          ok = mbar_wait_warp(raw_full + slot, static_cast<uint32_t>(half / C::kRawSlots) & 1u, ab) &&
                (u < R || mbar_wait_warp((y == 0 ? k_empty : v_empty) + st, static_cast<uint32_t>(u / R - 1) & 1u, ab));
           if (!ok) break;
-          uint8_t* raw = smem + C::kRawOff + y * C::kRawHalf;
+          uint8_t* raw = smem + C::kRawOff + slot * C::kRawHalf;
           uint8_t* scales = raw + C::kCodes + tid_e;
           if (edge) {
             // what no row sees may be anything: its scale could be a NaN
@@ -817,7 +848,7 @@ __global__ void __launch_bounds__(WCfg<D>::kThreads, 1) sdpa_paged4_many(const _
           fence_proxy_async_smem();
           mbar_arrive((y == 0 ? k_full : v_full) + st);
           __syncwarp();
-          if (lane == 0) mbar_arrive(raw_empty + y);
+          if (lane == 0) mbar_arrive(raw_empty + slot);
         }
       }
       if (!ok) break;
@@ -826,115 +857,119 @@ __global__ void __launch_bounds__(WCfg<D>::kThreads, 1) sdpa_paged4_many(const _
     }
   } else if (any) {
     if constexpr (C::kSub == 2) regs_decrease<C::kRestRegs>();
-    if (warp == C::kMmaWarp) {
+    if (warp < C::kMmaWarp + C::kSub) {
       // ---------------------------------------------------------- products
+      // A warp for each 128 rows, which take turns: while one's products are under way the
+      // other's P is waited for, and one's softmax runs beside the other's products.  (One warp
+      // for both takes 0.9 us for each one's share of a tile, 2.1 us a tile; without turns both
+      // do the same at the same time, 2.4 us.)
+      const int sub = warp - C::kMmaWarp;
       auto lo = [](uint32_t addr, uint32_t lbo) { return (addr >> 4) | ((lbo >> 4) << 16); };
-      // scores of tile u (us: of the sub's)
-      auto issue_s = [&](int sub, int u, int us) {
+      const uint32_t q_lo = lo(smem_base + sub * C::kQBytes, 16);
+      const uint32_t t_sub = tmem + sub * C::kSubCols;
+      // scores of tile u (us: of this sub's)
+      auto issue_s = [&](int u, int us) {
         const int buf = C::kBufs == 2 ? us & 1 : 0;
-        const uint32_t d = tmem + sub * C::kSubCols + static_cast<uint32_t>(buf * kBN);
-        const uint32_t a0 = lo(smem_base + sub * C::kQBytes, 16), b0 = lo(smem_base + C::kKOff + (u % R) * C::kKVBytes, 16);
+        const uint32_t d = t_sub + static_cast<uint32_t>(buf * kBN);
+        const uint32_t b0 = lo(smem_base + C::kKOff + (u % R) * C::kKVBytes, 16);
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
           constexpr int kS = C::kStepsPerRow;
-          mma_bf16_ss_warp(d, a0 + static_cast<uint32_t>(((k / kS) * C::kQBox + (k % kS) * 32) >> 4), C::kDescHi,
+          mma_bf16_ss_warp(d, q_lo + static_cast<uint32_t>(((k / kS) * C::kQBox + (k % kS) * 32) >> 4), C::kDescHi,
                            b0 + static_cast<uint32_t>(((k / kS) * C::kSBO + (k % kS) * 32) >> 4), C::kDescHiKV, C::kIdescS,
                            k > 0 ? 1u : 0u);
         }
         mma_commit_warp(s_full + (C::kBufs == 2 ? buf : sub));
+        mma_commit_warp(k_empty + u % R);
       };
-      // O += P V of tile u, as P's parts come
-      auto issue_pv = [&](int sub, int u, int us, bool accumulate) -> bool {
+      // O += P V of tile u
+      auto issue_pv = [&](int u, int us, bool accumulate) -> bool {
         const int buf = C::kBufs == 2 ? us & 1 : 0;
         const uint32_t phase = static_cast<uint32_t>(C::kBufs == 2 ? us >> 1 : us) & 1u;
-        const uint32_t pa = tmem + sub * C::kSubCols + static_cast<uint32_t>(buf * kBN);
+        if (!mbar_wait_warp(p_full + (C::kBufs == 2 ? buf : sub), phase, ab)) return false;
+        tc_fence_after();
+        const uint32_t pa = t_sub + static_cast<uint32_t>(buf * kBN);
         const uint32_t b0 = lo(smem_base + C::kVOff + (u % R) * C::kKVBytes, C::kSBO);
-        constexpr int kSteps = C::kPartKeys / 16;
-        bool ok = true;
 #pragma unroll
-        for (int y = 0; y < C::kParts; ++y) {
-          if (!ok) continue;
-          ok = mbar_wait_warp(p_full + (C::kBufs == 2 ? buf : sub * C::kParts + y), phase, ab);
-          if (!ok) continue;
-          tc_fence_after();
-#pragma unroll
-          for (int k = y * kSteps; k < (y + 1) * kSteps; ++k)
-            mma_bf16_ts_warp(tmem + sub * C::kSubCols + C::kOCol, pa + static_cast<uint32_t>(k * 8),
-                             b0 + static_cast<uint32_t>((k * 2 * C::kGroupBytes) >> 4), C::kDescHiKV, C::kIdescPV,
-                             (accumulate || k > 0) ? 1u : 0u);
-        }
-        if (C::kBufs == 2 && ok) mma_commit_warp(o_full);
-        return ok;
+        for (int k = 0; k < kBN / 16; ++k)
+          mma_bf16_ts_warp(t_sub + C::kOCol, pa + static_cast<uint32_t>(k * 8),
+                           b0 + static_cast<uint32_t>((k * 2 * C::kGroupBytes) >> 4), C::kDescHiKV, C::kIdescPV,
+                           (accumulate || k > 0) ? 1u : 0u);
+        if (C::kBufs == 2) mma_commit_warp(o_full);
+        return true;
       };
-      int u = 0, us0 = 0, us1 = 0, pieces0 = 0, pieces1 = 0;
+      auto k_ready = [&](int v) { return mbar_wait_warp(k_full + v % R, static_cast<uint32_t>(v / R) & 1u, ab); };
+      auto v_ready = [&](int v) { return mbar_wait_warp(v_full + v % R, static_cast<uint32_t>(v / R) & 1u, ab); };
+      int u = 0, us = 0, pieces = 0, turns = 0;
       bool ok = true;
       for (int k = 0; ok; ++k) {
         ok = mbar_wait_warp(ready + (k & 1), static_cast<uint32_t>(k >> 1) & 1u, ab);
         if (!ok) break;
         const int rows = units[k & 1].rows, n = units[k & 1].kt1 - units[k & 1].kt0;
         if (rows == 0) break;
-        if (n > 0) {
-          const int subs = rows > 128 ? 2 : 1;
-          auto k_ready = [&](int v) { return mbar_wait_warp(k_full + v % R, static_cast<uint32_t>(v / R) & 1u, ab); };
-          if (!(ok = k_ready(u))) break;
-#pragma unroll 1
-          for (int sub = 0; sub < subs && ok; ++sub) {
-            ok = mbar_wait_warp(q_full + sub, static_cast<uint32_t>(sub == 0 ? pieces0 : pieces1) & 1u, ab);
-            if (!ok) break;
-            tc_fence_after();
-            issue_s(sub, u, sub == 0 ? us0 : us1);
-          }
-          if (!ok) break;
-          mma_commit_warp(k_empty + u % R);
+        const bool both = rows > 128;
+        // waits for this warp's turn; gives it away
+        auto take = [&]() -> bool {
+          if (!both) return true;
+          const int t = turns++ - (sub == 0 ? 1 : 0);        // (the first is sub 0's)
+          return t < 0 || mbar_wait_warp(turn + sub, static_cast<uint32_t>(t) & 1u, ab);
+        };
+        auto pass = [&]() {
+          if (both && lane == 0) mbar_arrive(turn + (sub ^ 1));
+        };
+        if (sub * 128 >= rows) {
+          // no rows: the tiles are released as they come
 #pragma unroll 1
           for (int i = 0; i < n && ok; ++i, ++u) {
-            if (C::kBufs == 2 && i + 1 < n && !(ok = k_ready(u + 1))) break;
-            if (!(ok = mbar_wait_warp(v_full + u % R, static_cast<uint32_t>(u / R) & 1u, ab))) break;
-#pragma unroll 1
-            for (int sub = 0; sub < subs; ++sub) {
-              const int us = sub == 0 ? us0 : us1, pieces = sub == 0 ? pieces0 : pieces1;
-              tc_fence_after();
-              // With two buffers the next scores go ahead of this tile's O += P V (into the buffer
-              // of the P before: its product was issued before), with one behind it, into P's place.
-              auto next_s = [&]() {
-                if (i + 1 >= n) return;
-                issue_s(sub, u + 1, us + 1);
-                if (sub + 1 == subs) mma_commit_warp(k_empty + (u + 1) % R);
-              };
-              if (C::kBufs == 2) next_s();
-              // O of the piece before has been read out
-              if (i == 0 && pieces > 0) {
-                ok = mbar_wait_warp(o_free + sub, static_cast<uint32_t>(pieces - 1) & 1u, ab);
-                if (!ok) break;
-              }
-              if (!(ok = issue_pv(sub, u, us, i > 0))) break;
-              if (i + 1 == n) mma_commit_warp(o_last + sub);
-              if (sub + 1 == subs) mma_commit_warp(v_empty + u % R);
-              if (C::kBufs == 1) {
-                if (sub == 0 && i + 1 < n && !(ok = k_ready(u + 1))) break;
-                tc_fence_after();
-                next_s();
-              }
-              if (sub == 0) ++us0;
-              else ++us1;
-            }
+            if (!(ok = k_ready(u))) break;
+            if (lane == 0) mbar_arrive(k_empty + u % R);
+            if (!(ok = v_ready(u))) break;
+            if (lane == 0) mbar_arrive(v_empty + u % R);
           }
+        } else if (n > 0) {
+          ok = k_ready(u) && mbar_wait_warp(q_full + sub, static_cast<uint32_t>(pieces) & 1u, ab) && take();
           if (!ok) break;
-          ++pieces0;
-          if (subs > 1) ++pieces1;
+          tc_fence_after();
+          issue_s(u, us);
+          pass();
+#pragma unroll 1
+          for (int i = 0; i < n; ++i, ++u, ++us) {
+            // With two buffers the next scores go ahead of this tile's O += P V (into the buffer
+            // of the P before: its product was issued before), with one behind it, into P's place.
+            auto next_s = [&]() -> bool {
+              if (i + 1 >= n) return true;
+              if (!k_ready(u + 1)) return false;
+              tc_fence_after();
+              issue_s(u + 1, us + 1);
+              return true;
+            };
+            if (C::kBufs == 2 && !(ok = next_s())) break;
+            // O of the piece before has been read out
+            ok = take() && v_ready(u) &&
+                 (i > 0 || pieces == 0 || mbar_wait_warp(o_free + sub, static_cast<uint32_t>(pieces - 1) & 1u, ab)) &&
+                 issue_pv(u, us, i > 0);
+            if (!ok) break;
+            if (i + 1 == n) mma_commit_warp(o_last + sub);
+            mma_commit_warp(v_empty + u % R);
+            if (C::kBufs == 1 && !(ok = next_s())) break;
+            pass();
+          }
+          ++pieces;
         }
+        if (!ok) break;
         if (lane == 0) mbar_arrive(done + (k & 1));
       }
       mma_commit_warp(drain);
       mbar_wait_drain(drain, 0);
-    } else if (warp > C::kUnitWarp) {
+    } else if (warp >= C::kCopyWarp) {
       // ------------------------------------------------------------- copies
       // One warp K's, one V's, 16 bytes a lane, by 16 rows: they are one page's.  A lane
       // looks up the page of one of a tile's 16 rows, a tile ahead of their copies.
-      const int y = warp - C::kUnitWarp - 1;
+      const int y = warp - C::kCopyWarp;
       constexpr int kGroups = kBN / 16, kChunks = D / 2, kScaleChunks = D / 16;   // of 16 rows
       int u = 0;
       bool ok = true;
+      if (y == 0 && lane == 0) mbar_arrive(ready);           // (the first unit)
       for (int k = 0; ok; ++k) {
         ok = mbar_wait_warp(ready + (k & 1), static_cast<uint32_t>(k >> 1) & 1u, ab);
         if (!ok) break;
@@ -965,9 +1000,10 @@ __global__ void __launch_bounds__(WCfg<D>::kThreads, 1) sdpa_paged4_many(const _
             if (key <= hi_pos && (key + 15 > hidden || key < p.sinks)) atomicOr(p.status, kStatusBadPage);
           }
           __syncwarp();
-          ok = u == 0 || mbar_wait_warp(raw_empty + y, static_cast<uint32_t>(u - 1) & 1u, ab);
+          const int half = 2 * u + y, slot = half % C::kRawSlots;
+          ok = half < C::kRawSlots || mbar_wait_warp(raw_empty + slot, static_cast<uint32_t>(half / C::kRawSlots - 1) & 1u, ab);
           if (!ok) break;
-          const uint32_t dst = smem_base + C::kRawOff + y * C::kRawHalf + lane * 16;
+          const uint32_t dst = smem_base + C::kRawOff + slot * C::kRawHalf + lane * 16;
 #pragma unroll 2
           for (int g = 0; g < kGroups; ++g) {
             const int pg = __shfl_sync(0xffffffffu, shown, g);
@@ -981,26 +1017,26 @@ __global__ void __launch_bounds__(WCfg<D>::kThreads, 1) sdpa_paged4_many(const _
               cp_async16_or_zeros(dst + C::kCodes + g * D, src + (static_cast<long long>(D / 2) << p.page_shift) + r * (D / 16),
                                   pg >= 0);
           }
-          cp_async_arrive(raw_full + y);
+          cp_async_arrive(raw_full + slot);
           page = next;
         }
         if (!ok) break;
+        if (y == 0) {
+          // the next unit, once all are done with the one before this
+          Unit next = at;
+          const bool more = next_unit(plan, sched.cut, cta, &next);
+          if (!more) next.rows = 0;
+          ok = k == 0 || mbar_wait_warp(done + ((k + 1) & 1), static_cast<uint32_t>((k - 1) >> 1) & 1u, ab);
+          if (!ok) break;
+          if (lane == 0) {
+            units[(k + 1) & 1] = next;
+            mbar_arrive(ready + ((k + 1) & 1));
+          }
+        }
         __syncwarp();
         if (lane == 0) mbar_arrive(done + (k & 1));
       }
       cp_async_wait<0>();                                    // (a wait may have run out above)
-    } else if (warp == C::kUnitWarp && lane == 0) {
-      // ------------------------------------------------------------- units
-      mbar_arrive(ready);
-      Unit next = units[0];
-      for (int k = 1;; ++k) {
-        const bool more = next_unit(plan, sched.cut, cta, &next);
-        if (k > 1 && !mbar_wait(done + (k & 1), static_cast<uint32_t>((k >> 1) - 1) & 1u, ab)) break;
-        if (!more) next.rows = 0;
-        units[k & 1] = next;
-        mbar_arrive(ready + (k & 1));
-        if (!more) break;
-      }
     }
   }
 
