@@ -1119,9 +1119,6 @@ sdpa_status sdpa_paged4_read(const void* k_pages, const void* v_pages, void* k_o
   p.h_kv = h_kv;
   p.d = d;
   p.log_items = log2_of(d / 8);
-  // (as for the append; a block has up to 16 tokens)
-  const unsigned long long items = 2ull * h_kv * (d / 8);
-  p.items_magic = 16 * items * items < (1ull << 32) ? static_cast<unsigned>(((1ull << 32) + items - 1) / items) : 0;
   p.page_shift = log2_of(page_size);
   p.n_pages = n_pages;
   p.pages_per_seq = pages_per_seq;

@@ -183,7 +183,6 @@ struct Paged4ReadParams {
   unsigned* status;
   int b, n_tokens, h_kv, d;
   int log_items;              // of d / 8
-  unsigned items_magic;       // ceil(2^32 / (2 h_kv d / 8)), 0 if that is too large to divide by
   int page_shift, n_pages, pages_per_seq;
   float k_unit, v_unit;       // 2^exp
 };

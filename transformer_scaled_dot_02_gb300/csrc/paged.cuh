@@ -67,15 +67,14 @@ __device__ __forceinline__ int find_seq(const Params& p, int t, int lane) {
 
 // Where packed row t lies: its position (INT_MIN: no sequence's row) and the
 // page row of its first head, page * h_kv * P + position % P (-1: none; a page
-// number outside the cache is reported).  One warp, every lane.
+// number outside the cache is reported).
 struct RowPlace {
   int pos;
   long long row;
 };
 template <class Params>
-__device__ __forceinline__ RowPlace place_of_row(const Params& p, int t, int lane) {
+__device__ __forceinline__ RowPlace place_in_seq(const Params& p, int t, int s, bool report) {
   RowPlace r{INT_MIN, -1};
-  const int s = find_seq(p, t, lane);
   const int end = s >= 0 ? min(p.q_starts[s + 1], p.n_tokens) : 0;
   if (t >= end) return r;
   const int len = min(max(p.kv_lengths[s], 0), p.pages_per_seq << p.page_shift);
@@ -84,9 +83,32 @@ __device__ __forceinline__ RowPlace place_of_row(const Params& p, int t, int lan
   const int page = p.page_table[static_cast<long long>(s) * p.pages_per_seq + (r.pos >> p.page_shift)];
   if (page >= 0 && page < p.n_pages)
     r.row = (static_cast<long long>(page) * p.h_kv << p.page_shift) + (r.pos & ((1 << p.page_shift) - 1));
-  else if (lane == 0)
+  else if (report)
     atomicOr(p.status, kStatusBadPage);
   return r;
+}
+// One warp, every lane: one row's.
+template <class Params>
+__device__ __forceinline__ RowPlace place_of_row(const Params& p, int t, int lane) {
+  return place_in_seq(p, t, find_seq(p, t, lane), lane == 0);
+}
+// One warp, t0 + lane's for each of the first `rows` lanes.  (A warp for each row in
+// turn would wait four times for memory for each.)
+template <class Params>
+__device__ __forceinline__ RowPlace place_of_rows(const Params& p, int t0, int rows, int lane) {
+  const int t = t0 + min(lane, rows - 1);
+  int s = find_seq(p, t0, lane);
+  const int last = find_seq(p, t0 + rows - 1, lane);
+  if (s != last || s < 0) {
+    int lo = 0, hi = p.b + 1;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (p.q_starts[mid] <= t) lo = mid;
+      else hi = mid;
+    }
+    s = lo < p.b && p.q_starts[lo] <= t ? lo : -1;
+  }
+  return place_in_seq(p, t, s, lane < rows);
 }
 
 }  // namespace sdpa

@@ -1007,9 +1007,9 @@ __global__ void __launch_bounds__(WCfg<D>::kThreads, 1) sdpa_paged4_many(const _
 #pragma unroll 2
           for (int g = 0; g < kGroups; ++g) {
             const int pg = __shfl_sync(0xffffffffu, shown, g);
-            const int r = (key0 + g * 16) & ((1 << p.page_shift) - 1);
+            const long long r = (key0 + g * 16) & ((1 << p.page_shift) - 1);
             const uint8_t* src = from + (pg >= 0 ? pg * p.page_stride : 0);
-            const uint8_t* codes = src + static_cast<long long>(r) * (D / 2);
+            const uint8_t* codes = src + r * (D / 2);
 #pragma unroll
             for (int c = 0; c < kChunks; c += 32)
               if (kChunks >= 32 || lane < kChunks) cp_async16_or_zeros(dst + g * (8 * D) + c * 16, codes + c * 16, pg >= 0);
