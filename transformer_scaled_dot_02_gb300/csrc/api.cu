@@ -1070,12 +1070,6 @@ sdpa_status sdpa_paged4_append(const void* q, const void* k, const void* v, void
   p.d_rot = d_rot;
   p.interleaved = interleaved != 0;
   p.log_blocks = log2_of(d / 16);
-  // x / items as the high word of x * magic: exact while x (magic items - 2^32)
-  // < 2^32, and x is below a block's tokens (at most 8) times items
-  const unsigned long long items = static_cast<unsigned long long>(h + 2 * h_kv) * (d / 16);
-  p.items_magic = items > 1 && 8 * items * items < (1ull << 32)
-                      ? static_cast<unsigned>(((1ull << 32) + items - 1) / items)
-                      : 0;
   p.page_shift = log2_of(page_size);
   p.n_pages = n_pages;
   p.pages_per_seq = pages_per_seq;

@@ -169,7 +169,6 @@ struct Paged4AppendParams {
   long long q_stride, k_stride, v_stride;
   int b, n_tokens, h, h_kv, d, d_rot, interleaved;
   int log_blocks;             // of d / 16
-  unsigned items_magic;       // ceil(2^32 / ((h + 2 h_kv) d / 16)), 0 if that is too large to divide by
   int page_shift, n_pages, pages_per_seq;
   float k_unit, v_unit;       // 2^-exp
 };

@@ -9,6 +9,19 @@
 
 namespace sdpa {
 
+// freq / 2 pi as the sum of three floats, good to 2^-70 of itself.
+struct Turns {
+  float hi, mid, low;
+};
+__device__ __forceinline__ Turns turns_of(float freq) {
+  // 1 / (2 pi) = 0.15915494309189533576888376..., rounded to fp32, then what that left, twice
+  constexpr float kInvTwoPi0 = 0x1.45f306p-3f, kInvTwoPi1 = 0x1.b9391p-28f, kInvTwoPi2 = 0x1.529fc2p-54f;
+  const float th = freq * kInvTwoPi0, e0 = fmaf(freq, kInvTwoPi0, -th);
+  const float p1 = freq * kInvTwoPi1, e1 = fmaf(freq, kInvTwoPi1, -p1);
+  const float tm = e0 + p1, back = tm - e0;
+  return {th, tm, (e0 - (tm - back)) + (p1 - back) + fmaf(freq, kInvTwoPi2, e1)};
+}
+
 // cos and sin of pos * freq.  The angle in turns is formed from products whose
 // rounding errors are kept (fma): the position in two parts of at most 19 bits,
 // freq / 2 pi as a sum of three floats, good to 2^-70 of itself.  Whole turns are
@@ -18,12 +31,8 @@ namespace sdpa {
 // exact arithmetic, 300000 angles of positions up to 2^30 and frequencies up to 1e5
 // were off by 4.6e-7 rad at most.)
 __device__ __forceinline__ float2 cos_sin(int pos, float freq) {
-  // 1 / (2 pi) = 0.15915494309189533576888376..., rounded to fp32, then what that left, twice
-  constexpr float kInvTwoPi0 = 0x1.45f306p-3f, kInvTwoPi1 = 0x1.b9391p-28f, kInvTwoPi2 = 0x1.529fc2p-54f;
-  const float th = freq * kInvTwoPi0, e0 = fmaf(freq, kInvTwoPi0, -th);
-  const float p1 = freq * kInvTwoPi1, e1 = fmaf(freq, kInvTwoPi1, -p1);
-  const float tm = e0 + p1, back = tm - e0;
-  const float tl = (e0 - (tm - back)) + (p1 - back) + fmaf(freq, kInvTwoPi2, e1);
+  const Turns f = turns_of(freq);
+  const float th = f.hi, tm = f.mid, tl = f.low;
   float t = 0.f, rest = 0.f;
   auto add = [&](float part) {
     const float x = t + (part - rintf(part));

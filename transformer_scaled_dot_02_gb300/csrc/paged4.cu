@@ -30,6 +30,29 @@ __device__ __forceinline__ uint32_t e2m1x2(float lo, float hi) {
       : "f"(hi), "f"(lo));
   return r;
 }
+// An e2m1 number.
+__device__ __forceinline__ float e2m1_value(uint32_t code) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 t;\n\tcvt.u8.u32 t, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, t;\n\t}" : "=r"(r) : "r"(code));
+  float f;
+  asm("{\n\t.reg .f16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.f32.f16 %0, lo;\n\t}" : "=f"(f) : "r"(r));
+  return f;
+}
+// Eight floats as e2m1, the first in the low four bits.
+__device__ __forceinline__ uint32_t e2m1x8(const float (&x)[8]) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 a, b, c, d;\n\tcvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\tcvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\tmov.b32 %0, {a, b, c, d};\n\t}"
+      : "=r"(r)
+      : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]));
+  return r;
+}
+__device__ __forceinline__ float rcp_approx(float x) {        // within an ulp
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
 // Two floats as e4m3, `lo` in the low byte.
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
   uint16_t r;
@@ -60,36 +83,130 @@ __device__ __forceinline__ float e4m3_value(uint32_t byte) {
 // The rotation is in fp32 with angles good to 1.3e-6.  Where that leaves open
 // which scale or code is the nearest, some element of a block lies within kSlack
 // of a border between two (about one block in 3000): the block is worked out
-// again in 64 bits, so that the cache holds what the definition says.
-// Of |a| + |b|: the angle, cos and sin's own rounding, and three roundings of products and sum.
-constexpr float kSlack = 1.8e-6f;
+// again in 48 bits, so that the cache holds what the definition says.
+// Of |a| + |b|: the angle, cos and sin's own rounding, and three roundings of products and sum,
+// the sum or difference with it.
+constexpr float kSlack = 2e-6f;
 
-// Columns col .. col + 15 of key row `row` at position pos, in 64 bits, by all
-// lanes of a warp: a lane for each column, as a sine in 64 bits takes 2 us (one
-// lane for the 16 took 30 us, ten times a short call).
-__device__ __noinline__ void block_in_64_bits(const Paged4AppendParams& p, const uint16_t* row, int col, int pos,
+// A number as the sum of two floats, lo at most half a unit in hi's last place: 48
+// bits in Dekker's and Knuth's exact sums and products.  (The card's 64-bit unit takes
+// 300 clock cycles for each operation of a chain: a block took 9 us with them.)
+struct Two {
+  float hi, lo;
+};
+__device__ __forceinline__ Two quick_sum(float a, float b) {  // |a| >= |b|
+  const float s = __fadd_rn(a, b);
+  return {s, __fadd_rn(b, -__fadd_rn(s, -a))};
+}
+__device__ __forceinline__ Two exact_sum(float a, float b) {
+  const float s = __fadd_rn(a, b), z = __fadd_rn(s, -a);
+  return {s, __fadd_rn(__fadd_rn(a, -__fadd_rn(s, -z)), __fadd_rn(b, -z))};
+}
+__device__ __forceinline__ Two exact_product(float a, float b) {
+  const float x = __fmul_rn(a, b);
+  return {x, fmaf(a, b, -x)};
+}
+__device__ __forceinline__ Two operator+(Two a, Two b) {
+  const Two s = exact_sum(a.hi, b.hi);
+  return quick_sum(s.hi, __fadd_rn(s.lo, __fadd_rn(a.lo, b.lo)));
+}
+__device__ __forceinline__ Two operator*(Two a, Two b) {
+  const Two x = exact_product(a.hi, b.hi);
+  return quick_sum(x.hi, __fadd_rn(x.lo, fmaf(a.hi, b.lo, __fmul_rn(a.lo, b.hi))));
+}
+
+// cos and sin of pos * freq, good to 2^-40 while the angle is below 2^30: the angle in
+// turns as in cos_sin, with what its sums round off kept, less the nearest quarter,
+// then Taylor's series up to an eighth of a turn.
+__device__ __forceinline__ void cos_sin_in_48_bits(int pos, float freq, Two* cosine, Two* sine) {
+  const Turns f = turns_of(freq);
+  Two t{0.f, 0.f};
+  auto add = [&](float part) {
+    const Two x = exact_sum(t.hi, __fadd_rn(part, -rintf(part)));
+    t = {x.hi, __fadd_rn(x.lo, t.lo)};
+  };
+#pragma unroll 1
+  for (int i = 0; i < 2; ++i) {
+    const float x = i == 0 ? static_cast<float>(pos >> 12) * 4096.f : static_cast<float>(pos & 4095);
+    const Two a = exact_product(x, f.hi), b = exact_product(x, f.mid);
+    add(a.hi);
+    add(a.lo);
+    add(b.hi);
+    add(fmaf(x, f.low, b.lo));
+  }
+  t = quick_sum(t.hi, t.lo);
+  const float k = rintf(4.f * t.hi);
+  t = exact_sum(fmaf(k, -0.25f, t.hi), t.lo);
+  t = t * Two{0x1.921fb6p+2f, -0x1.777a5cp-23f};              // 2 pi
+  const Two z = t * t;
+  // what of the series is below 2^-15 in one float
+  const float s9 = fmaf(z.hi, fmaf(z.hi, 1.f / 6227020800.f, -1.f / 39916800.f), 1.f / 362880.f);
+  const float c8 = fmaf(z.hi, fmaf(z.hi, fmaf(z.hi, -1.f / 87178291200.f, 1.f / 479001600.f), -1.f / 3628800.f), 1.f / 40320.f);
+  // 1 / n! as two floats
+  Two s = Two{s9, 0.f} * z + Two{-0x1.a01a02p-13f, 0x1.7f97fap-39f}; // -1 / 7!
+  s = s * z + Two{0x1.111112p-7f, -0x1.dddddep-32f};          // 1 / 5!
+  s = s * z + Two{-0x1.555556p-3f, 0x1.555556p-28f};          // -1 / 3!
+  s = s * z * t + t;
+  Two c = Two{c8, 0.f} * z + Two{-0x1.6c16c2p-10f, 0x1.27d27ep-35f}; // -1 / 6!
+  c = c * z + Two{0x1.555556p-5f, -0x1.555556p-30f};          // 1 / 4!
+  c = c * z + Two{-0.5f, 0.f};
+  c = c * z + Two{1.f, 0.f};
+  const int quarter = static_cast<int>(k) & 3;
+  auto negated = [](Two x, bool negate) { return negate ? Two{-x.hi, -x.lo} : x; };
+  *cosine = negated(quarter & 1 ? s : c, quarter == 1 || quarter == 2);
+  *sine = negated(quarter & 1 ? c : s, quarter >= 2);
+}
+
+// Columns col .. col + 15 of key row `row` at position pos, in 48 bits, by all
+// lanes of a warp: a lane for each column (one lane for the 16 took 30 us, ten times a
+// short call).  Of the two scales or codes that 32 bits leave open the border between
+// them decides, which is a float.
+__device__ __noinline__ void block_in_48_bits(const Paged4AppendParams& p, const uint16_t* row, int col, int pos,
                                               int lane, uint2* codes, uint32_t* scale) {
+  constexpr float kDown = 1.f - 0x1p-21f, kUp = 1.f + 0x1p-21f;
   const int half = p.d_rot / 2;
-  auto value = [&](int x) { return static_cast<double>(__uint_as_float(static_cast<uint32_t>(row[x]) << 16)); };
+  auto value = [&](int x) { return __uint_as_float(static_cast<uint32_t>(row[x]) << 16); };
+  auto more = [](Two a, Two b) { return a.hi > b.hi || (a.hi == b.hi && a.lo > b.lo); };
   const int i = lane & 15, x = col + i;
   const int pair = p.interleaved ? x / 2 : (x < half ? x : x - half);
   const bool second = p.interleaved ? (x & 1) : x >= half;
-  const double own = value(x), other = value(p.interleaved ? x ^ 1 : (second ? x - half : x + half));
-  double sn, cs;
-  sincos(static_cast<double>(pos) * static_cast<double>(p.freqs[pair]), &sn, &cs);
-  const double y = (second ? own * cs + other * sn : own * cs - other * sn) * static_cast<double>(p.k_unit);
-  double top = fabs(y);
+  const float own = value(x);
+  float other = value(p.interleaved ? x ^ 1 : (second ? x - half : x + half));
+  if (!second) other = -other;
+  Two cs, sn;
+  cos_sin_in_48_bits(pos, p.freqs[pair], &cs, &sn);
+  const float plain = own * cs.hi + other * sn.hi;
+  Two y{plain, 0.f};
+  if (fabsf(plain) < INFINITY) {
+    const Two a = exact_product(own, cs.hi), b = exact_product(other, sn.hi);
+    y = Two{a.hi, fmaf(own, cs.lo, a.lo)} + Two{b.hi, fmaf(other, sn.lo, b.lo)};
+  }
+  y = {y.hi * p.k_unit, y.lo * p.k_unit};
+  const bool negative = y.hi < 0.f;
+  if (negative) y = {-y.hi, -y.lo};
+  Two top = y.hi == y.hi ? y : Two{0.f, 0.f};
 #pragma unroll
-  for (int z = 8; z > 0; z >>= 1) top = fmax(top, __shfl_xor_sync(0xffffffffu, top, z));
-  // rounded to a float that is odd where it is not exact, a second rounding is as if it were the first
-  auto odd = [](double v) {
-    const float f = __double2float_rz(v);
-    return static_cast<double>(f) != v && isfinite(f) ? __uint_as_float(__float_as_uint(f) | 1u) : f;
-  };
-  const uint32_t s8 = e4m3x2(odd(fmin(top / 6.0, 448.0)), 0.f) & 0xff;
+  for (int z = 8; z > 0; z >>= 1) {
+    const Two o{__shfl_xor_sync(0xffffffffu, top.hi, z), __shfl_xor_sync(0xffffffffu, top.lo, z)};
+    if (more(o, top)) top = o;
+  }
+  const float sixth = top.hi * (1.f / 6.f);
+  const uint32_t s2 = e4m3x2(sixth * kDown, sixth * kUp);
+  uint32_t s8 = s2 & 0xff;
+  if (s8 != s2 >> 8) {
+    const Two border{3.f * (e4m3_value(s8) + e4m3_value(s2 >> 8)), 0.f};
+    if (more(top, border) || (!more(border, top) && (s8 & 1))) s8 = s2 >> 8;
+  }
   const float s = e4m3_value(s8);
-  uint32_t c = s > 0.f ? e2m1x2(odd(fmin(fabs(y) / static_cast<double>(s), 8.0)), 0.f) & 7u : 0u;
-  c = (c | (y < 0.0 ? 8u : 0u)) << (4 * (i & 7));
+  // (a NaN has the largest code)
+  const float a = fminf(y.hi * (s > 0.f ? rcp_approx(s) : 0.f), 8.f);
+  const uint32_t c2 = e2m1x2(a * kDown, a * kUp);
+  uint32_t c = c2 & 7u;
+  if (c != c2 >> 4) {
+    const Two border{0.5f * (e2m1_value(c) + e2m1_value(c2 >> 4)) * s, 0.f};
+    if (more(y, border) || (!more(border, y) && (c & 1))) c = c2 >> 4;
+  }
+  c = (c | (negative ? 8u : 0u)) << (4 * (i & 7));
 #pragma unroll
   for (int z = 1; z < 8; z <<= 1) c |= __shfl_xor_sync(0xffffffffu, c, z);
   *codes = make_uint2(__shfl_sync(0xffffffffu, c, 0), __shfl_sync(0xffffffffu, c, 8));
@@ -103,95 +220,100 @@ __device__ __forceinline__ bool quantise(const float (&y)[16], float off, uint2*
   float top = 0.f;
 #pragma unroll
   for (int i = 0; i < 16; i += 2) top = fmax3(top, fabsf(y[i]), fabsf(y[i + 1]));
-  // a division, as the quotient of a bf16 number may lie between two scales
-  const uint32_t s8 = kOff ? e4m3x2(__fdiv_rn(top + off, 6.f), __fdiv_rn(top - off, 6.f))
-                           : e4m3x2(__fdiv_rn(top, 6.f), 0.f);
-  const float s = e4m3_value(s8 & 0xff);
-  const float inv = s > 0.f ? __frcp_rn(s) : 0.f;
-  uint32_t w[2] = {0, 0}, open = kOff ? (s8 & 0xff) ^ (s8 >> 8) : 0u;
+  uint32_t s8, open = 0;
   if constexpr (kOff) {
-    const float d = fmaf(off, inv * 1.000001f, 2e-6f);       // (and the product's rounding)
-#pragma unroll
-    for (int i = 0; i < 16; i += 2) {
-      const float a = fabsf(y[i]) * inv, b = fabsf(y[i + 1]) * inv;
-      const uint32_t hi = e2m1x2(a + d, b + d);
-      open |= hi ^ e2m1x2(fmaxf(a - d, 0.f), fmaxf(b - d, 0.f));
-      w[i >> 3] |= hi << (4 * (i & 7));
-    }
+    s8 = e4m3x2((top + off) * 0x1.555558p-3f, (top - off) * 0x1.555552p-3f);   // 1/6 from above and below
+    open = (s8 & 0xff) ^ (s8 >> 8);
   } else {
-    // Bf16 numbers may lie on a border itself, but none other lies nearer than 2^-10
-    // to one: the product with 1 / s (off by 2^-22) is rounded to whole 2^-12.
-    constexpr float kSnap = 0x1.8p11f;
+    // A bf16 number may be 6 times a border between two scales, but otherwise lies 2^-9 of
+    // itself or more beside it, as both have at most 8 bits: the product with 1/6 (off by
+    // 2^-23) is rounded to 13 bits.
+    const uint32_t sixth = __float_as_uint(top * 0x1.555556p-3f);
+    s8 = e4m3x2(__uint_as_float((sixth + 0x400u) & ~0x7ffu), 0.f);
+  }
+  s8 &= 0xff;
+  const float s = e4m3_value(s8);
+  const float inv = s > 0.f ? rcp_approx(s) : 0.f;
+  uint32_t w[2];
 #pragma unroll
-    for (int i = 0; i < 16; i += 2) {
-      const float a = __fadd_rn(__fadd_rn(fabsf(y[i]) * inv, kSnap), -kSnap);
-      const float b = __fadd_rn(__fadd_rn(fabsf(y[i + 1]) * inv, kSnap), -kSnap);
-      w[i >> 3] |= e2m1x2(a, b) << (4 * (i & 7));
+  for (int x = 0; x < 2; ++x) {
+    float a[8];
+    if constexpr (kOff) {
+      const float d = fmaf(off, inv * 1.000001f, 2e-6f);     // (and what 1 / s and the products are off by)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) a[i] = fmaf(y[8 * x + i], inv, d);
+      w[x] = e2m1x8(a);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) a[i] = fmaf(y[8 * x + i], inv, -d);
+      open |= (w[x] ^ e2m1x8(a)) & 0x77777777u;              // (a zero's sign is nothing)
+    } else {
+      // Bf16 numbers may lie on a border itself, but none other lies nearer than 2^-10
+      // to one: the product with 1 / s (off by 2^-20) is rounded to whole 2^-12.
+      constexpr float kSnap = 0x1.8p11f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) a[i] = __fadd_rn(fmaf(y[8 * x + i], inv, kSnap), -kSnap);
+      w[x] = e2m1x8(a);
     }
   }
-  uint32_t sign[2] = {0, 0};
-#pragma unroll
-  for (int i = 0; i < 16; ++i) sign[i >> 3] |= __float_as_uint(y[i]) >> 31 << (4 * (i & 7) + 3);
-  *codes = make_uint2(w[0] | sign[0], w[1] | sign[1]);
-  *scale = s8 & 0xff;
+  *codes = make_uint2(w[0], w[1]);
+  *scale = s8;
   return open == 0;
 }
 
 template <int kTokens, int kBlocks>
 __global__ void __launch_bounds__(kThreads, kBlocks) sdpa_paged4_append_kernel(const __grid_constant__ Paged4AppendParams p) {
-  static_assert(kTokens <= kThreads / 32, "a warp finds each token's place");
-  extern __shared__ __align__(16) float2 angles[];            // [kTokens][d_rot / 2]
+  constexpr int kWarps = kThreads / 32;
+  static_assert(kWarps % kTokens == 0, "a warp finds each token's place");
+  // [kTokens][4][d_rot / 16][2]: the pairs' (cos, sin), those of 8 pairs apart so that
+  // lanes that read 16 bytes of neighbouring eights do not meet in a bank
+  extern __shared__ __align__(16) float2 angles[];
   __shared__ long long row_of[kTokens];                       // page row of the token, head 0 (-1: not stored)
   __shared__ int pos_of[kTokens];                             // position (INT_MIN: no sequence's token)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int t0 = static_cast<int>(blockIdx.x) * kTokens;
-  const int half = p.d_rot / 2, rotated_blocks = p.d_rot / 16;
-  const int blocks_mask = (1 << p.log_blocks) - 1;            // items of a head, d / 16
-  const int items = (p.h + 2 * p.h_kv) << p.log_blocks;       // of a token
-  const int all = min(kTokens, p.n_tokens - t0) * items;
+  const int half = p.d_rot / 2;
+  const int heads = p.h + 2 * p.h_kv, warp_heads = 32 >> p.log_blocks;   // that a warp takes at a time
+  const int tokens = min(kTokens, p.n_tokens - t0);
   const int page_rows_mask = (1 << p.page_shift) - 1;
-  struct Item {
-    int token, head, c;                                       // c: of the head's items
-    bool rotated;
-    int c0, c1;                                               // columns of its chunks
-  };
-  auto item_of = [&](int x) {
-    Item it;
-    it.token = kTokens == 1 ? 0 : (p.items_magic != 0 ? __umulhi(x, p.items_magic) : x / items);
-    const int y = x - it.token * items;
-    it.head = y >> p.log_blocks;
-    it.c = y & blocks_mask;
-    it.rotated = it.c < rotated_blocks && it.head < p.h + p.h_kv;
-    const bool apart = it.rotated && !p.interleaved && it.head < p.h;
-    it.c0 = apart ? it.c * 8 : it.c * 16;
-    it.c1 = apart ? it.c0 + half : it.c0 + 8;
-    return it;
-  };
-  auto source = [&](const Item& it) -> const uint16_t* {
-    const long long t = t0 + it.token;
-    if (it.head < p.h) return p.q == nullptr ? nullptr : p.q + t * p.q_stride + it.head * p.d;
-    const int hk = it.head - p.h;
-    return hk < p.h_kv ? p.k + t * p.k_stride + hk * p.d : p.v + t * p.v_stride + (hk - p.h_kv) * p.d;
-  };
+  const int c = lane & ((1 << p.log_blocks) - 1);             // item of the head, in every head
+  const bool rotates = c < p.d_rot / 16;
+  const bool apart = rotates && !p.interleaved;
+  const int q0 = apart ? c * 8 : c * 16, q1 = apart ? q0 + half : q0 + 8;   // columns of a query's chunks
   // a key's column x of a chunk of 8 pairs up with column x + partner
   auto partner = [&](int x) { return x < half ? half : -half; };
+  auto source = [&](int token, int head) -> const uint16_t* {
+    const long long t = t0 + token;
+    if (head < p.h) return p.q == nullptr ? nullptr : p.q + t * p.q_stride + head * p.d;
+    const int hk = head - p.h;
+    return hk < p.h_kv ? p.k + t * p.k_stride + hk * p.d : p.v + t * p.v_stride + (hk - p.h_kv) * p.d;
+  };
   uint4 a, b, pa, pb;
-  auto load = [&](int x) {
-    if (x >= all) return;
-    const Item it = item_of(x);
-    const uint16_t* src = source(it);
+  auto load = [&](int token, int head) {
+    if (head >= heads || token >= tokens) return;
+    const uint16_t* src = source(token, head);
     if (src == nullptr) return;
-    a = *reinterpret_cast<const uint4*>(src + it.c0);
-    b = *reinterpret_cast<const uint4*>(src + it.c1);
-    if (it.rotated && it.head >= p.h && !p.interleaved) {
-      pa = *reinterpret_cast<const uint4*>(src + it.c0 + partner(it.c0));
-      pb = *reinterpret_cast<const uint4*>(src + it.c1 + partner(it.c1));
+    if (head < p.h) {
+      a = *reinterpret_cast<const uint4*>(src + q0);
+      b = *reinterpret_cast<const uint4*>(src + q1);
+      return;
+    }
+    a = *reinterpret_cast<const uint4*>(src + c * 16);
+    b = *reinterpret_cast<const uint4*>(src + c * 16 + 8);
+    if (apart && head < p.h + p.h_kv) {
+      pa = *reinterpret_cast<const uint4*>(src + c * 16 + partner(c * 16));
+      pb = *reinterpret_cast<const uint4*>(src + c * 16 + 8 + partner(c * 16 + 8));
     }
   };
+  // A warp takes warp_heads heads of a token, then the ones kWarps times as many further on.
+  int token = 0, head0 = warp * warp_heads;
+  auto carry = [&]() {
+    for (; head0 >= heads && token < tokens; ++token) head0 -= (heads + warp_heads - 1) & -warp_heads;
+  };
+  carry();
   griddep_launch_dependents();
   griddep_wait();
-  load(threadIdx.x);
-  if (warp < kTokens && t0 + warp < p.n_tokens) {
+  load(token, head0 + (lane >> p.log_blocks));
+  if (warp < tokens) {
     const RowPlace at = place_of_row(p, t0 + warp, lane);
     if (lane == 0) {
       row_of[warp] = at.row;
@@ -199,71 +321,75 @@ __global__ void __launch_bounds__(kThreads, kBlocks) sdpa_paged4_append_kernel(c
     }
   }
   __syncthreads();
-  for (int x = threadIdx.x; x < kTokens * half; x += kThreads) {
-    const int i = x / half;
-    if (t0 + i < p.n_tokens && pos_of[i] != INT_MIN) angles[x] = cos_sin(pos_of[i], p.freqs[x - i * half]);
+  {
+    const int mine = warp % kTokens;                          // token
+    if (mine < tokens && pos_of[mine] != INT_MIN)
+      for (int i = warp / kTokens * 32 + lane; i < half; i += kWarps / kTokens * 32)
+        angles[mine * half + (i >> 1 & 3) * (half >> 2) + (i >> 3) * 2 + (i & 1)] = cos_sin(pos_of[mine], p.freqs[i]);
   }
   __syncthreads();
   // stores a key's or value's block
-  auto store = [&](const Item& it, uint2 codes, uint32_t scale) {
+  auto store = [&](int token, int head, int c, uint2 codes, uint32_t scale) {
     // row_of: page h_kv P + r for page row r of head 0
-    const long long row = row_of[it.token];
+    const long long row = row_of[token];
     const long long r = row & page_rows_mask;
-    const int hk = it.head - p.h;
+    const int hk = head - p.h;
     const bool is_k = hk < p.h_kv;
     uint8_t* page = (is_k ? p.k_pages : p.v_pages) +
                     ((row >> p.page_shift) + (is_k ? hk : hk - p.h_kv)) * (static_cast<long long>(9 * p.d / 16) << p.page_shift);
-    *reinterpret_cast<uint2*>(page + r * (p.d / 2) + it.c * 8) = codes;
-    page[(static_cast<long long>(p.d / 2) << p.page_shift) + (r << p.log_blocks) + it.c] = static_cast<uint8_t>(scale);
+    *reinterpret_cast<uint2*>(page + r * (p.d / 2) + c * 8) = codes;
+    page[(static_cast<long long>(p.d / 2) << p.page_shift) + (r << p.log_blocks) + c] = static_cast<uint8_t>(scale);
   };
-  // Does an item; true: its block has to be worked out in 64 bits.
-  auto work = [&](const Item& it) -> bool {
-    if (pos_of[it.token] == INT_MIN) return false;
-    const float4* turn = reinterpret_cast<const float4*>(angles + it.token * half);   // (cos, sin) of two pairs
+  // Does this lane's item of a head; true: its block has to be worked out in 48 bits.
+  auto work = [&](int token, int head) -> bool {
+    if (head >= heads || pos_of[token] == INT_MIN) return false;
+    // (cos, sin) of pairs 8 c + 2 e and 8 c + 2 e + 1
+    auto turn = [&](int c, int e) { return reinterpret_cast<const float4*>(angles + token * half)[e * (half >> 3) + c]; };
     const uint32_t ua[4] = {a.x, a.y, a.z, a.w}, ub[4] = {b.x, b.y, b.z, b.w};
-    if (it.head < p.h) {
+    if (head < p.h) {
       if (p.q == nullptr) return false;
-      uint16_t* dst = p.q_out + (static_cast<long long>(t0 + it.token) * p.h + it.head) * p.d;
+      uint16_t* dst = p.q_out + (static_cast<long long>(t0 + token) * p.h + head) * p.d;
       uint32_t ra[4], rb[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         ra[e] = ua[e];
         rb[e] = ub[e];
-        if (!it.rotated) continue;
+        if (!rotates) continue;
         const float2 x0 = unpack_bf16x2(ua[e]), x1 = unpack_bf16x2(ub[e]);
         if (p.interleaved) {
-          const float4 r01 = turn[it.c * 4 + e / 2], r45 = turn[it.c * 4 + 2 + e / 2];
+          const float4 r01 = turn(c, e / 2), r45 = turn(c, 2 + e / 2);
           const float2 r0 = e % 2 ? make_float2(r01.z, r01.w) : make_float2(r01.x, r01.y);
           const float2 r1 = e % 2 ? make_float2(r45.z, r45.w) : make_float2(r45.x, r45.y);
           ra[e] = pack_bf16x2(x0.x * r0.x - x0.y * r0.y, x0.y * r0.x + x0.x * r0.y);
           rb[e] = pack_bf16x2(x1.x * r1.x - x1.y * r1.y, x1.y * r1.x + x1.x * r1.y);
         } else {
-          const float4 r = turn[it.c * 4 + e];                // pairs 8 c + 2 e, 8 c + 2 e + 1
+          const float4 r = turn(c, e);
           ra[e] = pack_bf16x2(x0.x * r.x - x1.x * r.y, x0.y * r.z - x1.y * r.w);
           rb[e] = pack_bf16x2(x1.x * r.x + x0.x * r.y, x1.y * r.z + x0.y * r.w);
         }
       }
-      *reinterpret_cast<uint4*>(dst + it.c0) = make_uint4(ra[0], ra[1], ra[2], ra[3]);
-      *reinterpret_cast<uint4*>(dst + it.c1) = make_uint4(rb[0], rb[1], rb[2], rb[3]);
+      *reinterpret_cast<uint4*>(dst + q0) = make_uint4(ra[0], ra[1], ra[2], ra[3]);
+      *reinterpret_cast<uint4*>(dst + q1) = make_uint4(rb[0], rb[1], rb[2], rb[3]);
       return false;
     }
-    if (row_of[it.token] < 0) return false;
-    const float unit = it.head < p.h + p.h_kv ? p.k_unit : p.v_unit;
+    if (row_of[token] < 0) return false;
+    const bool is_k = head < p.h + p.h_kv;
+    const float unit = is_k ? p.k_unit : p.v_unit;
     float y[16];
     uint2 codes;
     uint32_t scale;
-    if (it.rotated) {
+    if (rotates && is_k) {
       float off = 0.f;                                        // the largest |a| + |b|
 #pragma unroll
       for (int ch = 0; ch < 2; ++ch) {
         const uint4 o4 = ch ? b : a, p4 = ch ? pb : pa;
         const uint32_t own[4] = {o4.x, o4.y, o4.z, o4.w}, other[4] = {p4.x, p4.y, p4.z, p4.w};
-        const int x0 = it.c * 16 + ch * 8;
+        const int x0 = c * 16 + ch * 8;
         if (p.interleaved) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const float2 o = unpack_bf16x2(own[e]);
-            const float4 r2 = turn[x0 / 4 + e / 2];
+            const float4 r2 = turn(c, ch * 2 + e / 2);
             const float2 r = e % 2 ? make_float2(r2.z, r2.w) : make_float2(r2.x, r2.y);
             y[ch * 8 + 2 * e] = (o.x * r.x - o.y * r.y) * unit;
             y[ch * 8 + 2 * e + 1] = (o.y * r.x + o.x * r.y) * unit;
@@ -271,11 +397,11 @@ __global__ void __launch_bounds__(kThreads, kBlocks) sdpa_paged4_append_kernel(c
           }
         } else {
           const bool second = x0 >= half;
-          const int base = (second ? x0 - half : x0) / 2;
+          const int eight = (second ? x0 - half : x0) / 8;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const float2 o = unpack_bf16x2(own[e]), t = unpack_bf16x2(other[e]);
-            float4 r = turn[base + e];
+            float4 r = turn(eight, e);
             if (!second) {
               r.y = -r.y;
               r.w = -r.w;
@@ -298,21 +424,23 @@ __global__ void __launch_bounds__(kThreads, kBlocks) sdpa_paged4_append_kernel(c
       }
       quantise<false>(y, 0.f, &codes, &scale);
     }
-    store(it, codes, scale);
+    store(token, head, c, codes, scale);
     return false;
   };
-  for (int x0 = warp * 32; x0 < all; x0 += kThreads) {
-    const int x = x0 + lane;
-    if (x0 != warp * 32) load(x);
-    const Item it = item_of(min(x, all - 1));
-    const bool open = x < all && work(it);
+  for (bool first = true; token < tokens; first = false) {
+    const int head = head0 + (lane >> p.log_blocks);
+    if (!first) load(token, head);
+    const bool open = work(token, head);
     for (uint32_t left = __ballot_sync(0xffffffffu, open); left != 0; left &= left - 1) {
-      const Item its = item_of(x0 + __ffs(left) - 1);
+      const int from = __ffs(left) - 1, its_head = head0 + (from >> p.log_blocks);
+      const int its_c = from & ((1 << p.log_blocks) - 1);
       uint2 codes;
       uint32_t scale;
-      block_in_64_bits(p, source(its), its.c * 16, pos_of[its.token], lane, &codes, &scale);
-      if (lane == 0) store(its, codes, scale);
+      block_in_48_bits(p, source(token, its_head), its_c * 16, pos_of[token], lane, &codes, &scale);
+      if (lane == 0) store(token, its_head, its_c, codes, scale);
     }
+    head0 += kWarps * warp_heads;
+    carry();
   }
 }
 
