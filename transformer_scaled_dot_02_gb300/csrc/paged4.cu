@@ -570,7 +570,7 @@ __global__ void __launch_bounds__(kThreads) sdpa_paged4_read_few_kernel(const __
 cudaError_t launch_sdpa_paged4_append(const Paged4AppendParams& p, cudaStream_t stream) {
   const int sms = device_sm_count();
   if (p.n_tokens <= 4 * sms) return launch_append_impl<1, 4>(p, stream);
-  return launch_append_impl<4, 4>(p, stream);
+  return launch_append_impl<4, 5>(p, stream);
 }
 
 cudaError_t launch_sdpa_paged4_read(const Paged4ReadParams& p, cudaStream_t stream) {

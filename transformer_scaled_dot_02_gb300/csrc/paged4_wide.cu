@@ -347,8 +347,9 @@ struct WCfg {
   static constexpr uint32_t kIdescPV = idesc_f16(128, D, true);
   static constexpr uint32_t kDescHi = (kSBO >> 4) | (1u << 14) | (kLayout << 29);
   static constexpr uint32_t kDescHiKV = (kGroupBytes >> 4) | (1u << 14) | (kLayout << 29);
-  // registers a thread: the launch's 128 (kSub == 2) are split
-  static constexpr int kSoftmaxRegs = 176, kExpandRegs = 96, kRestRegs = 64;
+  // registers a thread: the launch's 128 (kSub == 2) are split (176, 96, 64: 139 us instead of
+  // 136 for 4 chunks of 512, a row's scores being 128 of them)
+  static constexpr int kSoftmaxRegs = 192, kExpandRegs = 72, kRestRegs = 56;
   static_assert(kSub == 1 || 2 * kSoftmaxRegs + kExpandRegs + kRestRegs <= 512, "registers");
 };
 
@@ -581,22 +582,22 @@ __global__ void __launch_bounds__(WCfg<D>::kThreads, 1) sdpa_paged4_many(const _
           // ---- Q: rows scaled by powers of two, as fp16 (the last scores are done with the ones before);
           // kLanes lanes read a row (rows apart by thread touch 32 lines with each load: 7 us)
           const long long mine = reinterpret_cast<long long>(p.q + static_cast<long long>(at.q.start + token) * p.q_stride + head * D);
-          constexpr int kLanes = D / 8, kRowsAtOnce = 32 / kLanes, kLoads = 32 / kRowsAtOnce;
+          constexpr int kLanes = D / 8, kRowsAtOnce = 32 / kLanes, kLoads = 32 / kRowsAtOnce, kAtOnce = 4;
           uint8_t* q_smem = smem + sub * C::kQBytes;
           const int row0 = sub * 128 + quarter * 32;
           float back = 1.f;
 #pragma unroll 1
-          for (int x0 = 0; x0 < kLoads; x0 += 4) {
-            uint4 v[4];
+          for (int x0 = 0; x0 < kLoads; x0 += kAtOnce) {
+            uint4 v[kAtOnce];
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
+            for (int x = 0; x < kAtOnce; ++x) {
               const int r = ((x0 + x) * kRowsAtOnce + lane / kLanes) & 31;
               const long long src = __shfl_sync(0xffffffffu, mine, r);
               v[x] = make_uint4(0, 0, 0, 0);
               if (row0 + r < rows && x0 + x < kLoads) v[x] = reinterpret_cast<const uint4*>(src)[lane % kLanes];
             }
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
+            for (int x = 0; x < kAtOnce; ++x) {
               if (x0 + x >= kLoads) continue;
               const int r = (x0 + x) * kRowsAtOnce + lane / kLanes;
               const uint32_t w[4] = {v[x].x, v[x].y, v[x].z, v[x].w};
@@ -770,10 +771,20 @@ __global__ void __launch_bounds__(WCfg<D>::kThreads, 1) sdpa_paged4_many(const _
           }
           if (!whole && valid) reinterpret_cast<float2*>(own + C::kRows * D * 4)[row] = make_float2(m_used, ll);
         }
-        if (active) {
+        auto release_o = [&]() {
+          if (!active) return;
           tc_fence_before();
           mbar_arrive(o_free + sub);
+        };
+        // This run's piece of two is merged from tensor memory, if no unit comes after it (a
+        // prompt of 4096 takes 90 us so, and 98 with both pieces read back; with d = 256 the
+        // code costs the loop over the keys registers, 65 us instead of 61 for 3 chunks of 200)
+        bool keep = D <= 128 && at.of == 2;
+        if (keep) {
+          if (!(ok = mbar_wait_warp(ready + ((k + 1) & 1), static_cast<uint32_t>((k + 1) >> 1) & 1u, ab))) break;
+          keep = units[(k + 1) & 1].rows == 0;
         }
+        if (!keep) release_o();
         if (!whole) {
           unsigned long long* count = p.counts + slot_of(at, 0);
           __threadfence();
@@ -784,8 +795,54 @@ __global__ void __launch_bounds__(WCfg<D>::kThreads, 1) sdpa_paged4_many(const _
             if (last_one) *count = 0;
           }
           if (!(ok = meet())) break;
-          if (last_one != 0 && busy && active)
-            merge_rows<D>(p, at, turn, out, rows_here, row);
+          if (last_one != 0 && busy && active) {
+            if (!keep) {
+              merge_rows<D>(p, at, turn, out, rows_here, row);
+            } else {
+              // the most frequent case: this run's piece from tensor memory, half the reading
+              const int mine = cta - at.first_run;
+              const uint8_t* slot = p.slots + static_cast<long long>(slot_of(at, 1 - mine)) * p.slot_bytes;
+              const int rw = min(row, rows - 1);
+              const float2 ml = __ldcg(reinterpret_cast<const float2*>(slot + C::kRows * D * 4) + rw);
+              const float4* src = reinterpret_cast<const float4*>(slot) + rw;
+              const float mm = fmaxf(m_used, ml.x), base = mm == -INFINITY ? 0.f : mm;
+              const float g = weight(m_used, base), g2 = weight(ml.x, base);
+              const float l0 = mine == 0 ? ll * g : ml.y * g2, l1 = mine == 0 ? ml.y * g2 : ll * g;
+              const float sum = l0 + l1, f = sum > 0.f ? p.v_unit / sum : 0.f;
+              constexpr int kVec = C::kOChunk / 4, kChunks = D / C::kOChunk;
+              float4 x[kVec], x2[kVec];
+              auto fetch = [&](int c, float4 (&to)[kVec]) {
+                if (c >= kChunks) return;
+#pragma unroll
+                for (int e = 0; e < kVec; ++e) to[e] = __ldcg(src + (c * kVec + e) * C::kRows);
+              };
+              fetch(0, x);
+              auto step = [&](int c, const float4 (&x)[kVec]) {
+                uint32_t o[C::kOChunk];
+                load_o(c, o);
+                // (the products are rounded before the sum: which piece is this run's does not show)
+                auto both = [&](uint32_t& a, float b) {
+                  a = __float_as_uint(__fadd_rn(__fmul_rn(__uint_as_float(a), g), __fmul_rn(b, g2)));
+                };
+#pragma unroll
+                for (int e = 0; e < kVec; ++e) {
+                  both(o[4 * e], x[e].x);
+                  both(o[4 * e + 1], x[e].y);
+                  both(o[4 * e + 2], x[e].z);
+                  both(o[4 * e + 3], x[e].w);
+                }
+                store_rows<D>(turn, out, rows_here, c, o, f);
+              };
+#pragma unroll 1
+              for (int c = 0; c < kChunks; c += 2) {
+                fetch(c + 1, x2);
+                step(c, x);
+                fetch(c + 2, x);
+                if (c + 1 < kChunks) step(c + 1, x2);
+              }
+            }
+          }
+          if (keep) release_o();
           // (last_one has been read)
           if (!(ok = meet())) break;
         }
