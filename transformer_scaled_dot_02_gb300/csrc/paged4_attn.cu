@@ -16,7 +16,7 @@
 // the piece ends.  CTAs are small, so that others on the SM work while one's
 // warps meet.  The copies are cp.async, 16 bytes a lane, 9 instructions a tile at
 // d = 128: as bulk copies, four for the codes and scales of K and V, a tile took
-// the SM's copy engine 600 clock cycles (41 us instead of @@ for 32 sequences of
+// the SM's copy engine 600 clock cycles (41 us instead of 38 for 32 sequences of
 // 4096 to 8192 positions).  A step for single tokens is bound by reading the cache, so what
 // counts is that few instructions stand between a byte and its products.  They
 // are mma.sync on registers: tcgen05 takes its operands from shared memory (or A
@@ -51,10 +51,9 @@ constexpr int kKeys = 32;                  // per tile
 constexpr int kKeysShift = 5;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units, as in the other forward kernels
 // What a unit costs beside its key tiles, in key tiles.
-#ifndef KSTART
-#define KSTART 20
-#endif
-constexpr int kStart = KSTART;
+// (32 single tokens of 4096 to 8192 positions: 39.3, 37.9 and 37.3 us with 8, 14 and 20;
+// 32 of 2000 to 4000 with one key-value head: 25.2, 21.9 and 20.5)
+constexpr int kStart = 20;
 constexpr int kMinRun = 16;                // items of a run, at least
 // How the work is cut.  kPieces: every unit into pieces of its own, a run for each,
 // where that many runs fit the GPU; a walk of up to kWhole key tiles is one piece,
@@ -582,14 +581,14 @@ __global__ void __launch_bounds__(kThreads, NCfg<D, NT>::kCtas) sdpa_paged4_few(
               if (n >= 32 || lane < n) cp_async16_or_zeros(to + y * 16, from + y * 16, get);
           };
           // (the scales of K and V by one instruction where 32 lanes do)
-          auto rows = [&](auto share, int page, int r, uint32_t codes_to, uint32_t scales_to) {
+          auto rows = [&](auto share, int page, long long r, uint32_t codes_to, uint32_t scales_to) {
             constexpr int n = decltype(share)::value;         // of the tile's rows, one in n
             std::integral_constant<int, C::kCodes / 16 / n> codes;
             std::integral_constant<int, C::kScales / 16 / n> scales;
             const bool get = page >= 0;
             const long long off = get ? page * p.page_stride : 0;
             const uint8_t *k = k_head + off + lane * 16, *v = v_head + off + lane * 16;
-            const int at_codes = r * (D / 2), at_scales = r * (D / 16);
+            const long long at_codes = r * (D / 2), at_scales = r * (D / 16);
             copy(dst + codes_to, k + at_codes, codes, get);
             copy(dst + C::kHalf + codes_to, v + at_codes, codes, get);
             const long long skip = (static_cast<long long>(D / 2) << p.page_shift) + at_scales;
