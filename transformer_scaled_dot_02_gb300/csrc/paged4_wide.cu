@@ -936,6 +936,9 @@ __global__ void __launch_bounds__(WCfg<D>::kThreads, 1) sdpa_paged4_many(const _
                            b0 + static_cast<uint32_t>(((k / kS) * C::kSBO + (k % kS) * 32) >> 4), C::kDescHiKV, C::kIdescS,
                            k > 0 ? 1u : 0u);
         }
+#ifdef SDPA_TEST_WITHHOLD_FIRST_S_COMMIT
+        if (us > 0)                                          // failure injection for the timeout test
+#endif
         mma_commit_warp(s_full + (C::kBufs == 2 ? buf : sub));
         mma_commit_warp(k_empty + u % R);
       };
