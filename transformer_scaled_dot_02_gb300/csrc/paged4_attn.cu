@@ -375,7 +375,9 @@ __device__ __forceinline__ void load_bytes(const uint8_t* at, uint32_t (&w)[N < 
 template <int D, int NT>
 struct NCfg {
   // CTAs on an SM: with 168 registers a thread nothing is spilled in the loop for up
-  // to 128 columns (of rows of 8), with 255 for twice as many
+  // to 128 columns (of rows of 8), with 255 for twice as many.  (A fourth CTA: with 128
+  // registers 58 us instead of 37 for 32 tokens of d = 128, spilled; for 64 columns,
+  // where nothing is spilled, 27.3 instead of 27.8 for 16 sequences of four rows.)
   static constexpr int kCtas = D * NT <= 128 ? 3 : 2;
   static constexpr int kStages = D * NT <= 128 ? 3 : D == 128 ? 3 : 2;   // tiles of a warp's ring
   static constexpr int kRows = 8 * NT;
@@ -679,20 +681,20 @@ __global__ void __launch_bounds__(kThreads, NCfg<D, NT>::kCtas) sdpa_paged4_few(
           }
           __syncwarp();
         }
-        const uint8_t* vs = ks + C::kHalf;
-#pragma unroll 2
-        for (int half = 0; half < 2; ++half, ks += 16 * (D / 2), vs += 16 * (D / 2)) {
-          // ---- scores of keys g and g + 8 in rows 2 t, 2 t + 1
-          float s[NT][4];
+        // ---- scores of keys g and g + 8 of each half in rows 2 t, 2 t + 1
+        float s[2][NT][4];
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
           {
+            const uint8_t* kh = ks + half * (16 * (D / 2));
             constexpr int kB = D / 8, kW = kB < 4 ? 1 : kB / 4;   // bytes, words of a lane's columns
             constexpr int kSB = D >= 64 ? D / 64 : 1;             // scales of a lane's columns
-            const uint8_t* scales = ks + C::kCodes - half * (16 * (D / 2 - D / 16)) + (D >= 64 ? t * kSB : t * D / 64);
+            const uint8_t* scales = kh + C::kCodes - half * (16 * (D / 2 - D / 16)) + (D >= 64 ? t * kSB : t * D / 64);
             uint32_t w[2][kW], sw[2];
 #pragma unroll
             for (int hh = 0; hh < 2; ++hh) {
               const int row = hh * 8 + g;
-              load_bytes<kB>(ks + row * (D / 2) + t * kB, w[hh]);
+              load_bytes<kB>(kh + row * (D / 2) + t * kB, w[hh]);
               uint32_t sb[1];
               load_bytes<kSB>(scales + row * (D / 16), sb);
               sw[hh] = sb[0];
@@ -700,7 +702,7 @@ __global__ void __launch_bounds__(kThreads, NCfg<D, NT>::kCtas) sdpa_paged4_few(
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-              for (int e = 0; e < 4; ++e) s[nt][e] = 0.f;
+              for (int e = 0; e < 4; ++e) s[half][nt][e] = 0.f;
 #pragma unroll
             for (int wi = 0; wi < kW; ++wi) {
               uint32_t a[2][4];
@@ -717,7 +719,7 @@ __global__ void __launch_bounds__(kThreads, NCfg<D, NT>::kCtas) sdpa_paged4_few(
               for (int e = 0; e < kSteps; ++e)
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
-                  mma_f16(s[nt], a[0][2 * e], a[1][2 * e], a[0][2 * e + 1], a[1][2 * e + 1], qf[wi * 2 + e][nt][0],
+                  mma_f16(s[half][nt], a[0][2 * e], a[1][2 * e], a[0][2 * e + 1], a[1][2 * e + 1], qf[wi * 2 + e][nt][0],
                           qf[wi * 2 + e][nt][1]);
             }
           }
@@ -731,10 +733,12 @@ __global__ void __launch_bounds__(kThreads, NCfg<D, NT>::kCtas) sdpa_paged4_few(
 #pragma unroll
                 for (int hh = 0; hh < 2; ++hh) {
                   const int j = key0 + half * 16 + hh * 8 + g;
-                  if (j > pp || (j <= pp - p.window && j >= p.sinks)) s[nt][2 * hh + c] = -INFINITY;
+                  if (j > pp || (j <= pp - p.window && j >= p.sinks)) s[half][nt][2 * hh + c] = -INFINITY;
                 }
               }
           }
+        }
+        {
           // ---- the running maxima: they move when one grew by more than the threshold
           bool need = false;
           float top[NT][2];
@@ -742,7 +746,7 @@ __global__ void __launch_bounds__(kThreads, NCfg<D, NT>::kCtas) sdpa_paged4_few(
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-              top[nt][c] = fmaxf(s[nt][c], s[nt][2 + c]) * sc[nt][c];
+              top[nt][c] = fmaxf(fmax3(s[0][nt][c], s[0][nt][2 + c], s[1][nt][c]), s[1][nt][2 + c]) * sc[nt][c];
               need |= top[nt][c] > m[nt][c] + kRescaleThreshold;
             }
           if (__any_sync(0xffffffffu, need)) {
@@ -764,20 +768,24 @@ __global__ void __launch_bounds__(kThreads, NCfg<D, NT>::kCtas) sdpa_paged4_few(
                 }
               }
           }
-          // ---- weights, turned so that a lane holds two keys of a row
-          uint32_t pb[NT][2];
+        }
+        // ---- weights, turned so that a lane holds two keys of a row
+        uint32_t pb[2][NT][2];
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            const float m0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0], m1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
+        for (int nt = 0; nt < NT; ++nt) {
+          const float m0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0], m1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
 #pragma unroll
-            for (int hh = 0; hh < 2; ++hh) {
-              const float p0 = ex2_approx(fmaf(s[nt][2 * hh], sc[nt][0], -m0));
-              const float p1 = ex2_approx(fmaf(s[nt][2 * hh + 1], sc[nt][1], -m1));
-              l[nt][0] += p0;
-              l[nt][1] += p1;
-              pb[nt][hh] = transpose8x8(pack_f16x2(p0, p1));
-            }
+          for (int x = 0; x < 4; ++x) {
+            const float p0 = ex2_approx(fmaf(s[x >> 1][nt][2 * (x & 1)], sc[nt][0], -m0));
+            const float p1 = ex2_approx(fmaf(s[x >> 1][nt][2 * (x & 1) + 1], sc[nt][1], -m1));
+            l[nt][0] += p0;
+            l[nt][1] += p1;
+            pb[x >> 1][nt][x & 1] = transpose8x8(pack_f16x2(p0, p1));
           }
+        }
+        const uint8_t* vs = ks + C::kHalf;
+#pragma unroll
+        for (int half = 0; half < 2; ++half, vs += 16 * (D / 2)) {
           // ---- O^T += V^T P: keys 2 t, 2 t + 1, 2 t + 8, 2 t + 9
           constexpr int kB = D / 16, kW = kB < 4 ? 1 : kB / 4;
           constexpr int kSB = D >= 128 ? D / 128 : 1;
@@ -811,7 +819,7 @@ __global__ void __launch_bounds__(kThreads, NCfg<D, NT>::kCtas) sdpa_paged4_few(
             for (int e = 0; e < (kB < 4 ? kB : 4); ++e)
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt)
-                mma_f16(o[wi * 4 + e][nt], a[0][e], a[1][e], a[2][e], a[3][e], pb[nt][0], pb[nt][1]);
+                mma_f16(o[wi * 4 + e][nt], a[0][e], a[1][e], a[2][e], a[3][e], pb[half][nt][0], pb[half][nt][1]);
           }
         }
       }
