@@ -154,6 +154,34 @@ def test_append_rotated_borders_at_position_zero():
     _append(rng, [1] * 5, [1] * 5, 4, 4, d, 16, d_rot=32, rows=(k, k.copy(), k.copy()))
 
 
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("d,d_rot", [(64, 64), (128, 128), (256, 96), (16, 16)])
+def test_append_angles_of_zero(d, d_rot, interleaved):
+    """Pairs that do not turn (a frequency of zero), whole eights of them and some
+    among others, at every position, and position 0: ties are as frequent as in
+    rows that are not rotated at all."""
+    import torch
+    rng = np.random.default_rng(1901 + d)
+    freqs = pu.freqs_of(d_rot)
+    freqs[rng.random(len(freqs)) < 0.3] = 0.0
+    freqs[len(freqs) // 2:] = 0.0
+    n, h_kv, page = 70, 2, 32
+    cache = pu.Cache(rng, [n], h_kv, d, page)
+    # few significant bits: many elements on borders
+    k = np.round(rng.standard_normal((n, h_kv, d)).astype(np.float32) * 4) / 4
+    kp, vp = (torch.zeros((cache.n_pages, h_kv, page, 9 * d // 16), dtype=torch.uint8, device="cuda") for _ in range(2))
+    sd.paged4_append(None, dev(k), dev(k), kp, vp, dev_int(cache.table), dev_int(pu.starts_of([n])), dev_int([n]),
+                     torch.from_numpy(freqs).cuda(), interleaved=interleaved)
+    sd.sdpa_device_check()
+    for pages, x in ((kp, pu.rotate(k, np.arange(n), freqs, interleaved)[0]), (vp, k.astype(np.float64))):
+        codes, scales = p4.quantise(x)
+        got_codes, got_scales = p4.parts(pages.cpu().numpy(), d)
+        for i in range(n):
+            at = cache.table[0, i // page], slice(None), i % page
+            assert np.array_equal(got_scales[at], scales[i])
+            assert not ((got_codes[at] != codes[i]) & ((got_codes[at] & 7 != 0) | (codes[i] & 7 != 0))).any()
+
+
 def test_append_without_finite_rows_holds_finite_scales():
     import torch
     rng = np.random.default_rng(1305)

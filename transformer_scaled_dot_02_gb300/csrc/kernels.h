@@ -213,7 +213,9 @@ int paged4_resident_ctas(int d, int rows);             // CTAs that share an SM
 long long paged4_most_runs(long long units, long long max_len);   // that this much work is cut into
 cudaError_t launch_sdpa_paged4(const Paged4Params& p, int d, cudaStream_t stream);
 // The kernel for the other sequences: p.slots, p.counts, p.runs and p.slot_bytes are its own.
-constexpr int kPaged4FewRows = 16;
+// (16 sequences of 2000 to 4000 positions with 16, 32 and 64 rows a head, 4 heads of d = 128: 27, 34
+// and 52 us there, 44, 45 and 47 in the kernel for many rows)
+constexpr int kPaged4FewRows = 32;
 constexpr int kPaged4WideMaxRuns = 160;
 int paged4_wide_rows(int d);                           // rows of a row tile
 long long paged4_wide_most_runs(long long units, long long max_len);

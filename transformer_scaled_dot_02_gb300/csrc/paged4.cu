@@ -74,23 +74,25 @@ __device__ __forceinline__ float e4m3_value(uint32_t byte) {
 // rounding to bf16.
 //
 // It reads (h + 2 h_kv) d bf16 a token and writes h d bf16 and 9/16 h_kv d
-// bytes, and is bound by HBM (by the launch for a few tokens).  An item is 16
-// columns of a head: of a query the two chunks of 8 whose columns pair up, of a
-// key or value a block (the rotation reads its partners' columns beside it).
-// Blocks take kTokens tokens: their angles once, into shared memory, then every
-// head of theirs.
+// bytes.  An item is 16 columns of a head: of a query the two chunks of 8 whose
+// columns pair up, of a key or value a block (the rotation reads its partners'
+// columns beside it).  Blocks take kTokens tokens: their angles once, into shared
+// memory, then every head of theirs.  16384 tokens (16 query heads, 4 of keys, d =
+// 128, all columns rotated): 45 us, 4.1 TB/s, issue slots 70 % busy, by the rotation
+// and the quantising (35 us where the queries were only copied, 34 where the keys
+// were too).  For a few tokens the launch and three dependent reads: 2.9 us for 8.
 //
 // The rotation is in fp32 with angles good to 1.3e-6.  Where that leaves open
 // which scale or code is the nearest, some element of a block lies within kSlack
-// of a border between two (about one block in 3000): the block is worked out
+// of a border between two (one block in 970 of normal numbers): the block is worked out
 // again in 48 bits, so that the cache holds what the definition says.
 // Of |a| + |b|: the angle, cos and sin's own rounding, and three roundings of products and sum,
 // the sum or difference with it.
 constexpr float kSlack = 2e-6f;
 
 // A number as the sum of two floats, lo at most half a unit in hi's last place: 48
-// bits in Dekker's and Knuth's exact sums and products.  (The card's 64-bit unit takes
-// 300 clock cycles for each operation of a chain: a block took 9 us with them.)
+// bits in Dekker's and Knuth's exact sums and products.  (The card has few 64-bit units:
+// with them a block in doubt took half as long again.)
 struct Two {
   float hi, lo;
 };
@@ -269,6 +271,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) sdpa_paged4_append_kernel(c
   extern __shared__ __align__(16) float2 angles[];
   __shared__ long long row_of[kTokens];                       // page row of the token, head 0 (-1: not stored)
   __shared__ int pos_of[kTokens];                             // position (INT_MIN: no sequence's token)
+  __shared__ uint8_t turned[kTokens][16];                     // of each eight pairs: some angle is not zero
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int t0 = static_cast<int>(blockIdx.x) * kTokens;
   const int half = p.d_rot / 2;
@@ -324,8 +327,16 @@ __global__ void __launch_bounds__(kThreads, kBlocks) sdpa_paged4_append_kernel(c
   {
     const int mine = warp % kTokens;                          // token
     if (mine < tokens && pos_of[mine] != INT_MIN)
-      for (int i = warp / kTokens * 32 + lane; i < half; i += kWarps / kTokens * 32)
-        angles[mine * half + (i >> 1 & 3) * (half >> 2) + (i >> 3) * 2 + (i & 1)] = cos_sin(pos_of[mine], p.freqs[i]);
+      for (int i0 = warp / kTokens * 32; i0 < half; i0 += kWarps / kTokens * 32) {
+        const int i = i0 + lane;
+        float2 r = make_float2(1.f, 0.f);
+        if (i < half) {
+          r = cos_sin(pos_of[mine], p.freqs[i]);
+          angles[mine * half + (i >> 1 & 3) * (half >> 2) + (i >> 3) * 2 + (i & 1)] = r;
+        }
+        const uint32_t turns = __ballot_sync(0xffffffffu, r.y != 0.f);
+        if ((lane & 7) == 0 && i < half) turned[mine][i >> 3] = (turns >> lane & 0xff) != 0;
+      }
   }
   __syncthreads();
   // stores a key's or value's block
@@ -378,7 +389,14 @@ __global__ void __launch_bounds__(kThreads, kBlocks) sdpa_paged4_append_kernel(c
     float y[16];
     uint2 codes;
     uint32_t scale;
-    if (rotates && is_k) {
+    // (Where every angle is zero, as at position 0, the rotation is exact, and ties are
+    // frequent: half of such blocks would be in doubt, one after another in their warp, 8 us.)
+    auto turns = [&]() {
+      if (p.interleaved) return turned[token][c] != 0;
+      const int eights = half >> 3, e0 = 2 * c < eights ? 2 * c : 2 * c - eights, e1 = 2 * c + 1 < eights ? 2 * c + 1 : 2 * c + 1 - eights;
+      return (turned[token][e0] | turned[token][e1]) != 0;
+    };
+    if (rotates && is_k && turns()) {
       float off = 0.f;                                        // the largest |a| + |b|
 #pragma unroll
       for (int ch = 0; ch < 2; ++ch) {
@@ -569,13 +587,16 @@ __global__ void __launch_bounds__(kThreads) sdpa_paged4_read_few_kernel(const __
 
 cudaError_t launch_sdpa_paged4_append(const Paged4AppendParams& p, cudaStream_t stream) {
   const int sms = device_sm_count();
-  if (p.n_tokens <= 4 * sms) return launch_append_impl<1, 4>(p, stream);
+  // (608, 1216 and 2432 tokens of 16 + 2 x 4 heads of d = 128: 5.0, 7.9 and 12.4 us with a
+  // block for each token, 6.4, 8.9 and 10.6 with one for four)
+  if (p.n_tokens <= 8 * sms) return launch_append_impl<1, 4>(p, stream);
   return launch_append_impl<4, 5>(p, stream);
 }
 
 cudaError_t launch_sdpa_paged4_read(const Paged4ReadParams& p, cudaStream_t stream) {
   const int sms = device_sm_count();
-  // (2258 tokens of 8 heads of d = 64: 4.2 us with a block each, 5.0 with one for 32)
+  // (1216, 2432 and 4864 tokens of 4 heads of d = 128: 3.0, 4.4 and 6.8 us with a block
+  // each, 4.8, 4.8 and 4.7 with one for 32)
   if (p.n_tokens <= 16 * sms)
     return launch_kernel(sdpa_paged4_read_few_kernel, dim3(static_cast<unsigned>(p.n_tokens)), dim3(kThreads), 0, stream,
                          true, p);

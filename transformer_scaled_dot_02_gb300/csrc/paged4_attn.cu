@@ -60,7 +60,10 @@ constexpr int kMinRun = 16;                // items of a run, at least
 // a longer one has pieces of about kPiece.  kItems: into
 // equal runs.
 enum Scheme { kItems, kPieces };
-constexpr int kWhole = 12, kPiece = 8;
+// (8 sequences of 300 to 500 positions, 8 heads of keys, d = 128: 10.7 us with kWhole = 16,
+// 11.5 with 12 or 8; one of 300 positions 7.1 and, with 8, 10.3.  4 of 1000: 11.4 us with kPiece
+// = 8, 13.3 with 6, 11.9 with 12.)
+constexpr int kWhole = 16, kPiece = 8;
 constexpr int kTogether = 16;              // pieces that one run merges, at most (more in two steps)
 
 // ------------------------------------------------------------------ schedule
@@ -948,6 +951,8 @@ cudaError_t launch_d(const Paged4Params& p, cudaStream_t stream) {
 
 }  // namespace
 
+// Rows of a row tile: 8 where the sequences have that many on average.  (16 sequences of
+// 4 rows: 28 us, and 34 with tiles of 16; of 16 rows: 26.9 with 16, 27.5 with 8.)
 int paged4_rows(int group, int n_tokens, int b) {
   return 1ll * group * n_tokens <= 8ll * b ? 8 : 16;
 }
