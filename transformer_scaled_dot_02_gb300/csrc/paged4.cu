@@ -79,8 +79,8 @@ __device__ __forceinline__ float e4m3_value(uint32_t byte) {
 // columns beside it).  Blocks take kTokens tokens: their angles once, into shared
 // memory, then every head of theirs.  16384 tokens (16 query heads, 4 of keys, d =
 // 128, all columns rotated): 46 us, 3.9 TB/s, issue slots 70 % busy, by the rotation
-// and the quantising (35 us where the queries were only copied, 34 where the keys
-// were too).  For a few tokens the launch and three dependent reads: 2.9 us for 8.
+// and the quantising (38 us where the queries were only copied, 35 where nothing
+// was rotated or quantised).  For a few tokens the launch and three dependent reads: 2.9 us for 8.
 //
 // The rotation is in fp32 with angles good to 1.3e-6.  Where that leaves open
 // which scale or code is the nearest, some element of a block lies within kSlack
