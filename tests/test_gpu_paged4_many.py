@@ -116,6 +116,30 @@ def test_repeats_bit_by_bit():
     sd.sdpa_device_check()
 
 
+def test_repeats_whichever_run_comes_last():
+    """Units in two pieces, merged by the run of the one or of the other: copies of
+    odd sizes in another stream change which of them is the last."""
+    import torch
+    rng = np.random.default_rng(4506)
+    other, junk = torch.cuda.Stream(), torch.empty(2, 1 << 22, device="cuda")
+    for new, lens, h, h_kv, d, window in (([700, 300], [1500, 4000], 12, 2, 128, 500), ([500], [500], 16, 2, 64, 0),
+                                          ([2000], [2000], 4, 2, 32, 0)):
+        c = _case(rng, new, lens, h, h_kv, d, 32, window=window, sinks=4 if window else 0)
+        args, kw = _args(c), _kw(c)
+        ws = sd.paged4_workspace(args[0], args[1], args[3])
+        want = sd.paged4_attention(*args, **kw, workspace=ws)
+        outs = [torch.empty_like(want) for _ in range(50)]
+        for i in range(100):
+            if i % 3 == 0:
+                n = int(rng.integers(1 << 10, 1 << 22))
+                with torch.cuda.stream(other):
+                    junk[0, :n].copy_(junk[1, :n])
+            sd.paged4_attention(*args, **kw, out=outs[i % 50], workspace=ws)
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, want) for x in outs)
+    sd.sdpa_device_check()
+
+
 def test_graphs_that_share_a_workspace_follow_starts_and_lengths():
     """Two graphs of calls of 200 rows, whose starts change between replays from one
     sequence's chunk to single tokens and back."""

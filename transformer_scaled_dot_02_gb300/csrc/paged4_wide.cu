@@ -807,8 +807,12 @@ __global__ void __launch_bounds__(WCfg<D>::kThreads, 1) sdpa_paged4_many(const _
               const float4* src = reinterpret_cast<const float4*>(slot) + rw;
               const float mm = fmaxf(m_used, ml.x), base = mm == -INFINITY ? 0.f : mm;
               const float g = weight(m_used, base), g2 = weight(ml.x, base);
-              const float l0 = mine == 0 ? ll * g : ml.y * g2, l1 = mine == 0 ? ml.y * g2 : ll * g;
-              const float sum = l0 + l1, f = sum > 0.f ? p.v_unit / sum : 0.f;
+              // (rounded as merge_rows does it, which merges this unit where the other run is the
+              // last: the first piece's product, then the second's added with one rounding)
+              auto sum_of = [&](float own, float other) {
+                return mine == 0 ? fmaf(other, g2, __fmul_rn(own, g)) : fmaf(own, g, __fmul_rn(other, g2));
+              };
+              const float sum = sum_of(ll, ml.y), f = sum > 0.f ? p.v_unit / sum : 0.f;
               constexpr int kVec = C::kOChunk / 4, kChunks = D / C::kOChunk;
               float4 x[kVec], x2[kVec];
               auto fetch = [&](int c, float4 (&to)[kVec]) {
@@ -820,10 +824,7 @@ __global__ void __launch_bounds__(WCfg<D>::kThreads, 1) sdpa_paged4_many(const _
               auto step = [&](int c, const float4 (&x)[kVec]) {
                 uint32_t o[C::kOChunk];
                 load_o(c, o);
-                // (the products are rounded before the sum: which piece is this run's does not show)
-                auto both = [&](uint32_t& a, float b) {
-                  a = __float_as_uint(__fadd_rn(__fmul_rn(__uint_as_float(a), g), __fmul_rn(b, g2)));
-                };
+                auto both = [&](uint32_t& a, float b) { a = __float_as_uint(sum_of(__uint_as_float(a), b)); };
 #pragma unroll
                 for (int e = 0; e < kVec; ++e) {
                   both(o[4 * e], x[e].x);
