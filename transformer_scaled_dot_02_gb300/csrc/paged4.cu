@@ -78,7 +78,7 @@ __device__ __forceinline__ float e4m3_value(uint32_t byte) {
 // columns pair up, of a key or value a block (the rotation reads its partners'
 // columns beside it).  Blocks take kTokens tokens: their angles once, into shared
 // memory, then every head of theirs.  16384 tokens (16 query heads, 4 of keys, d =
-// 128, all columns rotated): 46 us, 3.9 TB/s, issue slots 70 % busy, by the rotation
+// 128, all columns rotated): 45 us, 4 TB/s, issue slots 70 % busy, by the rotation
 // and the quantising (38 us where the queries were only copied, 35 where nothing
 // was rotated or quantised).  For a few tokens the launch and three dependent reads: 2.9 us for 8.
 //
@@ -236,6 +236,11 @@ __device__ __forceinline__ bool quantise(const float (&y)[16], float off, uint2*
   s8 &= 0xff;
   const float s = e4m3_value(s8);
   const float inv = s > 0.f ? rcp_approx(s) : 0.f;
+  auto near = [&](float* to, const float* from, float by) {
+    const float2 v = __ffma2_rn(make_float2(from[0], from[1]), make_float2(inv, inv), make_float2(by, by));
+    to[0] = v.x;
+    to[1] = v.y;
+  };
   uint32_t w[2];
 #pragma unroll
   for (int x = 0; x < 2; ++x) {
@@ -243,10 +248,10 @@ __device__ __forceinline__ bool quantise(const float (&y)[16], float off, uint2*
     if constexpr (kOff) {
       const float d = fmaf(off, inv * 1.000001f, 2e-6f);     // (and what 1 / s and the products are off by)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) a[i] = fmaf(y[8 * x + i], inv, d);
+      for (int i = 0; i < 8; i += 2) near(a + i, y + 8 * x + i, d);
       w[x] = e2m1x8(a);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) a[i] = fmaf(y[8 * x + i], inv, -d);
+      for (int i = 0; i < 8; i += 2) near(a + i, y + 8 * x + i, -d);
       open |= (w[x] ^ e2m1x8(a)) & 0x77777777u;              // (a zero's sign is nothing)
     } else {
       // Bf16 numbers may lie on a border itself, but none other lies nearer than 2^-10
@@ -266,7 +271,7 @@ template <int kTokens, int kBlocks>
 __global__ void __launch_bounds__(kThreads, kBlocks) sdpa_paged4_append_kernel(const __grid_constant__ Paged4AppendParams p) {
   constexpr int kWarps = kThreads / 32;
   static_assert(kWarps % kTokens == 0, "a warp finds each token's place");
-  // [kTokens][4][d_rot / 16][2]: the pairs' (cos, sin), those of 8 pairs apart so that
+  // [kTokens][4][d_rot / 16]: (cos, cos, sin, sin) of two pairs, those of 8 pairs apart so that
   // lanes that read 16 bytes of neighbouring eights do not meet in a bank
   extern __shared__ __align__(16) float2 angles[];
   __shared__ long long row_of[kTokens];                       // page row of the token, head 0 (-1: not stored)
@@ -332,7 +337,9 @@ __global__ void __launch_bounds__(kThreads, kBlocks) sdpa_paged4_append_kernel(c
         float2 r = make_float2(1.f, 0.f);
         if (i < half) {
           r = cos_sin(pos_of[mine], p.freqs[i]);
-          angles[mine * half + (i >> 1 & 3) * (half >> 2) + (i >> 3) * 2 + (i & 1)] = r;
+          float* at = reinterpret_cast<float*>(angles + mine * half + (i >> 1 & 3) * (half >> 2) + (i >> 3) * 2) + (i & 1);
+          at[0] = r.x;
+          at[2] = r.y;
         }
         const uint32_t turns = __ballot_sync(0xffffffffu, r.y != 0.f);
         if ((lane & 7) == 0 && i < half) turned[mine][i >> 3] = (turns >> lane & 0xff) != 0;
@@ -354,7 +361,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) sdpa_paged4_append_kernel(c
   // Does this lane's item of a head; true: its block has to be worked out in 48 bits.
   auto work = [&](int token, int head) -> bool {
     if (head >= heads || pos_of[token] == INT_MIN) return false;
-    // (cos, sin) of pairs 8 c + 2 e and 8 c + 2 e + 1
+    // of pairs 8 c + 2 e and 8 c + 2 e + 1: cos, cos, sin, sin
     auto turn = [&](int c, int e) { return reinterpret_cast<const float4*>(angles + token * half)[e * (half >> 3) + c]; };
     const uint32_t ua[4] = {a.x, a.y, a.z, a.w}, ub[4] = {b.x, b.y, b.z, b.w};
     if (head < p.h) {
@@ -369,14 +376,17 @@ __global__ void __launch_bounds__(kThreads, kBlocks) sdpa_paged4_append_kernel(c
         const float2 x0 = unpack_bf16x2(ua[e]), x1 = unpack_bf16x2(ub[e]);
         if (p.interleaved) {
           const float4 r01 = turn(c, e / 2), r45 = turn(c, 2 + e / 2);
-          const float2 r0 = e % 2 ? make_float2(r01.z, r01.w) : make_float2(r01.x, r01.y);
-          const float2 r1 = e % 2 ? make_float2(r45.z, r45.w) : make_float2(r45.x, r45.y);
+          const float2 r0 = e % 2 ? make_float2(r01.y, r01.w) : make_float2(r01.x, r01.z);
+          const float2 r1 = e % 2 ? make_float2(r45.y, r45.w) : make_float2(r45.x, r45.z);
           ra[e] = pack_bf16x2(x0.x * r0.x - x0.y * r0.y, x0.y * r0.x + x0.x * r0.y);
           rb[e] = pack_bf16x2(x1.x * r1.x - x1.y * r1.y, x1.y * r1.x + x1.x * r1.y);
         } else {
           const float4 r = turn(c, e);
-          ra[e] = pack_bf16x2(x0.x * r.x - x1.x * r.y, x0.y * r.z - x1.y * r.w);
-          rb[e] = pack_bf16x2(x1.x * r.x + x0.x * r.y, x1.y * r.z + x0.y * r.w);
+          const float2 cs = make_float2(r.x, r.y), sn = make_float2(r.z, r.w);
+          const float2 p0 = __fmul2_rn(x1, sn), p1 = __fmul2_rn(x0, sn);
+          const float2 y0 = __ffma2_rn(x0, cs, make_float2(-p0.x, -p0.y)), y1 = __ffma2_rn(x1, cs, p1);
+          ra[e] = pack_bf16x2(y0.x, y0.y);
+          rb[e] = pack_bf16x2(y1.x, y1.y);
         }
       }
       *reinterpret_cast<uint4*>(dst + q0) = make_uint4(ra[0], ra[1], ra[2], ra[3]);
@@ -408,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) sdpa_paged4_append_kernel(c
           for (int e = 0; e < 4; ++e) {
             const float2 o = unpack_bf16x2(own[e]);
             const float4 r2 = turn(c, ch * 2 + e / 2);
-            const float2 r = e % 2 ? make_float2(r2.z, r2.w) : make_float2(r2.x, r2.y);
+            const float2 r = e % 2 ? make_float2(r2.y, r2.w) : make_float2(r2.x, r2.z);
             y[ch * 8 + 2 * e] = (o.x * r.x - o.y * r.y) * unit;
             y[ch * 8 + 2 * e + 1] = (o.y * r.x + o.x * r.y) * unit;
             off = fmaxf(off, fabsf(o.x) + fabsf(o.y));
@@ -419,13 +429,11 @@ __global__ void __launch_bounds__(kThreads, kBlocks) sdpa_paged4_append_kernel(c
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const float2 o = unpack_bf16x2(own[e]), t = unpack_bf16x2(other[e]);
-            float4 r = turn(eight, e);
-            if (!second) {
-              r.y = -r.y;
-              r.w = -r.w;
-            }
-            y[ch * 8 + 2 * e] = (o.x * r.x + t.x * r.y) * unit;
-            y[ch * 8 + 2 * e + 1] = (o.y * r.z + t.y * r.w) * unit;
+            const float4 r = turn(eight, e);
+            const float2 sn = second ? make_float2(r.z, r.w) : make_float2(-r.z, -r.w);
+            const float2 v = __fmul2_rn(__ffma2_rn(o, make_float2(r.x, r.y), __fmul2_rn(t, sn)), make_float2(unit, unit));
+            y[ch * 8 + 2 * e] = v.x;
+            y[ch * 8 + 2 * e + 1] = v.y;
             off = fmax3(off, fabsf(o.x) + fabsf(t.x), fabsf(o.y) + fabsf(t.y));
           }
         }
