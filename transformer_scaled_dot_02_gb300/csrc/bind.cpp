@@ -61,8 +61,8 @@ bool check_cache(const at::Tensor& k, const at::Tensor& v, const at::Tensor& tab
   c->device = static_cast<int>(k.get_device());
   if (c->device != c10::cuda::current_device()) return false;
   const at::ScalarType held = d4 > 0 ? at::kByte : at::kBFloat16;
-  if (!plain(k, held, c->device) || !plain(v, held, c->device) || !plain(table, at::kInt, c->device) || !plain(starts, at::kInt, c->device) ||
-      !plain(lengths, at::kInt, c->device))
+  if (!plain(k, held, c->device) || !plain(v, held, c->device) || !plain(table, at::kInt, c->device) ||
+      !plain(starts, at::kInt, c->device) || !plain(lengths, at::kInt, c->device))
     return false;
   if (k.dim() != 4 || v.sizes() != k.sizes() || table.dim() != 2 || starts.dim() != 1 || lengths.dim() != 1)
     return false;
@@ -264,7 +264,8 @@ PyObject* forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
       ws = w->data_ptr();
       ws_bytes = w->nbytes();
     } else {
-      ws_bytes = (k4 ? workspace4_entry : workspace_entry)(c.b, static_cast<int>(t), static_cast<int>(h), c.h_kv, c.d, c.page, c.per_seq);
+      ws_bytes = (k4 ? workspace4_entry : workspace_entry)(c.b, static_cast<int>(t), static_cast<int>(h), c.h_kv, c.d,
+                                                          c.page, c.per_seq);
       if (ws_bytes > 0) {
         made_ws = at::empty({static_cast<int64_t>(ws_bytes)}, q.options().dtype(at::kByte));
         ws = made_ws.data_ptr();

@@ -37,9 +37,11 @@ namespace sdpa {
 namespace {
 
 constexpr float kRescaleThreshold = 8.0f;  // log2 units, as in the other forward kernels
-// What a unit costs beside its keys (loading Q, storing O), in keys.
+// What a unit costs beside its keys (loading Q, storing O), in keys.  (A prompt of 4096: 99, 90 and
+// 94 us with 256, 512 and 1024; 16 sequences of 128 rows 54, 50 and 52.)
 constexpr int kStartKeys = 512;
-constexpr int kMinRunKeys = 512;           // of a run, at least
+// Of a run, at least.  (3 chunks of 200 tokens of d = 256: 60.5, 60.8 and 62.3 us with 256, 512 and 1024.)
+constexpr int kMinRunKeys = 512;
 
 // ------------------------------------------------------------------ schedule
 struct Seq {
