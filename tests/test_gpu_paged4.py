@@ -346,6 +346,21 @@ def test_attention_uneven_walks():
     _check(_run(c), c)
 
 
+@pytest.mark.parametrize("b,length,window,h,h_kv", [
+    (28, 2000, 0, 8, 4), (28, 4000, 0, 8, 4), (100, 800, 0, 4, 4), (64, 1000, 0, 8, 4), (64, 2000, 0, 4, 4),
+    (24, 3000, 1000, 8, 8), (48, 2000, 700, 4, 4), (4, 1000, 0, 16, 1), (33, 500, 0, 40, 2)])
+def test_attention_cuts(b, length, window, h, h_kv):
+    """Walks of about one length, of which there are just as many as the ways to cut
+    them differ by, and lengths around them."""
+    rng = np.random.default_rng(3450 + b + length)
+    lens = [length + int(x) for x in rng.integers(-length // 3, length // 3, size=b)]
+    c = _case(rng, [1] * b, lens, h, h_kv, 64, 64, window=window, sinks=4 if window else 0)
+    _check(_run(c), c)
+    lens = [length] * b
+    c = _case(rng, [1] * b, lens, h, h_kv, 64, 64, window=window, sinks=4 if window else 0)
+    _check(_run(c), c)
+
+
 def test_attention_many_sequences():
     rng = np.random.default_rng(3401)
     lens = [int(x) for x in rng.integers(0, 200, size=600)]

@@ -55,15 +55,19 @@ constexpr float kRescaleThreshold = 8.0f;  // log2 units, as in the other forwar
 // 32 of 2000 to 4000 with one key-value head: 25.2, 21.9 and 20.5)
 constexpr int kStart = 20;
 constexpr int kMinRun = 16;                // items of a run, at least
-// How the work is cut.  kPieces: every unit into pieces of its own, a run for each,
-// where that many runs fit the GPU; a walk of up to kWhole key tiles is one piece,
-// a longer one has pieces of about kPiece.  kItems: into
-// equal runs.
-enum Scheme { kItems, kPieces };
-// (8 sequences of 300 to 500 positions, 8 heads of keys, d = 128: 10.7 us with kWhole = 16,
-// 11.5 with 12 or 8; one of 300 positions 7.1 and, with 8, 10.3.  4 of 1000: 11.4 us with kPiece
-// = 8, 13.3 with 6, 11.9 with 12.)
-constexpr int kWhole = 16, kPiece = 8;
+// How the work is cut.  At a level every unit is cut into pieces of its own, a run for
+// each, of up to 8 << level key tiles, where that many runs fit the GPU; a walk of up to
+// kWhole tiles is one piece, and at the last level one of more than 64 is cut as at the first.
+// kItems: into equal runs, which end and begin inside units.
+// Level 0: 8 sequences of 300 to 500 positions, 8 heads of keys, d = 128: 10.6 us with kWhole = 16,
+// 11.5 with 12 or 8; 4 of 1000: 11.4 us with pieces of 8, 13.3 of 6, 11.9 of 12.
+// Levels 1 to 3 instead of equal runs (sequences of single tokens, 4 heads of d = 128): 28 of 2000
+// 17.5 us instead of 19.0, 28 of 4000 24.2 instead of 25.5, 100 of 800 18.2 instead of 25.4, 96 with a
+// window of 1000 22.6 instead of 28.7.  With more runs left without work they lose: 27.9 instead of
+// 26.9 for 16 sequences of 16 rows (level 2, a third of the runs), 31.4 instead of 29.7 for 64 of 2000
+// (whole walks, 62 key tiles where an equal run has 46).
+constexpr int kItems = -1, kLevels = 4, kWhole = 16;
+constexpr int kMergeItems = 12;            // what publishing and merging a piece takes, in key tiles
 constexpr int kTogether = 16;              // pieces that one run merges, at most (more in two steps)
 
 // ------------------------------------------------------------------ schedule
@@ -123,10 +127,14 @@ struct Plan {
     }
     return tiles;
   }
-  __device__ __forceinline__ int pieces(int tiles) const { return tiles <= kWhole ? 1 : (tiles + kPiece - 1) / kPiece; }
+  __device__ __forceinline__ int pieces(int tiles, int level) const {
+    if (tiles <= kWhole) return 1;
+    const int shift = level == kLevels - 1 && tiles > 8 << level ? 3 : 3 + level;
+    return (tiles + (1 << shift) - 1) >> shift;
+  }
   // items of a unit
-  __device__ __forceinline__ int cost(const Seq& q, Scheme scheme) const {
-    return scheme == kPieces ? pieces(most_tiles(q)) : kStart + most_tiles(q);
+  __device__ __forceinline__ int cost(const Seq& q, int level) const {
+    return level != kItems ? pieces(most_tiles(q), level) : kStart + most_tiles(q);
   }
 };
 
@@ -152,10 +160,10 @@ struct Unit {
 struct Cut {
   long long each;
   int over, runs;
-  Scheme scheme;
-  __device__ void set(long long work, int most, Scheme how) {
-    scheme = how;
-    if (how == kPieces) {
+  int level;                               // or kItems
+  __device__ void set(long long work, int most, int at_level) {
+    level = at_level;
+    if (level != kItems) {
       runs = static_cast<int>(work);
       each = 1;
       over = 0;
@@ -186,10 +194,10 @@ __device__ __forceinline__ void set_piece(const Plan<R>& plan, const Cut& cut, i
   u->kt0 = u->kt1 = 0;
   u->first_run = c;
   u->of = 1;
-  if (cut.scheme == kPieces) {
+  if (cut.level != kItems) {
     // (as many as the sequence's longest walk is worth: this one may have fewer key tiles)
     const int j = static_cast<int>(x0 - u->begin);
-    u->of = min(plan.cost(u->q, kPieces), max(tiles.count, 1));
+    u->of = min(plan.cost(u->q, cut.level), max(tiles.count, 1));
     u->first_run = c - j;
     if (j < u->of) {
       u->kt0 = static_cast<int>(divide(1ll * j * tiles.count, u->of));
@@ -209,7 +217,8 @@ __device__ __forceinline__ void set_piece(const Plan<R>& plan, const Cut& cut, i
 // The whole block: the cut, and the unit in which run c begins.  Returns false
 // when there is no such run.
 struct Schedule {
-  long long items[kWarps], pieces[kWarps];
+  long long mine[kWarps];
+  uint32_t pieces[kWarps][kLevels + 1];
   Cut cut;
 };
 
@@ -221,56 +230,76 @@ __device__ bool find_place(const Plan<R>& plan, Schedule* sh, Unit* first, int c
   const bool alone = p.b <= 32;
   const int per = alone ? 1 : (p.b + kThreads - 1) / kThreads;
   const int s0 = min((alone ? lane : tid) * per, p.b), s1 = min(s0 + per, p.b);
-  long long items = 0, pieces = 0;
+  long long items = 0;
+  uint32_t pieces[kLevels] = {};                             // (as good as too many from 2^20 on)
   Seq q;
   for (int s = s0; s < s1; ++s) {
     q = plan.seq(s);
     const int tiles = plan.most_tiles(q);
     const long long units = 1ll * q.tiles * p.h_kv;
     items += (kStart + tiles) * units;
-    pieces += plan.pieces(tiles) * units;
-  }
-  long long items_to = items, pieces_to = pieces;            // of the threads up to this one
 #pragma unroll
-  for (int x = 1; x < 32; x <<= 1) {
-    const long long i = __shfl_up_sync(0xffffffffu, items_to, x), n = __shfl_up_sync(0xffffffffu, pieces_to, x);
-    if (lane >= x) {
-      items_to += i;
-      pieces_to += n;
-    }
+    for (int x = 0; x < kLevels; ++x)
+      pieces[x] = static_cast<uint32_t>(min(1ll << 20, pieces[x] + plan.pieces(tiles, x) * units));
   }
-  long long all_items = __shfl_sync(0xffffffffu, items_to, 31), all_pieces = __shfl_sync(0xffffffffu, pieces_to, 31);
   if (tid == 0) first->begin = LLONG_MAX;                    // (no unit, should the lengths change meanwhile)
+  uint32_t all[kLevels + 1];                                 // the last: items
+#pragma unroll
+  for (int x = 0; x < kLevels; ++x) all[x] = __reduce_add_sync(0xffffffffu, pieces[x]);
+  all[kLevels] = __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(min(1ll << 20, items)));
   if (!alone) {
-    if (lane == 31) {
-      sh->items[warp] = items_to;
-      sh->pieces[warp] = pieces_to;
+    if (lane == 0) {
+#pragma unroll
+      for (int x = 0; x <= kLevels; ++x) sh->pieces[warp][x] = all[x];
     }
     __syncthreads();
-    all_items = all_pieces = 0;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      if (w == warp) {
-        items_to += all_items;
-        pieces_to += all_pieces;
-      }
-      all_items += sh->items[w];
-      all_pieces += sh->pieces[w];
+    for (int x = 0; x <= kLevels; ++x) {
+      all[x] = 0;
+      for (int w = 0; w < kWarps; ++w) all[x] += sh->pieces[w][x];
     }
   }
-  if (all_items == 0) return false;
-  const Scheme scheme = all_pieces <= p.runs ? kPieces : kItems;
+  if (all[0] == 0) return false;
+  // The finest level that fits, if it leaves few runs without work.  Whole walks: if they are
+  // not longer on average than an equal run, by more than what merging takes.
+  int level = kItems;
+  const uint32_t runs = static_cast<uint32_t>(p.runs);
+  if (all[3] <= runs && 1ull * (all[kLevels] - all[3] * kStart) * runs <= (all[kLevels] + kMergeItems * runs) * 1ull * all[3])
+    level = 3;
+  if (16 * all[2] >= 13 * runs && all[2] <= runs) level = 2;
+  if (8 * all[1] >= 5 * runs && all[1] <= runs) level = 1;
+  if (all[0] <= runs) level = 0;
+  long long mine = items;
+#pragma unroll
+  for (int x = 0; x < kLevels; ++x)
+    if (level == x) mine = pieces[x];
+  long long to = mine;                                       // of the threads up to this one
+#pragma unroll
+  for (int x = 1; x < 32; x <<= 1) {
+    const long long i = __shfl_up_sync(0xffffffffu, to, x);
+    if (lane >= x) to += i;
+  }
+  long long work = __shfl_sync(0xffffffffu, to, 31);
+  if (!alone) {
+    if (lane == 31) sh->mine[warp] = to;
+    __syncthreads();
+    work = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      if (w == warp) to += work;
+      work += sh->mine[w];
+    }
+  }
   Cut cut;
-  cut.set(scheme == kPieces ? all_pieces : all_items, p.runs, scheme);
+  cut.set(work, p.runs, level);
   if (c >= cut.runs) return false;
   const long long x = cut.begin(c);
   if (tid == 0) sh->cut = cut;
-  const long long mine = scheme == kPieces ? pieces : items;
-  long long before = (scheme == kPieces ? pieces_to : items_to) - mine;
+  long long before = to - mine;
   if (mine > 0 && before <= x && x < before + mine && (!alone || warp == 0)) {
     for (int s = s0; s < s1; ++s) {
       if (per > 1) q = plan.seq(s);
-      const int unit = plan.cost(q, scheme);
+      const int unit = plan.cost(q, level);
       const long long all = 1ll * unit * q.tiles * p.h_kv;
       if (x < before + all) {
         const long long i = divide(x - before, unit);
@@ -294,7 +323,7 @@ __device__ bool find_place(const Plan<R>& plan, Schedule* sh, Unit* first, int c
 // One thread: the unit after *u, false if there is none of run c's.
 template <int R>
 __device__ __noinline__ bool next_unit(const Plan<R>& plan, const Cut& cut, int c, Unit* u) {
-  u->begin += plan.cost(u->q, cut.scheme);
+  u->begin += plan.cost(u->q, cut.level);
   if (u->begin >= cut.begin(c + 1)) return false;
   if (++u->r == u->q.tiles) {
     u->r = 0;
