@@ -466,10 +466,27 @@ __device__ __noinline__ void merge_rows(const Paged4Params& p, const Unit& at, u
   }
 }
 
+// The whole block: drafts and other short rows beside single tokens leave this kernel
+// nothing, which the starts alone tell before anything is set up.  (Looked at where rows are
+// few on average: 16 sequences of 16 rows 25.2 us instead of 26.9.)
+__device__ __noinline__ bool nothing_to_do(const Paged4Params& p) {
+  if (1ll * p.n_tokens * p.group > 1ll * p.few_rows * p.b) return false;
+  bool mine = false;
+  for (int s = threadIdx.x; s < p.b; s += blockDim.x) {
+    const int start = min(max(p.q_starts[s], 0), p.n_tokens);
+    mine |= 1ll * (min(max(p.q_starts[s + 1], start), p.n_tokens) - start) * p.group > p.few_rows;
+  }
+  return __syncthreads_or(mine) == 0;
+}
+
 template <int D>
 __global__ void __launch_bounds__(WCfg<D>::kThreads, 1) sdpa_paged4_many(const __grid_constant__ Paged4Params p) {
   using C = WCfg<D>;
   constexpr int R = C::kRing, kBN = C::kBN, kBNShift = C::kBNShift;
+  if (nothing_to_do(p)) {
+    griddep_wait();
+    return;
+  }
   extern __shared__ uint8_t smem_raw[];
   __shared__ Schedule sched;
   __shared__ Unit units[2];
