@@ -62,6 +62,11 @@ struct Plan {
   static constexpr int kBN = 1 << kBNShift;                  // keys of a tile
   const Paged4Params& p;
   __device__ explicit Plan(const Paged4Params& params) : p(params) {}
+  // rows of a head
+  __device__ __forceinline__ long long rows(int s) const {
+    const int start = min(max(p.q_starts[s], 0), p.n_tokens);
+    return 1ll * (min(max(p.q_starts[s + 1], start), p.n_tokens) - start) * p.group;
+  }
   __device__ __forceinline__ Seq seq(int s) const {
     Seq q;
     const int cap = p.pages_per_seq << p.page_shift;
@@ -349,9 +354,9 @@ struct WCfg {
   static constexpr uint32_t kIdescPV = idesc_f16(128, D, true);
   static constexpr uint32_t kDescHi = (kSBO >> 4) | (1u << 14) | (kLayout << 29);
   static constexpr uint32_t kDescHiKV = (kGroupBytes >> 4) | (1u << 14) | (kLayout << 29);
-  // registers a thread: the launch's 128 (kSub == 2) are split (176, 96, 64: 139 us instead of
-  // 136 for 4 chunks of 512, a row's scores being 128 of them)
-  static constexpr int kSoftmaxRegs = 192, kExpandRegs = 72, kRestRegs = 56;
+  // registers a thread: the launch's 128 (kSub == 2) are split, a row's scores being 128 of them
+  // (4 chunks of 512 tokens: 134 us; with 192, 72, 56 136, with 176, 96, 64 139, with 208, 32, 64 138)
+  static constexpr int kSoftmaxRegs = 200, kExpandRegs = 48, kRestRegs = 64;
   static_assert(kSub == 1 || 2 * kSoftmaxRegs + kExpandRegs + kRestRegs <= 512, "registers");
 };
 
@@ -466,26 +471,21 @@ __device__ __noinline__ void merge_rows(const Paged4Params& p, const Unit& at, u
   }
 }
 
-// The whole block: drafts and other short rows beside single tokens leave this kernel
-// nothing, which the starts alone tell before anything is set up.  (Looked at where rows are
-// few on average: 16 sequences of 16 rows 25.2 us instead of 26.9.)
-__device__ __noinline__ bool nothing_to_do(const Paged4Params& p) {
-  if (1ll * p.n_tokens * p.group > 1ll * p.few_rows * p.b) return false;
-  bool mine = false;
-  for (int s = threadIdx.x; s < p.b; s += blockDim.x) {
-    const int start = min(max(p.q_starts[s], 0), p.n_tokens);
-    mine |= 1ll * (min(max(p.q_starts[s + 1], start), p.n_tokens) - start) * p.group > p.few_rows;
-  }
-  return __syncthreads_or(mine) == 0;
-}
-
 template <int D>
 __global__ void __launch_bounds__(WCfg<D>::kThreads, 1) sdpa_paged4_many(const __grid_constant__ Paged4Params p) {
   using C = WCfg<D>;
   constexpr int R = C::kRing, kBN = C::kBN, kBNShift = C::kBNShift;
-  if (nothing_to_do(p)) {
-    griddep_wait();
-    return;
+  const Plan<C::kRows, kBNShift> plan(p);
+  // Drafts and other short rows beside single tokens leave this kernel nothing, which the
+  // starts alone tell before anything is set up.  (Looked at where rows are few on average: 16
+  // sequences of 16 rows 25.2 us instead of 26.9; looked at in any call a prompt of 4096 took 1.2 us more.)
+  if (1ll * p.n_tokens * p.group <= 1ll * p.few_rows * p.b) {
+    bool mine = false;
+    for (int s = threadIdx.x; s < p.b; s += C::kThreads) mine |= plan.rows(s) > p.few_rows;
+    if (__syncthreads_or(mine) == 0) {
+      griddep_wait();
+      return;
+    }
   }
   extern __shared__ uint8_t smem_raw[];
   __shared__ Schedule sched;
@@ -554,7 +554,6 @@ __global__ void __launch_bounds__(WCfg<D>::kThreads, 1) sdpa_paged4_many(const _
   // The kernel before is the one for the other sequences: it began when the one before
   // it was over, and is waited for at the end only.
 
-  const Plan<C::kRows, kBNShift> plan(p);
   const int cta = static_cast<int>(blockIdx.x);
   const bool any = find_place(plan, &sched, &units[0], cta) && units[0].begin != LLONG_MAX;
   tc_fence_after();
