@@ -343,7 +343,8 @@ sdpa_status sdpa_paged_forward(const void* q, const void* k_pages, const void* v
  *
  * sdpa_paged4_append is sdpa_paged_append into such a cache: queries are rotated
  * and rounded to bf16, keys are rotated and quantised from the rotation itself,
- * as if worked out exactly where the nearest scale or code is in doubt.  Rows
+ * worked out to 2^-40 where the nearest scale or code is in doubt (angles below
+ * 2^30, beyond that as well as the angle itself is known).  Rows
  * must be finite: infinities count as the largest number, of a NaN only that
  * something finite is stored.  Pages that overlap each other, the rows or q_out
  * return SDPA_ERR_INVALID_ARG.

@@ -182,6 +182,37 @@ def test_append_angles_of_zero(d, d_rot, interleaved):
             assert not ((got_codes[at] != codes[i]) & ((got_codes[at] & 7 != 0) | (codes[i] & 7 != 0))).any()
 
 
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("last", [(1 << 20) + 5, (1 << 29) - 3])
+def test_append_at_far_positions(last, interleaved):
+    """Angles of up to 2^29: the reference's products and functions in more than 64 bits."""
+    import torch
+    rng = np.random.default_rng(1950 + interleaved)
+    d, h_kv, page, n = 64, 3, 512, 300
+    per_seq = last // page + 1
+    table = np.full((1, per_seq), -1, np.int32)
+    table[0, -2:] = 1, 0
+    freqs = pu.freqs_of(d, 100.0)
+    k = _bf16(rng, (n, h_kv, d))
+    kp, vp = (torch.zeros((2, h_kv, page, 9 * d // 16), dtype=torch.uint8, device="cuda") for _ in range(2))
+    sd.paged4_append(None, dev(k), dev(k), kp, vp, dev_int(table), dev_int(pu.starts_of([n])), dev_int([last]),
+                     torch.from_numpy(freqs).cuda(), interleaved=interleaved)
+    sd.sdpa_device_check()
+    pos = np.arange(last - n, last)
+    angle = pos.astype(np.longdouble)[:, None, None] * freqs.astype(np.longdouble)
+    c, s = np.cos(angle), np.sin(angle)
+    lo, hi = (slice(0, d, 2), slice(1, d, 2)) if interleaved else (slice(0, d // 2), slice(d // 2, d))
+    x = k.astype(np.longdouble)
+    y = x.copy()
+    y[..., lo], y[..., hi] = x[..., lo] * c - x[..., hi] * s, x[..., hi] * c + x[..., lo] * s
+    codes, scales = p4.quantise(y.astype(np.float64))
+    got_codes, got_scales = p4.parts(kp.cpu().numpy(), d)
+    for i in range(n):
+        at = table[0, pos[i] // page], slice(None), pos[i] % page
+        assert np.array_equal(got_scales[at], scales[i])
+        assert not ((got_codes[at] != codes[i]) & ((got_codes[at] & 7 != 0) | (codes[i] & 7 != 0))).any()
+
+
 def test_append_without_finite_rows_holds_finite_scales():
     import torch
     rng = np.random.default_rng(1305)
