@@ -182,18 +182,14 @@ def test_append_angles_of_zero(d, d_rot, interleaved):
             assert not ((got_codes[at] != codes[i]) & ((got_codes[at] & 7 != 0) | (codes[i] & 7 != 0))).any()
 
 
-@pytest.mark.parametrize("interleaved", [False, True])
-@pytest.mark.parametrize("last", [(1 << 20) + 5, (1 << 29) - 3])
-def test_append_at_far_positions(last, interleaved):
-    """Angles of up to 2^29: the reference's products and functions in more than 64 bits."""
+def _append_far(rng, k, last, freqs, interleaved):
+    """Rows k as the last ones of a sequence of `last` positions, against a reference
+    whose angles and functions are worked out in more than 64 bits."""
     import torch
-    rng = np.random.default_rng(1950 + interleaved)
-    d, h_kv, page, n = 64, 3, 512, 300
-    per_seq = last // page + 1
-    table = np.full((1, per_seq), -1, np.int32)
+    n, h_kv, d = k.shape
+    page = 512
+    table = np.full((1, last // page + 1), -1, np.int32)
     table[0, -2:] = 1, 0
-    freqs = pu.freqs_of(d, 100.0)
-    k = _bf16(rng, (n, h_kv, d))
     kp, vp = (torch.zeros((2, h_kv, page, 9 * d // 16), dtype=torch.uint8, device="cuda") for _ in range(2))
     sd.paged4_append(None, dev(k), dev(k), kp, vp, dev_int(table), dev_int(pu.starts_of([n])), dev_int([last]),
                      torch.from_numpy(freqs).cuda(), interleaved=interleaved)
@@ -211,6 +207,23 @@ def test_append_at_far_positions(last, interleaved):
         at = table[0, pos[i] // page], slice(None), pos[i] % page
         assert np.array_equal(got_scales[at], scales[i])
         assert not ((got_codes[at] != codes[i]) & ((got_codes[at] & 7 != 0) | (codes[i] & 7 != 0))).any()
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("last", [(1 << 20) + 5, (1 << 29) - 3])
+def test_append_at_far_positions(last, interleaved):
+    rng = np.random.default_rng(1950 + interleaved)
+    _append_far(rng, _bf16(rng, (300, 3, 64)), last, pu.freqs_of(64, 100.0), interleaved)
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("pos", [491701844, 245850922, 710])
+def test_append_next_to_whole_and_half_turns(pos, interleaved):
+    """Angles that are a few 1e-9 (or 1e-5) beside a multiple of pi: elements on a border
+    but for that."""
+    rng = np.random.default_rng(1960 + interleaved)
+    k = np.round(rng.standard_normal((1, 40, 64)).astype(np.float32) * 4) / 4
+    _append_far(rng, k, pos + 1, np.ones(32, np.float32), interleaved)
 
 
 def test_append_without_finite_rows_holds_finite_scales():

@@ -334,14 +334,16 @@ __global__ void __launch_bounds__(kThreads, kBlocks) sdpa_paged4_append_kernel(c
     if (mine < tokens && pos_of[mine] != INT_MIN)
       for (int i0 = warp / kTokens * 32; i0 < half; i0 += kWarps / kTokens * 32) {
         const int i = i0 + lane;
-        float2 r = make_float2(1.f, 0.f);
+        bool turns_here = false;
         if (i < half) {
-          r = cos_sin(pos_of[mine], p.freqs[i]);
+          const float freq = p.freqs[i];
+          const float2 r = cos_sin(pos_of[mine], freq);
+          turns_here = pos_of[mine] != 0 && freq != 0.f;     // (a sine may be rounded to zero)
           float* at = reinterpret_cast<float*>(angles + mine * half + (i >> 1 & 3) * (half >> 2) + (i >> 3) * 2) + (i & 1);
           at[0] = r.x;
           at[2] = r.y;
         }
-        const uint32_t turns = __ballot_sync(0xffffffffu, r.y != 0.f);
+        const uint32_t turns = __ballot_sync(0xffffffffu, turns_here);
         if ((lane & 7) == 0 && i < half) turned[mine][i >> 3] = (turns >> lane & 0xff) != 0;
       }
   }
@@ -403,7 +405,8 @@ __global__ void __launch_bounds__(kThreads, kBlocks) sdpa_paged4_append_kernel(c
     // frequent: half of such blocks would be in doubt, one after another in their warp, 8 us.)
     auto turns = [&]() {
       if (p.interleaved) return turned[token][c] != 0;
-      const int eights = half >> 3, e0 = 2 * c < eights ? 2 * c : 2 * c - eights, e1 = 2 * c + 1 < eights ? 2 * c + 1 : 2 * c + 1 - eights;
+      const int eights = half >> 3, e0 = 2 * c < eights ? 2 * c : 2 * c - eights;
+      const int e1 = 2 * c + 1 < eights ? 2 * c + 1 : 2 * c + 1 - eights;
       return (turned[token][e0] | turned[token][e1]) != 0;
     };
     if (rotates && is_k && turns()) {
