@@ -599,7 +599,8 @@ __global__ void __launch_bounds__(kThreads) sdpa_paged4_read_few_kernel(const __
 cudaError_t launch_sdpa_paged4_append(const Paged4AppendParams& p, cudaStream_t stream) {
   const int sms = device_sm_count();
   // (608, 1216 and 2432 tokens of 16 + 2 x 4 heads of d = 128: 5.0, 7.9 and 12.4 us with a
-  // block for each token, 6.4, 8.9 and 10.6 with one for four)
+  // block for each token, 6.4, 8.9 and 10.6 with one for four.  Registers for five blocks on an SM:
+  // 2258 and 16384 tokens 8.7 and 44.6 us, for six 9.5 and 44.0; eight tokens a block 11.5 and 44.2)
   if (p.n_tokens <= 8 * sms) return launch_append_impl<1, 4>(p, stream);
   return launch_append_impl<4, 5>(p, stream);
 }

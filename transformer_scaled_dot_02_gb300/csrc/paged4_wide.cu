@@ -19,13 +19,14 @@
 // to fp16 (2^-12: bf16's 2^-9 would cost a third of the result's own half step).
 //
 // What bounds it: a key tile (128 keys, 256 rows, d = 128) takes 2048 clock cycles of
-// the tensor core, 1.0 us, and 2.0 us here: the softmax of a row (128 exponentials on
-// the unit that four warps share, maximum, sum, tensor memory to registers and back)
-// takes 0.95 us from S to P, and what the two halves of the rows overlap of it with the
-// other's products is 1.0 us.  The rest is a run's beginning (place, Q, the first tile:
-// 10 us) and its end (pieces out and merged: 15 us).  4 chunks of 512 tokens behind
-// 7680 positions (32 query heads, 8 of keys, d = 128): 136 us, the products' rate a
-// half of the peak; 814 us in the few-rows kernel.
+// the tensor core, and 3800 here.  Of the chain of each half of the rows a row's
+// softmax takes 1500 from S to P (128 exponentials, maximum, sum, tensor memory to
+// registers and back) and its products 1500 instead of 1024, as they share the shared
+// memory with the warps that expand; the rest is waiting for the other half's
+// products.  To the tiles come a run's beginning (place, Q, the first tile: 10 us) and
+// its end (pieces out and merged: up to 15 us).  4 chunks of 512 tokens behind 7680
+// positions (16 query heads, 4 of keys, d = 128): 134 us, half of the tensor core's
+// peak rate; 814 us in the few-rows kernel.
 #include <algorithm>
 #include <atomic>
 #include <climits>
