@@ -336,10 +336,12 @@ struct WCfg {
   static constexpr int kRawHalf = kCodes + kScales;
   static constexpr int kRawSlots = D == 256 ? 2 : 3;         // halves (K or V of a tile) under way, in turn
   static constexpr int kBarOff = kRawOff + kRawSlots * kRawHalf;
-  // rows on their way to the output lie over Q, where they fit
+  // A warp's rows on their way to the output lie over its own rows of Q, where they fit:
+  // the other warps of the 128 rows may be at the next unit's Q already.
   static constexpr int kTurnRow = 64 + 16;
   static constexpr int kTurnSlot = 32 * kTurnRow;
-  static constexpr bool kTurns = 4 * kTurnSlot <= kQBytes;
+  static constexpr int kWarpQ = 32 * kRowBytes;              // of a column block
+  static constexpr bool kTurns = kTurnSlot <= kWarpQ;
   // q_full, o_full, o_last, o_free, s_full, p_full [2]; k_full, v_full, k_empty, v_empty [R];
   // ready, done [2]; meet, drain; raw_full, raw_empty [3]; turn [2]
   static constexpr int kNumBars = 12 + 4 * kRing + 4 + 2 + 6 + 2;
@@ -769,7 +771,7 @@ __global__ void __launch_bounds__(WCfg<D>::kThreads, 1) sdpa_paged4_many(const _
           tmem_ld_wait();
           reg_fence(o);
         };
-        uint8_t* turn = smem + sub * C::kQBytes + quarter * C::kTurnSlot;   // (the products are done with Q)
+        uint8_t* turn = smem + sub * C::kQBytes + quarter * C::kWarpQ;   // (the products are done with Q)
         const int rows_here = rows - (sub * 128 + quarter * 32);
         if (busy && active) {
           const float f = ll > 0.f ? p.v_unit / ll : 0.f;
