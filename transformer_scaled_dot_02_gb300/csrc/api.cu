@@ -1189,8 +1189,10 @@ sdpa_status sdpa_paged4_forward(const void* q, const void* k_pages, const void* 
   // (positions stay below 2^30)
   p.window = window == 0 || window >= (1 << 30) ? INT_MAX : window;
   p.sinks = std::min(sinks, 1 << 30);
-  p.scale_log2 = effective_scale(scale, d) * 1.4426950408889634f;
-  p.k_unit = std::ldexp(1.f, k_exp);
+  int exponent;
+  const double fraction = std::frexp(effective_scale(scale, d) * 1.4426950408889634, &exponent);   // of 1/2 to 1
+  p.score_scale = static_cast<float>(2.0 * fraction);
+  p.score_exp = exponent - 1 + k_exp;
   p.v_unit = std::ldexp(1.f, v_exp);
   if (sdpa::launch_sdpa_paged4(p, d, static_cast<cudaStream_t>(stream)) != cudaSuccess) return SDPA_ERR_CUDA;
   if (!v.wide) return SDPA_OK;

@@ -204,7 +204,11 @@ struct Paged4Params {
   long long page_bytes, page_stride;  // of one key-value head, of all of them
   int few_rows;               // rows of a head (new tokens x group) of a sequence that is the few-rows kernel's, at most
   int window, sinks;          // window: keys p - window + 1 .. p (INT_MAX: all)
-  float scale_log2, k_unit, v_unit;   // scale log2(e); 2^exp
+  // scale log2(e) 2^k_exp = score_scale 2^score_exp, score_scale from 1 to 2: the
+  // exponents may be far beyond a float's until a row's own is added
+  float score_scale;
+  int score_exp;
+  float v_unit;               // 2^v_exp
 };
 constexpr int kPaged4MinPage = 16;
 constexpr int kPaged4MaxRuns = 3 * 160;

@@ -1,5 +1,5 @@
 // What the kernels that write and read paged caches share: the rotation's
-// angles and the place of a packed row.
+// angles, the place of a packed row, the scale of a cache in 4 bits' scores.
 #pragma once
 
 #include <climits>
@@ -118,6 +118,16 @@ __device__ __forceinline__ RowPlace place_of_rows(const Params& p, int t0, int r
     s = lo < p.b && p.q_starts[lo] <= t ? lo : -1;
   }
   return place_in_seq(p, t, s, lane < rows);
+}
+
+// What turns a score of a cache in 4 bits, of a row that was scaled by 2^up, into log2
+// units: score_scale 2^(score_exp - up).  The exponents are added before anything is
+// multiplied: up goes from -114 to 120, k_exp from -32 to 32 and the scale over all
+// floats, so that products of two of them may leave the range that the three's is in.
+// Below 2^-126 all weights are one (scores are below 2^34), and a factor of zero would
+// make a masked score of -infinity a NaN; up to 2^91 its products with scores are finite.
+__device__ __forceinline__ float score_factor(const Paged4Params& p, int up) {
+  return p.score_scale * __uint_as_float(static_cast<uint32_t>(127 + min(max(p.score_exp - up, -126), 90)) << 23);
 }
 
 }  // namespace sdpa

@@ -40,6 +40,7 @@
 #include <type_traits>
 
 #include "kernels.h"
+#include "paged.cuh"
 #include "ptx.cuh"
 
 namespace sdpa {
@@ -670,7 +671,6 @@ __global__ void __launch_bounds__(kThreads, NCfg<D, NT>::kCtas) sdpa_paged4_few(
         const int ex = static_cast<int>(top >> 7);           // biased; rows of zeros, infinities and NaN stay
         const int up = top == 0 || ex == 255 ? 0 : max(-120, min(120, 13 + 127 - ex));
         const float f = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
-        const float back = __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
 #pragma unroll
         for (int k = 0; k < KS; ++k) {
           const uint2 v = raw[nt][k];
@@ -678,8 +678,7 @@ __global__ void __launch_bounds__(kThreads, NCfg<D, NT>::kCtas) sdpa_paged4_few(
           qf[k][nt][1] = pack_f16x2(__uint_as_float(v.y << 16) * f, __uint_as_float(v.y & 0xffff0000u) * f);
         }
 #pragma unroll
-        for (int c = 0; c < 2; ++c)   // (never 0, which a masked score of -infinity would make a NaN)
-          sc[nt][c] = fmaxf(__shfl_sync(0xffffffffu, back, (2 * t + c) * 4) * p.k_unit * p.scale_log2, 1e-37f);
+        for (int c = 0; c < 2; ++c) sc[nt][c] = score_factor(p, __shfl_sync(0xffffffffu, up, (2 * t + c) * 4));
       }
       float o[KS][NT][4], m[NT][2], l[NT][2];
 #pragma unroll

@@ -32,6 +32,7 @@
 #include <climits>
 
 #include "kernels.h"
+#include "paged.cuh"
 #include "ptx.cuh"
 
 namespace sdpa {
@@ -606,7 +607,7 @@ __global__ void __launch_bounds__(WCfg<D>::kThreads, 1) sdpa_paged4_many(const _
           constexpr int kLanes = D / 8, kRowsAtOnce = 32 / kLanes, kLoads = 32 / kRowsAtOnce, kAtOnce = 4;
           uint8_t* q_smem = smem + sub * C::kQBytes;
           const int row0 = sub * 128 + quarter * 32;
-          float back = 1.f;
+          int up_here = 0;                                   // of this lane's row
 #pragma unroll 1
           for (int x0 = 0; x0 < kLoads; x0 += kAtOnce) {
             uint4 v[kAtOnce];
@@ -639,14 +640,12 @@ __global__ void __launch_bounds__(WCfg<D>::kThreads, 1) sdpa_paged4_many(const _
               *reinterpret_cast<uint4*>(q_smem + (c / kChunks) * C::kQBox +
                                         swizzle_offset<C::kRowBytes>(quarter * 32 + r, c % kChunks)) =
                   make_uint4(h[0], h[1], h[2], h[3]);
-              // 2^-up to the lane whose row it is
-              const float b = __shfl_sync(0xffffffffu, __uint_as_float(static_cast<uint32_t>(127 - up) << 23),
-                                          (lane % kRowsAtOnce) * kLanes);
-              if (lane / kRowsAtOnce == x0 + x) back = b;
+              // to the lane whose row it is
+              const int its = __shfl_sync(0xffffffffu, up, (lane % kRowsAtOnce) * kLanes);
+              if (lane / kRowsAtOnce == x0 + x) up_here = its;
             }
           }
-          // (never 0, which a masked score of -infinity would make a NaN)
-          sc = fmaxf(back * p.k_unit * p.scale_log2, 1e-37f);
+          sc = score_factor(p, up_here);
           fence_proxy_async_smem();
           mbar_arrive(q_full + sub);
           if (at.of > 1 && tid == 0) open_count(p.counts + slot_of(at, 0));
