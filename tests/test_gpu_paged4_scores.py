@@ -1,9 +1,12 @@
-"""What the scores of the attention over the cache in 4 bits go through, in the kernel
-for few rows (sequences of up to 32 rows a key-value head) and the one for many:
-ranges of queries, units and scales whose product is ordinary.  Against the plain fp64 implementation and bounds of paged4_util.py."""
+"""What the scores and weights of the attention over the cache in 4 bits go through,
+in the kernel for few rows (sequences of up to 32 rows a key-value head) and the one
+for many: ranges of queries, units and scales whose product is ordinary, weak keys
+behind strong ones.  Against the plain fp64 implementation and bounds of paged4_util.py."""
 import numpy as np
 import pytest
 
+import paged4_util as p4
+from gpu_util import host
 from test_gpu_paged4 import _case, _check, _run
 
 pytestmark = pytest.mark.gpu
@@ -28,3 +31,33 @@ def test_ranges_that_only_the_whole_product_fits(rows, d, k_std, q_by, scale, k_
     c["q"][1, 2] = 0.0
     scale = float(np.float32(scale / np.sqrt(d / 64)))
     _check(_run(c, scale=scale), c, scale)
+
+
+@pytest.mark.parametrize("rows", ["few", "many"])
+@pytest.mark.parametrize("d", [16, 64, 128, 256])
+def test_weak_keys_behind_a_strong_one_count(rows, d):
+    """The first key of a sequence has nearly all of the weight, and every other one
+    2^-25.6 of its: their values are all that the output has.  A weight is off by half
+    a step of fp16 at 2^-7 of it: 2^-11 of itself, or 2^-32."""
+    new, n = (2, 511) if rows == "few" else (200, 900)
+    rng = np.random.default_rng(4820 + d)
+    c = _case(rng, [new], [n], 2, 1, d, 32, exps=(0, 0))
+    k, v = np.zeros((n, 1, d), np.float32), np.ones((n, 1, d), np.float32)
+    k[:, 0, 0], k[0, 0, 0] = -6.0, 6.0
+    v[0] = 0.0
+    v[:, 0, ::16] = 6.0
+    v[0] = 0.0
+    made = [p4.pages_of(c["cache"], [x], 0xFF, 0) for x in (k, v)]
+    q = np.zeros((new, 2, d), np.float32)
+    q[..., 0] = 1.0
+    c.update(pages=[m[0] for m in made], held=[m[1] for m in made], q=q)
+    assert np.array_equal(c["held"][0][0], k) and np.array_equal(c["held"][1][0], v)
+    scale = float(np.float32(25.6 / 12.0 * np.log(2.0)))
+    got = host(_run(c, scale=scale))
+    for i in range(new):
+        weak = np.float64(n - new + i) * np.exp(-12.0 * scale)
+        want = weak / (1.0 + weak) * v[1, 0]
+        # fp32 scores and sums as in paged4_util: e = d 2^-23 scale 6
+        share = 2.0 ** -11 + 2.1 * d * 2.0 ** -23 * scale * 6.0 + 2.0 ** -14 + 2.0 ** -8
+        bound = (share * want + 2.0 ** -32 * (n - new + i) * v[1, 0]) * (1 + 2.0 ** -8)
+        assert np.all(np.abs(got[i] - want) <= bound), (i, got[i, 0, :2], want[:2], bound[:2])

@@ -1,5 +1,6 @@
 // What the kernels that write and read paged caches share: the rotation's
-// angles, the place of a packed row, the scale of a cache in 4 bits' scores.
+// angles, the place of a packed row, and the scales of a cache in 4 bits' scores
+// and weights.
 #pragma once
 
 #include <climits>
@@ -119,6 +120,14 @@ __device__ __forceinline__ RowPlace place_of_rows(const Params& p, int t0, int r
   }
   return place_in_seq(p, t, s, lane < rows);
 }
+
+// The softmax weights of a cache in 4 bits enter the products as fp16.  They are up to
+// 2^8 where the running maximum lags, so times 2^7 they stay below fp16's 2^16: half a
+// step is at most 2^-11 of a weight, and 2^-32 of the largest for those below 2^-21 of
+// it.  (Times 1 it was 2^-25: one strong key made the weaker ones at 2^-25 of its weight
+// drop out of O, but not out of the sum l, however many they were.)  bf16, of which half a
+// step is up to 2^-8, would cost as much as the result's own rounding.
+constexpr float kWeightUp = 7.f;   // log2
 
 // What turns a score of a cache in 4 bits, of a row that was scaled by 2^up, into log2
 // units: score_scale 2^(score_exp - up).  The exponents are added before anything is

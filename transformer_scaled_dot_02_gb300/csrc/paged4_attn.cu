@@ -32,8 +32,8 @@
 // Codes become fp16 in pairs (cvt.f16x2.e2m1x2) and are multiplied by the block's
 // scale, which is exact.  Q is bf16, whose range fp16 has not: each row is scaled
 // by a power of two to a largest element of 2^13 and more, which keeps every bit
-// of elements down to 2^-27 of it.  The softmax weights are rounded to fp16
-// (2^-12), P of S^T turned by movmatrix.
+// of elements down to 2^-27 of it.  The softmax weights are rounded to fp16, times
+// 2^7 (paged.cuh), P of S^T turned by movmatrix.
 #include <algorithm>
 #include <atomic>
 #include <climits>
@@ -804,7 +804,8 @@ __global__ void __launch_bounds__(kThreads, NCfg<D, NT>::kCtas) sdpa_paged4_few(
         uint32_t pb[2][NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          const float m0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0], m1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
+          const float m0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0] - kWeightUp;
+          const float m1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1] - kWeightUp;
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
             const float p0 = ex2_approx(fmaf(s[x >> 1][nt][2 * (x & 1)], sc[nt][0], -m0));

@@ -16,7 +16,7 @@
 // products (tcgen05.mma, kind::f16: S = Q K^T into tensor memory, O += P V with P
 // from there); four for each 128 rows do the softmax, a row a thread.  Queries are
 // scaled by a power of two for each row to fit fp16, the softmax weights are rounded
-// to fp16 (2^-12: bf16's 2^-9 would cost a third of the result's own half step).
+// to fp16, times 2^7 (paged.cuh).
 //
 // What bounds it: a key tile (128 keys, 256 rows, d = 128) takes 2048 clock cycles of
 // the tensor core, and 3800 here.  Of the chain of each half of the rows a row's
@@ -725,7 +725,7 @@ __global__ void __launch_bounds__(WCfg<D>::kThreads, 1) sdpa_paged4_many(const _
                   tmem_st_chunk(lane_base + C::kOCol + c * 16, o);
                 }
               }
-              const float m_sub = m_used == -INFINITY ? 0.f : m_used;
+              const float m_sub = m_used == -INFINITY ? 0.f : m_used - kWeightUp;
               const float2 neg2 = make_float2(-m_sub, -m_sub);
               float2 acc[4];
 #pragma unroll
