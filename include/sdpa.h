@@ -383,7 +383,8 @@ sdpa_status sdpa_paged4_read(const void* k_pages, const void* v_pages, void* k_o
  * scaled by a power of two for each row (elements down to 2^-27 of the row's
  * largest keep every bit), keys and values as what the codes stand for, and the
  * softmax weights rounded to fp16 times a power of two (off by at most 2^-11 of
- * themselves, or 2^-32 of the largest).  No block waits for another.
+ * themselves, or 2^-30 of the largest).  Scores scale q k are to be below 2^26.  No
+ * block waits for another.
  */
 size_t sdpa_paged4_workspace_size(int b, int n_tokens, int h, int h_kv, int d, int page_size,
                                   int pages_per_seq);

@@ -121,13 +121,21 @@ __device__ __forceinline__ RowPlace place_of_rows(const Params& p, int t0, int r
   return place_in_seq(p, t, s, lane < rows);
 }
 
-// The softmax weights of a cache in 4 bits enter the products as fp16.  They are up to
-// 2^8 where the running maximum lags, so times 2^7 they stay below fp16's 2^16: half a
-// step is at most 2^-11 of a weight, and 2^-32 of the largest for those below 2^-21 of
-// it.  (Times 1 it was 2^-25: one strong key made the weaker ones at 2^-25 of its weight
-// drop out of O, but not out of the sum l, however many they were.)  bf16, of which half a
-// step is up to 2^-8, would cost as much as the result's own rounding.
-constexpr float kWeightUp = 7.f;   // log2
+// The softmax weights of a cache in 4 bits enter the products as fp16, relative to what a
+// row's largest scaled score was, times 2^kWeightUp: half a step is at most 2^-11 of a
+// weight, and 2^-30 of the largest for those below 2^-19 of it.  (Times 1 it was 2^-25: one
+// strong key made the weaker ones at 2^-25 of its weight drop out of O, but not out of the
+// sum l, however many they were.)  bf16, of which half a step is up to 2^-8, would cost as
+// much as the result's own rounding.
+// What is kept and published is the reference itself, the largest score less kWeightUp: for
+// scores from 2^24 on that is rounded, and weights of two references can be added all the
+// same.  It moves when a score is more than kWeightMost above it.  For scores below 2^27 the
+// sum and the difference are off by at most 3, and a score that is the difference of a fused
+// product by half its step, 4: weights stay below fp16's 2^16.
+// (So a reference lags by up to 6.  By 8, 6 and 4: 4 chunks of 512 tokens behind 7680
+// positions 132.4, 132.2 and 134.6 us, with queries three times as large 143, 146 and 147, as
+// it moves more often.)
+constexpr float kWeightUp = 5.f, kWeightMost = 11.f;   // log2
 
 // What turns a score of a cache in 4 bits, of a row that was scaled by 2^up, into log2
 // units: score_scale 2^(score_exp - up).  The exponents are added before anything is

@@ -50,7 +50,6 @@ constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kKeys = 32;                  // per tile
 constexpr int kKeysShift = 5;
-constexpr float kRescaleThreshold = 8.0f;  // log2 units, as in the other forward kernels
 // What a unit costs beside its key tiles, in key tiles.
 // (32 single tokens of 4096 to 8192 positions: 39.3, 37.9 and 37.3 us with 8, 14 and 20;
 // 32 of 2000 to 4000 with one key-value head: 25.2, 21.9 and 20.5)
@@ -770,7 +769,7 @@ __global__ void __launch_bounds__(kThreads, NCfg<D, NT>::kCtas) sdpa_paged4_few(
           }
         }
         {
-          // ---- the running maxima: they move when one grew by more than the threshold
+          // ---- the references (m): they move when a score is too far above one
           bool need = false;
           float top[NT][2];
 #pragma unroll
@@ -778,7 +777,7 @@ __global__ void __launch_bounds__(kThreads, NCfg<D, NT>::kCtas) sdpa_paged4_few(
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
               top[nt][c] = fmaxf(fmax3(s[0][nt][c], s[0][nt][2 + c], s[1][nt][c]), s[1][nt][2 + c]) * sc[nt][c];
-              need |= top[nt][c] > m[nt][c] + kRescaleThreshold;
+              need |= top[nt][c] > m[nt][c] + kWeightMost;
             }
           if (__any_sync(0xffffffffu, need)) {
 #pragma unroll
@@ -788,7 +787,7 @@ __global__ void __launch_bounds__(kThreads, NCfg<D, NT>::kCtas) sdpa_paged4_few(
                 float x = top[nt][c];
 #pragma unroll
                 for (int y = 4; y < 32; y <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, y));
-                x = fmaxf(x, m[nt][c]);
+                x = fmaxf(x - kWeightUp, m[nt][c]);
                 const float f = x == -INFINITY ? 1.f : ex2_approx(m[nt][c] - x);
                 m[nt][c] = x;
                 l[nt][c] *= f;
@@ -804,8 +803,7 @@ __global__ void __launch_bounds__(kThreads, NCfg<D, NT>::kCtas) sdpa_paged4_few(
         uint32_t pb[2][NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          const float m0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0] - kWeightUp;
-          const float m1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1] - kWeightUp;
+          const float m0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0], m1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
             const float p0 = ex2_approx(fmaf(s[x >> 1][nt][2 * (x & 1)], sc[nt][0], -m0));

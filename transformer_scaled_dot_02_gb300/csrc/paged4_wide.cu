@@ -38,7 +38,6 @@
 namespace sdpa {
 namespace {
 
-constexpr float kRescaleThreshold = 8.0f;  // log2 units, as in the other forward kernels
 // What a unit costs beside its keys (loading Q, storing O), in keys.  (A prompt of 4096: 99, 90 and
 // 94 us with 256, 512 and 1024; 16 sequences of 128 rows 54, 50 and 52.)
 constexpr int kStartKeys = 512;
@@ -690,14 +689,14 @@ __global__ void __launch_bounds__(WCfg<D>::kThreads, 1) sdpa_paged4_many(const _
 #pragma unroll
                 for (int x = 0; x < 8; ++x) mx8[x] = fmax3(mx8[x], s[c + x], c + 8 + x < kBN ? s[c + 8 + x] : s[c + x]);
               const float mx = fmax3(fmax3(mx8[0], mx8[1], mx8[2]), fmax3(mx8[3], mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7]));
-              // the running maximum moves when it grew by more than the threshold
-              const float m_new = fmaxf(m_used, mx * sc);
+              // the reference moves when a score is too far above it
+              const float top = mx * sc, m_new = top - kWeightUp;
               float alpha = 1.f;
               bool rescale = false;
               if (i == 0) {
                 m_used = m_new;
               } else {
-                const bool need = valid && m_new > m_used + kRescaleThreshold;
+                const bool need = valid && top > m_used + kWeightMost;
                 rescale = __any_sync(0xffffffffu, need);
                 if (need) {
                   alpha = ex2_approx(m_used - m_new);
@@ -725,7 +724,7 @@ __global__ void __launch_bounds__(WCfg<D>::kThreads, 1) sdpa_paged4_many(const _
                   tmem_st_chunk(lane_base + C::kOCol + c * 16, o);
                 }
               }
-              const float m_sub = m_used == -INFINITY ? 0.f : m_used - kWeightUp;
+              const float m_sub = m_used == -INFINITY ? 0.f : m_used;
               const float2 neg2 = make_float2(-m_sub, -m_sub);
               float2 acc[4];
 #pragma unroll
