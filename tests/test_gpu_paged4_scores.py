@@ -1,7 +1,8 @@
 """What the scores and weights of the attention over the cache in 4 bits go through,
 in the kernel for few rows (sequences of up to 32 rows a key-value head) and the one
-for many: ranges of queries, units and scales whose product is ordinary, weak keys
-behind strong ones.  Against the plain fp64 implementation and bounds of paged4_util.py."""
+for many: units of keys, ranges of queries, units and scales whose product is
+ordinary, weak keys behind strong ones, scores of many bits.  Against the plain fp64
+implementation and bounds of paged4_util.py."""
 import numpy as np
 import pytest
 
@@ -25,12 +26,21 @@ ROWS = {"few": ([3, 1], [50, 700]), "many": ([200, 1], [500, 700])}
     (2.0 ** 30, 2.0 ** 78, 1.25 * 2.0 ** -143, 32)])
 def test_ranges_that_only_the_whole_product_fits(rows, d, k_std, q_by, scale, k_exp):
     rng = np.random.default_rng(4800 + d)
-    # (queries like keys of k_std, and q_by times that; a row of zeros, keys of zeros)
+    # (queries like keys of k_std, and q_by times that; a row of zeros)
     c = _case(rng, *ROWS[rows], 4, 2, d, 16, std=k_std, exps=(k_exp, -3))
     c["q"] = (c["q"] * np.float32(q_by)).astype(np.float32)
     c["q"][1, 2] = 0.0
     scale = float(np.float32(scale / np.sqrt(d / 64)))
     _check(_run(c, scale=scale), c, scale)
+
+
+@pytest.mark.parametrize("rows", ROWS)
+@pytest.mark.parametrize("d", [16, 64, 128, 256])
+@pytest.mark.parametrize("k_exp", [-3, 5])
+def test_units_of_keys(rows, d, k_exp):
+    rng = np.random.default_rng(4810 + d + k_exp)
+    c = _case(rng, *ROWS[rows], 6, 2, d, 32, exps=(k_exp, 2), window=300, sinks=5)
+    _check(_run(c), c)
 
 
 @pytest.mark.parametrize("rows", ["few", "many"])
