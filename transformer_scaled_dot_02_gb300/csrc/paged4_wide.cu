@@ -63,17 +63,20 @@ struct Plan {
   static constexpr int kBN = 1 << kBNShift;                  // keys of a tile
   const Paged4Params& p;
   __device__ explicit Plan(const Paged4Params& params) : p(params) {}
+  // (What the caller's kernels wrote is read past L1, here and below: this kernel does not
+  // wait for them itself, the one before it has.)
+  __device__ __forceinline__ int start_of(int s) const { return __ldcg(p.q_starts + s); }
   // rows of a head
   __device__ __forceinline__ long long rows(int s) const {
-    const int start = min(max(p.q_starts[s], 0), p.n_tokens);
-    return 1ll * (min(max(p.q_starts[s + 1], start), p.n_tokens) - start) * p.group;
+    const int start = min(max(start_of(s), 0), p.n_tokens);
+    return 1ll * (min(max(start_of(s + 1), start), p.n_tokens) - start) * p.group;
   }
   __device__ __forceinline__ Seq seq(int s) const {
     Seq q;
     const int cap = p.pages_per_seq << p.page_shift;
-    q.start = min(max(p.q_starts[s], 0), p.n_tokens);
-    q.n = min(max(p.q_starts[s + 1], q.start), p.n_tokens) - q.start;
-    q.len = min(max(p.kv_lengths[s], 0), cap);
+    q.start = min(max(start_of(s), 0), p.n_tokens);
+    q.n = min(max(start_of(s + 1), q.start), p.n_tokens) - q.start;
+    q.len = min(max(__ldcg(p.kv_lengths + s), 0), cap);
     const long long rows = 1ll * q.n * p.group;
     q.tiles = rows > p.few_rows ? static_cast<int>((rows + R - 1) / R) : 0;
     return q;
@@ -554,8 +557,9 @@ __global__ void __launch_bounds__(WCfg<D>::kThreads, 1) sdpa_paged4_many(const _
   // (not before the block holds its tensor memory: the next kernel's block could be
   // given it, and then wait for this grid, which waits for the memory)
   griddep_launch_dependents();
-  // The kernel before is the one for the other sequences: it began when the one before
-  // it was over, and is waited for at the end only.
+  // The kernel before is the one for the other sequences: all of its blocks had waited for
+  // the one before it before this one could begin, so everything that a call reads is in L2.
+  // That kernel itself is waited for at the end only.
 
   const int cta = static_cast<int>(blockIdx.x);
   const bool any = find_place(plan, &sched, &units[0], cta) && units[0].begin != LLONG_MAX;
@@ -615,7 +619,7 @@ __global__ void __launch_bounds__(WCfg<D>::kThreads, 1) sdpa_paged4_many(const _
               const int r = ((x0 + x) * kRowsAtOnce + lane / kLanes) & 31;
               const long long src = __shfl_sync(0xffffffffu, mine, r);
               v[x] = make_uint4(0, 0, 0, 0);
-              if (row0 + r < rows && x0 + x < kLoads) v[x] = reinterpret_cast<const uint4*>(src)[lane % kLanes];
+              if (row0 + r < rows && x0 + x < kLoads) v[x] = __ldcg(reinterpret_cast<const uint4*>(src) + lane % kLanes);
             }
 #pragma unroll
             for (int x = 0; x < kAtOnce; ++x) {
@@ -1063,7 +1067,7 @@ __global__ void __launch_bounds__(WCfg<D>::kThreads, 1) sdpa_paged4_many(const _
         auto ask = [&](int i) -> int {
           const int key = (at.tile(i) << kBNShift) + lane * 16;
           const bool seen = i < n && lane < kGroups && key <= hi_pos && (key + 15 > hidden || key < p.sinks);
-          return seen ? pages[key >> p.page_shift] : -1;
+          return seen ? __ldcg(pages + (key >> p.page_shift)) : -1;
         };
         int page = ask(0), shown = page;
 #pragma unroll 1
