@@ -243,6 +243,7 @@ __device__ bool find_place(const Plan<R>& plan, Schedule* sh, Unit* first, int c
       pieces[x] = static_cast<uint32_t>(min(1ll << 20, pieces[x] + plan.pieces(tiles, x) * units));
   }
   if (tid == 0) first->begin = LLONG_MAX;                    // (no unit, should the lengths change meanwhile)
+  __syncwarp();                                              // (another lane's unit comes after it)
   uint32_t all[kLevels + 1];                                 // the last: items
 #pragma unroll
   for (int x = 0; x < kLevels; ++x) all[x] = __reduce_add_sync(0xffffffffu, pieces[x]);
