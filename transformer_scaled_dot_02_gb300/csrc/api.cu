@@ -527,8 +527,14 @@ Paged4Division paged4_divide(int b, int n_tokens, int h_kv, int group, int d, lo
   v.few_runs = runs(std::min(sdpa::kPaged4MaxRuns, sdpa::paged4_resident_ctas(d, rows) * sdpa::device_sm_count()),
                     sdpa::paged4_most_runs(units, max_len));
   v.few_slot = round256(static_cast<size_t>(rows) * (d * 4 + 8));
-  // as many tokens as sequences: single tokens, in all likelihood, and the few-rows
-  // kernel takes whatever there is
+  // No more tokens than sequences: single tokens, in all likelihood, and the few-rows
+  // kernel takes whatever there is.  The other kernel's launch would cost a step of 32 single
+  // tokens 2.8 us of 35.7 for nothing, and where a group has more than 32 heads it loses (16
+  // single tokens over 2000 to 4000 positions, one key-value head, groups of 64 and 128: 22.9
+  // and 31.0 us here, 36.6 and 42.7 there).  What it would gain: one chunk of 500 tokens over
+  // 2000 and 8000 positions in 512 slots, all others empty, takes 75 and 229 us instead of 46
+  // and 71 (16 / 4 heads of 128); over 500 it makes no difference, and 40 tokens over 2000
+  // take 18 us instead of 38.
   v.wide = n_tokens > b && all_rows > sdpa::kPaged4FewRows;
   v.wide_runs = 0;
   v.wide_slot = 0;

@@ -78,9 +78,11 @@ __device__ __forceinline__ float e4m3_value(uint32_t byte) {
 // columns pair up, of a key or value a block (the rotation reads its partners'
 // columns beside it).  Blocks take kTokens tokens: their angles once, into shared
 // memory, then every head of theirs.  16384 tokens (16 query heads, 4 of keys, d =
-// 128, all columns rotated): 45 us, 4 TB/s, issue slots 70 % busy, by the rotation
-// and the quantising (38 us where the queries were only copied, 35 where nothing
-// was rotated or quantised).  For a few tokens the launch and three dependent reads: 2.9 us for 8.
+// 128, all columns rotated): 45 us, 4 TB/s.  10 of them are the rotation and the
+// quantising (38 us where the queries were only copied, 35 where nothing was rotated or
+// quantised; issue slots are 70 % busy).  What keeps those 35 above the bytes' 26 is not
+// known; the next item's loads ahead of this one's work did not help.  For a few tokens the
+// launch and three dependent reads: 2.9 us for 8.
 //
 // The rotation is in fp32 with angles good to 1.3e-6.  Where that leaves open
 // which scale or code is the nearest, some element of a block lies within kSlack

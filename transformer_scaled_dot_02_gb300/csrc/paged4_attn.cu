@@ -17,8 +17,10 @@
 // warps meet.  The copies are cp.async, 16 bytes a lane, 9 instructions a tile at
 // d = 128: as bulk copies, four for the codes and scales of K and V, a tile took
 // the SM's copy engine 600 clock cycles (41 us instead of 38 for 32 sequences of
-// 4096 to 8192 positions).  A step for single tokens is bound by reading the cache, so what
-// counts is that few instructions stand between a byte and its products.  They
+// 4096 to 8192 positions).  What bounds a step for single tokens is how long a tile's chain
+// of loads, conversions, products and exponentials is for the few warps that registers
+// leave room for (12 on an SM: issue slots 43 % busy, HBM 38 %), so what counts is that few
+// instructions stand between a byte and its products.  They
 // are mma.sync on registers: tcgen05 takes its operands from shared memory (or A
 // from tensor memory), where the expanded numbers, 4 bytes for each byte of the
 // cache, would be written and read again, more than an SM's shared memory moves
