@@ -34,8 +34,8 @@
 // Codes become fp16 in pairs (cvt.f16x2.e2m1x2) and are multiplied by the block's
 // scale, which is exact.  Q is bf16, whose range fp16 has not: each row is scaled
 // by a power of two to a largest element of 2^13 and more, which keeps every bit
-// of elements down to 2^-27 of it.  The softmax weights are rounded to fp16, times
-// 2^7 (paged.cuh), P of S^T turned by movmatrix.
+// of elements down to 2^-27 of it.  The softmax weights are taken against a
+// reference that lags and rounded to fp16 (paged.cuh), P of S^T turned by movmatrix.
 #include <algorithm>
 #include <atomic>
 #include <climits>

@@ -15,8 +15,8 @@
 // (exact) into the tensor core's swizzled operands; one for each 128 rows issues the
 // products (tcgen05.mma, kind::f16: S = Q K^T into tensor memory, O += P V with P
 // from there); four for each 128 rows do the softmax, a row a thread.  Queries are
-// scaled by a power of two for each row to fit fp16, the softmax weights are rounded
-// to fp16, times 2^7 (paged.cuh).
+// scaled by a power of two for each row to fit fp16, the softmax weights are taken
+// against a reference that lags and rounded to fp16 (paged.cuh).
 //
 // What bounds it: a key tile (128 keys, 256 rows, d = 128) takes 2048 clock cycles of
 // the tensor core, and 3800 here.  Of the chain of each half of the rows a row's
