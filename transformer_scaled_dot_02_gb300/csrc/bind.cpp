@@ -97,10 +97,10 @@ bool pages_overlap(const at::Tensor& k, const at::Tensor& v) {
 }
 
 // Packed rows [n_tokens, heads, d] whose heads are dense; the stride from token
-// to token (a single token's says nothing).
+// to token (a single token's says nothing, and no stride of a tensor without elements does).
 bool check_rows(const at::Tensor& x, int64_t n_tokens, int64_t heads, const Cache& c, long long* stride) {
   if (!plain(x, at::kBFloat16, c.device) || x.dim() != 3 || x.size(0) != n_tokens || x.size(1) != heads ||
-      x.size(2) != c.d || x.stride(2) != 1 || (x.stride(1) != c.d && heads != 1))
+      x.size(2) != c.d || (x.numel() > 0 && (x.stride(2) != 1 || (x.stride(1) != c.d && heads != 1))))
     return false;
   *stride = n_tokens > 1 ? x.stride(0) : heads * c.d;
   return true;
